@@ -24,6 +24,7 @@ __all__ = [
     "TsrError", "build", "lib", "make_mask", "Mask", "Plan", "tsr_plan", "tsr_plan_update",
     "tsr_bsa_forward",
     "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_temporal_permute", "tsr_svg_route",
+    "tsr_rope", "tsr_rope_backward", "tsr_block_select",
     "tsr_attention_host",
     "tsr_regime_load",
     "tsr_regime_lookup", "tsr_abi_version", "UNIFORM", "SEGMENTS", "SVG", "KEYLIST",
@@ -64,6 +65,24 @@ class _Mask(ctypes.Structure):
     ]
 
 
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis_dim", ctypes.c_int32 * 4), ("halves", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("positions", ctypes.c_void_p), ("positions_per_batch", ctypes.c_int32),
+                ("grid", ctypes.c_int32 * 4)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("H", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
+
+class _SelectDesc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("B", "H", "N", "d", "bq", "bk", "keep", "first", "diagonal")]
+
+
 class _Request(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("plan", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
@@ -94,7 +113,8 @@ class _Regime(ctypes.Structure):
 _LIB = None
 EXPORTS = ("tsr_abi_version", "tsr_status_string", "tsr_last_error", "tsr_plan", "tsr_plan_update",
            "tsr_bsa_forward", "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_plan_destroy", "tsr_plan_get_stats",
-           "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_attention_host",
+           "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope",
+           "tsr_block_select_workspace", "tsr_block_select", "tsr_attention_host",
            "tsr_release_host_buffers", "tsr_regime_load", "tsr_regime_lookup")
 
 
@@ -131,6 +151,9 @@ def lib():
         "tsr_plan_export": ([P, P, P], ctypes.c_int),
         "tsr_temporal_permute": ([P, P, I32, I32, I32, I32, I32, P, I32, P], ctypes.c_int),
         "tsr_svg_route": ([P, P, P, I32, I32, I32, I32, I32, I32, P, I32, P, P, P], ctypes.c_int),
+        "tsr_rope": ([P, P, I32, P], ctypes.c_int),
+        "tsr_block_select_workspace": ([P, P], ctypes.c_int),
+        "tsr_block_select": ([P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "tsr_attention_host": ([P, P, P, P, P, P, P], ctypes.c_int),
         "tsr_release_host_buffers": ([], None),
         "tsr_regime_load": ([ctypes.c_char_p], ctypes.c_int),
@@ -166,6 +189,25 @@ def _dptr(t: Optional[torch.Tensor]) -> int:
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
+
+
+def _on_device(*tensors) -> None:
+    """CUDA tensors of the current device: the library launches there."""
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensor arguments must be CUDA tensors")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _allocating_on(stream):
+    """Context in which new tensors belong to the stream that the call runs on, so
+    that a workspace freed on return is not reused before the call's kernels end."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 class Mask:
@@ -339,6 +381,109 @@ def tsr_svg_route(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_frames: i
                                temporal_radius, ctypes.cast(arr, ctypes.c_void_p), len(smp),
                                _dptr(stats), _dptr(head_kind), _stream_ptr(stream)))
     return stats, head_kind
+
+
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = None,
+             theta: float = 10000.0, halves: bool = False, inverse: bool = False, out=None,
+             stream=None):
+    """Rotary positions over several axes (see include/tsr.h).
+
+    ``x``: a tensor [B, H, N, d] (bf16, fp16 or fp32; any strides, d contiguous:
+    a [B, N, H, d] projection goes in as ``x.transpose(1, 2)``), or a sequence of
+    up to four that differ in H and strides only (Q and K), rotated in one launch.
+    ``axis_dims``: channels per axis.  ``grid``: tokens per axis, in row-major
+    order, or ``positions``: int32 [N, axes] or [B, N, axes].  ``out``: like x
+    (x itself: in place); default contiguous [B, H, N, d].  Returns out."""
+    xs = [x] if isinstance(x, torch.Tensor) else list(x)
+    if not 1 <= len(xs) <= 4:
+        raise ValueError("one to four tensors per call")
+    if (grid is None) == (positions is None):
+        raise ValueError("give grid or positions")
+    B, _, N, d = xs[0].shape
+    dims = [int(a) for a in axis_dims]
+    if not 1 <= len(dims) <= 4:
+        raise ValueError("one to four axes")
+    _on_device(*xs)
+    for t in xs:
+        if t.dim() != 4 or (t.shape[0], t.shape[2], t.shape[3]) != (B, N, d):
+            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N and d")
+        if t.dtype != xs[0].dtype or t.dtype not in _ROPE_DTYPES:
+            raise ValueError("the tensors of one call have one dtype: bf16, fp16 or fp32")
+    with _allocating_on(stream):
+        if out is None:
+            outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
+        else:
+            outs = [out] if isinstance(out, torch.Tensor) else list(out)
+    _on_device(*outs)
+    if len(outs) != len(xs):
+        raise ValueError("as many outputs as tensors")
+    desc = _RopeDesc()
+    desc.B, desc.N, desc.d, desc.dtype = B, N, d, _ROPE_DTYPES[xs[0].dtype]
+    desc.n_axes = len(dims)
+    desc.axis_dim[:len(dims)] = dims
+    desc.halves, desc.inverse, desc.theta = int(bool(halves)), int(bool(inverse)), float(theta)
+    if positions is not None:
+        _on_device(positions)
+        if positions.dtype != torch.int32 or tuple(positions.shape) not in ((N, len(dims)), (B, N, len(dims))):
+            raise ValueError("positions must be int32 [N, axes] or [B, N, axes]")
+        desc.positions = _dptr(positions)
+        desc.positions_per_batch = 1 if positions.dim() == 3 else 0
+    else:
+        cells = [int(g) for g in grid]
+        if len(cells) != len(dims):
+            raise ValueError("grid needs one size per axis")
+        desc.grid[:len(dims)] = cells
+    arr = (_RopeTensor * len(xs))()
+    for a, t, o in zip(arr, xs, outs):
+        if o.shape != t.shape or o.dtype != t.dtype:
+            raise ValueError("out must have x's shape and dtype")
+        if d > 1 and (t.stride(3) != 1 or o.stride(3) != 1):
+            raise ValueError("the last dimension must be contiguous")
+        a.x, a.out, a.H = t.data_ptr(), o.data_ptr(), t.shape[1]
+        a.x_stride[:] = [t.stride(0), t.stride(1), t.stride(2)]
+        a.out_stride[:] = [o.stride(0), o.stride(1), o.stride(2)]
+    L = lib()
+    _check(L.tsr_rope(ctypes.byref(desc), ctypes.cast(arr, ctypes.c_void_p), len(xs), _stream_ptr(stream)))
+    return outs[0] if isinstance(x, torch.Tensor) else outs
+
+
+def tsr_rope_backward(dout, axis_dims, **kw):
+    """The gradient of tsr_rope's input from its output's: the inverse rotation,
+    same arguments (``out``: where the gradient goes)."""
+    return tsr_rope(dout, axis_dims, inverse=not kw.pop("inverse", False), **kw)
+
+
+def tsr_block_select(q: torch.Tensor, k: torch.Tensor, keep: int, *, bq: int = 64, bk: int = 64,
+                     first: int = 0, diagonal: bool = False, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The key blocks each query block keeps, as a UNIFORM mask's ``blocks``: uint8
+    [B, H, ceil(N / bq), ceil(N / bk)] (see tsr_block_select in include/tsr.h).
+    ``workspace``: uint8, at least tsr_block_select_workspace() bytes; default: one
+    allocated for the call."""
+    if q.dim() != 4 or k.shape != q.shape or q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16:
+        raise ValueError("q, k must be bf16 [B, H, N, d] alike")
+    _on_device(q, k, out, workspace)
+    desc = _SelectDesc()
+    desc.B, desc.H, desc.N, desc.d = q.shape
+    desc.bq, desc.bk, desc.keep = int(bq), int(bk), int(keep)
+    desc.first, desc.diagonal = int(first), int(bool(diagonal))
+    L = lib()
+    need = ctypes.c_size_t(0)
+    _check(L.tsr_block_select_workspace(ctypes.byref(desc), ctypes.byref(need)))
+    shape = (desc.B, desc.H, -(-desc.N // desc.bq), -(-desc.N // desc.bk))
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.uint8, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    if tuple(out.shape) != shape or out.dtype != torch.uint8:
+        raise ValueError(f"out must be uint8 of shape {shape}")
+    _check(L.tsr_block_select(ctypes.byref(desc), _dptr(q), _dptr(k), _dptr(out), _dptr(workspace),
+                              workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+    return out
 
 
 def tsr_attention_host(kind: int, B: int, H: int, N: int, d: int, q, k, v, out, lse,

@@ -180,6 +180,14 @@ tsr_status launch_svg_temporal(const void* q, const void* k, const void* v, void
                                const int8_t* head_kind, int64_t bh_lo, int64_t bh_hi,
                                cudaStream_t stream);
 
+// multi-axis rotary positions (rope.cu)
+tsr_status launch_rope(const tsr_rope_desc& d, const tsr_rope_tensor* t, int32_t n, cudaStream_t stream);
+
+// block selection (select.cu)
+size_t select_workspace(const tsr_select_desc& s);
+tsr_status launch_select(const tsr_select_desc& s, const void* q, const void* k, uint8_t* blocks, void* ws,
+                         cudaStream_t stream);
+
 // permutation (permute.cu)
 tsr_status launch_permute(const void* src, void* dst, int32_t B, int32_t H, int32_t F, int32_t S,
                           int32_t row_bytes, const int8_t* head_kind_host, int32_t inverse,

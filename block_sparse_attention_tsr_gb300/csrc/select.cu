@@ -1,0 +1,507 @@
+// select.cu -- block selection: for each block of queries the key blocks whose
+// block means score highest, as the uint8 block mask that tsr_plan takes.
+//
+//   qm_i = mean of q over block i,  km_j = mean of k over block j,  s_ij = qm_i . km_j
+//   kept(i) = forced(i) + the highest s_ij of the others, ties to the lowest j
+//
+// Two kernels.  pool_kernel reads Q and K once (the bound: HBM) and writes the
+// block means; select_kernel computes a strip of scores and picks from it, the
+// scores never leaving shared memory.
+//
+// Exactness.  Which block is kept last turns on differences between scores that
+// fp32 sums do not resolve, so the selection is made exact in two steps.  The
+// means are sums with a running error term (two-sum), about 48 bits.  The scores
+// come from the tensor cores with each mean split into two bf16 terms (three
+// products; error at most kScoreErr * |qm_i| |km_j|), and any block whose score
+// is within twice that error of the last kept one is scored again in fp64 from
+// the 48-bit means; the order of those decides.  A row has a handful of such
+// blocks, where scoring everything in fp64 would cost 1.3 ms for a 480p layer at
+// the 1.25 TFLOP/s of fp64.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace tsr {
+
+namespace {
+
+// |approximate score - score| <= kScoreErr |qm| |km| (Cauchy-Schwarz over d):
+// a bf16 term is off by 2^-8 of its value at most, two terms by 2^-16, so the
+// dropped products are at most 3 * 2^-16; 24 accumulations of 16 products in
+// fp32, truncating, add less than 24 * 2^-22.  Together 5.2e-5.
+constexpr float kScoreErr = 1e-4f;
+
+constexpr int kPoolThreads = 128;
+constexpr int kSelThreads = 256;
+constexpr int kStrip = 32;            // query blocks per CTA of select_kernel
+constexpr int kStripBytes = 112 * 1024;   // a strip's scores, two CTAs per SM
+
+struct PoolParams {
+  const uint4* x[2];            // Q and K
+  float* hi[2];                 // block means [B*H][blocks][d], high and low parts
+  float* lo[2];
+  float* norm[2];               // |mean| [B*H][blocks]
+  int32_t block[2], n_blocks[2];
+  int64_t first_k;              // units of Q, then those of K
+  int32_t N;
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// s + e += x, exactly up to the rounding of e (Knuth's two-sum).
+__device__ __forceinline__ void two_sum(float& s, float& e, float x) {
+  const float t = __fadd_rn(s, x);
+  const float z = __fsub_rn(t, s);
+  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+  s = t;
+}
+
+// One CTA per block of rows of one head; D / 8 threads across a row, so that a
+// warp reads 512 contiguous bytes, kPoolThreads / (D / 8) rows at a time.
+template <int D>
+__global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ PoolParams p) {
+  constexpr int VR = D / 8, GROUPS = kPoolThreads / VR;
+  __shared__ double part[GROUPS][D];
+  const int64_t unit = blockIdx.x;
+  const int w = unit >= p.first_k ? 1 : 0;
+  const int64_t u = unit - (w ? p.first_k : 0);
+  const int64_t bh = u / p.n_blocks[w];
+  const int blk = static_cast<int>(u - bh * p.n_blocks[w]);
+  const int row0 = static_cast<int>(static_cast<int64_t>(blk) * p.block[w]);
+  const int rows = min(p.block[w], p.N - row0);
+  const int v = threadIdx.x % VR, g = threadIdx.x / VR;
+  const uint4* src = p.x[w] + (bh * p.N + row0) * VR + v;
+  float s[8], e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = e[i] = 0.f;
+  constexpr int U = 8;
+  for (int r = g; r < rows; r += GROUPS * U) {
+    uint4 x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int rr = r + k * GROUPS;
+      x[k] = rr < rows ? __ldcs(src + static_cast<int64_t>(rr) * VR) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        two_sum(s[2 * i], e[2 * i], bf16_lo(wd[i]));
+        two_sum(s[2 * i + 1], e[2 * i + 1], bf16_hi(wd[i]));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[g][v * 8 + i] = static_cast<double>(s[i]) + static_cast<double>(e[i]);
+  __syncthreads();
+  // in fp64: the squares of small means would vanish in fp32, and the error bound with them
+  __shared__ double sq[kPoolThreads / 32];
+  double n2 = 0.0;
+  if (threadIdx.x < D) {
+    double t = part[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) t += part[k][threadIdx.x];
+    t /= rows;
+    const float hi = static_cast<float>(t);
+    const float lo = static_cast<float>(t - static_cast<double>(hi));
+    const int64_t o = u * D + threadIdx.x;
+    p.hi[w][o] = hi;
+    p.lo[w][o] = lo;
+    n2 = t * t;
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, m);
+  if ((threadIdx.x & 31) == 0) sq[threadIdx.x >> 5] = n2;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (int k = 0; k < kPoolThreads / 32; ++k) t += sq[k];
+    p.norm[w][u] = static_cast<float>(sqrt(t) * 1.0001);
+  }
+}
+
+struct SelParams {
+  const float *q_hi, *q_lo, *k_hi, *k_lo, *q_norm, *k_norm;
+  float* scores;        // [CTA][kStrip][pitch] when the strip does not fit shared memory
+  uint8_t* blocks;
+  int32_t N, bq, bk, nq, nk, strips, pitch;
+  int32_t keep, first, diagonal;
+};
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two neighbouring values as two bf16 terms each: hi = bf16(x), lo = bf16(x - hi).
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  lo = pack_bf16x2(x.x - bf16_lo(hi), x.y - bf16_hi(hi));
+}
+
+// Order-preserving integer of a score: a larger score has a larger key, equal
+// scores (-0 and 0 too) equal ones, NaN the lowest, 0.
+__device__ __forceinline__ uint32_t key32(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t key64(double x) {
+  if (x != x) return 0ull;
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  return (u & 0x8000000000000000ull) ? ~u : (u | 0x8000000000000000ull);
+}
+
+// The score in fp64 from the 48-bit means, by one warp (every lane gets it).
+template <int D>
+__device__ __forceinline__ double exact_score(const float* qh, const float* ql, const float* kh, const float* kl,
+                                              int lane) {
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int c = i * 32 + lane;
+    const double a = static_cast<double>(__ldg(qh + c)) + static_cast<double>(__ldg(ql + c));
+    const double b = static_cast<double>(__ldg(kh + c)) + static_cast<double>(__ldg(kl + c));
+    t = fma(a, b, t);
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, m);
+  return t;
+}
+
+// The largest key T such that at least `want` of n keys are >= T, over the
+// entries that `in` admits (there are at least `want` of them).  key(j) and in(j)
+// are evaluated by lane j % 32.
+template <typename In, typename Key>
+__device__ __forceinline__ uint32_t kth_key(int n, int want, int lane, In in, Key key, uint32_t lo, uint32_t hi) {
+  // invariant: count(>= lo) >= want, count(>= hi + 1) < want
+  while (lo < hi) {
+    const uint32_t mid = lo + ((hi - lo) >> 1) + 1u;
+    int c = 0;
+    for (int j = lane; j < n; j += 32) c += (in(j) && key(j) >= mid) ? 1 : 0;
+    c = __reduce_add_sync(0xFFFFFFFFu, c);
+    if (c >= want) lo = mid;
+    else hi = mid - 1u;
+  }
+  return lo;
+}
+
+// One CTA: a strip of kStrip query blocks of one head.
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelParams p) {
+  extern __shared__ float smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t bh = blockIdx.x / p.strips;
+  const int i0 = static_cast<int>(blockIdx.x - bh * p.strips) * kStrip;
+  float* sc = p.scores ? p.scores + static_cast<int64_t>(blockIdx.x) * kStrip * p.pitch : smem;
+  __shared__ float k_max_w[kSelThreads / 32];
+
+  // the largest |km| of the head (NaN counts as infinite)
+  float km = 0.f;
+  for (int j = threadIdx.x; j < p.nk; j += kSelThreads) {
+    const float x = __ldg(p.k_norm + bh * p.nk + j);
+    km = x <= FLT_MAX ? fmaxf(km, x) : INFINITY;
+    if (km > FLT_MAX) break;
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) km = fmaxf(km, __shfl_xor_sync(0xFFFFFFFFu, km, m));
+  if (lane == 0) k_max_w[warp] = km;
+
+  // ---- scores: warp w takes the 16 query blocks (w & 1) and every fourth group
+  // of 8 key blocks; a fragments (both bf16 terms) stay in registers
+  {
+    const int g = lane >> 2, t = lane & 3;
+    const int r0 = i0 + (warp & 1) * 16 + g, r1 = r0 + 8;
+    uint32_t ah[D / 16][4], al[D / 16][4];
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int r = (f & 1) ? r1 : r0, c = kk * 16 + t * 2 + ((f & 2) ? 8 : 0);
+        const float2 x = r < p.nq ? __ldg(reinterpret_cast<const float2*>(p.q_hi + (bh * p.nq + r) * D + c))
+                                  : make_float2(0.f, 0.f);
+        split2(x, ah[kk][f], al[kk][f]);
+      }
+    }
+    for (int j0 = (warp >> 1) * 8; j0 < p.nk; j0 += 32) {
+      const int j = j0 + g;
+      const float* kr = p.k_hi + (bh * p.nk + (j < p.nk ? j : p.nk - 1)) * D;
+      float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t bh0, bl0, bh1, bl1;
+        split2(__ldg(reinterpret_cast<const float2*>(kr + kk * 16 + t * 2)), bh0, bl0);
+        split2(__ldg(reinterpret_cast<const float2*>(kr + kk * 16 + t * 2 + 8)), bh1, bl1);
+        mma_16816(c0, ah[kk], bh0, bh1);
+        mma_16816(c1, ah[kk], bl0, bl1);
+        mma_16816(c1, al[kk], bh0, bh1);
+      }
+      const int col = j0 + t * 2, row = (warp & 1) * 16 + g;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int cc = col + (x & 1), rr = row + ((x & 2) ? 8 : 0);
+        if (cc < p.nk) sc[rr * p.pitch + cc] = c0[x] + c1[x];
+      }
+    }
+  }
+  __syncthreads();
+  float k_max = k_max_w[0];
+#pragma unroll
+  for (int w = 1; w < kSelThreads / 32; ++w) k_max = fmaxf(k_max, k_max_w[w]);
+
+  // ---- selection: one warp per row
+  for (int rr = warp; rr < kStrip; rr += kSelThreads / 32) {
+    const int i = i0 + rr;
+    if (i >= p.nq) break;
+    float* row = sc + rr * p.pitch;
+    uint8_t* out = p.blocks + (bh * p.nq + i) * p.nk;
+    // forced blocks: [0, first) and, with `diagonal`, [d_lo, d_hi), the key blocks
+    // that share a token with the query block
+    const int first = min(p.first, p.nk);
+    int d_lo = 0, d_hi = 0;
+    if (p.diagonal) {
+      const int64_t a = static_cast<int64_t>(i) * p.bq;
+      const int64_t b = min(a + p.bq, static_cast<int64_t>(p.N)) - 1;
+      d_lo = max(static_cast<int>(a / p.bk), first);
+      d_hi = max(static_cast<int>(b / p.bk) + 1, d_lo);
+    }
+    auto forced = [&](int j) -> bool { return j < first || (j >= d_lo && j < d_hi); };
+    const int n_forced = first + (d_hi - d_lo), others = p.nk - n_forced;
+    const int want = min(p.keep - n_forced, others);
+    if (want <= 0 || want == others) {
+      const bool all = want == others && want > 0;
+      for (int j = lane; j < p.nk; j += 32) out[j] = (all || forced(j)) ? 1 : 0;
+      continue;
+    }
+    // the last two terms cover values that the bf16 terms or their products flush
+    const float q_norm = __ldg(p.q_norm + bh * p.nq + i);
+    const float err2 = 2.f * (kScoreErr * (q_norm * k_max) + 4e-37f * (q_norm + k_max) + 1e-36f);
+    float above = INFINITY, below = -INFINITY;   // kept for sure above, dropped for sure below
+    bool finite = q_norm * k_max <= FLT_MAX && err2 <= FLT_MAX;
+    if (finite) {
+      uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+      for (int j = lane; j < p.nk; j += 32) {
+        if (forced(j)) continue;
+        const uint32_t k = key32(row[j]);
+        kmin = min(kmin, k);
+        kmax = max(kmax, k);
+      }
+      kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
+      kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
+      const uint32_t t = kth_key(
+          p.nk, want, lane, [&](int j) { return !forced(j); }, [&](int j) { return key32(row[j]); }, kmin, kmax);
+      const float th = __uint_as_float((t & 0x80000000u) ? (t & 0x7FFFFFFFu) : ~t);
+      above = th + err2;
+      below = th - err2;
+      finite = above <= FLT_MAX && below >= -FLT_MAX;
+    }
+    if (!finite) above = INFINITY;
+    // without finite scores and bounds every block that is not forced is scored exactly
+    auto sure = [&](int j) -> bool { return finite && row[j] > above; };
+    auto near = [&](int j) -> bool { return !forced(j) && (!finite || (row[j] >= below && row[j] <= above)); };
+    int n_sure = 0, n_near = 0;
+    for (int j = lane; j < p.nk; j += 32) {
+      if (forced(j)) continue;
+      n_sure += sure(j) ? 1 : 0;
+      n_near += near(j) ? 1 : 0;
+    }
+    n_sure = __reduce_add_sync(0xFFFFFFFFu, n_sure);
+    n_near = __reduce_add_sync(0xFFFFFFFFu, n_near);
+    const int left = want - n_sure;               // of the near ones, 1 <= left <= n_near
+    const float* qh = p.q_hi + (bh * p.nq + i) * D;
+    const float* ql = p.q_lo + (bh * p.nq + i) * D;
+    const float* kh = p.k_hi + bh * p.nk * D;
+    const float* kl = p.k_lo + bh * p.nk * D;
+    if (left == n_near) {
+      for (int j = lane; j < p.nk; j += 32) out[j] = (forced(j) || sure(j) || near(j)) ? 1 : 0;
+      continue;
+    }
+    if (n_near <= 32) {
+      // lane c holds near block c (ascending j): its exact key, then its rank
+      uint64_t mine = 0;
+      int my_j = -1, c = 0;
+      for (int j0 = 0; j0 < p.nk; j0 += 32) {
+        const int j = j0 + lane;
+        const bool in = j < p.nk;
+        const bool nr = in && near(j);
+        if (in && !nr) out[j] = (forced(j) || sure(j)) ? 1 : 0;
+        uint32_t m = __ballot_sync(0xFFFFFFFFu, nr);
+        while (m) {
+          const int jj = j0 + __ffs(m) - 1;
+          m &= m - 1;
+          const uint64_t key = key64(exact_score<D>(qh, ql, kh + static_cast<int64_t>(jj) * D,
+                                                    kl + static_cast<int64_t>(jj) * D, lane));
+          if (lane == c) {
+            mine = key;
+            my_j = jj;
+          }
+          ++c;
+        }
+      }
+      int rank = 0;
+      for (int o = 0; o < n_near; ++o) {
+        const uint64_t other = __shfl_sync(0xFFFFFFFFu, mine, o);
+        rank += (other > mine || (other == mine && o < lane)) ? 1 : 0;
+      }
+      if (my_j >= 0) out[my_j] = rank < left ? 1 : 0;
+      continue;
+    }
+    // Many near blocks (a query block of zeros, equal key blocks, infinities):
+    // order them by the upper, then the lower 32 bits of the exact key, which
+    // take the place of their scores.  out[j] holds the state meanwhile.
+    enum : uint8_t { kOut = 0, kIn = 1, kNear = 2 };
+    for (int j = lane; j < p.nk; j += 32)
+      out[j] = near(j) ? kNear : (forced(j) || sure(j)) ? kIn : kOut;
+    __syncwarp();
+    auto is_near = [&](int j) { return out[j] == kNear; };
+    auto word = [&](int j) { return __float_as_uint(row[j]); };
+    int open = left;                              // places left among the kNear
+    for (int half = 0; half < 2; ++half) {
+      for (int j0 = 0; j0 < p.nk; j0 += 32) {
+        const int j = j0 + lane;
+        uint32_t m = __ballot_sync(0xFFFFFFFFu, j < p.nk && is_near(j));
+        while (m) {
+          const int jj = j0 + __ffs(m) - 1;
+          m &= m - 1;
+          const uint64_t key = key64(exact_score<D>(qh, ql, kh + static_cast<int64_t>(jj) * D,
+                                                    kl + static_cast<int64_t>(jj) * D, lane));
+          if (lane == 0) row[jj] = __uint_as_float(static_cast<uint32_t>(half ? key : key >> 32));
+        }
+      }
+      __syncwarp();
+      const uint32_t t = kth_key(p.nk, open, lane, is_near, word, 0u, 0xFFFFFFFFu);
+      int in = 0;
+      for (int j = lane; j < p.nk; j += 32) {
+        if (!is_near(j)) continue;
+        const uint32_t w = word(j);
+        if (w != t) out[j] = w > t ? kIn : kOut;
+        in += w > t ? 1 : 0;
+      }
+      open -= __reduce_add_sync(0xFFFFFFFFu, in);
+      __syncwarp();
+    }
+    // equal exact scores: the lowest j
+    for (int j0 = 0; j0 < p.nk; j0 += 32) {
+      const int j = j0 + lane;
+      const bool tie = j < p.nk && is_near(j);
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, tie);
+      if (tie) out[j] = __popc(m & ((1u << lane) - 1u)) < open ? kIn : kOut;
+      open -= min(open, __popc(m));
+    }
+  }
+}
+
+struct Layout {
+  int32_t nq, nk, strips, pitch;
+  bool in_smem;
+  size_t q_hi, q_lo, k_hi, k_lo, q_norm, k_norm, scores, total;
+};
+
+Layout layout_of(const tsr_select_desc& s) {
+  Layout l;
+  l.nq = (s.N + s.bq - 1) / s.bq;
+  l.nk = (s.N + s.bk - 1) / s.bk;
+  l.strips = (l.nq + kStrip - 1) / kStrip;
+  l.pitch = l.nk + ((l.nk & 31) ? 0 : 4);    // rows of a strip start in different banks
+  l.in_smem = static_cast<size_t>(kStrip) * l.pitch * 4 <= kStripBytes;   // else in the workspace
+  const size_t BH = static_cast<size_t>(s.B) * s.H;
+  size_t at = 0;
+  auto take = [&](size_t floats) {
+    const size_t o = at;
+    at += (floats * 4 + 255) / 256 * 256;
+    return o;
+  };
+  l.q_hi = take(BH * l.nq * s.d);
+  l.q_lo = take(BH * l.nq * s.d);
+  l.k_hi = take(BH * l.nk * s.d);
+  l.k_lo = take(BH * l.nk * s.d);
+  l.q_norm = take(BH * l.nq);
+  l.k_norm = take(BH * l.nk);
+  l.scores = take(l.in_smem ? 0 : BH * l.strips * kStrip * l.pitch);
+  l.total = at;
+  return l;
+}
+
+template <int D>
+tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, const void* k, uint8_t* blocks,
+                  uint8_t* ws, cudaStream_t st) {
+  const int64_t BH = static_cast<int64_t>(s.B) * s.H;
+  auto f = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  PoolParams pp;
+  pp.x[0] = static_cast<const uint4*>(q);
+  pp.x[1] = static_cast<const uint4*>(k);
+  pp.hi[0] = f(l.q_hi);
+  pp.lo[0] = f(l.q_lo);
+  pp.norm[0] = f(l.q_norm);
+  pp.hi[1] = f(l.k_hi);
+  pp.lo[1] = f(l.k_lo);
+  pp.norm[1] = f(l.k_norm);
+  pp.block[0] = s.bq;
+  pp.block[1] = s.bk;
+  pp.n_blocks[0] = l.nq;
+  pp.n_blocks[1] = l.nk;
+  pp.first_k = BH * l.nq;
+  pp.N = s.N;
+  const int64_t units = BH * (static_cast<int64_t>(l.nq) + l.nk);
+  SelParams sp;
+  sp.q_hi = pp.hi[0];
+  sp.q_lo = pp.lo[0];
+  sp.k_hi = pp.hi[1];
+  sp.k_lo = pp.lo[1];
+  sp.q_norm = pp.norm[0];
+  sp.k_norm = pp.norm[1];
+  sp.scores = l.in_smem ? nullptr : f(l.scores);
+  sp.blocks = blocks;
+  sp.N = s.N;
+  sp.bq = s.bq;
+  sp.bk = s.bk;
+  sp.nq = l.nq;
+  sp.nk = l.nk;
+  sp.strips = l.strips;
+  sp.pitch = l.pitch;
+  sp.keep = s.keep;
+  sp.first = s.first;
+  sp.diagonal = s.diagonal;
+  const size_t smem = l.in_smem ? static_cast<size_t>(kStrip) * l.pitch * 4 : 0;
+  auto kern = select_kernel<D>;
+  int dev = 0;
+  TSR_CUDA(cudaGetDevice(&dev));
+  static bool attr_set[64] = {false};
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripBytes));
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  pool_kernel<D><<<static_cast<unsigned>(units), kPoolThreads, 0, st>>>(pp);
+  TSR_CUDA(cudaGetLastError());
+  kern<<<static_cast<unsigned>(BH * l.strips), kSelThreads, smem, st>>>(sp);
+  TSR_CUDA(cudaGetLastError());
+  return TSR_OK;
+}
+
+}  // namespace
+
+size_t select_workspace(const tsr_select_desc& s) { return layout_of(s).total; }
+
+// The arguments have been checked (api_ops.cu).
+tsr_status launch_select(const tsr_select_desc& s, const void* q, const void* k, uint8_t* blocks, void* ws,
+                         cudaStream_t st) {
+  const Layout l = layout_of(s);
+  const int64_t BH = static_cast<int64_t>(s.B) * s.H;
+  if (BH * (static_cast<int64_t>(l.nq) + l.nk) >= (int64_t{1} << 31))
+    return fail(TSR_ERR_UNSUPPORTED, "more than 2^31 blocks");
+  if (s.d == 64) return launch<64>(s, l, q, k, blocks, static_cast<uint8_t*>(ws), st);
+  return launch<128>(s, l, q, k, blocks, static_cast<uint8_t*>(ws), st);
+}
+
+}  // namespace tsr

@@ -410,6 +410,98 @@ tsr_status tsr_svg_route(const void *q, const void *k, const void *v, int32_t B,
                          int8_t *head_kind, void *stream);
 
 /*
+ * tsr_rope -- rotary positions with several axes, applied to one to four tensors
+ * in one launch (Q and K of a layer), between any two layouts; with `inverse` the
+ * gradient of that.  It stands before the attention: it reads the projections in
+ * their own layout ([B][N][H][d], say) and writes the attention's [B][H][N][d].
+ *
+ * The first axis_dim[0] channels of every head belong to axis 0, the next
+ * axis_dim[1] to axis 1, and so on; channels past their sum are copied.  Pair j
+ * of axis x (0 <= j < axis_dim[x] / 2) of a token at position p_x turns by
+ * a = p_x * theta^(-2 j / axis_dim[x]):
+ *     (u, v) -> (u cos a - v sin a, u sin a + v cos a)         inverse: -a
+ * where (u, v) are channels (2j, 2j + 1) of the axis, or, with `halves`,
+ * (j, j + axis_dim[x] / 2).  The rotation is orthogonal: the gradient of the input
+ * is the inverse rotation of the gradient of the output.  fp32 arithmetic, one
+ * rounding to the tensors' type; a far position loses nothing (angles are taken
+ * on the circle in 64-bit integers).
+ *
+ * Positions: grid form (positions NULL): token n has the row-major coordinates of
+ * n in grid[0] x ... x grid[n_axes - 1], whose product is N (frame, row, column of
+ * a frame-major latent video).  Explicit form: positions[n][n_axes] (device
+ * int32, shared by the batch, or [B][N][n_axes] with positions_per_batch); any
+ * int32 value, negative ones too.
+ *
+ * Strides are in elements, for b, h and n; d is contiguous.  x and out may be the
+ * same tensor (same strides); otherwise their elements must not overlap, and no
+ * two elements of out may share an address.  x strides may be 0 (a broadcast
+ * input).  Any alignment of the element type; 16-byte aligned rows are fastest.
+ * Errors: TSR_ERR_INVALID_ARG for bad shapes, axes, pointers or strides,
+ * TSR_ERR_UNSUPPORTED for B above 65535 or N above 2^24.  Asynchronous on `stream`.
+ */
+typedef enum { TSR_DTYPE_BF16 = 0, TSR_DTYPE_F16 = 1, TSR_DTYPE_F32 = 2 } tsr_dtype;
+
+typedef struct {
+  int32_t B, N, d;              /* 2 <= d <= 256, even */
+  int32_t dtype;                /* tsr_dtype of every tensor */
+  int32_t n_axes;               /* 1 .. 4 */
+  int32_t axis_dim[4];          /* even, > 0, sum <= d */
+  int32_t halves, inverse;
+  double theta;                 /* > 0, finite */
+  const int32_t *positions;     /* device; NULL = grid */
+  int32_t positions_per_batch;
+  int32_t grid[4];
+} tsr_rope_desc;
+
+typedef struct {
+  const void *x;
+  void *out;
+  int32_t H;
+  int64_t x_stride[3], out_stride[3];   /* b, h, n */
+} tsr_rope_tensor;
+
+tsr_status tsr_rope(const tsr_rope_desc *desc, const tsr_rope_tensor *tensors, int32_t n_tensors,
+                    void *stream);
+
+/*
+ * tsr_block_select -- a block mask for tsr_plan from a cheap score per block pair
+ * (the step before the path, for callers without a mask; compare tsr_svg_route,
+ * which routes whole heads).
+ *
+ * With qm_i and km_j the means of q over query block i (bq tokens) and of k over
+ * key block j (bk tokens; the last block of each over its own tokens),
+ * s_ij = qm_i . km_j, and for every (b, h, i)
+ *     forced(i) = { j < first } and, with `diagonal`, { j : key block j shares a
+ *                 token index with query block i }
+ *     blocks[b][h][i][j] = 1 iff j is forced, or among the keep - |forced(i)|
+ *                 highest s_ij of the others (ties: the lowest j), else 0.
+ * A row so holds max(keep, |forced|) blocks (all when there are fewer).  The
+ * selection is that of exact scores (48-bit means, fp64 where a fast bound does
+ * not decide), so it does not depend on summation order.  Sums of bf16 values
+ * must stay inside the fp32 range.
+ *
+ * q, k: device bf16 [B][H][N][d], d in {64, 128}, 16-byte aligned.  blocks:
+ * device uint8 [B][H][ceil(N/bq)][ceil(N/bk)], a TSR_MASK_UNIFORM mask's `blocks`.
+ * bq, bk >= 16.  workspace: device, 256-byte aligned, tsr_block_select_workspace()
+ * bytes; its contents are not kept between calls, and calls that may run at the
+ * same time need one each.  Asynchronous on `stream`; nothing is allocated.
+ * Errors: TSR_ERR_INVALID_ARG, TSR_ERR_UNSUPPORTED (N above 2^24, more than 2^31
+ * blocks).
+ */
+typedef struct {
+  int32_t B, H, N, d;
+  int32_t bq, bk;
+  int32_t keep;                 /* >= 1 */
+  int32_t first;                /* >= 0 */
+  int32_t diagonal;
+} tsr_select_desc;
+
+tsr_status tsr_block_select_workspace(const tsr_select_desc *desc, size_t *bytes /* HOST */);
+
+tsr_status tsr_block_select(const tsr_select_desc *desc, const void *q, const void *k, uint8_t *blocks,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * tsr_attention_host -- one whole call from HOST memory: copies the mask arrays
  * and Q, K, V to the device, plans, runs the forward and copies O and lse back,
  * then synchronises.  Every pointer in `mask` and q, k, v, out, lse are HOST
