@@ -25,6 +25,7 @@ __all__ = [
     "tsr_bsa_forward",
     "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_temporal_permute", "tsr_svg_route",
     "tsr_rope", "tsr_rope_backward", "tsr_block_select",
+    "BackwardPlan", "tsr_backward_plan", "tsr_backward_plan_update", "tsr_bsa_backward",
     "tsr_attention_host",
     "tsr_regime_load",
     "tsr_regime_lookup", "tsr_abi_version", "UNIFORM", "SEGMENTS", "SVG", "KEYLIST",
@@ -114,7 +115,9 @@ _LIB = None
 EXPORTS = ("tsr_abi_version", "tsr_status_string", "tsr_last_error", "tsr_plan", "tsr_plan_update",
            "tsr_bsa_forward", "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_plan_destroy", "tsr_plan_get_stats",
            "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope",
-           "tsr_block_select_workspace", "tsr_block_select", "tsr_attention_host",
+           "tsr_block_select_workspace", "tsr_block_select", "tsr_backward_plan",
+           "tsr_backward_plan_update", "tsr_backward_plan_destroy", "tsr_backward_plan_device_status",
+           "tsr_bsa_backward_workspace", "tsr_bsa_backward", "tsr_attention_host",
            "tsr_release_host_buffers", "tsr_regime_load", "tsr_regime_lookup")
 
 
@@ -154,6 +157,12 @@ def lib():
         "tsr_rope": ([P, P, I32, P], ctypes.c_int),
         "tsr_block_select_workspace": ([P, P], ctypes.c_int),
         "tsr_block_select": ([P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "tsr_backward_plan": ([P, P, P], ctypes.c_int),
+        "tsr_backward_plan_update": ([P, P, P], ctypes.c_int),
+        "tsr_backward_plan_destroy": ([P], ctypes.c_int),
+        "tsr_backward_plan_device_status": ([P, P], ctypes.c_int),
+        "tsr_bsa_backward_workspace": ([P, P], ctypes.c_int),
+        "tsr_bsa_backward": ([P] * 11 + [ctypes.c_size_t, P], ctypes.c_int),
         "tsr_attention_host": ([P, P, P, P, P, P, P], ctypes.c_int),
         "tsr_release_host_buffers": ([], None),
         "tsr_regime_load": ([ctypes.c_char_p], ctypes.c_int),
@@ -326,6 +335,76 @@ def tsr_bsa_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: Pla
 
 def tsr_plan_device_status(plan: Plan, stream=None) -> None:
     _check(lib().tsr_plan_device_status(plan.handle, _stream_ptr(stream)))
+
+
+class BackwardPlan:
+    """Owner of a tsr_backward_plan_t; released by destroy() or garbage collection."""
+
+    def __init__(self, handle: int, mask: Mask):
+        self.handle = handle
+        self.mask = mask
+        self.B, self.H, self.N, self.d = mask.B, mask.H, mask.N, mask.d
+        need = ctypes.c_size_t(0)
+        _check(lib().tsr_bsa_backward_workspace(handle, ctypes.byref(need)))
+        self.workspace_bytes = need.value
+
+    def update(self, mask: Mask, stream=None) -> "BackwardPlan":
+        """Re-plan for a new mask of the same shape, reusing the plan's storage."""
+        _check(lib().tsr_backward_plan_update(self.handle, ctypes.byref(mask.struct), _stream_ptr(stream)))
+        self.mask = mask
+        return self
+
+    def device_status(self, stream=None) -> None:
+        _check(lib().tsr_backward_plan_device_status(self.handle, _stream_ptr(stream)))
+
+    def destroy(self) -> None:
+        if self.handle:
+            lib().tsr_backward_plan_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def tsr_backward_plan(mask: Mask, stream=None) -> BackwardPlan:
+    """The tiles of a UNIFORM or SEGMENTS mask by query and by key, for
+    tsr_bsa_backward (see include/tsr.h)."""
+    h = ctypes.c_void_p(0)
+    _check(lib().tsr_backward_plan(ctypes.byref(mask.struct), ctypes.byref(h), _stream_ptr(stream)))
+    return BackwardPlan(h.value, mask)
+
+
+def tsr_backward_plan_update(plan: BackwardPlan, mask: Mask, stream=None) -> BackwardPlan:
+    return plan.update(mask, stream)
+
+
+def tsr_bsa_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                     lse: torch.Tensor, dout: torch.Tensor, plan: BackwardPlan,
+                     dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                     dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None):
+    """Gradients of tsr_bsa_forward: returns (dq, dk, dv), bf16 [B, H, N, d].  ``out``
+    and ``lse`` are the forward's over the plan's mask.  ``workspace``: uint8, at
+    least plan.workspace_bytes; default: one allocated for the call."""
+    shape = (plan.B, plan.H, plan.N, plan.d)
+    for t in (q, k, v, out, dout, dq, dk, dv):
+        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape):
+            raise ValueError(f"q, k, v, out, dout and the gradients must be bf16 of shape {shape}")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != shape[:3]:
+        raise ValueError(f"lse must be fp32 of shape {shape[:3]}")
+    _on_device(q, k, v, out, lse, dout, dq, dk, dv, workspace)
+    with _allocating_on(stream):
+        dq, dk, dv = (torch.empty(shape, dtype=torch.bfloat16, device=q.device) if t is None else t
+                      for t in (dq, dk, dv))
+        if workspace is None:
+            workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+    _check(lib().tsr_bsa_backward(_dptr(q), _dptr(k), _dptr(v), _dptr(out), _dptr(lse), _dptr(dout),
+                                  plan.handle, _dptr(dq), _dptr(dk), _dptr(dv), _dptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+    return dq, dk, dv
 
 
 def tsr_temporal_permute(src: torch.Tensor, dst: torch.Tensor, n_frames: int, frame_size: int,

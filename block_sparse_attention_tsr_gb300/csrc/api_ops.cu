@@ -1,13 +1,79 @@
 // api_ops.cu -- the C ABI of the operators beside the attention forward: argument
-// checks of the position rotation (rope.cu) and the block selection (select.cu).
+// checks of the position rotation (rope.cu), the block selection (select.cu) and
+// the attention backward (bwd.cu) with its plans.
 #include <cmath>
+#include <cstring>
+#include <new>
 #include <string>
 
 #include "internal.h"
 
 using namespace tsr;
 
+// The mask's tiles by query (q: the mask's plan) and by key (k: the plan of its
+// transpose, whose block array is held here).
+struct tsr_backward_plan_s {
+  tsr_plan_t q = nullptr, k = nullptr;
+  DevBuf blocks_t;
+  bool ready = false;
+};
+
 namespace {
+
+void free_backward(tsr_backward_plan_s* p) {
+  if (!p) return;
+  if (p->q) tsr_plan_destroy(p->q);
+  if (p->k) tsr_plan_destroy(p->k);
+  devbuf_free(p->blocks_t);
+  delete p;
+}
+
+// Both plans for `mask`, made or rebuilt in place.
+tsr_status fill_backward(tsr_backward_plan_s* p, const tsr_mask* mask, cudaStream_t st) {
+  p->ready = false;
+  tsr_plan_opts opts;
+  memset(&opts, 0, sizeof opts);
+  opts.bn = 64;
+  opts.orient = TSR_ORIENT_ROWS;
+  opts.kv_split = 1;
+  // the mask first: its checks cover the transpose's arguments
+  if (tsr_status e = p->q ? tsr_plan_update(p->q, mask, st) : tsr_plan(mask, &opts, &p->q, st)) return e;
+  tsr_mask t = *mask;
+  int64_t nq, nk;
+  if (mask->kind == TSR_MASK_UNIFORM) {
+    nq = (static_cast<int64_t>(mask->N) + mask->bq - 1) / mask->bq;
+    nk = (static_cast<int64_t>(mask->N) + mask->bk - 1) / mask->bk;
+    t.bq = mask->bk;
+    t.bk = mask->bq;
+  } else {
+    nq = mask->n_qseg;
+    nk = mask->n_kseg;
+    t.n_qseg = mask->n_kseg;
+    t.n_kseg = mask->n_qseg;
+    t.q_bounds = mask->k_bounds;
+    t.k_bounds = mask->q_bounds;
+  }
+  const int64_t heads = static_cast<int64_t>(mask->B) * mask->H;
+  if (tsr_status e = devbuf_reserve(p->blocks_t, static_cast<size_t>(heads * nq * nk))) return e;
+  t.blocks = static_cast<const uint8_t*>(p->blocks_t.p);
+  if (tsr_status e = launch_transpose_blocks(mask->blocks, static_cast<uint8_t*>(p->blocks_t.p), heads,
+                                             static_cast<int32_t>(nq), static_cast<int32_t>(nk), st))
+    return e;
+  if (tsr_status e = p->k ? tsr_plan_update(p->k, &t, st) : tsr_plan(&t, &opts, &p->k, st)) return e;
+  p->ready = true;
+  return TSR_OK;
+}
+
+tsr_status check_backward_kind(const tsr_mask* mask) {
+  if (!mask) return fail(TSR_ERR_INVALID_ARG, "mask is NULL");
+  if (mask->kind == TSR_MASK_SVG || mask->kind == TSR_MASK_KEYLIST)
+    return fail(TSR_ERR_UNSUPPORTED, "the backward pass takes UNIFORM and SEGMENTS masks");
+  return TSR_OK;
+}
+
+size_t backward_workspace(const tsr_plan_s* p) {
+  return static_cast<size_t>(2) * p->B * p->H * ((static_cast<size_t>(p->N) + 63) / 64 * 64) * sizeof(float);
+}
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -97,6 +163,93 @@ tsr_status tsr_block_select(const tsr_select_desc* desc, const void* q, const vo
   if (!aligned(workspace, 256)) return fail(TSR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (workspace_bytes < select_workspace(*desc)) return fail(TSR_ERR_INVALID_ARG, "workspace too small");
   return launch_select(*desc, q, k, blocks, workspace, static_cast<cudaStream_t>(stream));
+}
+
+tsr_status tsr_backward_plan(const tsr_mask* mask, tsr_backward_plan_t* out, void* stream) {
+  set_error("");
+  if (!out) return fail(TSR_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (tsr_status e = check_backward_kind(mask)) return e;
+  tsr_backward_plan_s* p = new (std::nothrow) tsr_backward_plan_s();
+  if (!p) return fail(TSR_ERR_OOM, "host allocation failed");
+  if (tsr_status e = fill_backward(p, mask, static_cast<cudaStream_t>(stream))) {
+    const std::string why = last_error_cstr();
+    free_backward(p);
+    return fail(e, why);
+  }
+  *out = p;
+  return TSR_OK;
+}
+
+tsr_status tsr_backward_plan_update(tsr_backward_plan_t plan, const tsr_mask* mask, void* stream) {
+  set_error("");
+  if (!plan) return fail(TSR_ERR_INVALID_ARG, "plan is NULL");
+  if (tsr_status e = check_backward_kind(mask)) return e;
+  // a mask that the plan cannot take leaves it as it was
+  const tsr_plan_s* q = plan->q;
+  if (mask->B != q->B || mask->H != q->H || mask->N != q->N || mask->d != q->d)
+    return fail(TSR_ERR_INVALID_ARG, "tsr_backward_plan_update needs the plan's B, H, N and d");
+  return fill_backward(plan, mask, static_cast<cudaStream_t>(stream));
+}
+
+tsr_status tsr_backward_plan_destroy(tsr_backward_plan_t plan) {
+  free_backward(plan);
+  return TSR_OK;
+}
+
+tsr_status tsr_backward_plan_device_status(tsr_backward_plan_t plan, void* stream) {
+  set_error("");
+  if (!plan) return fail(TSR_ERR_INVALID_ARG, "plan is NULL");
+  return tsr_plan_device_status(plan->q, stream);
+}
+
+tsr_status tsr_bsa_backward_workspace(tsr_backward_plan_t plan, size_t* bytes) {
+  set_error("");
+  if (!plan || !bytes) return fail(TSR_ERR_INVALID_ARG, "plan / bytes is NULL");
+  *bytes = backward_workspace(plan->q);
+  return TSR_OK;
+}
+
+tsr_status tsr_bsa_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                            const void* dout, tsr_backward_plan_t plan, void* dq, void* dk, void* dv,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  set_error("");
+  if (!plan) return fail(TSR_ERR_INVALID_ARG, "plan is NULL");
+  if (!plan->ready) return fail(TSR_ERR_INVALID_ARG, "the plan's last update failed");
+  const void* in[6] = {q, k, v, out, dout, lse};
+  void* grad[3] = {dq, dk, dv};
+  for (const void* t : in) {
+    if (!t) return fail(TSR_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (!aligned(t, 16)) return fail(TSR_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (!grad[i]) return fail(TSR_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (!aligned(grad[i], 16)) return fail(TSR_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    for (const void* t : in)
+      if (grad[i] == t) return fail(TSR_ERR_INVALID_ARG, "a gradient aliases an input");
+    for (int j = 0; j < i; ++j)
+      if (grad[i] == grad[j]) return fail(TSR_ERR_INVALID_ARG, "two gradients alias");
+  }
+  if (!workspace || !aligned(workspace, 256))
+    return fail(TSR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (workspace_bytes < backward_workspace(plan->q)) return fail(TSR_ERR_INVALID_ARG, "workspace too small");
+  int dev = 0;
+  TSR_CUDA(cudaGetDevice(&dev));
+  if (dev != plan->q->device) return fail(TSR_ERR_INVALID_ARG, "plan was made on another device");
+  BwdArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.workspace = workspace;
+  a.plan_q = plan->q;
+  a.plan_k = plan->k;
+  return launch_backward(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,624 @@
+// bwd.cu -- the backward pass of block-sparse attention on tcgen05 tensor cores.
+//
+// With P = exp(S / sqrt(d) - lse) on the allowed pairs (S = Q K^T), O = P V and
+// the gradient dO of O:
+//     dV = P^T dO,   dP = dO V^T,   delta_i = sum_c dO_ic O_ic,
+//     dS = P o (dP - delta),   dQ = dS K / sqrt(d),   dK = dS^T Q / sqrt(d).
+//
+// Two kinds of work item share one launch, each owning its output rows, so every
+// gradient is summed in registers of the tensor core in a fixed order: no atomics,
+// the same bits every run.
+//   key items    128 keys with the list of query tiles that see them: dK and dV
+//   query items  128 queries with the list of key tiles they see: dQ
+// Both recompute S and dP, so a pair costs 7 products (4 + 3) of 2 d flops where one
+// pass with atomics on dQ would take 5.  The lists come from two plans of the
+// forward's planner: the mask's own and its transpose's, 128-row tiles 64 wide.
+//
+// Both kinds run the same kernel: 128 stationary rows X1, X2 in shared memory (K, V
+// or Q, dO) against a stream of 128-row steps Y1, Y2 (Q, dO or K, V), a step being
+// two tiles of the list, not necessarily neighbours:
+//     S = X1 Y1^T, dP = X2 Y2^T;   acc1 += dS Y1;   key items: acc2 += P Y2
+// so the softmax sees S with the stationary rows on the TMEM lanes.  P and dS are
+// rounded to bf16, the operand type of the second products, and written over S
+// and dP in TMEM (512 columns: S, dP and the two accumulators of d).
+//
+// Order of the tensor pipe, one thread issuing: S(j+1) right after acc2(j) (which
+// frees P's columns), then acc1(j), dP(j+1), acc2(j+1) ...  While the pipe runs
+// acc1(j) and dP(j+1), the softmax turns S(j+1) into P; while it runs acc2(j+1) and
+// S(j+2), dP(j+1) into dS.
+//   warps 0..7  softmax: row = TMEM lane, warps 0..3 the step's first tile (64
+//               columns), warps 4..7 its second; then the epilogue
+//   warp 8      producer: TMA tiles and the rows' statistics
+//   warp 9      MMA issuer
+// Every wait is bounded: on expiry the error word is set and the kernel winds down.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "fwd_kernel.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace tsr {
+
+namespace bwd {
+
+constexpr int kThreads = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+  CUtensorMap tq, tk, tv, tdo;     // 3-D {d, N, B*H}, 64 x 64 boxes
+  const int4 *items_k, *items_q;   // tsr_plan_item, key items (transposed plan), query items
+  const int2 *entries_k, *entries_q;
+  const uint4 *descs_k, *descs_q;
+  const float* lse2;               // [B*H][Np] lse * log2(e), +inf for rows with no key and past N
+  const float* delta;              // [B*H][Np]
+  __nv_bfloat16 *dq, *dk, *dv;
+  uint32_t* err;
+  int32_t n_key_items, N, Np;
+  float scale_log2, scale;
+};
+
+template <int D>
+struct Cfg {
+  // Y1 is read by the first product of a step and again by the last, one step
+  // later, so it gets a stage more than Y2 where shared memory is short
+  static constexpr int S1 = D == 128 ? 3 : 4, S2 = D == 128 ? 2 : 4;
+  static constexpr int TILE = 128 * D * 2;          // one 128-row operand
+  static constexpr int STAT = 2 * 128 * 4;          // lse2 and delta of a step's rows
+  static constexpr int X1 = 0, X2 = TILE, Y1 = 2 * TILE, Y2 = Y1 + S1 * TILE, ST = Y2 + S2 * TILE;
+  static constexpr int CTRL = ST + 2 * STAT;
+  static constexpr int SMEM = CTRL + 512;
+  static constexpr int S_COL = 0, DP_COL = 128, A1_COL = 256, A2_COL = 256 + D;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
+  static constexpr uint32_t IDESC_A = idesc_bf16(128, D, false, true);
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // more than half an SM: one CTA per SM, so the 512 TMEM columns are free at launch
+  static_assert(SMEM > 114 * 1024, "one CTA per SM");
+};
+
+struct alignas(8) Ctrl {
+  uint64_t x1_full, x2_full;
+  uint64_t y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
+  uint64_t st_full[2], st_empty[2];
+  uint64_t s_full, p_full, dp_full, ds_full, acc_full;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+static_assert(sizeof(Ctrl) <= 512, "Ctrl");
+
+// Untiled copy global -> shared (16-byte aligned, completion on an mbarrier).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ float4 lds128(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// (y0, y1) = (x0, x1) * s + (b0, b1)
+__device__ __forceinline__ void fma2b(float& y0, float& y1, float x0, float x1, float s, float b0, float b1) {
+  asm("{\n\t.reg .b64 xa, sa, ba;\n\tmov.b64 xa, {%2, %3};\n\tmov.b64 sa, {%4, %4};\n\t"
+      "mov.b64 ba, {%5, %6};\n\tfma.rn.f32x2 xa, xa, sa, ba;\n\tmov.b64 {%0, %1}, xa;\n\t}"
+      : "=f"(y0), "=f"(y1)
+      : "f"(x0), "f"(x1), "f"(s), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
+      "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
+// Allowed columns of row r of a 64-wide boundary tile (grid descriptor).
+__device__ __forceinline__ uint64_t row_mask(const uint4& d0, const uint4& d1, int r) {
+  const int n_r = d0.x & 0xFF, n_c = (d0.x >> 8) & 0xFF;
+  int rs = 0;
+#pragma unroll
+  for (int k = 1; k < 8; ++k)
+    if (k < n_r && static_cast<int>(fwd::desc_byte(d0, d1, 2 + k)) <= r) rs = k;
+  const uint64_t bits = (static_cast<uint64_t>(d1.w) << 32) | d1.z;
+  const uint32_t rb = static_cast<uint32_t>(bits >> (rs * 8)) & ((1u << n_c) - 1u);
+  uint32_t words[2] = {0u, 0u};
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (c < n_c && ((rb >> c) & 1u))
+      fwd::add_range<64>(words, static_cast<int>(fwd::desc_byte(d0, d1, 10 + c)),
+                         static_cast<int>(fwd::desc_byte(d0, d1, 11 + c)));
+  return (static_cast<uint64_t>(words[1]) << 32) | words[0];
+}
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int4 it,
+                                             const int2* entries, const uint4* descs, int warp, int lane) {
+  using C = Cfg<D>;
+  volatile int32_t* abort_flag = &ctrl.abort_flag;
+  const int half = warp >> 2;
+  const int r = (warp & 3) * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const int32_t n = it.w - it.z, steps = (n + 1) / 2;
+  const int64_t row = static_cast<int64_t>(it.y) * 128 + r;
+  const bool valid = row < p.N;
+  const uint32_t s_col = tmem + lanes + C::S_COL + 64 * half, dp_col = tmem + lanes + C::DP_COL + 64 * half;
+  float lse2 = 0.f, delta = 0.f;
+  if (!KEYS) {
+    lse2 = valid ? __ldg(p.lse2 + static_cast<int64_t>(it.x) * p.Np + row) : INFINITY;
+    delta = valid ? __ldg(p.delta + static_cast<int64_t>(it.x) * p.Np + row) : 0.f;
+  }
+  // the tile's descriptor, fetched one step ahead
+  int32_t desc_next = -1;
+  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+  auto fetch = [&](int32_t j) {
+    const int32_t e = 2 * j + half;
+    desc_next = -1;
+    if (e < n) {
+      desc_next = __ldg(&entries[it.z + e]).y;
+      if (desc_next >= 0) {
+        n0 = __ldg(&descs[2 * desc_next]);
+        n1 = __ldg(&descs[2 * desc_next + 1]);
+      }
+    }
+  };
+  fetch(0);
+  bool ok = true;
+  for (int32_t j = 0; j < steps; ++j) {
+    const bool on = 2 * j + half < n;        // the last step may hold one tile
+    const int32_t desc = desc_next;
+    const uint4 d0 = n0, d1 = n1;
+    fetch(j + 1);
+    const uint32_t st = base + C::ST + (j & 1) * C::STAT + half * 256;   // [lse2 128][delta 128]
+    if (KEYS) {
+      if (!mbar_wait(smem_u32(&ctrl.st_full[j & 1]), (j >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
+    }
+    if (!mbar_wait(smem_u32(&ctrl.s_full), j & 1, abort_flag, p.err)) { ok = false; break; }
+    tc_fence_after();
+    float pr[64];
+    uint64_t allowed = ~0ull;
+    if (on) {
+      uint32_t a[32], b[32];
+      tmem_ld32(s_col, a);
+      tmem_ld32(s_col + 32, b);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        pr[i] = __uint_as_float(a[i]);
+        pr[32 + i] = __uint_as_float(b[i]);
+      }
+    }
+    if (!KEYS) {
+      // S is in registers: its columns are free for the next step
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full));
+    }
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        float4 l = make_float4(lse2, lse2, lse2, lse2);
+        if (KEYS) l = lds128(st + i * 4);
+        fma2b(pr[i], pr[i + 1], pr[i], pr[i + 1], p.scale_log2, -l.x, -l.y);
+        fma2b(pr[i + 2], pr[i + 3], pr[i + 2], pr[i + 3], p.scale_log2, -l.z, -l.w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pr[i + k] = ex2_approx(pr[i + k]);
+      }
+      if (desc >= 0) {
+        allowed = row_mask(d0, d1, r);
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (!((allowed >> i) & 1u)) pr[i] = 0.f;
+      }
+      if (KEYS) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(pr[2 * i], pr[2 * i + 1]);
+        tmem_st32(s_col, pk);
+        tc_wait_st();
+      }
+    }
+    if (KEYS) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full));
+    }
+    if (!mbar_wait(smem_u32(&ctrl.dp_full), j & 1, abort_flag, p.err)) { ok = false; break; }
+    tc_fence_after();
+    if (on) {
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t a[32];
+        tmem_ld32(dp_col + c, a);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float4 dl = make_float4(delta, delta, delta, delta);
+          if (KEYS) dl = lds128(st + 512 + (c + i) * 4);
+          float x0 = __uint_as_float(a[i]), x1 = __uint_as_float(a[i + 1]);
+          float x2 = __uint_as_float(a[i + 2]), x3 = __uint_as_float(a[i + 3]);
+          fwd::add2(x0, x1, -dl.x, -dl.y);
+          fwd::add2(x2, x3, -dl.z, -dl.w);
+          mul2(x0, x1, pr[c + i], pr[c + i + 1]);
+          mul2(x2, x3, pr[c + i + 2], pr[c + i + 3]);
+          pk[(c + i) / 2] = pack_bf16x2(x0, x1);
+          pk[(c + i) / 2 + 1] = pack_bf16x2(x2, x3);
+        }
+      }
+      if (desc >= 0) {
+        // masked pairs: 0 whatever dP holds (P is 0 there, but dP need not be finite)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t two = static_cast<uint32_t>(allowed >> (2 * i)) & 3u;
+          pk[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+        }
+      }
+      tmem_st32(dp_col, pk);
+      tc_wait_st();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&ctrl.ds_full));
+      if (KEYS) mbar_arrive(smem_u32(&ctrl.st_empty[j & 1]));
+    }
+  }
+  // ---- epilogue: half the columns of each accumulator
+  if (ok && steps > 0) {
+    if (mbar_wait(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err)) {
+      tc_fence_after();
+#pragma unroll
+      for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
+        __nv_bfloat16* out = KEYS ? (w ? p.dv : p.dk) : p.dq;
+        const float f = w ? 1.f : p.scale;
+        const uint32_t col = tmem + lanes + (w ? C::A2_COL : C::A1_COL) + half * (D / 2);
+        uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + (valid ? row : 0)) * D +
+                                              half * (D / 2));
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 32) {
+          uint32_t a[32];
+          tmem_ld32(col + c, a);
+          tc_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[c / 8 + i] = make_uint4(
+                  pack_bf16x2(__uint_as_float(a[8 * i]) * f, __uint_as_float(a[8 * i + 1]) * f),
+                  pack_bf16x2(__uint_as_float(a[8 * i + 2]) * f, __uint_as_float(a[8 * i + 3]) * f),
+                  pack_bf16x2(__uint_as_float(a[8 * i + 4]) * f, __uint_as_float(a[8 * i + 5]) * f),
+                  pack_bf16x2(__uint_as_float(a[8 * i + 6]) * f, __uint_as_float(a[8 * i + 7]) * f));
+          }
+        }
+      }
+    }
+  } else if (ok && valid) {
+#pragma unroll
+    for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
+      __nv_bfloat16* out = KEYS ? (w ? p.dv : p.dk) : p.dq;
+      uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + row) * D + half * (D / 2));
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint32_t base, int4 it,
+                                              const int2* entries) {
+  using C = Cfg<D>;
+  volatile int32_t* abort_flag = &ctrl.abort_flag;
+  const int32_t n = it.w - it.z, steps = (n + 1) / 2, bh = it.x;
+  const CUtensorMap *x1 = KEYS ? &p.tk : &p.tq, *x2 = KEYS ? &p.tv : &p.tdo;
+  const CUtensorMap *y1 = KEYS ? &p.tq : &p.tk, *y2 = KEYS ? &p.tdo : &p.tv;
+  if (steps == 0) return;
+  // one 64-row tile into rows [64 * part, +64) of a 128-row operand
+  auto tile = [&](const CUtensorMap* map, uint32_t dst, int part, int32_t row, uint32_t bar) {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * 128 * 128 + part * 64 * 128, map, bar, c * 64, row, bh);
+  };
+  auto stationary = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar) {
+    mbar_arrive_expect_tx(smem_u32(bar), C::TILE);
+    tile(map, dst, 0, it.y * 128, smem_u32(bar));
+    tile(map, dst, 1, it.y * 128 + 64, smem_u32(bar));
+  };
+  int32_t i1 = 0, i2 = 0, is = 0;       // stages filled, for the drain
+  bool x2_issued = false;
+  stationary(x1, base + C::X1, &ctrl.x1_full);
+  for (int32_t j = 0; j < steps; ++j) {
+    const int parts = 2 * j + 1 < n ? 2 : 1;
+    const int32_t k0 = __ldg(&entries[it.z + 2 * j]).x;
+    const int32_t k1 = parts == 2 ? __ldg(&entries[it.z + 2 * j + 1]).x : 0;
+    const int a = j % C::S1, b = j % C::S2;
+    if (!mbar_wait(smem_u32(&ctrl.y1_empty[a]), ((j / C::S1) & 1) ^ 1, abort_flag, p.err)) break;
+    mbar_arrive_expect_tx(smem_u32(&ctrl.y1_full[a]), parts * (C::TILE / 2));
+    tile(y1, base + C::Y1 + a * C::TILE, 0, k0, smem_u32(&ctrl.y1_full[a]));
+    if (parts == 2) tile(y1, base + C::Y1 + a * C::TILE, 1, k1, smem_u32(&ctrl.y1_full[a]));
+    ++i1;
+    if (KEYS) {
+      const uint32_t bar = smem_u32(&ctrl.st_full[j & 1]), dst = base + C::ST + (j & 1) * C::STAT;
+      if (!mbar_wait(smem_u32(&ctrl.st_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag, p.err)) break;
+      mbar_arrive_expect_tx(bar, parts * 512);
+      const int64_t o = static_cast<int64_t>(bh) * p.Np;
+      bulk_load(dst, p.lse2 + o + k0, 256, bar);
+      bulk_load(dst + 512, p.delta + o + k0, 256, bar);
+      if (parts == 2) {
+        bulk_load(dst + 256, p.lse2 + o + k1, 256, bar);
+        bulk_load(dst + 768, p.delta + o + k1, 256, bar);
+      }
+      ++is;
+    }
+    if (j == 0) {
+      stationary(x2, base + C::X2, &ctrl.x2_full);
+      x2_issued = true;
+    }
+    if (!mbar_wait(smem_u32(&ctrl.y2_empty[b]), ((j / C::S2) & 1) ^ 1, abort_flag, p.err)) break;
+    mbar_arrive_expect_tx(smem_u32(&ctrl.y2_full[b]), parts * (C::TILE / 2));
+    tile(y2, base + C::Y2 + b * C::TILE, 0, k0, smem_u32(&ctrl.y2_full[b]));
+    if (parts == 2) tile(y2, base + C::Y2 + b * C::TILE, 1, k1, smem_u32(&ctrl.y2_full[b]));
+    ++i2;
+  }
+  if (*abort_flag) {
+    // let the copies in flight land before the CTA ends
+    volatile int32_t no = 0;
+    mbar_wait(smem_u32(&ctrl.x1_full), 0, &no, p.err);
+    if (x2_issued) mbar_wait(smem_u32(&ctrl.x2_full), 0, &no, p.err);
+    for (int32_t k = max(0, i1 - C::S1); k < i1; ++k)
+      mbar_wait(smem_u32(&ctrl.y1_full[k % C::S1]), (k / C::S1) & 1, &no, p.err);
+    for (int32_t k = max(0, i2 - C::S2); k < i2; ++k)
+      mbar_wait(smem_u32(&ctrl.y2_full[k % C::S2]), (k / C::S2) & 1, &no, p.err);
+    for (int32_t k = max(0, is - 2); k < is; ++k)
+      mbar_wait(smem_u32(&ctrl.st_full[k & 1]), (k >> 1) & 1, &no, p.err);
+  }
+}
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int4 it) {
+  using C = Cfg<D>;
+  volatile int32_t* abort_flag = &ctrl.abort_flag;
+  const int32_t n = it.w - it.z, steps = (n + 1) / 2;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(smem_u32(bar), parity, abort_flag, p.err); };
+  // D[128 x 128] = X Y^T over d
+  auto outer = [&](uint32_t col, uint32_t sx, uint32_t sy) {
+    tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t o = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
+      mma_bf16_ss(tmem + col, sdesc_sw128(sx + o, 16, 1024), sdesc_sw128(sy + o, 16, 1024), C::IDESC_S, kk > 0);
+    }
+  };
+  // acc[128 x D] += A (bf16, TMEM) Y over the step's rows; P and dS lie 32 columns
+  // per tile, 64 apart
+  auto inner = [&](uint32_t acc, uint32_t col, uint32_t sy, int32_t j) {
+    tc_fence_after();
+    const int kks = 2 * j + 1 < n ? 8 : 4;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      if (kk < kks)
+        mma_bf16_ts(tmem + acc, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8,
+                    sdesc_sw128(sy + kk * 16 * 128, 128 * 128, 1024), C::IDESC_A, (j > 0 || kk > 0) ? 1u : 0u);
+  };
+  const uint32_t sx1 = base + C::X1, sx2 = base + C::X2;
+  auto y1 = [&](int32_t j) { return base + C::Y1 + (j % C::S1) * C::TILE; };
+  auto y2 = [&](int32_t j) { return base + C::Y2 + (j % C::S2) * C::TILE; };
+  auto do_s = [&](int32_t j) -> bool {
+    if (!wait(&ctrl.y1_full[j % C::S1], (j / C::S1) & 1)) return false;
+    outer(C::S_COL, sx1, y1(j));
+    mma_commit(smem_u32(&ctrl.s_full));
+    return true;
+  };
+  auto do_dp = [&](int32_t j) -> bool {
+    if (!wait(&ctrl.y2_full[j % C::S2], (j / C::S2) & 1)) return false;
+    outer(C::DP_COL, sx2, y2(j));
+    mma_commit(smem_u32(&ctrl.dp_full));
+    if (!KEYS) mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
+    return true;
+  };
+  bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && wait(&ctrl.x2_full, 0) && do_dp(0);
+  for (int32_t j = 0; ok && j < steps; ++j) {
+    if (!wait(&ctrl.p_full, j & 1)) break;
+    if (KEYS) {
+      inner(C::A2_COL, C::S_COL, y2(j), j);
+      mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
+    }
+    if (j + 1 < steps && !do_s(j + 1)) break;
+    if (!wait(&ctrl.ds_full, j & 1)) break;
+    inner(C::A1_COL, C::DP_COL, y1(j), j);
+    mma_commit(smem_u32(&ctrl.y1_empty[j % C::S1]));
+    if (j + 1 < steps && !do_dp(j + 1)) break;
+  }
+  // complete once everything issued has: the accumulators are whole (or, after an
+  // abort, TMEM can be released)
+  mma_commit(smem_u32(&ctrl.acc_full));
+  volatile int32_t no = 0;
+  mbar_wait(smem_u32(&ctrl.acc_full), 0, &no, p.err);
+}
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void roles(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int32_t item,
+                                      int warp, int lane) {
+  const int4 it = __ldg((KEYS ? p.items_k : p.items_q) + 2 * static_cast<int64_t>(item));
+  const int2* entries = KEYS ? p.entries_k : p.entries_q;
+  if (warp < 8) {
+    softmax_role<D, KEYS>(p, ctrl, base, tmem, it, entries, KEYS ? p.descs_k : p.descs_q, warp, lane);
+  } else if (warp == 8) {
+    if (lane == 0) producer_role<D, KEYS>(p, ctrl, base, it, entries);
+  } else if (lane == 0) {
+    mma_role<D, KEYS>(p, ctrl, base, tmem, it);
+  }
+  __syncwarp();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + C::CTRL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (base & 1023u) {       // swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(p.err, DEV_ERR_INTERNAL);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (uint64_t* b : {&ctrl.x1_full, &ctrl.x2_full, &ctrl.s_full, &ctrl.dp_full, &ctrl.acc_full})
+      mbar_init(smem_u32(b), 1);
+    for (int i = 0; i < 4; ++i)
+      for (uint64_t* b : {&ctrl.y1_full[i], &ctrl.y1_empty[i], &ctrl.y2_full[i], &ctrl.y2_empty[i]})
+        mbar_init(smem_u32(b), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctrl.st_full[i]), 1);
+      mbar_init(smem_u32(&ctrl.st_empty[i]), 8);
+    }
+    mbar_init(smem_u32(&ctrl.p_full), 8);
+    mbar_init(smem_u32(&ctrl.ds_full), 8);
+    ctrl.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&ctrl.tmem_base), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl.tmem_base;
+  const int32_t b = blockIdx.x;
+  if (b < p.n_key_items) roles<D, true>(p, ctrl, base, tmem, b, warp, lane);
+  else roles<D, false>(p, ctrl, base, tmem, b - p.n_key_items, warp, lane);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Per query row: lse in base 2 and delta = sum dO o O (fp32), one row per D / 8
+// lanes; rows past N of the padded arrays get P = 0.  HBM-bound: reads O and dO.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_stats_kernel(const uint4* __restrict__ o, const uint4* __restrict__ g,
+                                                        const float* __restrict__ lse, float* __restrict__ lse2,
+                                                        float* __restrict__ delta, int64_t rows_p, int32_t N,
+                                                        int32_t Np) {
+  constexpr int VR = D / 8;
+  const int64_t row = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / VR;
+  const int v = threadIdx.x % VR;
+  if (row >= rows_p) return;       // whole groups of VR lanes leave together
+  const int64_t bh = row / Np;
+  const int32_t i = static_cast<int32_t>(row - bh * Np);
+  float s = 0.f;
+  float l = INFINITY;
+  if (i < N) {
+    const int64_t src = (bh * N + i) * VR + v;
+    const uint4 a = __ldg(o + src), b = __ldg(g + src);
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), s);
+      s = fmaf(__uint_as_float(x[k] & 0xFFFF0000u), __uint_as_float(y[k] & 0xFFFF0000u), s);
+    }
+    l = __ldg(lse + bh * N + i) * kLog2e;
+    if (l == -INFINITY) l = INFINITY;        // no allowed key: P = 2^(s - inf) = 0
+  }
+  const uint32_t grp = VR == 32 ? 0xFFFFFFFFu : ((1u << VR) - 1u) << ((threadIdx.x & 31) / VR * VR);
+#pragma unroll
+  for (int m = VR / 2; m; m >>= 1) s += __shfl_xor_sync(grp, s, m);
+  if (v == 0) {
+    lse2[row] = l;
+    delta[row] = s;
+  }
+}
+
+// blocks [heads][nq][nk] -> [heads][nk][nq]
+__global__ void transpose_blocks_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, int32_t nq,
+                                        int32_t nk, int32_t tiles_k) {
+  __shared__ uint8_t t[32][33];
+  const int64_t base = static_cast<int64_t>(blockIdx.y) * nq * nk;
+  const int q0 = (blockIdx.x / tiles_k) * 32, k0 = (blockIdx.x % tiles_k) * 32;
+  for (int y = threadIdx.y; y < 32; y += 8) {
+    const int q = q0 + y, k = k0 + threadIdx.x;
+    if (q < nq && k < nk) t[y][threadIdx.x] = src[base + static_cast<int64_t>(q) * nk + k];
+  }
+  __syncthreads();
+  for (int y = threadIdx.y; y < 32; y += 8) {
+    const int k = k0 + y, q = q0 + threadIdx.x;
+    if (q < nq && k < nk) dst[base + static_cast<int64_t>(k) * nq + q] = t[threadIdx.x][y];
+  }
+}
+
+template <int D>
+tsr_status launch(const Params& prm, int64_t ctas, int device, cudaStream_t st) {
+  using C = Cfg<D>;
+  auto kern = bsa_bwd_kernel<D>;
+  static bool attr_set[64] = {false};
+  if (device < 0 || device >= 64 || !attr_set[device]) {
+    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    if (device >= 0 && device < 64) attr_set[device] = true;
+  }
+  kern<<<static_cast<unsigned>(ctas), kThreads, C::SMEM, st>>>(prm);
+  TSR_CUDA(cudaGetLastError());
+  return TSR_OK;
+}
+
+}  // namespace bwd
+
+tsr_status launch_transpose_blocks(const uint8_t* src, uint8_t* dst, int64_t heads, int32_t nq, int32_t nk,
+                                   cudaStream_t st) {
+  const int32_t tq = (nq + 31) / 32, tk = (nk + 31) / 32;
+  if (static_cast<int64_t>(tq) * tk >= (int64_t{1} << 31)) return fail(TSR_ERR_UNSUPPORTED, "too many blocks");
+  for (int64_t h0 = 0; h0 < heads; h0 += 65535) {     // the grid's y limit
+    const int64_t n = std::min<int64_t>(65535, heads - h0), o = h0 * nq * nk;
+    bwd::transpose_blocks_kernel<<<dim3(static_cast<unsigned>(tq * tk), static_cast<unsigned>(n)), dim3(32, 8), 0,
+                                   st>>>(src + o, dst + o, nq, nk, tk);
+    TSR_CUDA(cudaGetLastError());
+  }
+  return TSR_OK;
+}
+
+tsr_status launch_backward(const BwdArgs& a, cudaStream_t st) {
+  const tsr_plan_impl *Q = a.plan_q, *K = a.plan_k;
+  const int32_t N = Q->N, D = Q->d, Np = (N + 63) / 64 * 64;
+  const int64_t BH = static_cast<int64_t>(Q->B) * Q->H;
+  bwd::Params p;
+  memset(&p, 0, sizeof p);
+  const uint64_t d = D, n = N, bh = BH;
+  if (!encode_tmap_3d(&p.tq, a.q, d, n, bh, 64, 64) || !encode_tmap_3d(&p.tk, a.k, d, n, bh, 64, 64) ||
+      !encode_tmap_3d(&p.tv, a.v, d, n, bh, 64, 64) || !encode_tmap_3d(&p.tdo, a.dout, d, n, bh, 64, 64))
+    return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled failed (pointer alignment or shape)");
+  p.items_k = static_cast<const int4*>(K->items);
+  p.items_q = static_cast<const int4*>(Q->items);
+  p.entries_k = static_cast<const int2*>(K->entries);
+  p.entries_q = static_cast<const int2*>(Q->entries);
+  p.descs_k = static_cast<const uint4*>(K->descs);
+  p.descs_q = static_cast<const uint4*>(Q->descs);
+  float* lse2 = static_cast<float*>(a.workspace);
+  float* delta = lse2 + BH * Np;
+  p.lse2 = lse2;
+  p.delta = delta;
+  p.dq = static_cast<__nv_bfloat16*>(a.dq);
+  p.dk = static_cast<__nv_bfloat16*>(a.dk);
+  p.dv = static_cast<__nv_bfloat16*>(a.dv);
+  p.err = Q->err;
+  p.n_key_items = static_cast<int32_t>(K->n_items);
+  p.N = N;
+  p.Np = Np;
+  p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+  const int64_t rows = BH * Np, ctas = K->n_items + Q->n_items;
+  const int64_t stat_blocks = (rows * (D / 8) + 255) / 256;
+  if (stat_blocks >= (int64_t{1} << 31)) return fail(TSR_ERR_UNSUPPORTED, "too many rows");
+  const uint4 *o = static_cast<const uint4*>(a.out), *g = static_cast<const uint4*>(a.dout);
+  if (D == 64)
+    bwd::bwd_stats_kernel<64><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, lse2, delta, rows, N, Np);
+  else
+    bwd::bwd_stats_kernel<128><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, lse2, delta, rows, N, Np);
+  TSR_CUDA(cudaGetLastError());
+  return D == 64 ? bwd::launch<64>(p, ctas, Q->device, st) : bwd::launch<128>(p, ctas, Q->device, st);
+}
+
+}  // namespace tsr

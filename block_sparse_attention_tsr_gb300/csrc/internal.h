@@ -188,6 +188,21 @@ size_t select_workspace(const tsr_select_desc& s);
 tsr_status launch_select(const tsr_select_desc& s, const void* q, const void* k, uint8_t* blocks, void* ws,
                          cudaStream_t stream);
 
+// backward pass (bwd.cu): the mask's plan (query items) and its transpose's (key
+// items), both 128-row tiles 64 wide
+struct BwdArgs {
+  const void *q, *k, *v, *out;
+  const float* lse;
+  const void* dout;
+  void *dq, *dk, *dv;
+  void* workspace;              // lse in base 2 and delta, fp32 [2][B*H][N rounded up to 64]
+  const tsr_plan_impl *plan_q, *plan_k;
+};
+tsr_status launch_backward(const BwdArgs& a, cudaStream_t stream);
+// blocks uint8 [heads][nq][nk] -> [heads][nk][nq]
+tsr_status launch_transpose_blocks(const uint8_t* src, uint8_t* dst, int64_t heads, int32_t nq, int32_t nk,
+                                   cudaStream_t stream);
+
 // permutation (permute.cu)
 tsr_status launch_permute(const void* src, void* dst, int32_t B, int32_t H, int32_t F, int32_t S,
                           int32_t row_bytes, const int8_t* head_kind_host, int32_t inverse,

@@ -282,6 +282,52 @@ typedef struct {
 
 tsr_status tsr_bsa_forward_batch(const tsr_request *reqs, int32_t n, void *stream);
 
+/*
+ * tsr_bsa_backward -- the gradients of tsr_bsa_forward's q, k and v, for
+ * TSR_MASK_UNIFORM and TSR_MASK_SEGMENTS masks.  Other kinds, and masks whose
+ * blocks are so small that 128 tokens overlap more than 8 of them (on the query or
+ * the key side; blocks of 17 and 18 tokens can), give TSR_ERR_UNSUPPORTED when the
+ * backward plan is made.
+ *
+ * With P = exp(q.k / sqrt(d) - lse) on the allowed pairs, dP = dO V^T and
+ * delta = rowsum(dO o O):  dS = P o (dP - delta) / sqrt(d),
+ *     dq = dS K,   dk = dS^T Q,   dv = P^T dO.
+ * q, k, v, out, dout, dq, dk, dv: device bf16 [B][H][N][d]; lse: device fp32
+ * [B][H][N]; out and lse are the forward's, over the same mask.  Every row of dq,
+ * dk and dv is written: queries with no allowed key and keys that no query sees
+ * get 0.  Sums are fp32; P and dS are rounded to bf16 for the second products (as
+ * P is in the forward).  No atomics: the same inputs give the same bits.  The
+ * inputs must be finite (masked rows included: a tile's products run over all of
+ * its rows).  dq, dk, dv must not alias each other or an input.
+ *
+ * A backward plan holds the mask's tiles by query and by key; it is made on
+ * `stream` (tsr_plan twice: the mask and its transpose, synchronising as it does),
+ * belongs to the device it was made on and may serve any number of calls, at the
+ * same time too, on any streams.  tsr_backward_plan_update re-plans a new mask of
+ * the same B, H, N and d into the same storage; no queued call may be using the
+ * plan on another stream, and a plan whose update failed is refused until one
+ * succeeds.  workspace: device, 256-byte aligned, tsr_bsa_backward_workspace()
+ * bytes, contents not kept; calls that may run at the same time need one each.
+ * tsr_bsa_backward is asynchronous, allocates nothing and may be captured into a
+ * CUDA graph.  A bounded device wait that gave up is reported by
+ * tsr_backward_plan_device_status (TSR_ERR_TIMEOUT), which synchronises `stream`.
+ */
+typedef struct tsr_backward_plan_s *tsr_backward_plan_t;
+
+tsr_status tsr_backward_plan(const tsr_mask *mask, tsr_backward_plan_t *out, void *stream);
+
+tsr_status tsr_backward_plan_update(tsr_backward_plan_t plan, const tsr_mask *mask, void *stream);
+
+tsr_status tsr_backward_plan_destroy(tsr_backward_plan_t plan);
+
+tsr_status tsr_backward_plan_device_status(tsr_backward_plan_t plan, void *stream);
+
+tsr_status tsr_bsa_backward_workspace(tsr_backward_plan_t plan, size_t *bytes /* HOST */);
+
+tsr_status tsr_bsa_backward(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                            const void *dout, tsr_backward_plan_t plan, void *dq, void *dk, void *dv,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronise `stream` and return the plan's device error word as a status
    (TSR_OK, TSR_ERR_TIMEOUT or TSR_ERR_INTERNAL); clears it. */
 tsr_status tsr_plan_device_status(tsr_plan_t plan, void *stream);

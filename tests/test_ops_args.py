@@ -109,3 +109,34 @@ def test_select_refuses_bad_pointers(L):
     assert b"too small" in L.tsr_last_error()
     assert L.tsr_block_select_workspace(None, ctypes.byref(n)) == INVALID
     assert L.tsr_block_select_workspace(ctypes.byref(d), None) == INVALID
+
+
+def _mask(**kw):
+    m = tsr._Mask()
+    base = dict(kind=0, B=1, H=1, N=128, d=64, bq=64, bk=64, blocks=16)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(m, k, v)
+    return m
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(d=96), INVALID), (dict(bq=8), INVALID), (dict(blocks=0), INVALID), (dict(N=0), INVALID),
+    (dict(kind=9), INVALID), (dict(kind=2, n_frames=4, frame_size=32, head_kind=16), UNSUPPORTED),
+    (dict(kind=3, slice_m=64, indptr=16), UNSUPPORTED),
+])
+def test_backward_plan_refuses_bad_masks(L, kw, code):
+    h, m = ctypes.c_void_p(0), _mask(**kw)
+    assert L.tsr_backward_plan(ctypes.byref(m), ctypes.byref(h), None) == code
+    assert not h.value and len(L.tsr_last_error()) > 0
+
+
+def test_backward_refuses_null(L):
+    h, n = ctypes.c_void_p(0), ctypes.c_size_t(0)
+    assert L.tsr_backward_plan(None, ctypes.byref(h), None) == INVALID
+    assert L.tsr_backward_plan(ctypes.byref(_mask()), None, None) == INVALID
+    assert L.tsr_backward_plan_update(None, ctypes.byref(_mask()), None) == INVALID
+    assert L.tsr_bsa_backward_workspace(None, ctypes.byref(n)) == INVALID
+    assert L.tsr_backward_plan_device_status(None, None) == INVALID
+    assert L.tsr_bsa_backward(*([4096] * 6), None, 4096, 4096, 4096, 4096, 1 << 20, None) == INVALID
+    assert L.tsr_backward_plan_destroy(None) == 0
