@@ -22,14 +22,15 @@
 // rounded to bf16, the operand type of the second products, and written over S
 // and dP in TMEM (512 columns: S, dP and the two accumulators of d).
 //
-// Order of the tensor pipe, one thread issuing: S(j+1) right after acc2(j) (which
-// frees P's columns), then acc1(j), dP(j+1), acc2(j+1) ...  While the pipe runs
-// acc1(j) and dP(j+1), the softmax turns S(j+1) into P; while it runs acc2(j+1) and
-// S(j+2), dP(j+1) into dS.
-//   warps 0..7  softmax: row = TMEM lane, warps 0..3 the step's first tile (64
-//               columns), warps 4..7 its second; then the epilogue
-//   warp 8      producer: TMA tiles and the rows' statistics
-//   warp 9      MMA issuer
+// Two threads issue, because the pipe runs dry while a lone issuer waits on a
+// barrier: one S(j+1) right after acc2(j) (which frees P's columns), the other
+// dP(j+1) right after acc1(j).  The softmax turns S(j+1) into P while the pipe runs
+// acc1(j) and dP(j+1), and dP(j+1) into dS while it runs acc2(j+1) and S(j+2).
+// Query items have TMEM to spare for a second dP, so dP(j+1) runs before acc1(j).
+//   warps 0..15 softmax: row = TMEM lane, four warps for each 32 of the step's 128
+//               columns; then the epilogue
+//   warp 16     producer: TMA tiles and the rows' statistics
+//   warps 17, 18 MMA issuers
 // Every wait is bounded: on expiry the error word is set and the kernel winds down.
 #include <cuda_bf16.h>
 
@@ -45,7 +46,7 @@ namespace tsr {
 
 namespace bwd {
 
-constexpr int kThreads = 320;
+constexpr int kSoftmaxWarps = 16, kThreads = (kSoftmaxWarps + 3) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
@@ -53,8 +54,8 @@ struct Params {
   const int4 *items_k, *items_q;   // tsr_plan_item, key items (transposed plan), query items
   const int2 *entries_k, *entries_q;
   const uint4 *descs_k, *descs_q;
-  const float* lse2;               // [B*H][Np] lse * log2(e), +inf for rows with no key and past N
-  const float* delta;              // [B*H][Np]
+  const float* nlse2;              // [B*H][Np] -lse * log2(e), -inf for rows with no key and past N
+  const float* ndelta;             // [B*H][Np] -delta
   __nv_bfloat16 *dq, *dk, *dv;
   uint32_t* err;
   int32_t n_key_items, N, Np;
@@ -67,11 +68,14 @@ struct Cfg {
   // later, so it gets a stage more than Y2 where shared memory is short
   static constexpr int S1 = D == 128 ? 3 : 4, S2 = D == 128 ? 2 : 4;
   static constexpr int TILE = 128 * D * 2;          // one 128-row operand
-  static constexpr int STAT = 2 * 128 * 4;          // lse2 and delta of a step's rows
+  static constexpr int STAT = 2 * 128 * 4;          // -lse2 and -delta of a step's rows
   static constexpr int X1 = 0, X2 = TILE, Y1 = 2 * TILE, Y2 = Y1 + S1 * TILE, ST = Y2 + S2 * TILE;
   static constexpr int CTRL = ST + 2 * STAT;
   static constexpr int SMEM = CTRL + 512;
+  // TMEM columns.  Key items: S, dP, dK, dV.  Query items have one accumulator and
+  // room for a second dP.
   static constexpr int S_COL = 0, DP_COL = 128, A1_COL = 256, A2_COL = 256 + D;
+  static constexpr int DPQ_COL = 128, AQ_COL = 384;
   static constexpr int TMEM_COLS = 512;
   static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
   static constexpr uint32_t IDESC_A = idesc_bf16(128, D, false, true);
@@ -84,7 +88,7 @@ struct alignas(8) Ctrl {
   uint64_t x1_full, x2_full;
   uint64_t y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
   uint64_t st_full[2], st_empty[2];
-  uint64_t s_full, p_full, dp_full, ds_full, acc_full;
+  uint64_t s_full, p_full, dp_full[2], ds_full[2], acc_full;
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -117,22 +121,42 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
       : "f"(b0), "f"(b1));
 }
 
-// Allowed columns of row r of a 64-wide boundary tile (grid descriptor).
-__device__ __forceinline__ uint64_t row_mask(const uint4& d0, const uint4& d1, int r) {
+// Allowed columns [32 sub, 32 sub + 32) of row r of a 64-wide boundary tile (grid
+// descriptor).  The segment counts are the same for the whole warp, so the loops
+// end early; most tiles have one column segment and need no ranges.
+__device__ __forceinline__ uint32_t row_mask(const uint4& d0, const uint4& d1, int r, int sub) {
   const int n_r = d0.x & 0xFF, n_c = (d0.x >> 8) & 0xFF;
   int rs = 0;
 #pragma unroll
-  for (int k = 1; k < 8; ++k)
-    if (k < n_r && static_cast<int>(fwd::desc_byte(d0, d1, 2 + k)) <= r) rs = k;
+  for (int k = 1; k < 8; ++k) {
+    if (k >= n_r) break;
+    if (static_cast<int>(fwd::desc_byte(d0, d1, 2 + k)) <= r) rs = k;
+  }
   const uint64_t bits = (static_cast<uint64_t>(d1.w) << 32) | d1.z;
-  const uint32_t rb = static_cast<uint32_t>(bits >> (rs * 8)) & ((1u << n_c) - 1u);
-  uint32_t words[2] = {0u, 0u};
+  const uint32_t all = (1u << n_c) - 1u;
+  const uint32_t rb = static_cast<uint32_t>(bits >> (rs * 8)) & all;
+  if (rb == all && fwd::desc_byte(d0, d1, 10 + n_c) >= 64u) return 0xFFFFFFFFu;
+  uint32_t word = 0u;
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    if (c < n_c && ((rb >> c) & 1u))
-      fwd::add_range<64>(words, static_cast<int>(fwd::desc_byte(d0, d1, 10 + c)),
-                         static_cast<int>(fwd::desc_byte(d0, d1, 11 + c)));
-  return (static_cast<uint64_t>(words[1]) << 32) | words[0];
+  for (int c = 0; c < 8; ++c) {
+    if (c >= n_c) break;
+    if ((rb >> c) & 1u) {
+      const int lo = max(static_cast<int>(fwd::desc_byte(d0, d1, 10 + c)) - 32 * sub, 0);
+      const int hi = min(static_cast<int>(fwd::desc_byte(d0, d1, 11 + c)) - 32 * sub, 32);
+      if (lo < hi) word |= (hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+    }
+  }
+  return word;
+}
+
+// 32 lanes x 16 consecutive 32-bit TMEM columns <- 16 registers per thread.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 template <int D, bool KEYS>
@@ -140,23 +164,24 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
                                              const int2* entries, const uint4* descs, int warp, int lane) {
   using C = Cfg<D>;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
-  const int half = warp >> 2;
+  const int grp = warp >> 2;               // columns [32 grp, +32) of the step
+  const int part = grp >> 1, sub = grp & 1;
   const int r = (warp & 3) * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const int32_t n = it.w - it.z, steps = (n + 1) / 2;
   const int64_t row = static_cast<int64_t>(it.y) * 128 + r;
   const bool valid = row < p.N;
-  const uint32_t s_col = tmem + lanes + C::S_COL + 64 * half, dp_col = tmem + lanes + C::DP_COL + 64 * half;
-  float lse2 = 0.f, delta = 0.f;
+  const uint32_t s_col = tmem + lanes + C::S_COL + 32 * grp;
+  float nlse = 0.f, ndelta = 0.f;
   if (!KEYS) {
-    lse2 = valid ? __ldg(p.lse2 + static_cast<int64_t>(it.x) * p.Np + row) : INFINITY;
-    delta = valid ? __ldg(p.delta + static_cast<int64_t>(it.x) * p.Np + row) : 0.f;
+    nlse = valid ? __ldg(p.nlse2 + static_cast<int64_t>(it.x) * p.Np + row) : -INFINITY;
+    ndelta = valid ? __ldg(p.ndelta + static_cast<int64_t>(it.x) * p.Np + row) : 0.f;
   }
   // the tile's descriptor, fetched one step ahead
   int32_t desc_next = -1;
   uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
   auto fetch = [&](int32_t j) {
-    const int32_t e = 2 * j + half;
+    const int32_t e = 2 * j + part;
     desc_next = -1;
     if (e < n) {
       desc_next = __ldg(&entries[it.z + e]).y;
@@ -169,28 +194,24 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
   fetch(0);
   bool ok = true;
   for (int32_t j = 0; j < steps; ++j) {
-    const bool on = 2 * j + half < n;        // the last step may hold one tile
-    const int32_t desc = desc_next;
-    const uint4 d0 = n0, d1 = n1;
+    const bool on = 2 * j + part < n;        // the last step may hold one tile
+    const uint32_t allowed = !on ? 0u : desc_next >= 0 ? row_mask(n0, n1, r, sub) : 0xFFFFFFFFu;
     fetch(j + 1);
-    const uint32_t st = base + C::ST + (j & 1) * C::STAT + half * 256;   // [lse2 128][delta 128]
+    // a warp whose rows all see nothing here (half of a tile whose other half does)
+    // has no arithmetic to do, one whose rows see everything no masking
+    const bool none = __all_sync(0xFFFFFFFFu, allowed == 0u);
+    const bool mixed = !__all_sync(0xFFFFFFFFu, allowed == 0xFFFFFFFFu);
+    const uint32_t st = base + C::ST + (j & 1) * C::STAT + grp * 128;   // [-lse2 128][-delta 128]
+    const uint32_t dp_col = tmem + lanes + (KEYS ? C::DP_COL : C::DPQ_COL + 128 * (j & 1)) + 32 * grp;
     if (KEYS) {
       if (!mbar_wait(smem_u32(&ctrl.st_full[j & 1]), (j >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
     }
     if (!mbar_wait(smem_u32(&ctrl.s_full), j & 1, abort_flag, p.err)) { ok = false; break; }
     tc_fence_after();
-    float pr[64];
-    uint64_t allowed = ~0ull;
-    if (on) {
-      uint32_t a[32], b[32];
-      tmem_ld32(s_col, a);
-      tmem_ld32(s_col + 32, b);
+    uint32_t x[32];                          // S, then P, as float bits
+    if (!none) {
+      tmem_ld32(s_col, x);
       tc_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        pr[i] = __uint_as_float(a[i]);
-        pr[32 + i] = __uint_as_float(b[i]);
-      }
     }
     if (!KEYS) {
       // S is in registers: its columns are free for the next step
@@ -198,77 +219,81 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full));
     }
-    if (on) {
+    if (!none) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        float4 l = make_float4(lse2, lse2, lse2, lse2);
+      for (int i = 0; i < 32; i += 4) {
+        float4 l = make_float4(nlse, nlse, nlse, nlse);
         if (KEYS) l = lds128(st + i * 4);
-        fma2b(pr[i], pr[i + 1], pr[i], pr[i + 1], p.scale_log2, -l.x, -l.y);
-        fma2b(pr[i + 2], pr[i + 3], pr[i + 2], pr[i + 3], p.scale_log2, -l.z, -l.w);
+        float y[4];
+        fma2b(y[0], y[1], __uint_as_float(x[i]), __uint_as_float(x[i + 1]), p.scale_log2, l.x, l.y);
+        fma2b(y[2], y[3], __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]), p.scale_log2, l.z, l.w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) pr[i + k] = ex2_approx(pr[i + k]);
+        for (int k = 0; k < 4; ++k) x[i + k] = __float_as_uint(ex2_approx(y[k]));
       }
-      if (desc >= 0) {
-        allowed = row_mask(d0, d1, r);
+      if (mixed) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (!((allowed >> i) & 1u)) pr[i] = 0.f;
-      }
-      if (KEYS) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(pr[2 * i], pr[2 * i + 1]);
-        tmem_st32(s_col, pk);
-        tc_wait_st();
+        for (int i = 0; i < 32; ++i)
+          if (!((allowed >> i) & 1u)) x[i] = 0u;
       }
     }
     if (KEYS) {
+      if (on) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          pk[i] = none ? 0u : pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+        tmem_st16(s_col, pk);
+        tc_wait_st();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full));
     }
-    if (!mbar_wait(smem_u32(&ctrl.dp_full), j & 1, abort_flag, p.err)) { ok = false; break; }
+    if (!mbar_wait(smem_u32(&ctrl.dp_full[j & 1]), (j >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
     tc_fence_after();
     if (on) {
-      uint32_t pk[32];
+      uint32_t pk[16];
+      if (none) {
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
+        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+      } else {
         uint32_t a[32];
-        tmem_ld32(dp_col + c, a);
+        tmem_ld32(dp_col, a);
         tc_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          float4 dl = make_float4(delta, delta, delta, delta);
-          if (KEYS) dl = lds128(st + 512 + (c + i) * 4);
+          float4 dl = make_float4(ndelta, ndelta, ndelta, ndelta);
+          if (KEYS) dl = lds128(st + 512 + i * 4);
           float x0 = __uint_as_float(a[i]), x1 = __uint_as_float(a[i + 1]);
           float x2 = __uint_as_float(a[i + 2]), x3 = __uint_as_float(a[i + 3]);
-          fwd::add2(x0, x1, -dl.x, -dl.y);
-          fwd::add2(x2, x3, -dl.z, -dl.w);
-          mul2(x0, x1, pr[c + i], pr[c + i + 1]);
-          mul2(x2, x3, pr[c + i + 2], pr[c + i + 3]);
-          pk[(c + i) / 2] = pack_bf16x2(x0, x1);
-          pk[(c + i) / 2 + 1] = pack_bf16x2(x2, x3);
+          fwd::add2(x0, x1, dl.x, dl.y);
+          fwd::add2(x2, x3, dl.z, dl.w);
+          mul2(x0, x1, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          mul2(x2, x3, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          pk[i / 2] = pack_bf16x2(x0, x1);
+          pk[i / 2 + 1] = pack_bf16x2(x2, x3);
         }
-      }
-      if (desc >= 0) {
-        // masked pairs: 0 whatever dP holds (P is 0 there, but dP need not be finite)
+        if (mixed) {
+          // masked pairs: 0 whatever dP holds (P is 0 there, but dP need not be finite)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t two = static_cast<uint32_t>(allowed >> (2 * i)) & 3u;
-          pk[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t two = (allowed >> (2 * i)) & 3u;
+            pk[i] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+          }
         }
       }
-      tmem_st32(dp_col, pk);
+      tmem_st16(dp_col, pk);
       tc_wait_st();
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(smem_u32(&ctrl.ds_full));
+      mbar_arrive(smem_u32(&ctrl.ds_full[j & 1]));
       if (KEYS) mbar_arrive(smem_u32(&ctrl.st_empty[j & 1]));
     }
   }
-  // ---- epilogue: half the columns of each accumulator
+  // ---- epilogue: a quarter of the columns of each accumulator
+  constexpr int W = D / 4;
   if (ok && steps > 0) {
     if (mbar_wait(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err)) {
       tc_fence_after();
@@ -276,17 +301,17 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
         __nv_bfloat16* out = KEYS ? (w ? p.dv : p.dk) : p.dq;
         const float f = w ? 1.f : p.scale;
-        const uint32_t col = tmem + lanes + (w ? C::A2_COL : C::A1_COL) + half * (D / 2);
-        uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + (valid ? row : 0)) * D +
-                                              half * (D / 2));
+        const uint32_t col = tmem + lanes + (KEYS ? (w ? C::A2_COL : C::A1_COL) : C::AQ_COL) + grp * W;
+        uint4* dst =
+            reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + (valid ? row : 0)) * D + grp * W);
 #pragma unroll
-        for (int c = 0; c < D / 2; c += 32) {
-          uint32_t a[32];
-          tmem_ld32(col + c, a);
+        for (int c = 0; c < W; c += 16) {
+          uint32_t a[16];
+          tmem_ld16(col + c, a);
           tc_wait_ld();
           if (valid) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
               dst[c / 8 + i] = make_uint4(
                   pack_bf16x2(__uint_as_float(a[8 * i]) * f, __uint_as_float(a[8 * i + 1]) * f),
                   pack_bf16x2(__uint_as_float(a[8 * i + 2]) * f, __uint_as_float(a[8 * i + 3]) * f),
@@ -300,9 +325,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
 #pragma unroll
     for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
       __nv_bfloat16* out = KEYS ? (w ? p.dv : p.dk) : p.dq;
-      uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + row) * D + half * (D / 2));
+      uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + row) * D + grp * W);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < W / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
 }
@@ -344,11 +369,11 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
       if (!mbar_wait(smem_u32(&ctrl.st_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag, p.err)) break;
       mbar_arrive_expect_tx(bar, parts * 512);
       const int64_t o = static_cast<int64_t>(bh) * p.Np;
-      bulk_load(dst, p.lse2 + o + k0, 256, bar);
-      bulk_load(dst + 512, p.delta + o + k0, 256, bar);
+      bulk_load(dst, p.nlse2 + o + k0, 256, bar);
+      bulk_load(dst + 512, p.ndelta + o + k0, 256, bar);
       if (parts == 2) {
-        bulk_load(dst + 256, p.lse2 + o + k1, 256, bar);
-        bulk_load(dst + 768, p.delta + o + k1, 256, bar);
+        bulk_load(dst + 256, p.nlse2 + o + k1, 256, bar);
+        bulk_load(dst + 768, p.ndelta + o + k1, 256, bar);
       }
       ++is;
     }
@@ -376,7 +401,11 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
   }
 }
 
-template <int D, bool KEYS>
+// The two MMA issuers.  FIRST owns S's columns: S, and acc2 (which reads P there).
+// The other owns dP's: dP, and acc1 (which reads dS there).  MMAs of one thread run
+// in issue order, so a product may overwrite columns that the thread's previous
+// product reads without waiting for it.
+template <int D, bool KEYS, bool FIRST>
 __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int4 it) {
   using C = Cfg<D>;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
@@ -391,48 +420,58 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       mma_bf16_ss(tmem + col, sdesc_sw128(sx + o, 16, 1024), sdesc_sw128(sy + o, 16, 1024), C::IDESC_S, kk > 0);
     }
   };
-  // acc[128 x D] += A (bf16, TMEM) Y over the step's rows; P and dS lie 32 columns
-  // per tile, 64 apart
+  // acc[128 x D] += A (bf16, TMEM) Y over the step's rows; P and dS lie 16 columns
+  // (32 rows of Y) per softmax group, 32 apart
   auto inner = [&](uint32_t acc, uint32_t col, uint32_t sy, int32_t j) {
     tc_fence_after();
     const int kks = 2 * j + 1 < n ? 8 : 4;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
       if (kk < kks)
-        mma_bf16_ts(tmem + acc, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8,
+        mma_bf16_ts(tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8,
                     sdesc_sw128(sy + kk * 16 * 128, 128 * 128, 1024), C::IDESC_A, (j > 0 || kk > 0) ? 1u : 0u);
   };
-  const uint32_t sx1 = base + C::X1, sx2 = base + C::X2;
   auto y1 = [&](int32_t j) { return base + C::Y1 + (j % C::S1) * C::TILE; };
   auto y2 = [&](int32_t j) { return base + C::Y2 + (j % C::S2) * C::TILE; };
-  auto do_s = [&](int32_t j) -> bool {
-    if (!wait(&ctrl.y1_full[j % C::S1], (j / C::S1) & 1)) return false;
-    outer(C::S_COL, sx1, y1(j));
-    mma_commit(smem_u32(&ctrl.s_full));
-    return true;
-  };
-  auto do_dp = [&](int32_t j) -> bool {
-    if (!wait(&ctrl.y2_full[j % C::S2], (j / C::S2) & 1)) return false;
-    outer(C::DP_COL, sx2, y2(j));
-    mma_commit(smem_u32(&ctrl.dp_full));
-    if (!KEYS) mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
-    return true;
-  };
-  bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && wait(&ctrl.x2_full, 0) && do_dp(0);
-  for (int32_t j = 0; ok && j < steps; ++j) {
-    if (!wait(&ctrl.p_full, j & 1)) break;
-    if (KEYS) {
-      inner(C::A2_COL, C::S_COL, y2(j), j);
-      mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
+  auto y2_full = [&](int32_t j) { return wait(&ctrl.y2_full[j % C::S2], (j / C::S2) & 1); };
+  if constexpr (FIRST) {
+    auto do_s = [&](int32_t j) -> bool {
+      if (!wait(&ctrl.y1_full[j % C::S1], (j / C::S1) & 1)) return false;
+      outer(C::S_COL, base + C::X1, y1(j));
+      mma_commit(smem_u32(&ctrl.s_full));
+      return true;
+    };
+    bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0);
+    for (int32_t j = 0; ok && j < steps; ++j) {
+      if (KEYS && !y2_full(j)) break;
+      if (!wait(&ctrl.p_full, j & 1)) break;
+      if (KEYS) {
+        inner(C::A2_COL, C::S_COL, y2(j), j);
+        mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
+      }
+      if (j + 1 < steps && !do_s(j + 1)) break;
     }
-    if (j + 1 < steps && !do_s(j + 1)) break;
-    if (!wait(&ctrl.ds_full, j & 1)) break;
-    inner(C::A1_COL, C::DP_COL, y1(j), j);
-    mma_commit(smem_u32(&ctrl.y1_empty[j % C::S1]));
-    if (j + 1 < steps && !do_dp(j + 1)) break;
+  } else {
+    auto dp_col = [&](int32_t j) { return KEYS ? C::DP_COL : C::DPQ_COL + 128 * (j & 1); };
+    auto do_dp = [&](int32_t j) -> bool {
+      if (!y2_full(j)) return false;
+      outer(dp_col(j), base + C::X2, y2(j));
+      mma_commit(smem_u32(&ctrl.dp_full[j & 1]));
+      mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
+      return true;
+    };
+    bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0);
+    for (int32_t j = 0; ok && j < steps; ++j) {
+      if (!KEYS && j + 1 < steps && !do_dp(j + 1)) break;
+      if (!wait(&ctrl.ds_full[j & 1], (j >> 1) & 1)) break;
+      // Y1 has landed: S of this step was computed from it
+      inner(KEYS ? C::A1_COL : C::AQ_COL, dp_col(j), y1(j), j);
+      mma_commit(smem_u32(&ctrl.y1_empty[j % C::S1]));
+      if (KEYS && j + 1 < steps && !do_dp(j + 1)) break;
+    }
   }
-  // complete once everything issued has: the accumulators are whole (or, after an
-  // abort, TMEM can be released)
+  // complete once everything that both threads issued has: the accumulators are
+  // whole (or, after an abort, TMEM can be released)
   mma_commit(smem_u32(&ctrl.acc_full));
   volatile int32_t no = 0;
   mbar_wait(smem_u32(&ctrl.acc_full), 0, &no, p.err);
@@ -443,12 +482,14 @@ __device__ __forceinline__ void roles(const Params& p, Ctrl& ctrl, uint32_t base
                                       int warp, int lane) {
   const int4 it = __ldg((KEYS ? p.items_k : p.items_q) + 2 * static_cast<int64_t>(item));
   const int2* entries = KEYS ? p.entries_k : p.entries_q;
-  if (warp < 8) {
+  if (warp < kSoftmaxWarps) {
     softmax_role<D, KEYS>(p, ctrl, base, tmem, it, entries, KEYS ? p.descs_k : p.descs_q, warp, lane);
-  } else if (warp == 8) {
+  } else if (warp == kSoftmaxWarps) {
     if (lane == 0) producer_role<D, KEYS>(p, ctrl, base, it, entries);
+  } else if (warp == kSoftmaxWarps + 1) {
+    if (lane == 0) mma_role<D, KEYS, true>(p, ctrl, base, tmem, it);
   } else if (lane == 0) {
-    mma_role<D, KEYS>(p, ctrl, base, tmem, it);
+    mma_role<D, KEYS, false>(p, ctrl, base, tmem, it);
   }
   __syncwarp();
 }
@@ -465,21 +506,25 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
     return;
   }
   if (threadIdx.x == 0) {
-    for (uint64_t* b : {&ctrl.x1_full, &ctrl.x2_full, &ctrl.s_full, &ctrl.dp_full, &ctrl.acc_full})
+    for (uint64_t* b : {&ctrl.x1_full, &ctrl.x2_full, &ctrl.s_full, &ctrl.dp_full[0], &ctrl.dp_full[1]})
       mbar_init(smem_u32(b), 1);
+    mbar_init(smem_u32(&ctrl.acc_full), 2);
+    // a step's Y2 is released by dP and, for key items, by acc2
     for (int i = 0; i < 4; ++i)
-      for (uint64_t* b : {&ctrl.y1_full[i], &ctrl.y1_empty[i], &ctrl.y2_full[i], &ctrl.y2_empty[i]})
+      for (uint64_t* b : {&ctrl.y1_full[i], &ctrl.y1_empty[i], &ctrl.y2_full[i]})
         mbar_init(smem_u32(b), 1);
+    for (int i = 0; i < 4; ++i)
+      mbar_init(smem_u32(&ctrl.y2_empty[i]), static_cast<int32_t>(blockIdx.x) < p.n_key_items ? 2 : 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctrl.st_full[i]), 1);
-      mbar_init(smem_u32(&ctrl.st_empty[i]), 8);
+      mbar_init(smem_u32(&ctrl.st_empty[i]), kSoftmaxWarps);
+      mbar_init(smem_u32(&ctrl.ds_full[i]), kSoftmaxWarps);
     }
-    mbar_init(smem_u32(&ctrl.p_full), 8);
-    mbar_init(smem_u32(&ctrl.ds_full), 8);
+    mbar_init(smem_u32(&ctrl.p_full), kSoftmaxWarps);
     ctrl.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kSoftmaxWarps + 1) {
     tmem_alloc(smem_u32(&ctrl.tmem_base), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -492,18 +537,18 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   else roles<D, false>(p, ctrl, base, tmem, b - p.n_key_items, warp, lane);
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kSoftmaxWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
-// Per query row: lse in base 2 and delta = sum dO o O (fp32), one row per D / 8
+// Per query row: -lse in base 2 and -delta, delta = sum dO o O (fp32), one row per D / 8
 // lanes; rows past N of the padded arrays get P = 0.  HBM-bound: reads O and dO.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_stats_kernel(const uint4* __restrict__ o, const uint4* __restrict__ g,
-                                                        const float* __restrict__ lse, float* __restrict__ lse2,
-                                                        float* __restrict__ delta, int64_t rows_p, int32_t N,
+                                                        const float* __restrict__ lse, float* __restrict__ nlse2,
+                                                        float* __restrict__ ndelta, int64_t rows_p, int32_t N,
                                                         int32_t Np) {
   constexpr int VR = D / 8;
   const int64_t row = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / VR;
@@ -512,7 +557,7 @@ __global__ void __launch_bounds__(256) bwd_stats_kernel(const uint4* __restrict_
   const int64_t bh = row / Np;
   const int32_t i = static_cast<int32_t>(row - bh * Np);
   float s = 0.f;
-  float l = INFINITY;
+  float l = -INFINITY;
   if (i < N) {
     const int64_t src = (bh * N + i) * VR + v;
     const uint4 a = __ldg(o + src), b = __ldg(g + src);
@@ -522,15 +567,15 @@ __global__ void __launch_bounds__(256) bwd_stats_kernel(const uint4* __restrict_
       s = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), s);
       s = fmaf(__uint_as_float(x[k] & 0xFFFF0000u), __uint_as_float(y[k] & 0xFFFF0000u), s);
     }
-    l = __ldg(lse + bh * N + i) * kLog2e;
-    if (l == -INFINITY) l = INFINITY;        // no allowed key: P = 2^(s - inf) = 0
+    l = -__ldg(lse + bh * N + i) * kLog2e;
+    if (l == INFINITY) l = -INFINITY;        // no allowed key: P = 2^(s - inf) = 0
   }
   const uint32_t grp = VR == 32 ? 0xFFFFFFFFu : ((1u << VR) - 1u) << ((threadIdx.x & 31) / VR * VR);
 #pragma unroll
   for (int m = VR / 2; m; m >>= 1) s += __shfl_xor_sync(grp, s, m);
   if (v == 0) {
-    lse2[row] = l;
-    delta[row] = s;
+    nlse2[row] = l;
+    ndelta[row] = -s;
   }
 }
 
@@ -596,10 +641,10 @@ tsr_status launch_backward(const BwdArgs& a, cudaStream_t st) {
   p.entries_q = static_cast<const int2*>(Q->entries);
   p.descs_k = static_cast<const uint4*>(K->descs);
   p.descs_q = static_cast<const uint4*>(Q->descs);
-  float* lse2 = static_cast<float*>(a.workspace);
-  float* delta = lse2 + BH * Np;
-  p.lse2 = lse2;
-  p.delta = delta;
+  float* nlse2 = static_cast<float*>(a.workspace);
+  float* ndelta = nlse2 + BH * Np;
+  p.nlse2 = nlse2;
+  p.ndelta = ndelta;
   p.dq = static_cast<__nv_bfloat16*>(a.dq);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
@@ -614,9 +659,9 @@ tsr_status launch_backward(const BwdArgs& a, cudaStream_t st) {
   if (stat_blocks >= (int64_t{1} << 31)) return fail(TSR_ERR_UNSUPPORTED, "too many rows");
   const uint4 *o = static_cast<const uint4*>(a.out), *g = static_cast<const uint4*>(a.dout);
   if (D == 64)
-    bwd::bwd_stats_kernel<64><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, lse2, delta, rows, N, Np);
+    bwd::bwd_stats_kernel<64><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np);
   else
-    bwd::bwd_stats_kernel<128><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, lse2, delta, rows, N, Np);
+    bwd::bwd_stats_kernel<128><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np);
   TSR_CUDA(cudaGetLastError());
   return D == 64 ? bwd::launch<64>(p, ctas, Q->device, st) : bwd::launch<128>(p, ctas, Q->device, st);
 }
