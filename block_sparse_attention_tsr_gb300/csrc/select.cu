@@ -38,7 +38,7 @@ constexpr float kScoreErr = 1e-4f;
 
 constexpr int kPoolThreads = 128;
 constexpr int kSelThreads = 256;
-constexpr int kStrip = 32;            // query blocks per CTA of select_kernel
+constexpr int kStrip = 16;            // query blocks per CTA of select_kernel
 constexpr int kStripBytes = 112 * 1024;   // a strip's scores, two CTAs per SM
 
 struct PoolParams {
@@ -54,20 +54,39 @@ struct PoolParams {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// s + e += x, exactly up to the rounding of e (Knuth's two-sum).
-__device__ __forceinline__ void two_sum(float& s, float& e, float x) {
-  const float t = __fadd_rn(s, x);
-  const float z = __fsub_rn(t, s);
-  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+// (s, e) += x on two channels at once: s + e grows by exactly x up to the rounding
+// of e (Knuth's two-sum, seven packed adds).
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {      // a - b, rounded once
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(b), "l"(0xBF800000BF800000ull), "l"(a));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  return (static_cast<uint64_t>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float lane2(uint64_t v, int i) {
+  return __uint_as_float(static_cast<uint32_t>(i ? v >> 32 : v));
+}
+__device__ __forceinline__ void two_sum(uint64_t& s, uint64_t& e, uint64_t x) {
+  const uint64_t t = add2(s, x);
+  const uint64_t z = sub2(t, s);
+  e = add2(e, add2(sub2(s, sub2(t, z)), sub2(x, z)));
   s = t;
 }
 
 // One CTA per block of rows of one head; D / 8 threads across a row, so that a
-// warp reads 512 contiguous bytes, kPoolThreads / (D / 8) rows at a time.
+// warp reads 512 contiguous bytes, kPoolThreads / (D / 8) rows at a time, eight
+// loads in flight per thread.  Everything is fp32 pairs: fp64 sums, at two lanes a
+// clock per SM, took 320 us for a 480p layer.
 template <int D>
 __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ PoolParams p) {
   constexpr int VR = D / 8, GROUPS = kPoolThreads / VR;
-  __shared__ double part[GROUPS][D];
+  __shared__ float2 part[GROUPS][D];
   const int64_t unit = blockIdx.x;
   const int w = unit >= p.first_k ? 1 : 0;
   const int64_t u = unit - (w ? p.first_k : 0);
@@ -77,54 +96,70 @@ __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constan
   const int rows = min(p.block[w], p.N - row0);
   const int v = threadIdx.x % VR, g = threadIdx.x / VR;
   const uint4* src = p.x[w] + (bh * p.N + row0) * VR + v;
-  float s[8], e[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = e[i] = 0.f;
+  uint64_t s[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};
   constexpr int U = 8;
   for (int r = g; r < rows; r += GROUPS * U) {
     uint4 x[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int rr = r + k * GROUPS;
-      x[k] = rr < rows ? __ldcs(src + static_cast<int64_t>(rr) * VR) : make_uint4(0u, 0u, 0u, 0u);
+      x[k] = rr < rows ? __ldg(src + static_cast<int64_t>(rr) * VR) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        two_sum(s[2 * i], e[2 * i], bf16_lo(wd[i]));
-        two_sum(s[2 * i + 1], e[2 * i + 1], bf16_hi(wd[i]));
-      }
+      for (int i = 0; i < 4; ++i) two_sum(s[i], e[i], pair2(bf16_lo(wd[i]), bf16_hi(wd[i])));
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[g][v * 8 + i] = static_cast<double>(s[i]) + static_cast<double>(e[i]);
+  for (int i = 0; i < 4; ++i) {
+    part[g][v * 8 + 2 * i] = make_float2(lane2(s[i], 0), lane2(e[i], 0));
+    part[g][v * 8 + 2 * i + 1] = make_float2(lane2(s[i], 1), lane2(e[i], 1));
+  }
   __syncthreads();
-  // in fp64: the squares of small means would vanish in fp32, and the error bound with them
-  __shared__ double sq[kPoolThreads / 32];
-  double n2 = 0.0;
+  __shared__ float red[2][kPoolThreads / 32];
+  float hi = 0.f;
   if (threadIdx.x < D) {
-    double t = part[0][threadIdx.x];
+    float2 t = part[0][threadIdx.x];
 #pragma unroll
-    for (int k = 1; k < GROUPS; ++k) t += part[k][threadIdx.x];
-    t /= rows;
-    const float hi = static_cast<float>(t);
-    const float lo = static_cast<float>(t - static_cast<double>(hi));
+    for (int k = 1; k < GROUPS; ++k) {
+      const float2 o = part[k][threadIdx.x];
+      const float n = __fadd_rn(t.x, o.x), z = __fsub_rn(n, t.x);
+      t.y = __fadd_rn(__fadd_rn(t.y, o.y),
+                      __fadd_rn(__fsub_rn(t.x, __fsub_rn(n, z)), __fsub_rn(o.x, z)));
+      t.x = n;
+    }
+    // (t.x + t.y) / rows: the quotient of t.x, then that of its exact remainder
+    const float n = static_cast<float>(rows);
+    const float q = __fdiv_rn(t.x, n);
+    const float q2 = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n, t.x), t.y), n);
+    hi = __fadd_rn(q, q2);
+    const float lo = __fadd_rn(__fsub_rn(q, hi), q2);
     const int64_t o = u * D + threadIdx.x;
     p.hi[w][o] = hi;
     p.lo[w][o] = lo;
-    n2 = t * t;
   }
+  // |mean|, over the largest component so that small means do not vanish squared
+  float m = fabsf(hi);
 #pragma unroll
-  for (int m = 16; m; m >>= 1) n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, m);
-  if ((threadIdx.x & 31) == 0) sq[threadIdx.x >> 5] = n2;
+  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+  if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPoolThreads / 32; ++k) m = fmaxf(m, red[0][k]);
+  m = fmaxf(m, FLT_MIN);
+  const float h = hi / m;
+  float n2 = h * h;
+#pragma unroll
+  for (int x = 16; x; x >>= 1) n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, x);
+  if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = n2;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double t = 0.0;
+    float t = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPoolThreads / 32; ++k) t += sq[k];
-    p.norm[w][u] = static_cast<float>(sqrt(t) * 1.0001);
+    for (int k = 0; k < kPoolThreads / 32; ++k) t += red[1][k];
+    p.norm[w][u] = sqrtf(t) * m * 1.0001f;     // NaN where a mean is
   }
 }
 
@@ -157,6 +192,9 @@ __device__ __forceinline__ uint32_t key32(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float unkey32(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
 __device__ __forceinline__ uint64_t key64(double x) {
   if (x != x) return 0ull;
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
@@ -165,28 +203,25 @@ __device__ __forceinline__ uint64_t key64(double x) {
 
 // The score in fp64 from the 48-bit means, by one warp (every lane gets it).
 template <int D>
-__device__ __forceinline__ double exact_score(const float* qh, const float* ql, const float* kh, const float* kl,
-                                              int lane) {
+__device__ __forceinline__ double exact_score(const double (&q)[D / 32], const float* kh, const float* kl, int lane) {
   double t = 0.0;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const int c = i * 32 + lane;
-    const double a = static_cast<double>(__ldg(qh + c)) + static_cast<double>(__ldg(ql + c));
-    const double b = static_cast<double>(__ldg(kh + c)) + static_cast<double>(__ldg(kl + c));
-    t = fma(a, b, t);
+    t = fma(q[i], static_cast<double>(__ldg(kh + c)) + static_cast<double>(__ldg(kl + c)), t);
   }
 #pragma unroll
   for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, m);
   return t;
 }
 
-// The largest key T such that at least `want` of n keys are >= T, over the
-// entries that `in` admits (there are at least `want` of them).  key(j) and in(j)
-// are evaluated by lane j % 32.
+// The largest key T such that at least `want` of the n keys that `in` admits are
+// >= T (there are at least `want` of them).  in(j) and key(j) are evaluated by lane
+// j % 32.
 template <typename In, typename Key>
-__device__ __forceinline__ uint32_t kth_key(int n, int want, int lane, In in, Key key, uint32_t lo, uint32_t hi) {
-  // invariant: count(>= lo) >= want, count(>= hi + 1) < want
-  while (lo < hi) {
+__device__ __forceinline__ uint32_t kth_key(int n, int want, int lane, In in, Key key) {
+  uint32_t lo = 0u, hi = 0xFFFFFFFFu;
+  while (lo < hi) {      // count(>= lo) >= want, count(>= hi + 1) < want
     const uint32_t mid = lo + ((hi - lo) >> 1) + 1u;
     int c = 0;
     for (int j = lane; j < n; j += 32) c += (in(j) && key(j) >= mid) ? 1 : 0;
@@ -197,9 +232,196 @@ __device__ __forceinline__ uint32_t kth_key(int n, int want, int lane, In in, Ke
   return lo;
 }
 
+// Selection of one row by one warp, its scores row[0 .. nk) (used as scratch).
+// KPL > 0: nk <= 32 KPL, the scores in registers, score m * 32 + lane in v[m];
+// KPL = 0: any nk, read again where needed.
+template <int D, int KPL>
+__device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i, float* row, float k_max, int lane) {
+  uint8_t* out = p.blocks + (bh * p.nq + i) * p.nk;
+  // forced blocks: [0, first) and, with `diagonal`, [d_lo, d_hi), the key blocks
+  // that share a token with the query block
+  const int first = min(p.first, p.nk);
+  int d_lo = 0, d_hi = 0;
+  if (p.diagonal) {
+    const int64_t a = static_cast<int64_t>(i) * p.bq;
+    const int64_t b = min(a + p.bq, static_cast<int64_t>(p.N)) - 1;
+    d_lo = max(static_cast<int>(a / p.bk), first);
+    d_hi = max(static_cast<int>(b / p.bk) + 1, d_lo);
+  }
+  auto forced = [&](int j) -> bool { return j < first || (j >= d_lo && j < d_hi); };
+  const int n_forced = first + (d_hi - d_lo), others = p.nk - n_forced;
+  const int want = min(p.keep - n_forced, others);
+  if (want <= 0 || want == others) {
+    const bool all = want == others && want > 0;
+    for (int j = lane; j < p.nk; j += 32) out[j] = (all || forced(j)) ? 1 : 0;
+    return;
+  }
+  // the last two terms cover values that the bf16 terms or their products flush
+  const float q_norm = __ldg(p.q_norm + bh * p.nq + i);
+  const float err2 = 2.f * (kScoreErr * (q_norm * k_max) + 4e-37f * (q_norm + k_max) + 1e-36f);
+  bool finite = q_norm * k_max <= FLT_MAX && err2 <= FLT_MAX;
+  // with finite norms every score is finite; forced blocks and those past nk hold
+  // -inf and are never counted
+  constexpr int REGS = KPL > 0 ? KPL : 1;
+  float v[REGS];
+  const int chunks = KPL > 0 ? KPL : (p.nk + 31) / 32;
+  auto load = [&](int m) -> float {
+    const int j = m * 32 + lane;
+    return (j < p.nk && !forced(j)) ? row[j] : -INFINITY;
+  };
+  if (KPL > 0) {
+#pragma unroll
+    for (int m = 0; m < REGS; ++m) v[m] = load(m);
+  }
+  auto val = [&](int m) -> float { return KPL > 0 ? v[KPL > 0 ? m : 0] : load(m); };
+  float above = INFINITY, below = -INFINITY;    // kept for sure above, dropped for sure below
+  if (finite) {
+    uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+#pragma unroll
+    for (int m = 0; m < chunks; ++m) {
+      const uint32_t k = key32(val(m));
+      kmax = max(kmax, k);
+      if (k != key32(-INFINITY)) kmin = min(kmin, k);
+    }
+    kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
+    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
+    // the want-th largest lies in [lo, hi]: count(>= lo) >= want, count(> hi) < want.
+    // Bisected until the bracket is inside the fast bound, or exactly `want` are
+    // above (then it is the smallest of those).
+    float lo = unkey32(kmin), hi = unkey32(kmax);
+    while (hi - lo > 0.25f * err2) {
+      const float mid = lo + 0.5f * (hi - lo);
+      if (!(mid > lo && mid < hi)) break;
+      int c = 0;
+#pragma unroll
+      for (int m = 0; m < chunks; ++m) c += val(m) > mid ? 1 : 0;
+      c = __reduce_add_sync(0xFFFFFFFFu, c);
+      if (c == want) {
+        uint32_t k = 0xFFFFFFFFu;
+#pragma unroll
+        for (int m = 0; m < chunks; ++m) k = val(m) > mid ? min(k, key32(val(m))) : k;
+        lo = hi = unkey32(__reduce_min_sync(0xFFFFFFFFu, k));
+        break;
+      }
+      if (c > want) lo = mid;
+      else hi = mid;
+    }
+    above = hi + err2;
+    below = lo - err2;
+    finite = above <= FLT_MAX && below >= -FLT_MAX;
+  }
+  if (!finite) above = INFINITY;
+  // without finite scores and bounds every block that is not forced is scored exactly
+  auto sure = [&](float x) -> bool { return finite && x > above; };
+  auto near = [&](int m, float x) -> bool {
+    return finite ? x >= below && x <= above : m * 32 + lane < p.nk && !forced(m * 32 + lane);
+  };
+  int n_sure = 0, n_near = 0;
+#pragma unroll
+  for (int m = 0; m < chunks; ++m) {
+    n_sure += sure(val(m)) ? 1 : 0;
+    n_near += near(m, val(m)) ? 1 : 0;
+  }
+  n_sure = __reduce_add_sync(0xFFFFFFFFu, n_sure);
+  n_near = __reduce_add_sync(0xFFFFFFFFu, n_near);
+  const int left = want - n_sure;               // of the near ones, 1 <= left <= n_near
+  if (left == n_near) {
+#pragma unroll
+    for (int m = 0; m < chunks; ++m) {
+      const int j = m * 32 + lane;
+      if (j < p.nk) out[j] = (forced(j) || sure(val(m)) || near(m, val(m))) ? 1 : 0;
+    }
+    return;
+  }
+  double q[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    const int64_t o = (bh * p.nq + i) * D + c * 32 + lane;
+    q[c] = static_cast<double>(__ldg(p.q_hi + o)) + static_cast<double>(__ldg(p.q_lo + o));
+  }
+  const float* kh = p.k_hi + bh * p.nk * D;
+  const float* kl = p.k_lo + bh * p.nk * D;
+  auto exact_key = [&](int j) -> uint64_t {
+    return key64(exact_score<D>(q, kh + static_cast<int64_t>(j) * D, kl + static_cast<int64_t>(j) * D, lane));
+  };
+  if (n_near <= 32) {
+    // lane c holds near block c (ascending j): its exact key, then its rank
+    int my_j = -1, c = 0;
+#pragma unroll
+    for (int m = 0; m < chunks; ++m) {
+      const int j = m * 32 + lane;
+      const float x = val(m);
+      const bool nr = near(m, x);
+      if (j < p.nk && !nr) out[j] = (forced(j) || sure(x)) ? 1 : 0;
+      uint32_t b = __ballot_sync(0xFFFFFFFFu, nr);
+      while (b) {
+        if (lane == c++) my_j = m * 32 + __ffs(b) - 1;
+        b &= b - 1;
+      }
+    }
+    uint64_t mine = 0;
+#pragma unroll 2
+    for (int o = 0; o < n_near; ++o) {
+      const uint64_t key = exact_key(__shfl_sync(0xFFFFFFFFu, my_j, o));
+      if (lane == o) mine = key;
+    }
+    int rank = 0;
+    for (int o = 0; o < n_near; ++o) {
+      const uint64_t other = __shfl_sync(0xFFFFFFFFu, mine, o);
+      rank += (other > mine || (other == mine && o < lane)) ? 1 : 0;
+    }
+    if (my_j >= 0) out[my_j] = rank < left ? 1 : 0;
+    return;
+  }
+  // Many near blocks (a query block of zeros, equal key blocks, infinities):
+  // order them by the upper, then the lower 32 bits of the exact key, which
+  // take the place of their scores.  out[j] holds the state meanwhile.
+  enum : uint8_t { kOut = 0, kIn = 1, kNear = 2 };
+#pragma unroll
+  for (int m = 0; m < chunks; ++m) {
+    const int j = m * 32 + lane;
+    if (j < p.nk) out[j] = near(m, val(m)) ? kNear : (forced(j) || sure(val(m))) ? kIn : kOut;
+  }
+  __syncwarp();
+  auto is_near = [&](int j) { return out[j] == kNear; };
+  auto word = [&](int j) { return __float_as_uint(row[j]); };
+  int open = left;                              // places left among the kNear
+  for (int half = 0; half < 2; ++half) {
+    for (int j0 = 0; j0 < p.nk; j0 += 32) {
+      const int j = j0 + lane;
+      uint32_t b = __ballot_sync(0xFFFFFFFFu, j < p.nk && is_near(j));
+      while (b) {
+        const int jj = j0 + __ffs(b) - 1;
+        b &= b - 1;
+        const uint64_t key = exact_key(jj);
+        if (lane == 0) row[jj] = __uint_as_float(static_cast<uint32_t>(half ? key : key >> 32));
+      }
+    }
+    __syncwarp();
+    const uint32_t t = kth_key(p.nk, open, lane, is_near, word);
+    int in = 0;
+    for (int j = lane; j < p.nk; j += 32) {
+      if (!is_near(j)) continue;
+      const uint32_t w = word(j);
+      if (w != t) out[j] = w > t ? kIn : kOut;
+      in += w > t ? 1 : 0;
+    }
+    open -= __reduce_add_sync(0xFFFFFFFFu, in);
+    __syncwarp();
+  }
+  // equal exact scores: the lowest j
+  for (int j0 = 0; j0 < p.nk; j0 += 32) {
+    const int j = j0 + lane;
+    const bool tie = j < p.nk && is_near(j);
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, tie);
+    if (tie) out[j] = __popc(b & ((1u << lane) - 1u)) < open ? kIn : kOut;
+    open -= min(open, __popc(b));
+  }
+}
+
 // One CTA: a strip of kStrip query blocks of one head.
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelParams p) {
+template <int D, int KPL>
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelParams p) {
   extern __shared__ float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t bh = blockIdx.x / p.strips;
@@ -218,11 +440,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   for (int m = 16; m; m >>= 1) km = fmaxf(km, __shfl_xor_sync(0xFFFFFFFFu, km, m));
   if (lane == 0) k_max_w[warp] = km;
 
-  // ---- scores: warp w takes the 16 query blocks (w & 1) and every fourth group
-  // of 8 key blocks; a fragments (both bf16 terms) stay in registers
+  // ---- scores: every warp takes the strip's 16 query blocks (both bf16 terms of
+  // the A fragments stay in registers) and every eighth group of 8 key blocks
   {
     const int g = lane >> 2, t = lane & 3;
-    const int r0 = i0 + (warp & 1) * 16 + g, r1 = r0 + 8;
+    const int r0 = i0 + g, r1 = r0 + 8;
     uint32_t ah[D / 16][4], al[D / 16][4];
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -234,24 +456,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         split2(x, ah[kk][f], al[kk][f]);
       }
     }
-    for (int j0 = (warp >> 1) * 8; j0 < p.nk; j0 += 32) {
+    for (int j0 = warp * 8; j0 < p.nk; j0 += 8 * (kSelThreads / 32)) {
       const int j = j0 + g;
-      const float* kr = p.k_hi + (bh * p.nk + (j < p.nk ? j : p.nk - 1)) * D;
+      const float* kr = p.k_hi + (bh * p.nk + (j < p.nk ? j : p.nk - 1)) * D + t * 2;
+      float2 x[D / 8];
+#pragma unroll
+      for (int kk = 0; kk < D / 8; ++kk) x[kk] = __ldg(reinterpret_cast<const float2*>(kr + kk * 8));
       float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t bh0, bl0, bh1, bl1;
-        split2(__ldg(reinterpret_cast<const float2*>(kr + kk * 16 + t * 2)), bh0, bl0);
-        split2(__ldg(reinterpret_cast<const float2*>(kr + kk * 16 + t * 2 + 8)), bh1, bl1);
+        split2(x[2 * kk], bh0, bl0);
+        split2(x[2 * kk + 1], bh1, bl1);
         mma_16816(c0, ah[kk], bh0, bh1);
         mma_16816(c1, ah[kk], bl0, bl1);
         mma_16816(c1, al[kk], bh0, bh1);
       }
-      const int col = j0 + t * 2, row = (warp & 1) * 16 + g;
+      const int col = j0 + t * 2;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int cc = col + (x & 1), rr = row + ((x & 2) ? 8 : 0);
-        if (cc < p.nk) sc[rr * p.pitch + cc] = c0[x] + c1[x];
+      for (int e = 0; e < 4; ++e) {
+        const int cc = col + (e & 1), rr = g + ((e & 2) ? 8 : 0);
+        if (cc < p.nk) sc[rr * p.pitch + cc] = c0[e] + c1[e];
       }
     }
   }
@@ -259,147 +484,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   float k_max = k_max_w[0];
 #pragma unroll
   for (int w = 1; w < kSelThreads / 32; ++w) k_max = fmaxf(k_max, k_max_w[w]);
-
-  // ---- selection: one warp per row
-  for (int rr = warp; rr < kStrip; rr += kSelThreads / 32) {
-    const int i = i0 + rr;
-    if (i >= p.nq) break;
-    float* row = sc + rr * p.pitch;
-    uint8_t* out = p.blocks + (bh * p.nq + i) * p.nk;
-    // forced blocks: [0, first) and, with `diagonal`, [d_lo, d_hi), the key blocks
-    // that share a token with the query block
-    const int first = min(p.first, p.nk);
-    int d_lo = 0, d_hi = 0;
-    if (p.diagonal) {
-      const int64_t a = static_cast<int64_t>(i) * p.bq;
-      const int64_t b = min(a + p.bq, static_cast<int64_t>(p.N)) - 1;
-      d_lo = max(static_cast<int>(a / p.bk), first);
-      d_hi = max(static_cast<int>(b / p.bk) + 1, d_lo);
-    }
-    auto forced = [&](int j) -> bool { return j < first || (j >= d_lo && j < d_hi); };
-    const int n_forced = first + (d_hi - d_lo), others = p.nk - n_forced;
-    const int want = min(p.keep - n_forced, others);
-    if (want <= 0 || want == others) {
-      const bool all = want == others && want > 0;
-      for (int j = lane; j < p.nk; j += 32) out[j] = (all || forced(j)) ? 1 : 0;
-      continue;
-    }
-    // the last two terms cover values that the bf16 terms or their products flush
-    const float q_norm = __ldg(p.q_norm + bh * p.nq + i);
-    const float err2 = 2.f * (kScoreErr * (q_norm * k_max) + 4e-37f * (q_norm + k_max) + 1e-36f);
-    float above = INFINITY, below = -INFINITY;   // kept for sure above, dropped for sure below
-    bool finite = q_norm * k_max <= FLT_MAX && err2 <= FLT_MAX;
-    if (finite) {
-      uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
-      for (int j = lane; j < p.nk; j += 32) {
-        if (forced(j)) continue;
-        const uint32_t k = key32(row[j]);
-        kmin = min(kmin, k);
-        kmax = max(kmax, k);
-      }
-      kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
-      kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
-      const uint32_t t = kth_key(
-          p.nk, want, lane, [&](int j) { return !forced(j); }, [&](int j) { return key32(row[j]); }, kmin, kmax);
-      const float th = __uint_as_float((t & 0x80000000u) ? (t & 0x7FFFFFFFu) : ~t);
-      above = th + err2;
-      below = th - err2;
-      finite = above <= FLT_MAX && below >= -FLT_MAX;
-    }
-    if (!finite) above = INFINITY;
-    // without finite scores and bounds every block that is not forced is scored exactly
-    auto sure = [&](int j) -> bool { return finite && row[j] > above; };
-    auto near = [&](int j) -> bool { return !forced(j) && (!finite || (row[j] >= below && row[j] <= above)); };
-    int n_sure = 0, n_near = 0;
-    for (int j = lane; j < p.nk; j += 32) {
-      if (forced(j)) continue;
-      n_sure += sure(j) ? 1 : 0;
-      n_near += near(j) ? 1 : 0;
-    }
-    n_sure = __reduce_add_sync(0xFFFFFFFFu, n_sure);
-    n_near = __reduce_add_sync(0xFFFFFFFFu, n_near);
-    const int left = want - n_sure;               // of the near ones, 1 <= left <= n_near
-    const float* qh = p.q_hi + (bh * p.nq + i) * D;
-    const float* ql = p.q_lo + (bh * p.nq + i) * D;
-    const float* kh = p.k_hi + bh * p.nk * D;
-    const float* kl = p.k_lo + bh * p.nk * D;
-    if (left == n_near) {
-      for (int j = lane; j < p.nk; j += 32) out[j] = (forced(j) || sure(j) || near(j)) ? 1 : 0;
-      continue;
-    }
-    if (n_near <= 32) {
-      // lane c holds near block c (ascending j): its exact key, then its rank
-      uint64_t mine = 0;
-      int my_j = -1, c = 0;
-      for (int j0 = 0; j0 < p.nk; j0 += 32) {
-        const int j = j0 + lane;
-        const bool in = j < p.nk;
-        const bool nr = in && near(j);
-        if (in && !nr) out[j] = (forced(j) || sure(j)) ? 1 : 0;
-        uint32_t m = __ballot_sync(0xFFFFFFFFu, nr);
-        while (m) {
-          const int jj = j0 + __ffs(m) - 1;
-          m &= m - 1;
-          const uint64_t key = key64(exact_score<D>(qh, ql, kh + static_cast<int64_t>(jj) * D,
-                                                    kl + static_cast<int64_t>(jj) * D, lane));
-          if (lane == c) {
-            mine = key;
-            my_j = jj;
-          }
-          ++c;
-        }
-      }
-      int rank = 0;
-      for (int o = 0; o < n_near; ++o) {
-        const uint64_t other = __shfl_sync(0xFFFFFFFFu, mine, o);
-        rank += (other > mine || (other == mine && o < lane)) ? 1 : 0;
-      }
-      if (my_j >= 0) out[my_j] = rank < left ? 1 : 0;
-      continue;
-    }
-    // Many near blocks (a query block of zeros, equal key blocks, infinities):
-    // order them by the upper, then the lower 32 bits of the exact key, which
-    // take the place of their scores.  out[j] holds the state meanwhile.
-    enum : uint8_t { kOut = 0, kIn = 1, kNear = 2 };
-    for (int j = lane; j < p.nk; j += 32)
-      out[j] = near(j) ? kNear : (forced(j) || sure(j)) ? kIn : kOut;
-    __syncwarp();
-    auto is_near = [&](int j) { return out[j] == kNear; };
-    auto word = [&](int j) { return __float_as_uint(row[j]); };
-    int open = left;                              // places left among the kNear
-    for (int half = 0; half < 2; ++half) {
-      for (int j0 = 0; j0 < p.nk; j0 += 32) {
-        const int j = j0 + lane;
-        uint32_t m = __ballot_sync(0xFFFFFFFFu, j < p.nk && is_near(j));
-        while (m) {
-          const int jj = j0 + __ffs(m) - 1;
-          m &= m - 1;
-          const uint64_t key = key64(exact_score<D>(qh, ql, kh + static_cast<int64_t>(jj) * D,
-                                                    kl + static_cast<int64_t>(jj) * D, lane));
-          if (lane == 0) row[jj] = __uint_as_float(static_cast<uint32_t>(half ? key : key >> 32));
-        }
-      }
-      __syncwarp();
-      const uint32_t t = kth_key(p.nk, open, lane, is_near, word, 0u, 0xFFFFFFFFu);
-      int in = 0;
-      for (int j = lane; j < p.nk; j += 32) {
-        if (!is_near(j)) continue;
-        const uint32_t w = word(j);
-        if (w != t) out[j] = w > t ? kIn : kOut;
-        in += w > t ? 1 : 0;
-      }
-      open -= __reduce_add_sync(0xFFFFFFFFu, in);
-      __syncwarp();
-    }
-    // equal exact scores: the lowest j
-    for (int j0 = 0; j0 < p.nk; j0 += 32) {
-      const int j = j0 + lane;
-      const bool tie = j < p.nk && is_near(j);
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, tie);
-      if (tie) out[j] = __popc(m & ((1u << lane) - 1u)) < open ? kIn : kOut;
-      open -= min(open, __popc(m));
-    }
-  }
+  for (int rr = warp; rr < kStrip && i0 + rr < p.nq; rr += kSelThreads / 32)
+    select_row<D, KPL>(p, bh, i0 + rr, sc + rr * p.pitch, k_max, lane);
 }
 
 struct Layout {
@@ -431,6 +517,21 @@ Layout layout_of(const tsr_select_desc& s) {
   l.scores = take(l.in_smem ? 0 : BH * l.strips * kStrip * l.pitch);
   l.total = at;
   return l;
+}
+
+template <int D, int KPL>
+tsr_status launch_strips(const SelParams& sp, unsigned ctas, size_t smem, cudaStream_t st) {
+  auto kern = select_kernel<D, KPL>;
+  int dev = 0;
+  TSR_CUDA(cudaGetDevice(&dev));
+  static bool attr_set[64] = {false};
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripBytes));
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  kern<<<ctas, kSelThreads, smem, st>>>(sp);
+  TSR_CUDA(cudaGetLastError());
+  return TSR_OK;
 }
 
 template <int D>
@@ -474,19 +575,15 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   sp.first = s.first;
   sp.diagonal = s.diagonal;
   const size_t smem = l.in_smem ? static_cast<size_t>(kStrip) * l.pitch * 4 : 0;
-  auto kern = select_kernel<D>;
-  int dev = 0;
-  TSR_CUDA(cudaGetDevice(&dev));
-  static bool attr_set[64] = {false};
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripBytes));
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
-  }
   pool_kernel<D><<<static_cast<unsigned>(units), kPoolThreads, 0, st>>>(pp);
   TSR_CUDA(cudaGetLastError());
-  kern<<<static_cast<unsigned>(BH * l.strips), kSelThreads, smem, st>>>(sp);
-  TSR_CUDA(cudaGetLastError());
-  return TSR_OK;
+  // scores per lane held in registers: as many as a row has, up to 32
+  const unsigned ctas = static_cast<unsigned>(BH * l.strips);
+  if (l.nk <= 64) return launch_strips<D, 2>(sp, ctas, smem, st);
+  if (l.nk <= 256) return launch_strips<D, 8>(sp, ctas, smem, st);
+  if (l.nk <= 640) return launch_strips<D, 20>(sp, ctas, smem, st);
+  if (l.nk <= 1024) return launch_strips<D, 32>(sp, ctas, smem, st);
+  return launch_strips<D, 0>(sp, ctas, smem, st);
 }
 
 }  // namespace
