@@ -12,6 +12,7 @@ The names follow the C ABI:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -202,19 +203,19 @@ def _dptr(t: Optional[torch.Tensor]) -> int:
 
 def _on_device(*tensors) -> None:
     """CUDA tensors of the current device: the library launches there."""
+    current = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensor arguments must be CUDA tensors")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"tensor on {t.device}: arguments must be CUDA tensors of the current device, "
+                             f"cuda:{current}")
 
 
 def _allocating_on(stream):
     """Context in which new tensors belong to the stream that the call runs on, so
     that a workspace freed on return is not reused before the call's kernels end."""
-    if stream is not None and not hasattr(stream, "cuda_stream"):
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
 
@@ -396,11 +397,12 @@ def tsr_bsa_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: tor
     if lse.dtype != torch.float32 or tuple(lse.shape) != shape[:3]:
         raise ValueError(f"lse must be fp32 of shape {shape[:3]}")
     _on_device(q, k, v, out, lse, dout, dq, dk, dv, workspace)
-    with _allocating_on(stream):
-        dq, dk, dv = (torch.empty(shape, dtype=torch.bfloat16, device=q.device) if t is None else t
-                      for t in (dq, dk, dv))
-        if workspace is None:
-            workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+    if dq is None or dk is None or dv is None or workspace is None:
+        with _allocating_on(stream):
+            dq, dk, dv = (torch.empty(shape, dtype=torch.bfloat16, device=q.device) if t is None else t
+                          for t in (dq, dk, dv))
+            if workspace is None:
+                workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
     _check(lib().tsr_bsa_backward(_dptr(q), _dptr(k), _dptr(v), _dptr(out), _dptr(lse), _dptr(dout),
                                   plan.handle, _dptr(dq), _dptr(dk), _dptr(dv), _dptr(workspace),
                                   workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
@@ -482,50 +484,43 @@ def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = Non
     if (grid is None) == (positions is None):
         raise ValueError("give grid or positions")
     B, _, N, d = xs[0].shape
+    dtype = xs[0].dtype
     dims = [int(a) for a in axis_dims]
     if not 1 <= len(dims) <= 4:
         raise ValueError("one to four axes")
-    _on_device(*xs)
-    for t in xs:
-        if t.dim() != 4 or (t.shape[0], t.shape[2], t.shape[3]) != (B, N, d):
-            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N and d")
-        if t.dtype != xs[0].dtype or t.dtype not in _ROPE_DTYPES:
-            raise ValueError("the tensors of one call have one dtype: bf16, fp16 or fp32")
-    with _allocating_on(stream):
-        if out is None:
-            outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
-        else:
-            outs = [out] if isinstance(out, torch.Tensor) else list(out)
-    _on_device(*outs)
+    if dtype not in _ROPE_DTYPES:
+        raise ValueError("the tensors are bf16, fp16 or fp32")
+    if out is None:
+        with _allocating_on(stream):
+            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
+    else:
+        outs = [out] if isinstance(out, torch.Tensor) else list(out)
     if len(outs) != len(xs):
         raise ValueError("as many outputs as tensors")
-    desc = _RopeDesc()
-    desc.B, desc.N, desc.d, desc.dtype = B, N, d, _ROPE_DTYPES[xs[0].dtype]
-    desc.n_axes = len(dims)
-    desc.axis_dim[:len(dims)] = dims
-    desc.halves, desc.inverse, desc.theta = int(bool(halves)), int(bool(inverse)), float(theta)
+    _on_device(*xs, *outs, positions)
+    arr = (_RopeTensor * len(xs))()
+    for i, (t, o) in enumerate(zip(xs, outs)):
+        if t.dim() != 4 or t.dtype != dtype or t.shape[0] != B or t.shape[2] != N or t.shape[3] != d:
+            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
+        if o.shape != t.shape or o.dtype != dtype:
+            raise ValueError("out must have x's shape and dtype")
+        xs4, os4 = t.stride(), o.stride()
+        if xs4[3] != 1 or os4[3] != 1:
+            raise ValueError("the last dimension must be contiguous")
+        arr[i] = _RopeTensor(t.data_ptr(), o.data_ptr(), t.shape[1], xs4[:3], os4[:3])
+    pad = (0,) * (4 - len(dims))
     if positions is not None:
-        _on_device(positions)
         if positions.dtype != torch.int32 or tuple(positions.shape) not in ((N, len(dims)), (B, N, len(dims))):
             raise ValueError("positions must be int32 [N, axes] or [B, N, axes]")
-        desc.positions = _dptr(positions)
-        desc.positions_per_batch = 1 if positions.dim() == 3 else 0
+        where = (_dptr(positions), int(positions.dim() == 3), (0, 0, 0, 0))
     else:
         cells = [int(g) for g in grid]
         if len(cells) != len(dims):
             raise ValueError("grid needs one size per axis")
-        desc.grid[:len(dims)] = cells
-    arr = (_RopeTensor * len(xs))()
-    for a, t, o in zip(arr, xs, outs):
-        if o.shape != t.shape or o.dtype != t.dtype:
-            raise ValueError("out must have x's shape and dtype")
-        if d > 1 and (t.stride(3) != 1 or o.stride(3) != 1):
-            raise ValueError("the last dimension must be contiguous")
-        a.x, a.out, a.H = t.data_ptr(), o.data_ptr(), t.shape[1]
-        a.x_stride[:] = [t.stride(0), t.stride(1), t.stride(2)]
-        a.out_stride[:] = [o.stride(0), o.stride(1), o.stride(2)]
-    L = lib()
-    _check(L.tsr_rope(ctypes.byref(desc), ctypes.cast(arr, ctypes.c_void_p), len(xs), _stream_ptr(stream)))
+        where = (None, 0, (*cells, *pad))
+    desc = _RopeDesc(B, N, d, _ROPE_DTYPES[dtype], len(dims), (*dims, *pad), int(bool(halves)),
+                     int(bool(inverse)), float(theta), *where)
+    _check(lib().tsr_rope(ctypes.byref(desc), arr, len(xs), _stream_ptr(stream)))
     return outs[0] if isinstance(x, torch.Tensor) else outs
 
 
@@ -545,19 +540,18 @@ def tsr_block_select(q: torch.Tensor, k: torch.Tensor, keep: int, *, bq: int = 6
     if q.dim() != 4 or k.shape != q.shape or q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16:
         raise ValueError("q, k must be bf16 [B, H, N, d] alike")
     _on_device(q, k, out, workspace)
-    desc = _SelectDesc()
-    desc.B, desc.H, desc.N, desc.d = q.shape
-    desc.bq, desc.bk, desc.keep = int(bq), int(bk), int(keep)
-    desc.first, desc.diagonal = int(first), int(bool(diagonal))
+    B, H, N, d = q.shape
+    desc = _SelectDesc(B, H, N, d, int(bq), int(bk), int(keep), int(first), int(bool(diagonal)))
     L = lib()
     need = ctypes.c_size_t(0)
     _check(L.tsr_block_select_workspace(ctypes.byref(desc), ctypes.byref(need)))
-    shape = (desc.B, desc.H, -(-desc.N // desc.bq), -(-desc.N // desc.bk))
-    with _allocating_on(stream):
-        if out is None:
-            out = torch.empty(shape, dtype=torch.uint8, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    shape = (B, H, -(-N // desc.bq), -(-N // desc.bk))
+    if out is None or workspace is None:
+        with _allocating_on(stream):
+            if out is None:
+                out = torch.empty(shape, dtype=torch.uint8, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
     if tuple(out.shape) != shape or out.dtype != torch.uint8:
         raise ValueError(f"out must be uint8 of shape {shape}")
     _check(L.tsr_block_select(ctypes.byref(desc), _dptr(q), _dptr(k), _dptr(out), _dptr(workspace),

@@ -15,7 +15,7 @@
 // Bound: HBM, one read and one write of every element.  A thread owns one unit of
 // pairs of one token (16 bytes, or two 16-byte pieces for half-split pairs),
 // computes its few cosines and sines once, and applies them to every head of
-// every tensor of the call, four rows' loads in flight; the angles so cost
+// every tensor of the call, 128 bytes of loads in flight; the angles so cost
 // 1 / (heads * tensors) of a sincos per pair.  Strides are free, so the
 // projections' [B, N, H, d] is read in place and the attention's [B, H, N, d]
 // written without a transposing copy.
@@ -35,7 +35,7 @@ namespace {
 constexpr int kMaxPairs = 128;     // d <= 256
 constexpr int kMaxTensors = 4;
 constexpr int kThreads = 256;
-constexpr int kRows = 4;           // rows (heads) whose loads are in flight together
+constexpr int kRows = 4;           // heads a CTA takes at least, where there are enough
 
 struct RopeParams {
   const void* x[kMaxTensors];
@@ -51,50 +51,117 @@ struct RopeParams {
   uint16_t c0[kMaxPairs], c1[kMaxPairs];   // a unit's first channels (halves: both pieces)
 };
 
+// Two values of type T as floats, and back (16-bit types: one 32-bit word).
 template <typename T>
-__device__ __forceinline__ float to_f(T v);
+struct Two;
 template <>
-__device__ __forceinline__ float to_f<float>(float v) { return v; }
+struct Two<float> {
+  using Word = float2;
+  static __device__ __forceinline__ float2 load(Word w) { return w; }
+  static __device__ __forceinline__ Word store(float2 v) { return v; }
+};
 template <>
-__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+struct Two<__half> {
+  using Word = uint32_t;
+  static __device__ __forceinline__ float2 load(Word w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ Word store(float2 v) {
+    const __half2 h = __float22half2_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
 template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-template <typename T, int NE>
-struct alignas(sizeof(T) * NE) Piece {
-  T v[NE];
+struct Two<__nv_bfloat16> {
+  using Word = uint32_t;
+  static __device__ __forceinline__ float2 load(Word w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ Word store(float2 v) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 };
 
-// ADJ: a unit is P pairs of neighbouring channels (one piece of 2 P elements; for
-// P = 1 two single elements).  Otherwise two pieces of P elements.
+template <typename T>
+__device__ __forceinline__ float to_f(T v) { return static_cast<float>(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v) { return static_cast<T>(v); }   // to nearest even
+
+// A row's unit in registers.  ADJ: P pairs of neighbouring channels, one piece.
+// Otherwise two pieces of P channels.  P = 1: two single elements either way.
+template <typename T, int P, bool ADJ>
+struct Unit {
+  static constexpr int WORDS = P == 1 ? 1 : ADJ ? P : P / 2;     // per piece
+  using Word = typename Two<T>::Word;
+  struct alignas(sizeof(Word) * WORDS) Piece {
+    Word w[WORDS];
+  };
+  Piece a, b;
+  T e0, e1;
+  __device__ __forceinline__ void load(const T* p0, const T* p1) {
+    if constexpr (P == 1) {
+      e0 = *p0;
+      e1 = *p1;
+    } else {
+      a = *reinterpret_cast<const Piece*>(p0);
+      if constexpr (!ADJ) b = *reinterpret_cast<const Piece*>(p1);
+    }
+  }
+  __device__ __forceinline__ void store(T* p0, T* p1) const {
+    if constexpr (P == 1) {
+      *p0 = e0;
+      *p1 = e1;
+    } else {
+      *reinterpret_cast<Piece*>(p0) = a;
+      if constexpr (!ADJ) *reinterpret_cast<Piece*>(p1) = b;
+    }
+  }
+  // channels past the rotated ones (pairs from `n` on) stay bit for bit
+  __device__ __forceinline__ void turn(const float (&cs)[P], const float (&sn)[P], int n) {
+    if constexpr (P == 1) {
+      if (n > 0) {
+        const float u = to_f(e0), v = to_f(e1);
+        e0 = from_f<T>(u * cs[0] - v * sn[0]);
+        e1 = from_f<T>(u * sn[0] + v * cs[0]);
+      }
+    } else if constexpr (ADJ) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 x = Two<T>::load(a.w[i]);
+        const Word y = Two<T>::store(make_float2(x.x * cs[i] - x.y * sn[i], x.x * sn[i] + x.y * cs[i]));
+        if (i < n) a.w[i] = y;
+      }
+    } else {
+      // n is 0 or P: a unit of half-split pairs lies in one axis or past them all
+      if (n == 0) return;
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) {
+        const float2 u = Two<T>::load(a.w[i]), v = Two<T>::load(b.w[i]);
+        const float c0 = cs[2 * i], c1 = cs[2 * i + 1], s0 = sn[2 * i], s1 = sn[2 * i + 1];
+        a.w[i] = Two<T>::store(make_float2(u.x * c0 - v.x * s0, u.y * c1 - v.y * s1));
+        b.w[i] = Two<T>::store(make_float2(u.x * s0 + v.x * c0, u.y * s1 + v.y * c1));
+      }
+    }
+  }
+};
+
 template <typename T, int P, bool ADJ>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr bool ONE = ADJ && P > 1;
-  constexpr int NE = ONE ? 2 * P : P;
-  constexpr int PIECES = ONE ? 1 : 2;
-  using Pc = Piece<T, NE>;
+  // heads whose loads are in flight together: 128 bytes a thread
+  constexpr int R = P == 1 ? 8 : (ADJ ? 8 : 4);
   const int tok = threadIdx.x / p.units, unit = threadIdx.x - tok * p.units;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * p.tokens + tok;
   if (tok >= p.tokens || n >= p.N) return;
   const int64_t b = blockIdx.z;
   float cs[P], sn[P];
-  bool turns[P];
+  const int turning = min(max(p.n_pairs - unit * P, 0), P);
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int pair = unit * P + i;
-    turns[i] = pair < p.n_pairs;
     cs[i] = 1.f;
     sn[i] = 0.f;
-    if (turns[i]) {
-      const int ax = p.axis[pair];
+    if (i < turning) {
+      const int pair = unit * P + i, ax = p.axis[pair];
       int64_t pos;
       if (p.positions) {
         pos = __ldg(p.positions + b * p.pos_batch + n * p.n_axes + ax);
@@ -112,37 +179,27 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
   const int ch0 = p.c0[unit], ch1 = p.c1[unit];
   const int lo = blockIdx.y * p.rows_per_cta, hi = min(lo + p.rows_per_cta, p.row0[p.n_tensors]);
-  for (int r = lo; r < hi; r += kRows) {
-    Pc in[kRows][PIECES];
-    T* dst[kRows];
+  for (int t = 0; t < p.n_tensors; ++t) {
+    const int h0 = max(lo - p.row0[t], 0), h1 = min(hi, p.row0[t + 1]) - p.row0[t];
+    const int64_t xs = p.xs[t][1], os = p.os[t][1];
+    const T* src = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + n * p.xs[t][2] + h0 * xs;
+    T* dst = static_cast<T*>(p.out[t]) + b * p.os[t][0] + n * p.os[t][2] + h0 * os;
+    int h = h0;
+    for (; h + R <= h1; h += R, src += R * xs, dst += R * os) {
+      Unit<T, P, ADJ> u[R];
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int row = r + k;
-      if (row >= hi) break;
-      int t = 0;
-      for (int i = 1; i < p.n_tensors; ++i) t += row >= p.row0[i] ? 1 : 0;
-      const int64_t h = row - p.row0[t];
-      const T* src = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + h * p.xs[t][1] + n * p.xs[t][2];
-      dst[k] = static_cast<T*>(p.out[t]) + b * p.os[t][0] + h * p.os[t][1] + n * p.os[t][2];
-      in[k][0] = *reinterpret_cast<const Pc*>(src + ch0);
-      if (PIECES == 2) in[k][PIECES - 1] = *reinterpret_cast<const Pc*>(src + ch1);
-    }
+      for (int k = 0; k < R; ++k) u[k].load(src + k * xs + ch0, src + k * xs + ch1);
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (r + k >= hi) break;
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        T& ea = ONE ? in[k][0].v[(2 * i) % NE] : in[k][0].v[i];
-        T& eb = ONE ? in[k][0].v[(2 * i + 1) % NE] : in[k][PIECES - 1].v[i];
-        const float a = to_f(ea), c = to_f(eb);
-        // channels past the rotated ones are copied bit for bit
-        if (turns[i]) {
-          ea = from_f<T>(a * cs[i] - c * sn[i]);
-          eb = from_f<T>(a * sn[i] + c * cs[i]);
-        }
+      for (int k = 0; k < R; ++k) {
+        u[k].turn(cs, sn, turning);
+        u[k].store(dst + k * os + ch0, dst + k * os + ch1);
       }
-      *reinterpret_cast<Pc*>(dst[k] + ch0) = in[k][0];
-      if (PIECES == 2) *reinterpret_cast<Pc*>(dst[k] + ch1) = in[k][PIECES - 1];
+    }
+    for (; h < h1; ++h, src += xs, dst += os) {
+      Unit<T, P, ADJ> u;
+      u.load(src + ch0, src + ch1);
+      u.turn(cs, sn, turning);
+      u.store(dst + ch0, dst + ch1);
     }
   }
 }

@@ -47,7 +47,7 @@ struct PoolParams {
   float* lo[2];
   float* norm[2];               // |mean| [B*H][blocks]
   int32_t block[2], n_blocks[2];
-  int64_t first_k;              // units of Q, then those of K
+  int64_t first_k, n_units;     // blocks of Q, then those of K
   int32_t N;
 };
 
@@ -79,30 +79,31 @@ __device__ __forceinline__ void two_sum(uint64_t& s, uint64_t& e, uint64_t x) {
   s = t;
 }
 
-// One CTA per block of rows of one head; D / 8 threads across a row, so that a
-// warp reads 512 contiguous bytes, kPoolThreads / (D / 8) rows at a time, eight
-// loads in flight per thread.  Everything is fp32 pairs: fp64 sums, at two lanes a
-// clock per SM, took 320 us for a 480p layer.
-template <int D>
+// Block means: one warp per block of rows of one head, or (SHARED: blocks of many
+// rows) the four warps of a CTA.  D / 8 lanes across a row, eight loads of 16 bytes
+// in flight per lane, no barrier between blocks.  Everything is fp32 pairs: fp64
+// sums, at two lanes a clock per SM, took 320 us for a 480p layer, one CTA per block
+// (whose loads wait out its barriers) 104 us.
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ PoolParams p) {
-  constexpr int VR = D / 8, GROUPS = kPoolThreads / VR;
-  __shared__ float2 part[GROUPS][D];
-  const int64_t unit = blockIdx.x;
+  constexpr int VR = D / 8, RPW = 32 / VR, WARPS = kPoolThreads / 32;   // RPW rows per warp load
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t unit = SHARED ? blockIdx.x : blockIdx.x * static_cast<int64_t>(WARPS) + warp;
+  if (unit >= p.n_units) return;
   const int w = unit >= p.first_k ? 1 : 0;
   const int64_t u = unit - (w ? p.first_k : 0);
   const int64_t bh = u / p.n_blocks[w];
   const int blk = static_cast<int>(u - bh * p.n_blocks[w]);
   const int row0 = static_cast<int>(static_cast<int64_t>(blk) * p.block[w]);
   const int rows = min(p.block[w], p.N - row0);
-  const int v = threadIdx.x % VR, g = threadIdx.x / VR;
-  const uint4* src = p.x[w] + (bh * p.N + row0) * VR + v;
+  const uint4* src = p.x[w] + (bh * p.N + row0) * VR + lane % VR;
   uint64_t s[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};
-  constexpr int U = 8;
-  for (int r = g; r < rows; r += GROUPS * U) {
+  constexpr int U = 8, STEP = RPW * (SHARED ? WARPS : 1);
+  for (int r = lane / VR + (SHARED ? warp * RPW : 0); r < rows; r += STEP * U) {
     uint4 x[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int rr = r + k * GROUPS;
+      const int rr = r + k * STEP;
       x[k] = rr < rows ? __ldg(src + static_cast<int64_t>(rr) * VR) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
@@ -112,55 +113,83 @@ __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constan
       for (int i = 0; i < 4; ++i) two_sum(s[i], e[i], pair2(bf16_lo(wd[i]), bf16_hi(wd[i])));
     }
   }
+  // rows of a warp's other lanes
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    part[g][v * 8 + 2 * i] = make_float2(lane2(s[i], 0), lane2(e[i], 0));
-    part[g][v * 8 + 2 * i + 1] = make_float2(lane2(s[i], 1), lane2(e[i], 1));
-  }
-  __syncthreads();
-  __shared__ float red[2][kPoolThreads / 32];
-  float hi = 0.f;
-  if (threadIdx.x < D) {
-    float2 t = part[0][threadIdx.x];
+  for (int m = 16; m >= VR; m >>= 1) {
 #pragma unroll
-    for (int k = 1; k < GROUPS; ++k) {
-      const float2 o = part[k][threadIdx.x];
-      const float n = __fadd_rn(t.x, o.x), z = __fsub_rn(n, t.x);
-      t.y = __fadd_rn(__fadd_rn(t.y, o.y),
-                      __fadd_rn(__fsub_rn(t.x, __fsub_rn(n, z)), __fsub_rn(o.x, z)));
-      t.x = n;
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t os = __shfl_xor_sync(0xFFFFFFFFu, s[i], m), oe = __shfl_xor_sync(0xFFFFFFFFu, e[i], m);
+      two_sum(s[i], e[i], os);
+      e[i] = add2(e[i], oe);
     }
-    // (t.x + t.y) / rows: the quotient of t.x, then that of its exact remainder
-    const float n = static_cast<float>(rows);
-    const float q = __fdiv_rn(t.x, n);
-    const float q2 = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n, t.x), t.y), n);
-    hi = __fadd_rn(q, q2);
-    const float lo = __fadd_rn(__fsub_rn(q, hi), q2);
-    const int64_t o = u * D + threadIdx.x;
-    p.hi[w][o] = hi;
-    p.lo[w][o] = lo;
+  }
+  if constexpr (SHARED) {
+    __shared__ uint64_t part[WARPS - 1][2][4][32];
+    if (warp > 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        part[warp - 1][0][i][lane] = s[i];
+        part[warp - 1][1][i][lane] = e[i];
+      }
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int k = 0; k < WARPS - 1; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        two_sum(s[i], e[i], part[k][0][i][lane]);
+        e[i] = add2(e[i], part[k][1][i][lane]);
+      }
+    }
+  }
+  // every lane of a column holds its 8 channels; lane group g finishes 8 / RPW of them
+  constexpr int CH = 8 / RPW;
+  const int g = lane / VR;
+  const float n = static_cast<float>(rows);
+  const bool exact = (rows & (rows - 1)) == 0;
+  const float inv = 1.f / n;
+  float hi[CH], lo[CH], m = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    float ts = 0.f, te = 0.f;
+#pragma unroll
+    for (int k = 0; k < RPW; ++k)
+      if (g == k) {
+        ts = lane2(s[(k * CH + c) / 2], (k * CH + c) & 1);
+        te = lane2(e[(k * CH + c) / 2], (k * CH + c) & 1);
+      }
+    float q, q2;
+    if (exact) {                 // a power of two: exact
+      q = ts * inv;
+      q2 = te * inv;
+    } else {                     // the quotient of ts, then that of its exact remainder
+      q = __fdiv_rn(ts, n);
+      q2 = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, n, ts), te), n);
+    }
+    hi[c] = __fadd_rn(q, q2);
+    lo[c] = __fadd_rn(__fsub_rn(q, hi[c]), q2);
+    m = fmaxf(m, fabsf(hi[c]));
+  }
+  const int64_t o = u * D + (lane % VR) * 8 + g * CH;
+  if constexpr (CH == 4) {
+    *reinterpret_cast<float4*>(p.hi[w] + o) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<float4*>(p.lo[w] + o) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+  } else {
+    *reinterpret_cast<float2*>(p.hi[w] + o) = make_float2(hi[0], hi[1]);
+    *reinterpret_cast<float2*>(p.lo[w] + o) = make_float2(lo[0], lo[1]);
   }
   // |mean|, over the largest component so that small means do not vanish squared
-  float m = fabsf(hi);
 #pragma unroll
   for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-  if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kPoolThreads / 32; ++k) m = fmaxf(m, red[0][k]);
   m = fmaxf(m, FLT_MIN);
-  const float h = hi / m;
-  float n2 = h * h;
+  const float over = 1.f / m;
+  float n2 = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) n2 = fmaf(hi[c] * over, hi[c] * over, n2);
 #pragma unroll
   for (int x = 16; x; x >>= 1) n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, x);
-  if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = n2;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float t = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPoolThreads / 32; ++k) t += red[1][k];
-    p.norm[w][u] = sqrtf(t) * m * 1.0001f;     // NaN where a mean is
-  }
+  if (lane == 0) p.norm[w][u] = sqrtf(n2) * m * 1.0001f;     // NaN where a mean is
 }
 
 struct SelParams {
@@ -171,12 +200,12 @@ struct SelParams {
   int32_t keep, first, diagonal;
 };
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 // Two neighbouring values as two bf16 terms each: hi = bf16(x), lo = bf16(x - hi).
@@ -276,15 +305,15 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   auto val = [&](int m) -> float { return KPL > 0 ? v[KPL > 0 ? m : 0] : load(m); };
   float above = INFINITY, below = -INFINITY;    // kept for sure above, dropped for sure below
   if (finite) {
-    uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+    float vmin = INFINITY, vmax = -INFINITY;
 #pragma unroll
     for (int m = 0; m < chunks; ++m) {
-      const uint32_t k = key32(val(m));
-      kmax = max(kmax, k);
-      if (k != key32(-INFINITY)) kmin = min(kmin, k);
+      const float x = val(m);
+      vmax = fmaxf(vmax, x);
+      vmin = fminf(vmin, x == -INFINITY ? INFINITY : x);
     }
-    kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
-    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
+    const uint32_t kmin = __reduce_min_sync(0xFFFFFFFFu, key32(vmin));
+    const uint32_t kmax = __reduce_max_sync(0xFFFFFFFFu, key32(vmax));
     // the want-th largest lies in [lo, hi]: count(>= lo) >= want, count(> hi) < want.
     // Bisected until the bracket is inside the fast bound, or exactly `want` are
     // above (then it is the smallest of those).
@@ -421,7 +450,7 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
 
 // One CTA: a strip of kStrip query blocks of one head.
 template <int D, int KPL>
-__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelParams p) {
+__global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(const __grid_constant__ SelParams p) {
   extern __shared__ float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t bh = blockIdx.x / p.strips;
@@ -440,22 +469,25 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   for (int m = 16; m; m >>= 1) km = fmaxf(km, __shfl_xor_sync(0xFFFFFFFFu, km, m));
   if (lane == 0) k_max_w[warp] = km;
 
-  // ---- scores: every warp takes the strip's 16 query blocks (both bf16 terms of
-  // the A fragments stay in registers) and every eighth group of 8 key blocks
+  // ---- scores: every warp takes the strip's 16 query blocks, whose A fragments
+  // (both bf16 terms) lie in shared memory in the order of their use, and every
+  // eighth group of 8 key blocks
   {
+    __shared__ uint4 frag[2][D / 16][32];
     const int g = lane >> 2, t = lane & 3;
-    const int r0 = i0 + g, r1 = r0 + 8;
-    uint32_t ah[D / 16][4], al[D / 16][4];
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
+    if (warp < D / 16) {
+      uint32_t ah[4], al[4];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        const int r = (f & 1) ? r1 : r0, c = kk * 16 + t * 2 + ((f & 2) ? 8 : 0);
+        const int r = i0 + g + ((f & 1) ? 8 : 0), c = warp * 16 + t * 2 + ((f & 2) ? 8 : 0);
         const float2 x = r < p.nq ? __ldg(reinterpret_cast<const float2*>(p.q_hi + (bh * p.nq + r) * D + c))
                                   : make_float2(0.f, 0.f);
-        split2(x, ah[kk][f], al[kk][f]);
+        split2(x, ah[f], al[f]);
       }
+      frag[0][warp][lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
+      frag[1][warp][lane] = make_uint4(al[0], al[1], al[2], al[3]);
     }
+    __syncthreads();
     for (int j0 = warp * 8; j0 < p.nk; j0 += 8 * (kSelThreads / 32)) {
       const int j = j0 + g;
       const float* kr = p.k_hi + (bh * p.nk + (j < p.nk ? j : p.nk - 1)) * D + t * 2;
@@ -468,9 +500,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
         uint32_t bh0, bl0, bh1, bl1;
         split2(x[2 * kk], bh0, bl0);
         split2(x[2 * kk + 1], bh1, bl1);
-        mma_16816(c0, ah[kk], bh0, bh1);
-        mma_16816(c1, ah[kk], bl0, bl1);
-        mma_16816(c1, al[kk], bh0, bh1);
+        const uint4 ah = frag[0][kk][lane], al = frag[1][kk][lane];
+        mma_16816(c0, ah, bh0, bh1);
+        mma_16816(c1, ah, bl0, bl1);
+        mma_16816(c1, al, bh0, bh1);
       }
       const int col = j0 + t * 2;
 #pragma unroll
@@ -554,7 +587,7 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   pp.n_blocks[1] = l.nk;
   pp.first_k = BH * l.nq;
   pp.N = s.N;
-  const int64_t units = BH * (static_cast<int64_t>(l.nq) + l.nk);
+  pp.n_units = BH * (static_cast<int64_t>(l.nq) + l.nk);
   SelParams sp;
   sp.q_hi = pp.hi[0];
   sp.q_lo = pp.lo[0];
@@ -575,7 +608,13 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   sp.first = s.first;
   sp.diagonal = s.diagonal;
   const size_t smem = l.in_smem ? static_cast<size_t>(kStrip) * l.pitch * 4 : 0;
-  pool_kernel<D><<<static_cast<unsigned>(units), kPoolThreads, 0, st>>>(pp);
+  // a CTA per block where a block holds more rows than a warp should read alone
+  // (256 rows are 64 kB at d = 128), or where there are too few blocks to fill the GPU
+  constexpr int kWarps = kPoolThreads / 32;
+  if (std::max(s.bq, s.bk) > 256 || pp.n_units < 2048)
+    pool_kernel<D, true><<<static_cast<unsigned>(pp.n_units), kPoolThreads, 0, st>>>(pp);
+  else
+    pool_kernel<D, false><<<static_cast<unsigned>((pp.n_units + kWarps - 1) / kWarps), kPoolThreads, 0, st>>>(pp);
   TSR_CUDA(cudaGetLastError());
   // scores per lane held in registers: as many as a row has, up to 32
   const unsigned ctas = static_cast<unsigned>(BH * l.strips);
