@@ -85,7 +85,7 @@ __device__ __forceinline__ void two_sum(uint64_t& s, uint64_t& e, uint64_t x) {
 // sums, at two lanes a clock per SM, took 320 us for a 480p layer, one CTA per block
 // (whose loads wait out its barriers) 104 us.
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ PoolParams p) {
+__global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_constant__ PoolParams p) {
   constexpr int VR = D / 8, RPW = 32 / VR, WARPS = kPoolThreads / 32;   // RPW rows per warp load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t unit = SHARED ? blockIdx.x : blockIdx.x * static_cast<int64_t>(WARPS) + warp;
@@ -290,18 +290,19 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   const float err2 = 2.f * (kScoreErr * (q_norm * k_max) + 4e-37f * (q_norm + k_max) + 1e-36f);
   bool finite = q_norm * k_max <= FLT_MAX && err2 <= FLT_MAX;
   // with finite norms every score is finite; forced blocks and those past nk hold
-  // -inf and are never counted
+  // -inf and are never counted (a row has room for whole chunks of 32)
   constexpr int REGS = KPL > 0 ? KPL : 1;
-  float v[REGS];
   const int chunks = KPL > 0 ? KPL : (p.nk + 31) / 32;
-  auto load = [&](int m) -> float {
-    const int j = m * 32 + lane;
-    return (j < p.nk && !forced(j)) ? row[j] : -INFINITY;
-  };
+  for (int j = lane; j < first; j += 32) row[j] = -INFINITY;
+  for (int j = d_lo + lane; j < d_hi; j += 32) row[j] = -INFINITY;
+  for (int j = p.nk + lane; j < chunks * 32; j += 32) row[j] = -INFINITY;
+  __syncwarp();
+  float v[REGS];
   if (KPL > 0) {
 #pragma unroll
-    for (int m = 0; m < REGS; ++m) v[m] = load(m);
+    for (int m = 0; m < REGS; ++m) v[m] = row[m * 32 + lane];
   }
+  auto load = [&](int m) -> float { return row[m * 32 + lane]; };
   auto val = [&](int m) -> float { return KPL > 0 ? v[KPL > 0 ? m : 0] : load(m); };
   float above = INFINITY, below = -INFINITY;    // kept for sure above, dropped for sure below
   if (finite) {
@@ -314,26 +315,35 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
     }
     const uint32_t kmin = __reduce_min_sync(0xFFFFFFFFu, key32(vmin));
     const uint32_t kmax = __reduce_max_sync(0xFFFFFFFFu, key32(vmax));
-    // the want-th largest lies in [lo, hi]: count(>= lo) >= want, count(> hi) < want.
-    // Bisected until the bracket is inside the fast bound, or exactly `want` are
-    // above (then it is the smallest of those).
+    // the want-th largest lies in [lo, hi]: c_lo = count(>= lo) >= want, c_hi =
+    // count(> hi) < want.  Narrowed, by interpolating the counts and every third
+    // time by halving, until the bracket is inside the fast bound or exactly `want`
+    // are above (then it is the smallest of those).
     float lo = unkey32(kmin), hi = unkey32(kmax);
-    while (hi - lo > 0.25f * err2) {
-      const float mid = lo + 0.5f * (hi - lo);
+    float c_lo = static_cast<float>(others), c_hi = 0.f;
+    for (int turn = 0; hi - lo > 0.25f * err2; ++turn) {
+      const float f = turn % 3 == 2 ? 0.5f : (c_lo - static_cast<float>(want) + 0.5f) / (c_lo - c_hi);
+      float mid = lo + f * (hi - lo);
+      if (!(mid > lo && mid < hi)) mid = lo + 0.5f * (hi - lo);
       if (!(mid > lo && mid < hi)) break;
       int c = 0;
 #pragma unroll
       for (int m = 0; m < chunks; ++m) c += val(m) > mid ? 1 : 0;
       c = __reduce_add_sync(0xFFFFFFFFu, c);
       if (c == want) {
-        uint32_t k = 0xFFFFFFFFu;
+        float low = INFINITY;
 #pragma unroll
-        for (int m = 0; m < chunks; ++m) k = val(m) > mid ? min(k, key32(val(m))) : k;
-        lo = hi = unkey32(__reduce_min_sync(0xFFFFFFFFu, k));
+        for (int m = 0; m < chunks; ++m) low = val(m) > mid ? fminf(low, val(m)) : low;
+        lo = hi = unkey32(__reduce_min_sync(0xFFFFFFFFu, key32(low)));
         break;
       }
-      if (c > want) lo = mid;
-      else hi = mid;
+      if (c > want) {
+        lo = mid;
+        c_lo = static_cast<float>(c);
+      } else {
+        hi = mid;
+        c_hi = static_cast<float>(c);
+      }
     }
     above = hi + err2;
     below = lo - err2;
@@ -344,6 +354,11 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   auto sure = [&](float x) -> bool { return finite && x > above; };
   auto near = [&](int m, float x) -> bool {
     return finite ? x >= below && x <= above : m * 32 + lane < p.nk && !forced(m * 32 + lane);
+  };
+  // lanes store the bytes of their own j, so a forced block's 1 comes after its 0
+  auto keep_forced = [&]() {
+    for (int j = lane; j < first; j += 32) out[j] = 1;
+    for (int j = d_lo + ((lane - d_lo) & 31); j < d_hi; j += 32) out[j] = 1;
   };
   int n_sure = 0, n_near = 0;
 #pragma unroll
@@ -358,8 +373,9 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
 #pragma unroll
     for (int m = 0; m < chunks; ++m) {
       const int j = m * 32 + lane;
-      if (j < p.nk) out[j] = (forced(j) || sure(val(m)) || near(m, val(m))) ? 1 : 0;
+      if (j < p.nk) out[j] = sure(val(m)) || near(m, val(m)) ? 1 : 0;
     }
+    keep_forced();
     return;
   }
   double q[D / 32];
@@ -381,13 +397,14 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
       const int j = m * 32 + lane;
       const float x = val(m);
       const bool nr = near(m, x);
-      if (j < p.nk && !nr) out[j] = (forced(j) || sure(x)) ? 1 : 0;
+      if (j < p.nk && !nr) out[j] = sure(x) ? 1 : 0;
       uint32_t b = __ballot_sync(0xFFFFFFFFu, nr);
       while (b) {
         if (lane == c++) my_j = m * 32 + __ffs(b) - 1;
         b &= b - 1;
       }
     }
+    keep_forced();
     uint64_t mine = 0;
 #pragma unroll 2
     for (int o = 0; o < n_near; ++o) {
@@ -521,6 +538,9 @@ __global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(c
     select_row<D, KPL>(p, bh, i0 + rr, sc + rr * p.pitch, k_max, lane);
 }
 
+// Scores per lane that the variants of select_kernel hold in registers.
+constexpr int kRowRegs[] = {2, 8, 16, 20, 32};
+
 struct Layout {
   int32_t nq, nk, strips, pitch;
   bool in_smem;
@@ -532,7 +552,13 @@ Layout layout_of(const tsr_select_desc& s) {
   l.nq = (s.N + s.bq - 1) / s.bq;
   l.nk = (s.N + s.bk - 1) / s.bk;
   l.strips = (l.nq + kStrip - 1) / kStrip;
-  l.pitch = l.nk + ((l.nk & 31) ? 0 : 4);    // rows of a strip start in different banks
+  l.pitch = (l.nk + 31) / 32 * 32;           // whole chunks of 32,
+  for (int kpl : kRowRegs)                   // as many as the kernel takes,
+    if (l.nk <= 32 * kpl) {
+      l.pitch = 32 * kpl;
+      break;
+    }
+  l.pitch += 4;                              // rows of a strip starting in different banks
   l.in_smem = static_cast<size_t>(kStrip) * l.pitch * 4 <= kStripBytes;   // else in the workspace
   const size_t BH = static_cast<size_t>(s.B) * s.H;
   size_t at = 0;
@@ -620,6 +646,7 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   const unsigned ctas = static_cast<unsigned>(BH * l.strips);
   if (l.nk <= 64) return launch_strips<D, 2>(sp, ctas, smem, st);
   if (l.nk <= 256) return launch_strips<D, 8>(sp, ctas, smem, st);
+  if (l.nk <= 512) return launch_strips<D, 16>(sp, ctas, smem, st);
   if (l.nk <= 640) return launch_strips<D, 20>(sp, ctas, smem, st);
   if (l.nk <= 1024) return launch_strips<D, 32>(sp, ctas, smem, st);
   return launch_strips<D, 0>(sp, ctas, smem, st);
