@@ -13,8 +13,8 @@
 // means are sums with a running error term (two-sum), about 48 bits.  The scores
 // come from the tensor cores with each mean split into two bf16 terms (three
 // products; error at most kScoreErr * |qm_i| |km_j|), and any block whose score
-// is within twice that error of the last kept one is scored again in fp64 from
-// the 48-bit means; the order of those decides.  A row has a handful of such
+// is within twice that error of the last kept one is scored again from the 48-bit
+// means with error terms; the order of those decides.  A row has two or so such
 // blocks, where scoring everything in fp64 would cost 1.3 ms for a 480p layer at
 // the 1.25 TFLOP/s of fp64.
 #include <cuda_bf16.h>
@@ -46,6 +46,12 @@ struct PoolParams {
   float* hi[2];                 // block means [B*H][blocks][d], high and low parts
   float* lo[2];
   float* norm[2];               // |mean| [B*H][blocks]
+  // the means' two bf16 terms in the order of the MMA fragments: [B*H][blocks / 8]
+  // [d / 16][32] of {hi(c, c+1), lo(c, c+1), hi(c+2, c+3), lo(c+2, c+3)}, lane 4 g + t
+  // holding row g's channels c = 16 kk + 4 t.  (Which channels make a k index is free
+  // as long as A and B agree; so a lane's four lie together.)
+  uint4* frag[2];
+  int32_t frag_rows[2];         // blocks rounded up to 8
   int32_t block[2], n_blocks[2];
   int64_t first_k, n_units;     // blocks of Q, then those of K
   int32_t N;
@@ -53,6 +59,12 @@ struct PoolParams {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two neighbouring values as two bf16 terms each: hi = bf16(x), lo = bf16(x - hi).
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  lo = pack_bf16x2(x.x - bf16_lo(hi), x.y - bf16_hi(hi));
+}
 
 // (s, e) += x on two channels at once: s + e grows by exactly x up to the rounding
 // of e (Knuth's two-sum, seven packed adds).
@@ -179,6 +191,16 @@ __global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_cons
     *reinterpret_cast<float2*>(p.hi[w] + o) = make_float2(hi[0], hi[1]);
     *reinterpret_cast<float2*>(p.lo[w] + o) = make_float2(lo[0], lo[1]);
   }
+  {
+    // a lane's channels are 4 (d = 128) or 2 (d = 64) of a fragment's
+    const int c = (lane % VR) * 8 + g * CH;
+    const int64_t at = ((bh * (p.frag_rows[w] / 8) + blk / 8) * (D / 16) + c / 16) * 32 + (blk % 8) * 4 + (c % 16) / 4;
+    uint2 t[CH / 2];
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) split2(make_float2(hi[2 * i], hi[2 * i + 1]), t[i].x, t[i].y);
+    if constexpr (CH == 4) p.frag[w][at] = make_uint4(t[0].x, t[0].y, t[CH / 2 - 1].x, t[CH / 2 - 1].y);
+    else reinterpret_cast<uint2*>(p.frag[w] + at)[(c % 4) / 2] = t[0];
+  }
   // |mean|, over the largest component so that small means do not vanish squared
 #pragma unroll
   for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
@@ -194,6 +216,8 @@ __global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_cons
 
 struct SelParams {
   const float *q_hi, *q_lo, *k_hi, *k_lo, *q_norm, *k_norm;
+  const uint4 *q_frag, *k_frag;
+  int32_t q_frag_rows, k_frag_rows;
   float* scores;        // [CTA][kStrip][pitch] when the strip does not fit shared memory
   uint8_t* blocks;
   int32_t N, bq, bk, nq, nk, strips, pitch;
@@ -206,12 +230,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4& a, uint32_
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-// Two neighbouring values as two bf16 terms each: hi = bf16(x), lo = bf16(x - hi).
-__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x.x, x.y);
-  lo = pack_bf16x2(x.x - bf16_lo(hi), x.y - bf16_hi(hi));
 }
 
 // Order-preserving integer of a score: a larger score has a larger key, equal
@@ -230,18 +248,59 @@ __device__ __forceinline__ uint64_t key64(double x) {
   return (u & 0x8000000000000000ull) ? ~u : (u | 0x8000000000000000ull);
 }
 
-// The score in fp64 from the 48-bit means, by one warp (every lane gets it).
+// A power of two that brings a mean of this norm near 1, and its inverse.
+__device__ __forceinline__ float scale_of(float norm, double& back) {
+  const int e = min(max(static_cast<int>((__float_as_uint(norm) >> 23) & 255u), 1), 253);
+  back = __longlong_as_double(static_cast<int64_t>(e - 127 + 1023) << 52);
+  return __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+}
+
+__device__ __forceinline__ void two_sum1(float& s, float& e, float x) {
+  const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+  s = t;
+}
+
+// The order keys of four scores from the 48-bit means, by one warp: lanes 8 c .. 8 c
+// + 7 take key block j of their own (all eight get the key; j < 0: 0).  Products with
+// their error terms (fma) summed with theirs (two-sum), in fp32 on means scaled to 1
+// by powers of two, so that nothing leaves fp32's range; about 2^-46 of |qm| |km|.
+// (fp64 runs at two lanes a clock per SM here.)
 template <int D>
-__device__ __forceinline__ double exact_score(const double (&q)[D / 32], const float* kh, const float* kl, int lane) {
-  double t = 0.0;
+__device__ __forceinline__ uint64_t exact_keys(const float* qh, const float* ql, float q_norm, const float* kh,
+                                               const float* kl, const float* k_norm, int j, int lane) {
+  double q_back, k_back;
+  const bool on = j >= 0;
+  const int64_t o = static_cast<int64_t>(on ? j : 0);
+  const float q_scale = scale_of(q_norm, q_back), k_scale = scale_of(__ldg(k_norm + o), k_back);
+  float s = 0.f, e = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    const int c = i * 32 + lane;
-    t = fma(q[i], static_cast<double>(__ldg(kh + c)) + static_cast<double>(__ldg(kl + c)), t);
+    const int c = i * 8 + (lane & 7);           // float4 of channels
+    const float4 a = __ldg(reinterpret_cast<const float4*>(qh) + c), b = __ldg(reinterpret_cast<const float4*>(ql) + c);
+    const float4 x = __ldg(reinterpret_cast<const float4*>(kh + o * D) + c);
+    const float4 y = __ldg(reinterpret_cast<const float4*>(kl + o * D) + c);
+    const float ah[4] = {a.x, a.y, a.z, a.w}, al[4] = {b.x, b.y, b.z, b.w};
+    const float xh[4] = {x.x, x.y, x.z, x.w}, xl[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float u = ah[k] * q_scale, ul = al[k] * q_scale, v = xh[k] * k_scale, vl = xl[k] * k_scale;
+      const float p = __fmul_rn(u, v);
+      e = __fadd_rn(e, __fmaf_rn(ul, v, __fmaf_rn(u, vl, __fmaf_rn(u, v, -p))));
+      two_sum1(s, e, p);
+    }
   }
 #pragma unroll
-  for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, m);
-  return t;
+  for (int m = 4; m; m >>= 1) {
+    // lane i and lane i ^ m add in the same order, the lower lane's sum first
+    const float os = __shfl_xor_sync(0xFFFFFFFFu, s, m), oe = __shfl_xor_sync(0xFFFFFFFFu, e, m);
+    const bool low = (lane & m) == 0;
+    float a = low ? s : os, b = low ? e : oe;
+    two_sum1(a, b, low ? os : s);
+    s = a;
+    e = __fadd_rn(b, low ? oe : e);
+  }
+  return on ? key64((static_cast<double>(s) + static_cast<double>(e)) * (q_back * k_back)) : 0ull;
 }
 
 // The largest key T such that at least `want` of the n keys that `in` admits are
@@ -321,8 +380,8 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
     // are above (then it is the smallest of those).
     float lo = unkey32(kmin), hi = unkey32(kmax);
     float c_lo = static_cast<float>(others), c_hi = 0.f;
-    for (int turn = 0; hi - lo > 0.25f * err2; ++turn) {
-      const float f = turn % 3 == 2 ? 0.5f : (c_lo - static_cast<float>(want) + 0.5f) / (c_lo - c_hi);
+    for (int turn = 0; hi - lo > 0.25f * err2; turn = turn == 2 ? 0 : turn + 1) {
+      const float f = turn == 2 ? 0.5f : __fdividef(c_lo - static_cast<float>(want) + 0.5f, c_lo - c_hi);
       float mid = lo + f * (hi - lo);
       if (!(mid > lo && mid < hi)) mid = lo + 0.5f * (hi - lo);
       if (!(mid > lo && mid < hi)) break;
@@ -355,68 +414,73 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   auto near = [&](int m, float x) -> bool {
     return finite ? x >= below && x <= above : m * 32 + lane < p.nk && !forced(m * 32 + lane);
   };
-  // lanes store the bytes of their own j, so a forced block's 1 comes after its 0
-  auto keep_forced = [&]() {
-    for (int j = lane; j < first; j += 32) out[j] = 1;
-    for (int j = d_lo + ((lane - d_lo) & 31); j < d_hi; j += 32) out[j] = 1;
-  };
+  // the sure ones' bytes, and the number of the near ones
   int n_sure = 0, n_near = 0;
+  uint32_t near_bits = 0u;                      // KPL > 0: bit m
 #pragma unroll
   for (int m = 0; m < chunks; ++m) {
-    n_sure += sure(val(m)) ? 1 : 0;
-    n_near += near(m, val(m)) ? 1 : 0;
+    const int j = m * 32 + lane;
+    const float x = val(m);
+    const bool in = sure(x), nr = near(m, x);
+    n_sure += in ? 1 : 0;
+    if (KPL > 0) near_bits |= nr ? 1u << (m & 31) : 0u;
+    else n_near += nr ? 1 : 0;
+    if (j < p.nk) out[j] = in ? 1 : 0;
   }
+  if (KPL > 0) n_near = __popc(near_bits);
+  // lanes store the bytes of their own j, so a forced block's 1 comes after its 0
+  for (int j = lane; j < first; j += 32) out[j] = 1;
+  for (int j = d_lo + ((lane - d_lo) & 31); j < d_hi; j += 32) out[j] = 1;
   n_sure = __reduce_add_sync(0xFFFFFFFFu, n_sure);
   n_near = __reduce_add_sync(0xFFFFFFFFu, n_near);
   const int left = want - n_sure;               // of the near ones, 1 <= left <= n_near
   if (left == n_near) {
-#pragma unroll
-    for (int m = 0; m < chunks; ++m) {
-      const int j = m * 32 + lane;
-      if (j < p.nk) out[j] = sure(val(m)) || near(m, val(m)) ? 1 : 0;
+    if (KPL > 0) {
+      for (; near_bits; near_bits &= near_bits - 1) out[(__ffs(near_bits) - 1) * 32 + lane] = 1;
+    } else {
+      for (int m = 0; m < chunks; ++m)
+        if (near(m, val(m))) out[m * 32 + lane] = 1;
     }
-    keep_forced();
     return;
   }
-  double q[D / 32];
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    const int64_t o = (bh * p.nq + i) * D + c * 32 + lane;
-    q[c] = static_cast<double>(__ldg(p.q_hi + o)) + static_cast<double>(__ldg(p.q_lo + o));
-  }
-  const float* kh = p.k_hi + bh * p.nk * D;
-  const float* kl = p.k_lo + bh * p.nk * D;
-  auto exact_key = [&](int j) -> uint64_t {
-    return key64(exact_score<D>(q, kh + static_cast<int64_t>(j) * D, kl + static_cast<int64_t>(j) * D, lane));
+  auto keys_of = [&](int j) -> uint64_t {
+    const int64_t qo = (bh * p.nq + i) * D, ko = bh * p.nk;
+    return exact_keys<D>(p.q_hi + qo, p.q_lo + qo, q_norm, p.k_hi + ko * D, p.k_lo + ko * D, p.k_norm + ko, j, lane);
   };
   if (n_near <= 32) {
-    // lane c holds near block c (ascending j): its exact key, then its rank
+    // lane c takes near block c (in any order): its exact key, then its rank
     int my_j = -1, c = 0;
-#pragma unroll
-    for (int m = 0; m < chunks; ++m) {
-      const int j = m * 32 + lane;
-      const float x = val(m);
-      const bool nr = near(m, x);
-      if (j < p.nk && !nr) out[j] = sure(x) ? 1 : 0;
-      uint32_t b = __ballot_sync(0xFFFFFFFFu, nr);
-      while (b) {
-        if (lane == c++) my_j = m * 32 + __ffs(b) - 1;
-        b &= b - 1;
+    auto list = [&](int m0, uint32_t bits) {    // bits: this lane's near blocks of chunks m0 ..
+      for (uint32_t any; (any = __ballot_sync(0xFFFFFFFFu, bits != 0u)) != 0u; ++c) {
+        const int from = __ffs(any) - 1;
+        const int m = __ffs(__shfl_sync(0xFFFFFFFFu, bits, from)) - 1;
+        if (lane == c) my_j = (m0 + m) * 32 + from;
+        if (lane == from) bits &= bits - 1;
+      }
+    };
+    if (KPL > 0) {
+      list(0, near_bits);
+    } else {
+      for (int m0 = 0; m0 < chunks; m0 += 32) {
+        uint32_t bits = 0u;
+        for (int m = m0; m < min(m0 + 32, chunks); ++m) bits |= near(m, val(m)) ? 1u << (m - m0) : 0u;
+        list(m0, bits);
       }
     }
-    keep_forced();
     uint64_t mine = 0;
-#pragma unroll 2
-    for (int o = 0; o < n_near; ++o) {
-      const uint64_t key = exact_key(__shfl_sync(0xFFFFFFFFu, my_j, o));
-      if (lane == o) mine = key;
+    for (int o = 0; o < n_near; o += 4) {
+      const uint64_t key = keys_of(__shfl_sync(0xFFFFFFFFu, my_j, o + (lane >> 3)));   // o + 3 < 32
+      const uint64_t got = __shfl_sync(0xFFFFFFFFu, key, ((lane - o) & 3) * 8);
+      if (lane >= o && lane < o + 4) mine = got;
     }
     int rank = 0;
     for (int o = 0; o < n_near; ++o) {
       const uint64_t other = __shfl_sync(0xFFFFFFFFu, mine, o);
-      rank += (other > mine || (other == mine && o < lane)) ? 1 : 0;
+      const int other_j = __shfl_sync(0xFFFFFFFFu, my_j, o);
+      rank += (other > mine || (other == mine && other_j < my_j)) ? 1 : 0;
     }
-    if (my_j >= 0) out[my_j] = rank < left ? 1 : 0;
+    __syncwarp();                               // after the owners' zeros
+    if (my_j >= 0 && rank < left) out[my_j] = 1;
     return;
   }
   // Many near blocks (a query block of zeros, equal key blocks, infinities):
@@ -436,11 +500,15 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
     for (int j0 = 0; j0 < p.nk; j0 += 32) {
       const int j = j0 + lane;
       uint32_t b = __ballot_sync(0xFFFFFFFFu, j < p.nk && is_near(j));
-      while (b) {
-        const int jj = j0 + __ffs(b) - 1;
-        b &= b - 1;
-        const uint64_t key = exact_key(jj);
-        if (lane == 0) row[jj] = __uint_as_float(static_cast<uint32_t>(half ? key : key >> 32));
+      while (b) {                               // four at a time
+        int jj = -1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (b && lane >> 3 == c) jj = j0 + __ffs(b) - 1;
+          b &= b - 1;
+        }
+        const uint64_t key = keys_of(jj);
+        if (jj >= 0 && (lane & 7) == 0) row[jj] = __uint_as_float(static_cast<uint32_t>(half ? key : key >> 32));
       }
     }
     __syncwarp();
@@ -467,7 +535,7 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
 
 // One CTA: a strip of kStrip query blocks of one head.
 template <int D, int KPL>
-__global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(const __grid_constant__ SelParams p) {
+__global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : KPL > 16 ? 3 : 4) select_kernel(const __grid_constant__ SelParams p) {
   extern __shared__ float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t bh = blockIdx.x / p.strips;
@@ -487,46 +555,44 @@ __global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(c
   if (lane == 0) k_max_w[warp] = km;
 
   // ---- scores: every warp takes the strip's 16 query blocks, whose A fragments
-  // (both bf16 terms) lie in shared memory in the order of their use, and every
-  // eighth group of 8 key blocks
+  // (both bf16 terms) are copied to shared memory, and every eighth pair of groups of
+  // 8 key blocks, whose B fragments are read 512 bytes in a row
   {
-    __shared__ uint4 frag[2][D / 16][32];
+    constexpr int KK = D / 16;
+    __shared__ uint4 frag[2][KK][32];
     const int g = lane >> 2, t = lane & 3;
-    if (warp < D / 16) {
-      uint32_t ah[4], al[4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int r = i0 + g + ((f & 1) ? 8 : 0), c = warp * 16 + t * 2 + ((f & 2) ? 8 : 0);
-        const float2 x = r < p.nq ? __ldg(reinterpret_cast<const float2*>(p.q_hi + (bh * p.nq + r) * D + c))
-                                  : make_float2(0.f, 0.f);
-        split2(x, ah[f], al[f]);
-      }
-      frag[0][warp][lane] = make_uint4(ah[0], ah[1], ah[2], ah[3]);
-      frag[1][warp][lane] = make_uint4(al[0], al[1], al[2], al[3]);
+    for (int x = threadIdx.x; x < 2 * KK * 32; x += kSelThreads) {
+      const int group = i0 / 8 + x / (KK * 32);
+      frag[x / (KK * 32)][x / 32 % KK][lane] =
+          group < p.q_frag_rows / 8 ? __ldg(p.q_frag + (bh * (p.q_frag_rows / 8) + group) * KK * 32 + x % (KK * 32))
+                                    : make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
-    for (int j0 = warp * 8; j0 < p.nk; j0 += 8 * (kSelThreads / 32)) {
-      const int j = j0 + g;
-      const float* kr = p.k_hi + (bh * p.nk + (j < p.nk ? j : p.nk - 1)) * D + t * 2;
-      float2 x[D / 8];
+    const uint4* kf = p.k_frag + bh * (p.k_frag_rows / 8) * KK * 32 + lane;
+    const int groups = p.k_frag_rows / 8;
+    for (int j = warp * 2; j < groups; j += 2 * (kSelThreads / 32)) {
+      const int j1 = min(j + 1, groups - 1);
+      float c0[2][4] = {}, c1[2][4] = {};
 #pragma unroll
-      for (int kk = 0; kk < D / 8; ++kk) x[kk] = __ldg(reinterpret_cast<const float2*>(kr + kk * 8));
-      float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t bh0, bl0, bh1, bl1;
-        split2(x[2 * kk], bh0, bl0);
-        split2(x[2 * kk + 1], bh1, bl1);
-        const uint4 ah = frag[0][kk][lane], al = frag[1][kk][lane];
-        mma_16816(c0, ah, bh0, bh1);
-        mma_16816(c1, ah, bl0, bl1);
-        mma_16816(c1, al, bh0, bh1);
+      for (int kk = 0; kk < KK; ++kk) {
+        const uint4 b0 = __ldg(kf + (j * KK + kk) * 32), b1 = __ldg(kf + (j1 * KK + kk) * 32);
+        const uint4 a0 = frag[0][kk][lane], a1 = frag[1][kk][lane];
+        const uint4 ah = make_uint4(a0.x, a1.x, a0.z, a1.z), al = make_uint4(a0.y, a1.y, a0.w, a1.w);
+        mma_16816(c0[0], ah, b0.x, b0.z);
+        mma_16816(c0[1], ah, b1.x, b1.z);
+        mma_16816(c1[0], ah, b0.y, b0.w);
+        mma_16816(c1[1], ah, b1.y, b1.w);
+        mma_16816(c1[0], al, b0.x, b0.z);
+        mma_16816(c1[1], al, b1.x, b1.z);
       }
-      const int col = j0 + t * 2;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int cc = col + (e & 1), rr = g + ((e & 2) ? 8 : 0);
-        if (cc < p.nk) sc[rr * p.pitch + cc] = c0[e] + c1[e];
+      for (int n = 0; n < 2; ++n) {
+        const int col = (j + n) * 8 + t * 2;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int cc = col + (e & 1), rr = g + ((e & 2) ? 8 : 0);
+          if (cc < p.nk) sc[rr * p.pitch + cc] = c0[n][e] + c1[n][e];
+        }
       }
     }
   }
@@ -544,7 +610,8 @@ constexpr int kRowRegs[] = {2, 8, 16, 20, 32};
 struct Layout {
   int32_t nq, nk, strips, pitch;
   bool in_smem;
-  size_t q_hi, q_lo, k_hi, k_lo, q_norm, k_norm, scores, total;
+  int32_t q_frag_rows, k_frag_rows;          // blocks rounded up to 8
+  size_t q_hi, q_lo, k_hi, k_lo, q_norm, k_norm, q_frag, k_frag, scores, total;
 };
 
 Layout layout_of(const tsr_select_desc& s) {
@@ -573,6 +640,10 @@ Layout layout_of(const tsr_select_desc& s) {
   l.k_lo = take(BH * l.nk * s.d);
   l.q_norm = take(BH * l.nq);
   l.k_norm = take(BH * l.nk);
+  l.q_frag_rows = (l.nq + 7) / 8 * 8;
+  l.k_frag_rows = (l.nk + 7) / 8 * 8;
+  l.q_frag = take(BH * l.q_frag_rows * s.d);
+  l.k_frag = take(BH * l.k_frag_rows * s.d);
   l.scores = take(l.in_smem ? 0 : BH * l.strips * kStrip * l.pitch);
   l.total = at;
   return l;
@@ -607,6 +678,10 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   pp.hi[1] = f(l.k_hi);
   pp.lo[1] = f(l.k_lo);
   pp.norm[1] = f(l.k_norm);
+  pp.frag[0] = reinterpret_cast<uint4*>(ws + l.q_frag);
+  pp.frag[1] = reinterpret_cast<uint4*>(ws + l.k_frag);
+  pp.frag_rows[0] = l.q_frag_rows;
+  pp.frag_rows[1] = l.k_frag_rows;
   pp.block[0] = s.bq;
   pp.block[1] = s.bk;
   pp.n_blocks[0] = l.nq;
@@ -619,6 +694,10 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   sp.q_lo = pp.lo[0];
   sp.k_hi = pp.hi[1];
   sp.k_lo = pp.lo[1];
+  sp.q_frag = pp.frag[0];
+  sp.k_frag = pp.frag[1];
+  sp.q_frag_rows = l.q_frag_rows;
+  sp.k_frag_rows = l.k_frag_rows;
   sp.q_norm = pp.norm[0];
   sp.k_norm = pp.norm[1];
   sp.scores = l.in_smem ? nullptr : f(l.scores);
