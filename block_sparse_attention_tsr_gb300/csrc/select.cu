@@ -535,7 +535,7 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
 
 // One CTA: a strip of kStrip query blocks of one head.
 template <int D, int KPL>
-__global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : KPL > 16 ? 3 : 4) select_kernel(const __grid_constant__ SelParams p) {
+__global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(const __grid_constant__ SelParams p) {
   extern __shared__ float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t bh = blockIdx.x / p.strips;
