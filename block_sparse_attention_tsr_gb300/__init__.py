@@ -466,6 +466,7 @@ def tsr_svg_route(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_frames: i
 
 
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ROPE_ARRAYS = tuple(_RopeTensor * n for n in range(1, 5))
 
 
 def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = None,
@@ -479,11 +480,14 @@ def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = Non
     ``axis_dims``: channels per axis.  ``grid``: tokens per axis, in row-major
     order, or ``positions``: int32 [N, axes] or [B, N, axes].  ``out``: like x
     (x itself: in place); default contiguous [B, H, N, d].  Returns out."""
-    xs = [x] if isinstance(x, torch.Tensor) else list(x)
+    one = isinstance(x, torch.Tensor)
+    xs = (x,) if one else tuple(x)
     if not 1 <= len(xs) <= 4:
         raise ValueError("one to four tensors per call")
     if (grid is None) == (positions is None):
         raise ValueError("give grid or positions")
+    if any(t.dim() != 4 for t in xs):
+        raise ValueError("the tensors are [B, H, N, d]")
     B, _, N, d = xs[0].shape
     dtype = xs[0].dtype
     dims = [int(a) for a in axis_dims]
@@ -491,24 +495,31 @@ def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = Non
         raise ValueError("one to four axes")
     if dtype not in _ROPE_DTYPES:
         raise ValueError("the tensors are bf16, fp16 or fp32")
-    if out is None:
+    if out is not None:
+        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != len(xs):
+            raise ValueError("as many outputs as tensors")
+        _on_device(*xs, *outs, positions)
+    else:
+        _on_device(*xs, positions)
         with _allocating_on(stream):
             outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
-    else:
-        outs = [out] if isinstance(out, torch.Tensor) else list(out)
-    if len(outs) != len(xs):
-        raise ValueError("as many outputs as tensors")
-    _on_device(*xs, *outs, positions)
-    arr = (_RopeTensor * len(xs))()
+    arr = _ROPE_ARRAYS[len(xs) - 1]()
     for i, (t, o) in enumerate(zip(xs, outs)):
-        if t.dim() != 4 or t.dtype != dtype or t.shape[0] != B or t.shape[2] != N or t.shape[3] != d:
+        b, h, n, width = t.shape
+        if b != B or n != N or width != d or t.dtype != dtype:
             raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
-        if o.shape != t.shape or o.dtype != dtype:
-            raise ValueError("out must have x's shape and dtype")
-        xs4, os4 = t.stride(), o.stride()
-        if xs4[3] != 1 or os4[3] != 1:
+        sb, sh, sn, last = t.stride()
+        if out is None:
+            at = (h * N * d, N * d, d)
+        else:
+            if o.shape != t.shape or o.dtype != dtype:
+                raise ValueError("out must have x's shape and dtype")
+            *at, out_last = o.stride()
+            last = max(last, out_last)
+        if last != 1:
             raise ValueError("the last dimension must be contiguous")
-        arr[i] = _RopeTensor(t.data_ptr(), o.data_ptr(), t.shape[1], xs4[:3], os4[:3])
+        arr[i] = (t.data_ptr(), o.data_ptr(), h, (sb, sh, sn), tuple(at))
     pad = (0,) * (4 - len(dims))
     if positions is not None:
         if positions.dtype != torch.int32 or tuple(positions.shape) not in ((N, len(dims)), (B, N, len(dims))):
@@ -522,7 +533,7 @@ def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = Non
     desc = _RopeDesc(B, N, d, _ROPE_DTYPES[dtype], len(dims), (*dims, *pad), int(bool(halves)),
                      int(bool(inverse)), float(theta), *where)
     _check(lib().tsr_rope(ctypes.byref(desc), arr, len(xs), _stream_ptr(stream)))
-    return outs[0] if isinstance(x, torch.Tensor) else outs
+    return outs[0] if one else list(outs)
 
 
 def tsr_rope_backward(dout, axis_dims, **kw):

@@ -532,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl.tmem_base;
+  grid_wait();              // the rows' statistics
   const int32_t b = blockIdx.x;
   if (b < p.n_key_items) roles<D, true>(p, ctrl, base, tmem, b, warp, lane);
   else roles<D, false>(p, ctrl, base, tmem, b - p.n_key_items, warp, lane);
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(256) bwd_stats_kernel(const uint4* __restrict_
   constexpr int VR = D / 8;
   const int64_t row = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / VR;
   const int v = threadIdx.x % VR;
+  grid_launch_dependents();
   if (row >= rows_p) return;       // whole groups of VR lanes leave together
   const int64_t bh = row / Np;
   const int32_t i = static_cast<int32_t>(row - bh * Np);
@@ -605,8 +607,7 @@ tsr_status launch(const Params& prm, int64_t ctas, int device, cudaStream_t st) 
     TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
     if (device >= 0 && device < 64) attr_set[device] = true;
   }
-  kern<<<static_cast<unsigned>(ctas), kThreads, C::SMEM, st>>>(prm);
-  TSR_CUDA(cudaGetLastError());
+  TSR_CUDA(launch_dependent(kern, static_cast<unsigned>(ctas), kThreads, C::SMEM, st, prm));
   return TSR_OK;
 }
 

@@ -217,6 +217,25 @@ bool encode_tmap_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t r
 
 int num_sms(int device);
 
+// Launch a kernel that may start while the stream's previous kernel finishes
+// (programmatic dependent launch): it has to call grid_wait() before it touches
+// anything that kernel reads or writes.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                             A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<A&&>(args)...);
+}
+
 }  // namespace tsr
 
 struct tsr_plan_s : tsr::tsr_plan_impl {};

@@ -12,7 +12,7 @@
 // fp32 sums do not resolve, so the selection is made exact in two steps.  The
 // means are sums with a running error term (two-sum), about 48 bits.  The scores
 // come from the tensor cores with each mean split into two bf16 terms (three
-// products; error at most kScoreErr * |qm_i| |km_j|), and any block whose score
+// products; error about 3e-5 |qm_i| |km_j|, below), and any block whose score
 // is within twice that error of the last kept one is scored again from the 48-bit
 // means with error terms; the order of those decides.  A row has two or so such
 // blocks, where scoring everything in fp64 would cost 1.3 ms for a 480p layer at
@@ -30,11 +30,15 @@ namespace tsr {
 
 namespace {
 
-// |approximate score - score| <= kScoreErr |qm| |km| (Cauchy-Schwarz over d):
-// a bf16 term is off by 2^-8 of its value at most, two terms by 2^-16, so the
-// dropped products are at most 3 * 2^-16; 24 accumulations of 16 products in
-// fp32, truncating, add less than 24 * 2^-22.  Together 5.2e-5.
-constexpr float kScoreErr = 1e-4f;
+// Fast scores.  A mean x is split as x = h + l + r, h = bf16(x), l = bf16(x - h).
+// The tensor cores sum h h', h l' and l h' in fp32, so a score is off by at most
+//     |r| |x'| + |x| |r'| + |l| |l'|                (Cauchy-Schwarz over d)
+//     + kSumErr |x| |x'|
+// with the norms of both blocks' parts, which pool_kernel takes.  The last term: an
+// MMA adds 16 products and the sum so far, each cut no higher than 2^-23 of the
+// largest, so the 8 MMAs of h h' are off by 8 * 17 * 2^-23 = 1.6e-5 at most, and the
+// other chain's terms are 2^-8 of these.
+constexpr float kSumErr = 2e-5f;
 
 constexpr int kPoolThreads = 128;
 constexpr int kSelThreads = 256;
@@ -45,7 +49,7 @@ struct PoolParams {
   const uint4* x[2];            // Q and K
   float* hi[2];                 // block means [B*H][blocks][d], high and low parts
   float* lo[2];
-  float* norm[2];               // |mean| [B*H][blocks]
+  float4* norm[2];              // |x|, |l|, |r| of the means [B*H][blocks]
   // the means' two bf16 terms in the order of the MMA fragments: [B*H][blocks / 8]
   // [d / 16][32] of {hi(c, c+1), lo(c, c+1), hi(c+2, c+3), lo(c+2, c+3)}, lane 4 g + t
   // holding row g's channels c = 16 kk + 4 t.  (Which channels make a k index is free
@@ -101,6 +105,7 @@ __global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_cons
   constexpr int VR = D / 8, RPW = 32 / VR, WARPS = kPoolThreads / 32;   // RPW rows per warp load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t unit = SHARED ? blockIdx.x : blockIdx.x * static_cast<int64_t>(WARPS) + warp;
+  grid_launch_dependents();      // select_kernel's blocks take the room of the last of these
   if (unit >= p.n_units) return;
   const int w = unit >= p.first_k ? 1 : 0;
   const int64_t u = unit - (w ? p.first_k : 0);
@@ -191,31 +196,48 @@ __global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_cons
     *reinterpret_cast<float2*>(p.hi[w] + o) = make_float2(hi[0], hi[1]);
     *reinterpret_cast<float2*>(p.lo[w] + o) = make_float2(lo[0], lo[1]);
   }
-  {
-    // a lane's channels are 4 (d = 128) or 2 (d = 64) of a fragment's
-    const int c = (lane % VR) * 8 + g * CH;
-    const int64_t at = ((bh * (p.frag_rows[w] / 8) + blk / 8) * (D / 16) + c / 16) * 32 + (blk % 8) * 4 + (c % 16) / 4;
-    uint2 t[CH / 2];
+  // the two bf16 terms; l and r for the norms
+  const int c0 = (lane % VR) * 8 + g * CH;      // 4 (d = 128) or 2 (d = 64) of a fragment's channels
+  const int64_t at = ((bh * (p.frag_rows[w] / 8) + blk / 8) * (D / 16) + c0 / 16) * 32 + (blk % 8) * 4 + (c0 % 16) / 4;
+  uint2 t[CH / 2];
+  float ll[CH], rr[CH];
 #pragma unroll
-    for (int i = 0; i < CH / 2; ++i) split2(make_float2(hi[2 * i], hi[2 * i + 1]), t[i].x, t[i].y);
-    if constexpr (CH == 4) p.frag[w][at] = make_uint4(t[0].x, t[0].y, t[CH / 2 - 1].x, t[CH / 2 - 1].y);
-    else reinterpret_cast<uint2*>(p.frag[w] + at)[(c % 4) / 2] = t[0];
+  for (int i = 0; i < CH / 2; ++i) {
+    split2(make_float2(hi[2 * i], hi[2 * i + 1]), t[i].x, t[i].y);
+    ll[2 * i] = bf16_lo(t[i].y);
+    ll[2 * i + 1] = bf16_hi(t[i].y);
+    rr[2 * i] = hi[2 * i] - bf16_lo(t[i].x) - ll[2 * i] + lo[2 * i];
+    rr[2 * i + 1] = hi[2 * i + 1] - bf16_hi(t[i].x) - ll[2 * i + 1] + lo[2 * i + 1];
   }
-  // |mean|, over the largest component so that small means do not vanish squared
+  if constexpr (CH == 4) p.frag[w][at] = make_uint4(t[0].x, t[0].y, t[CH / 2 - 1].x, t[CH / 2 - 1].y);
+  else reinterpret_cast<uint2*>(p.frag[w] + at)[(c0 % 4) / 2] = t[0];
+  // norms over the largest component, so that small means do not vanish squared
 #pragma unroll
   for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
   m = fmaxf(m, FLT_MIN);
   const float over = 1.f / m;
-  float n2 = 0.f;
+  float n2 = 0.f, l2 = 0.f, r2 = 0.f;
 #pragma unroll
-  for (int c = 0; c < CH; ++c) n2 = fmaf(hi[c] * over, hi[c] * over, n2);
+  for (int c = 0; c < CH; ++c) {
+    n2 = fmaf(hi[c] * over, hi[c] * over, n2);
+    l2 = fmaf(ll[c] * over, ll[c] * over, l2);
+    r2 = fmaf(rr[c] * over, rr[c] * over, r2);
+  }
 #pragma unroll
-  for (int x = 16; x; x >>= 1) n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, x);
-  if (lane == 0) p.norm[w][u] = sqrtf(n2) * m * 1.0001f;     // NaN where a mean is
+  for (int x = 16; x; x >>= 1) {
+    n2 += __shfl_xor_sync(0xFFFFFFFFu, n2, x);
+    l2 += __shfl_xor_sync(0xFFFFFFFFu, l2, x);
+    r2 += __shfl_xor_sync(0xFFFFFFFFu, r2, x);
+  }
+  if (lane == 0) {                              // NaN where a mean is
+    const float f = m * 1.0001f;
+    p.norm[w][u] = make_float4(sqrtf(n2) * f, sqrtf(l2) * f, sqrtf(r2) * f, 0.f);
+  }
 }
 
 struct SelParams {
-  const float *q_hi, *q_lo, *k_hi, *k_lo, *q_norm, *k_norm;
+  const float *q_hi, *q_lo, *k_hi, *k_lo;
+  const float4 *q_norm, *k_norm;
   const uint4 *q_frag, *k_frag;
   int32_t q_frag_rows, k_frag_rows;
   float* scores;        // [CTA][kStrip][pitch] when the strip does not fit shared memory
@@ -268,11 +290,11 @@ __device__ __forceinline__ void two_sum1(float& s, float& e, float x) {
 // (fp64 runs at two lanes a clock per SM here.)
 template <int D>
 __device__ __forceinline__ uint64_t exact_keys(const float* qh, const float* ql, float q_norm, const float* kh,
-                                               const float* kl, const float* k_norm, int j, int lane) {
+                                               const float* kl, const float4* k_norm, int j, int lane) {
   double q_back, k_back;
   const bool on = j >= 0;
   const int64_t o = static_cast<int64_t>(on ? j : 0);
-  const float q_scale = scale_of(q_norm, q_back), k_scale = scale_of(__ldg(k_norm + o), k_back);
+  const float q_scale = scale_of(q_norm, q_back), k_scale = scale_of(__ldg(&k_norm[o].x), k_back);
   float s = 0.f, e = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
@@ -324,7 +346,7 @@ __device__ __forceinline__ uint32_t kth_key(int n, int want, int lane, In in, Ke
 // KPL > 0: nk <= 32 KPL, the scores in registers, score m * 32 + lane in v[m];
 // KPL = 0: any nk, read again where needed.
 template <int D, int KPL>
-__device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i, float* row, float k_max, int lane) {
+__device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i, float* row, float3 k_max, int lane) {
   uint8_t* out = p.blocks + (bh * p.nq + i) * p.nk;
   // forced blocks: [0, first) and, with `diagonal`, [d_lo, d_hi), the key blocks
   // that share a token with the query block
@@ -345,9 +367,11 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
     return;
   }
   // the last two terms cover values that the bf16 terms or their products flush
-  const float q_norm = __ldg(p.q_norm + bh * p.nq + i);
-  const float err2 = 2.f * (kScoreErr * (q_norm * k_max) + 4e-37f * (q_norm + k_max) + 1e-36f);
-  bool finite = q_norm * k_max <= FLT_MAX && err2 <= FLT_MAX;
+  const float4 qn = __ldg(p.q_norm + bh * p.nq + i);
+  const float q_norm = qn.x;
+  const float err2 = 2.002f * (kSumErr * (q_norm * k_max.x) + qn.z * k_max.x + q_norm * k_max.z + qn.y * k_max.y +
+                               4e-37f * (q_norm + k_max.x) + 1e-36f);
+  bool finite = q_norm * k_max.x <= FLT_MAX && err2 <= FLT_MAX;
   // with finite norms every score is finite; forced blocks and those past nk hold
   // -inf and are never counted (a row has room for whole chunks of 32)
   constexpr int REGS = KPL > 0 ? KPL : 1;
@@ -365,24 +389,41 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   auto val = [&](int m) -> float { return KPL > 0 ? v[KPL > 0 ? m : 0] : load(m); };
   float above = INFINITY, below = -INFINITY;    // kept for sure above, dropped for sure below
   if (finite) {
-    float vmin = INFINITY, vmax = -INFINITY;
+    float vmin = INFINITY, vmax = -INFINITY, s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int m = 0; m < chunks; ++m) {
       const float x = val(m);
+      const bool real = x != -INFINITY;
       vmax = fmaxf(vmax, x);
-      vmin = fminf(vmin, x == -INFINITY ? INFINITY : x);
+      vmin = fminf(vmin, real ? x : INFINITY);
+      const float y = real ? x : 0.f;
+      s1 += y;
+      s2 = fmaf(y, y, s2);
     }
     const uint32_t kmin = __reduce_min_sync(0xFFFFFFFFu, key32(vmin));
     const uint32_t kmax = __reduce_max_sync(0xFFFFFFFFu, key32(vmax));
     // the want-th largest lies in [lo, hi]: c_lo = count(>= lo) >= want, c_hi =
-    // count(> hi) < want.  Narrowed, by interpolating the counts and every third
-    // time by halving, until the bracket is inside the fast bound or exactly `want`
-    // are above (then it is the smallest of those).
+    // count(> hi) < want.  Narrowed until the bracket is inside the fast bound or
+    // exactly `want` are above (then it is the smallest of those): first at the
+    // quantile of a normal distribution with the row's mean and deviation, then a
+    // step by its density there, then by interpolating the counts and every third
+    // time by halving, which ends for any distribution.
     float lo = unkey32(kmin), hi = unkey32(kmax);
     float c_lo = static_cast<float>(others), c_hi = 0.f;
-    for (int turn = 0; hi - lo > 0.25f * err2; turn = turn == 2 ? 0 : turn + 1) {
-      const float f = turn == 2 ? 0.5f : __fdividef(c_lo - static_cast<float>(want) + 0.5f, c_lo - c_hi);
-      float mid = lo + f * (hi - lo);
+    const float n_want = static_cast<float>(want);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) {
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, x);
+      s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, x);
+    }
+    const float mean = s1 / c_lo, dev = sqrtf(fmaxf(s2 / c_lo - mean * mean, 0.f));
+    const float z = normcdfinvf(1.f - (n_want - 0.5f) / c_lo);
+    float guess = mean + z * dev;
+    const float per_count = dev * 2.5066283f * __expf(0.5f * z * z) / c_lo;   // 1 / density
+    for (int turn = 0; hi - lo > 0.25f * err2; turn = turn == 4 ? 2 : turn + 1) {
+      float mid = guess;
+      if (turn >= 2)
+        mid = lo + (turn == 4 ? 0.5f : __fdividef(c_lo - n_want + 0.5f, c_lo - c_hi)) * (hi - lo);
       if (!(mid > lo && mid < hi)) mid = lo + 0.5f * (hi - lo);
       if (!(mid > lo && mid < hi)) break;
       int c = 0;
@@ -396,6 +437,7 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
         lo = hi = unkey32(__reduce_min_sync(0xFFFFFFFFu, key32(low)));
         break;
       }
+      guess = mid + (static_cast<float>(c) - n_want + 0.5f) * per_count;
       if (c > want) {
         lo = mid;
         c_lo = static_cast<float>(c);
@@ -541,17 +583,24 @@ __global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(c
   const int64_t bh = blockIdx.x / p.strips;
   const int i0 = static_cast<int>(blockIdx.x - bh * p.strips) * kStrip;
   float* sc = p.scores ? p.scores + static_cast<int64_t>(blockIdx.x) * kStrip * p.pitch : smem;
-  __shared__ float k_max_w[kSelThreads / 32];
+  __shared__ float3 k_max_w[kSelThreads / 32];
+  grid_wait();
 
-  // the largest |km| of the head (NaN counts as infinite)
-  float km = 0.f;
+  // the head's largest norms of the key blocks' parts (NaN counts as infinite)
+  float3 km = make_float3(0.f, 0.f, 0.f);
   for (int j = threadIdx.x; j < p.nk; j += kSelThreads) {
-    const float x = __ldg(p.k_norm + bh * p.nk + j);
-    km = x <= FLT_MAX ? fmaxf(km, x) : INFINITY;
-    if (km > FLT_MAX) break;
+    const float4 x = __ldg(p.k_norm + bh * p.nk + j);
+    km.x = x.x <= FLT_MAX ? fmaxf(km.x, x.x) : INFINITY;
+    if (km.x > FLT_MAX) break;
+    km.y = fmaxf(km.y, x.y);
+    km.z = fmaxf(km.z, x.z);
   }
 #pragma unroll
-  for (int m = 16; m; m >>= 1) km = fmaxf(km, __shfl_xor_sync(0xFFFFFFFFu, km, m));
+  for (int m = 16; m; m >>= 1) {
+    km.x = fmaxf(km.x, __shfl_xor_sync(0xFFFFFFFFu, km.x, m));
+    km.y = fmaxf(km.y, __shfl_xor_sync(0xFFFFFFFFu, km.y, m));
+    km.z = fmaxf(km.z, __shfl_xor_sync(0xFFFFFFFFu, km.z, m));
+  }
   if (lane == 0) k_max_w[warp] = km;
 
   // ---- scores: every warp takes the strip's 16 query blocks, whose A fragments
@@ -597,9 +646,10 @@ __global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(c
     }
   }
   __syncthreads();
-  float k_max = k_max_w[0];
+  float3 k_max = k_max_w[0];
 #pragma unroll
-  for (int w = 1; w < kSelThreads / 32; ++w) k_max = fmaxf(k_max, k_max_w[w]);
+  for (int w = 1; w < kSelThreads / 32; ++w)
+    k_max = make_float3(fmaxf(k_max.x, k_max_w[w].x), fmaxf(k_max.y, k_max_w[w].y), fmaxf(k_max.z, k_max_w[w].z));
   for (int rr = warp; rr < kStrip && i0 + rr < p.nq; rr += kSelThreads / 32)
     select_row<D, KPL>(p, bh, i0 + rr, sc + rr * p.pitch, k_max, lane);
 }
@@ -638,8 +688,8 @@ Layout layout_of(const tsr_select_desc& s) {
   l.q_lo = take(BH * l.nq * s.d);
   l.k_hi = take(BH * l.nk * s.d);
   l.k_lo = take(BH * l.nk * s.d);
-  l.q_norm = take(BH * l.nq);
-  l.k_norm = take(BH * l.nk);
+  l.q_norm = take(BH * l.nq * 4);
+  l.k_norm = take(BH * l.nk * 4);
   l.q_frag_rows = (l.nq + 7) / 8 * 8;
   l.k_frag_rows = (l.nk + 7) / 8 * 8;
   l.q_frag = take(BH * l.q_frag_rows * s.d);
@@ -659,8 +709,7 @@ tsr_status launch_strips(const SelParams& sp, unsigned ctas, size_t smem, cudaSt
     TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripBytes));
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  kern<<<ctas, kSelThreads, smem, st>>>(sp);
-  TSR_CUDA(cudaGetLastError());
+  TSR_CUDA(launch_dependent(kern, ctas, kSelThreads, smem, st, sp));
   return TSR_OK;
 }
 
@@ -674,10 +723,10 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   pp.x[1] = static_cast<const uint4*>(k);
   pp.hi[0] = f(l.q_hi);
   pp.lo[0] = f(l.q_lo);
-  pp.norm[0] = f(l.q_norm);
+  pp.norm[0] = reinterpret_cast<float4*>(ws + l.q_norm);
   pp.hi[1] = f(l.k_hi);
   pp.lo[1] = f(l.k_lo);
-  pp.norm[1] = f(l.k_norm);
+  pp.norm[1] = reinterpret_cast<float4*>(ws + l.k_norm);
   pp.frag[0] = reinterpret_cast<uint4*>(ws + l.q_frag);
   pp.frag[1] = reinterpret_cast<uint4*>(ws + l.k_frag);
   pp.frag_rows[0] = l.q_frag_rows;
