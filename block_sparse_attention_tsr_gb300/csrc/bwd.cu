@@ -14,24 +14,31 @@
 // pass with atomics on dQ would take 5.  The lists come from two plans of the
 // forward's planner: the mask's own and its transpose's, 128-row tiles 64 wide.
 //
-// Both kinds run the same kernel: 128 stationary rows X1, X2 in shared memory (K, V
-// or Q, dO) against a stream of 128-row steps Y1, Y2 (Q, dO or K, V), a step being
-// two tiles of the list, not necessarily neighbours:
+// Both kinds work alike: 128 stationary rows X1, X2 in shared memory (K, V or Q, dO)
+// against a stream of 128-row steps Y1, Y2 (Q, dO or K, V), a step being two tiles of
+// the list, not necessarily neighbours:
 //     S = X1 Y1^T, dP = X2 Y2^T;   acc1 += dS Y1;   key items: acc2 += P Y2
 // so the softmax sees S with the stationary rows on the TMEM lanes.  P and dS are
 // rounded to bf16, the operand type of the second products, and written over S
-// and dP in TMEM (512 columns: S, dP and the two accumulators of d).
+// and dP in TMEM.
 //
-// Two threads issue, because the pipe runs dry while a lone issuer waits on a
-// barrier: one S(j+1) right after acc2(j) (which frees P's columns), the other
-// dP(j+1) right after acc1(j).  The softmax turns S(j+1) into P while the pipe runs
-// acc1(j) and dP(j+1), and dP(j+1) into dS while it runs acc2(j+1) and S(j+2).
-// Query items have TMEM to spare for a second dP, so dP(j+1) runs before acc1(j).
-//   warps 0..15 softmax: row = TMEM lane, four warps for each 32 of the step's 128
-//               columns; then the epilogue
-//   warp 16     producer: TMA tiles and the rows' statistics
-//   warps 17, 18 MMA issuers
-// Every wait is bounded: on expiry the error word is set and the kernel winds down.
+// Two threads issue MMAs, because the pipe runs dry while a lone issuer waits on a
+// barrier (a step took 3,635 clocks against 2,240 of MMAs): one S and acc2, the other
+// dP and acc1.  MMAs of one thread run in issue order, so a product may overwrite
+// columns that the thread's previous product reads.
+//
+// The 512 TMEM columns decide how far S and dP run ahead of the softmax:
+//   query items         S is free once the softmax holds it in registers; two dP
+//   key items, d = 64   two S (acc2 has to read P before an S may overwrite it), one dP
+//   key items, d = 128  the accumulators leave 256: one dP, and S in two halves of 64
+//                       columns, one per tile, each with its own eight softmax warps,
+//                       so that one half's acc2 and next S run during the other's
+//                       softmax.  (Half-wide S products cost as much as whole ones;
+//                       a whole S waits out the softmax, and half-wide dP as well
+//                       cost more than it gained.)
+// Warps: 16 softmax (row = TMEM lane, 32 columns each), which also store the
+// gradients, a producer (TMA tiles, the rows' statistics) and the two issuers.  Every
+// wait is bounded: on expiry the error word is set and the kernel winds down.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -62,33 +69,34 @@ struct Params {
   float scale_log2, scale;
 };
 
-template <int D>
+// Shared memory and TMEM of an item.
+template <int D, bool KEYS>
 struct Cfg {
-  // Y1 is read by the first product of a step and again by the last, one step
-  // later, so it gets a stage more than Y2 where shared memory is short
+  // Y1 is read by the first product of a step and again by the last, one step later,
+  // so it gets a stage more than Y2 where shared memory is short
   static constexpr int S1 = D == 128 ? 3 : 4, S2 = D == 128 ? 2 : 4;
   static constexpr int TILE = 128 * D * 2;          // one 128-row operand
   static constexpr int STAT = 2 * 128 * 4;          // -lse2 and -delta of a step's rows
   static constexpr int X1 = 0, X2 = TILE, Y1 = 2 * TILE, Y2 = Y1 + S1 * TILE, ST = Y2 + S2 * TILE;
   static constexpr int CTRL = ST + 2 * STAT;
   static constexpr int SMEM = CTRL + 512;
-  // TMEM columns.  Key items: S, dP, dK, dV.  Query items have one accumulator and
-  // room for a second dP.
-  static constexpr int S_COL = 0, DP_COL = 128, A1_COL = 256, A2_COL = 256 + D;
-  static constexpr int DPQ_COL = 128, AQ_COL = 384;
-  static constexpr int TMEM_COLS = 512;
+  // TMEM: S and dP buffers, then the accumulators
+  static constexpr int N_S = KEYS && D == 64 ? 2 : 1, N_DP = KEYS ? 1 : 2;
+  static constexpr int S_COL = 0, DP_COL = N_S * 128, A1_COL = DP_COL + N_DP * 128, A2_COL = A1_COL + D;
+  static_assert((KEYS ? A2_COL : A1_COL) + D <= 512, "TMEM");
   static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
   static constexpr uint32_t IDESC_A = idesc_bf16(128, D, false, true);
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // more than half an SM: one CTA per SM, so the 512 TMEM columns are free at launch
   static_assert(SMEM > 114 * 1024, "one CTA per SM");
 };
+constexpr int kTmemCols = 512;
 
 struct alignas(8) Ctrl {
   uint64_t x1_full, x2_full;
   uint64_t y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
   uint64_t st_full[2], st_empty[2];
-  uint64_t s_full, p_full, dp_full[2], ds_full[2], acc_full;
+  uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2], acc_full;
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -159,10 +167,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// Softmax warps.  A warp takes 32 rows and 32 columns of every step.
 template <int D, bool KEYS>
 __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int4 it,
                                              const int2* entries, const uint4* descs, int warp, int lane) {
-  using C = Cfg<D>;
+  using C = Cfg<D, KEYS>;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
   const int grp = warp >> 2;               // columns [32 grp, +32) of the step
   const int part = grp >> 1, sub = grp & 1;
@@ -171,7 +180,6 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
   const int32_t n = it.w - it.z, steps = (n + 1) / 2;
   const int64_t row = static_cast<int64_t>(it.y) * 128 + r;
   const bool valid = row < p.N;
-  const uint32_t s_col = tmem + lanes + C::S_COL + 32 * grp;
   float nlse = 0.f, ndelta = 0.f;
   if (!KEYS) {
     nlse = valid ? __ldg(p.nlse2 + static_cast<int64_t>(it.x) * p.Np + row) : -INFINITY;
@@ -201,12 +209,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
     // has no arithmetic to do, one whose rows see everything no masking
     const bool none = __all_sync(0xFFFFFFFFu, allowed == 0u);
     const bool mixed = !__all_sync(0xFFFFFFFFu, allowed == 0xFFFFFFFFu);
+    const int ab = j & 1;                    // barriers alternate
+    const uint32_t phase = (j >> 1) & 1;
+    const uint32_t s_col = tmem + lanes + C::S_COL + 32 * grp + (C::N_S == 2 ? 128 * (j & 1) : 0);
+    const uint32_t dp_col = tmem + lanes + C::DP_COL + 32 * grp + (C::N_DP == 2 ? 128 * (j & 1) : 0);
     const uint32_t st = base + C::ST + (j & 1) * C::STAT + grp * 128;   // [-lse2 128][-delta 128]
-    const uint32_t dp_col = tmem + lanes + (KEYS ? C::DP_COL : C::DPQ_COL + 128 * (j & 1)) + 32 * grp;
     if (KEYS) {
-      if (!mbar_wait(smem_u32(&ctrl.st_full[j & 1]), (j >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
+      if (!mbar_wait(smem_u32(&ctrl.st_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
     }
-    if (!mbar_wait(smem_u32(&ctrl.s_full), j & 1, abort_flag, p.err)) { ok = false; break; }
+    if (!mbar_wait(smem_u32(&ctrl.s_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
     tc_fence_after();
     uint32_t x[32];                          // S, then P, as float bits
     if (!none) {
@@ -214,10 +225,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       tc_wait_ld();
     }
     if (!KEYS) {
-      // S is in registers: its columns are free for the next step
+      // S is in registers: its columns are free for the next product
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full));
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full[ab]));
     }
     if (!none) {
 #pragma unroll
@@ -247,9 +258,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full));
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full[ab]));
     }
-    if (!mbar_wait(smem_u32(&ctrl.dp_full[j & 1]), (j >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
+    if (!mbar_wait(smem_u32(&ctrl.dp_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
     tc_fence_after();
     if (on) {
       uint32_t pk[16];
@@ -288,20 +299,20 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(smem_u32(&ctrl.ds_full[j & 1]));
-      if (KEYS) mbar_arrive(smem_u32(&ctrl.st_empty[j & 1]));
+      mbar_arrive(smem_u32(&ctrl.ds_full[ab]));
+      if (KEYS) mbar_arrive(smem_u32(&ctrl.st_empty[ab]));
     }
   }
   // ---- epilogue: a quarter of the columns of each accumulator
   constexpr int W = D / 4;
-  if (ok && steps > 0) {
+  if (ok && n > 0) {
     if (mbar_wait(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err)) {
       tc_fence_after();
 #pragma unroll
       for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
         __nv_bfloat16* out = KEYS ? (w ? p.dv : p.dk) : p.dq;
         const float f = w ? 1.f : p.scale;
-        const uint32_t col = tmem + lanes + (KEYS ? (w ? C::A2_COL : C::A1_COL) : C::AQ_COL) + grp * W;
+        const uint32_t col = tmem + lanes + (w ? C::A2_COL : C::A1_COL) + grp * W;
         uint4* dst =
             reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + (valid ? row : 0)) * D + grp * W);
 #pragma unroll
@@ -335,7 +346,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
 template <int D, bool KEYS>
 __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint32_t base, int4 it,
                                               const int2* entries) {
-  using C = Cfg<D>;
+  using C = Cfg<D, KEYS>;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
   const int32_t n = it.w - it.z, steps = (n + 1) / 2, bh = it.x;
   const CUtensorMap *x1 = KEYS ? &p.tk : &p.tq, *x2 = KEYS ? &p.tv : &p.tdo;
@@ -359,10 +370,13 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
     const int32_t k0 = __ldg(&entries[it.z + 2 * j]).x;
     const int32_t k1 = parts == 2 ? __ldg(&entries[it.z + 2 * j + 1]).x : 0;
     const int a = j % C::S1, b = j % C::S2;
+    auto stream = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar) {
+      mbar_arrive_expect_tx(smem_u32(bar), parts * (C::TILE / 2));
+      tile(map, dst, 0, k0, smem_u32(bar));
+      if (parts == 2) tile(map, dst, 1, k1, smem_u32(bar));
+    };
     if (!mbar_wait(smem_u32(&ctrl.y1_empty[a]), ((j / C::S1) & 1) ^ 1, abort_flag, p.err)) break;
-    mbar_arrive_expect_tx(smem_u32(&ctrl.y1_full[a]), parts * (C::TILE / 2));
-    tile(y1, base + C::Y1 + a * C::TILE, 0, k0, smem_u32(&ctrl.y1_full[a]));
-    if (parts == 2) tile(y1, base + C::Y1 + a * C::TILE, 1, k1, smem_u32(&ctrl.y1_full[a]));
+    stream(y1, base + C::Y1 + a * C::TILE, &ctrl.y1_full[a]);
     ++i1;
     if (KEYS) {
       const uint32_t bar = smem_u32(&ctrl.st_full[j & 1]), dst = base + C::ST + (j & 1) * C::STAT;
@@ -382,9 +396,7 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
       x2_issued = true;
     }
     if (!mbar_wait(smem_u32(&ctrl.y2_empty[b]), ((j / C::S2) & 1) ^ 1, abort_flag, p.err)) break;
-    mbar_arrive_expect_tx(smem_u32(&ctrl.y2_full[b]), parts * (C::TILE / 2));
-    tile(y2, base + C::Y2 + b * C::TILE, 0, k0, smem_u32(&ctrl.y2_full[b]));
-    if (parts == 2) tile(y2, base + C::Y2 + b * C::TILE, 1, k1, smem_u32(&ctrl.y2_full[b]));
+    stream(y2, base + C::Y2 + b * C::TILE, &ctrl.y2_full[b]);
     ++i2;
   }
   if (*abort_flag) {
@@ -402,15 +414,15 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
 }
 
 // The two MMA issuers.  FIRST owns S's columns: S, and acc2 (which reads P there).
-// The other owns dP's: dP, and acc1 (which reads dS there).  MMAs of one thread run
-// in issue order, so a product may overwrite columns that the thread's previous
-// product reads without waiting for it.
+// The other owns dP's: dP, and acc1 (which reads dS there).
 template <int D, bool KEYS, bool FIRST>
 __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int4 it) {
-  using C = Cfg<D>;
+  using C = Cfg<D, KEYS>;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
   const int32_t n = it.w - it.z, steps = (n + 1) / 2;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(smem_u32(bar), parity, abort_flag, p.err); };
+  // barriers of step j alternate, so that no phase runs two ahead of a waiter
+  auto done = [&](uint64_t (&b)[2], int32_t j) { return wait(&b[j & 1], (j >> 1) & 1); };
   // D[128 x 128] = X Y^T over d
   auto outer = [&](uint32_t col, uint32_t sx, uint32_t sy) {
     tc_fence_after();
@@ -421,7 +433,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
     }
   };
   // acc[128 x D] += A (bf16, TMEM) Y over the step's rows; P and dS lie 16 columns
-  // (32 rows of Y) per softmax group, 32 apart
+  // (32 rows of Y) per softmax warp, 32 apart
   auto inner = [&](uint32_t acc, uint32_t col, uint32_t sy, int32_t j) {
     tc_fence_after();
     const int kks = 2 * j + 1 < n ? 8 : 4;
@@ -435,24 +447,25 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
   auto y2 = [&](int32_t j) { return base + C::Y2 + (j % C::S2) * C::TILE; };
   auto y2_full = [&](int32_t j) { return wait(&ctrl.y2_full[j % C::S2], (j / C::S2) & 1); };
   if constexpr (FIRST) {
+    auto s_col = [&](int32_t j) { return static_cast<uint32_t>(C::S_COL + (C::N_S == 2 ? 128 * (j & 1) : 0)); };
     auto do_s = [&](int32_t j) -> bool {
       if (!wait(&ctrl.y1_full[j % C::S1], (j / C::S1) & 1)) return false;
-      outer(C::S_COL, base + C::X1, y1(j));
-      mma_commit(smem_u32(&ctrl.s_full));
+      outer(s_col(j), base + C::X1, y1(j));
+      mma_commit(smem_u32(&ctrl.s_full[j & 1]));
       return true;
     };
-    bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0);
+    bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && (C::N_S == 1 || steps == 1 || do_s(1));
     for (int32_t j = 0; ok && j < steps; ++j) {
       if (KEYS && !y2_full(j)) break;
-      if (!wait(&ctrl.p_full, j & 1)) break;
+      if (!done(ctrl.p_full, j)) break;
       if (KEYS) {
-        inner(C::A2_COL, C::S_COL, y2(j), j);
+        inner(C::A2_COL, s_col(j), y2(j), j);
         mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
       }
-      if (j + 1 < steps && !do_s(j + 1)) break;
+      if (j + C::N_S < steps && !do_s(j + C::N_S)) break;
     }
   } else {
-    auto dp_col = [&](int32_t j) { return KEYS ? C::DP_COL : C::DPQ_COL + 128 * (j & 1); };
+    auto dp_col = [&](int32_t j) { return static_cast<uint32_t>(C::DP_COL + (C::N_DP == 2 ? 128 * (j & 1) : 0)); };
     auto do_dp = [&](int32_t j) -> bool {
       if (!y2_full(j)) return false;
       outer(dp_col(j), base + C::X2, y2(j));
@@ -460,14 +473,16 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
       return true;
     };
-    bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0);
+    bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0) && (C::N_DP == 1 || steps == 1 || do_dp(1));
     for (int32_t j = 0; ok && j < steps; ++j) {
-      if (!KEYS && j + 1 < steps && !do_dp(j + 1)) break;
-      if (!wait(&ctrl.ds_full[j & 1], (j >> 1) & 1)) break;
+      if (!done(ctrl.ds_full, j)) break;
+      // one S and one dP: acc1 and dP(j+1) wait for S(j+1), so that the pipe works on
+      // them while the softmax has S(j+1) to work on, and on acc2 and S while it has dP
+      if (KEYS && C::N_S == 1 && j + 1 < steps && !done(ctrl.s_full, j + 1)) break;
       // Y1 has landed: S of this step was computed from it
-      inner(KEYS ? C::A1_COL : C::AQ_COL, dp_col(j), y1(j), j);
+      inner(C::A1_COL, dp_col(j), y1(j), j);
       mma_commit(smem_u32(&ctrl.y1_empty[j % C::S1]));
-      if (KEYS && j + 1 < steps && !do_dp(j + 1)) break;
+      if (j + C::N_DP < steps && !do_dp(j + C::N_DP)) break;
     }
   }
   // complete once everything that both threads issued has: the accumulators are
@@ -496,36 +511,31 @@ __device__ __forceinline__ void roles(const Params& p, Ctrl& ctrl, uint32_t base
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + C::CTRL);
+  Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + Cfg<D, true>::CTRL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool keys = static_cast<int32_t>(blockIdx.x) < p.n_key_items;
   if (base & 1023u) {       // swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(p.err, DEV_ERR_INTERNAL);
     return;
   }
   if (threadIdx.x == 0) {
-    for (uint64_t* b : {&ctrl.x1_full, &ctrl.x2_full, &ctrl.s_full, &ctrl.dp_full[0], &ctrl.dp_full[1]})
-      mbar_init(smem_u32(b), 1);
+    for (uint64_t* b : {&ctrl.x1_full, &ctrl.x2_full}) mbar_init(smem_u32(b), 1);
     mbar_init(smem_u32(&ctrl.acc_full), 2);
-    // a step's Y2 is released by dP and, for key items, by acc2
-    for (int i = 0; i < 4; ++i)
-      for (uint64_t* b : {&ctrl.y1_full[i], &ctrl.y1_empty[i], &ctrl.y2_full[i]})
-        mbar_init(smem_u32(b), 1);
-    for (int i = 0; i < 4; ++i)
-      mbar_init(smem_u32(&ctrl.y2_empty[i]), static_cast<int32_t>(blockIdx.x) < p.n_key_items ? 2 : 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctrl.st_full[i]), 1);
-      mbar_init(smem_u32(&ctrl.st_empty[i]), kSoftmaxWarps);
-      mbar_init(smem_u32(&ctrl.ds_full[i]), kSoftmaxWarps);
+    for (int i = 0; i < 4; ++i) {
+      for (uint64_t* b : {&ctrl.y1_full[i], &ctrl.y1_empty[i], &ctrl.y2_full[i]}) mbar_init(smem_u32(b), 1);
+      mbar_init(smem_u32(&ctrl.y2_empty[i]), keys ? 2 : 1);     // dP, and acc2 of key items
     }
-    mbar_init(smem_u32(&ctrl.p_full), kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) {
+      for (uint64_t* b : {&ctrl.s_full[i], &ctrl.dp_full[i], &ctrl.st_full[i]}) mbar_init(smem_u32(b), 1);
+      for (uint64_t* b : {&ctrl.p_full[i], &ctrl.ds_full[i], &ctrl.st_empty[i]}) mbar_init(smem_u32(b), kSoftmaxWarps);
+    }
     ctrl.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kSoftmaxWarps + 1) {
-    tmem_alloc(smem_u32(&ctrl.tmem_base), C::TMEM_COLS);
+    tmem_alloc(smem_u32(&ctrl.tmem_base), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -534,13 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   const uint32_t tmem = ctrl.tmem_base;
   grid_wait();              // the rows' statistics
   const int32_t b = blockIdx.x;
-  if (b < p.n_key_items) roles<D, true>(p, ctrl, base, tmem, b, warp, lane);
+  if (keys) roles<D, true>(p, ctrl, base, tmem, b, warp, lane);
   else roles<D, false>(p, ctrl, base, tmem, b - p.n_key_items, warp, lane);
   tc_fence_before();
   __syncthreads();
   if (warp == kSoftmaxWarps + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -600,14 +610,13 @@ __global__ void transpose_blocks_kernel(const uint8_t* __restrict__ src, uint8_t
 
 template <int D>
 tsr_status launch(const Params& prm, int64_t ctas, int device, cudaStream_t st) {
-  using C = Cfg<D>;
   auto kern = bsa_bwd_kernel<D>;
   static bool attr_set[64] = {false};
   if (device < 0 || device >= 64 || !attr_set[device]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, true>::SMEM));
     if (device >= 0 && device < 64) attr_set[device] = true;
   }
-  TSR_CUDA(launch_dependent(kern, static_cast<unsigned>(ctas), kThreads, C::SMEM, st, prm));
+  TSR_CUDA(launch_dependent(kern, static_cast<unsigned>(ctas), kThreads, Cfg<D, true>::SMEM, st, prm));
   return TSR_OK;
 }
 
