@@ -129,6 +129,37 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
       : "f"(b0), "f"(b1));
 }
 
+// The issuers run whole warps, one lane of which issues: addresses and descriptors
+// then stay in the warp's uniform registers, where the MMA wants them.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t elect, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t elect, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t elect, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(elect)
+      : "memory");
+}
+
 // Allowed columns [32 sub, 32 sub + 32) of row r of a 64-wide boundary tile (grid
 // descriptor).  The segment counts are the same for the whole warp, so the loops
 // end early; most tiles have one column segment and need no ranges.
@@ -420,7 +451,10 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
   using C = Cfg<D, KEYS>;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
   const int32_t n = it.w - it.z, steps = (n + 1) / 2;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(smem_u32(bar), parity, abort_flag, p.err); };
+  const uint32_t elect = elect_lane();
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity, abort_flag, p.err));
+  };
   // barriers of step j alternate, so that no phase runs two ahead of a waiter
   auto done = [&](uint64_t (&b)[2], int32_t j) { return wait(&b[j & 1], (j >> 1) & 1); };
   // D[128 x 128] = X Y^T over d
@@ -429,7 +463,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t o = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
-      mma_bf16_ss(tmem + col, sdesc_sw128(sx + o, 16, 1024), sdesc_sw128(sy + o, 16, 1024), C::IDESC_S, kk > 0);
+      mma_ss(elect, tmem + col, sdesc_sw128(sx + o, 16, 1024), sdesc_sw128(sy + o, 16, 1024), C::IDESC_S, kk > 0);
     }
   };
   // acc[128 x D] += A (bf16, TMEM) Y over the step's rows; P and dS lie 16 columns
@@ -440,7 +474,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
       if (kk < kks)
-        mma_bf16_ts(tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8,
+        mma_ts(elect, tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8,
                     sdesc_sw128(sy + kk * 16 * 128, 128 * 128, 1024), C::IDESC_A, (j > 0 || kk > 0) ? 1u : 0u);
   };
   auto y1 = [&](int32_t j) { return base + C::Y1 + (j % C::S1) * C::TILE; };
@@ -451,7 +485,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
     auto do_s = [&](int32_t j) -> bool {
       if (!wait(&ctrl.y1_full[j % C::S1], (j / C::S1) & 1)) return false;
       outer(s_col(j), base + C::X1, y1(j));
-      mma_commit(smem_u32(&ctrl.s_full[j & 1]));
+      commit(elect, smem_u32(&ctrl.s_full[j & 1]));
       return true;
     };
     bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && (C::N_S == 1 || steps == 1 || do_s(1));
@@ -460,7 +494,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       if (!done(ctrl.p_full, j)) break;
       if (KEYS) {
         inner(C::A2_COL, s_col(j), y2(j), j);
-        mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
+        commit(elect, smem_u32(&ctrl.y2_empty[j % C::S2]));
       }
       if (j + C::N_S < steps && !do_s(j + C::N_S)) break;
     }
@@ -469,8 +503,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
     auto do_dp = [&](int32_t j) -> bool {
       if (!y2_full(j)) return false;
       outer(dp_col(j), base + C::X2, y2(j));
-      mma_commit(smem_u32(&ctrl.dp_full[j & 1]));
-      mma_commit(smem_u32(&ctrl.y2_empty[j % C::S2]));
+      commit(elect, smem_u32(&ctrl.dp_full[j & 1]));
+      commit(elect, smem_u32(&ctrl.y2_empty[j % C::S2]));
       return true;
     };
     bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0) && (C::N_DP == 1 || steps == 1 || do_dp(1));
@@ -481,13 +515,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       if (KEYS && C::N_S == 1 && j + 1 < steps && !done(ctrl.s_full, j + 1)) break;
       // Y1 has landed: S of this step was computed from it
       inner(C::A1_COL, dp_col(j), y1(j), j);
-      mma_commit(smem_u32(&ctrl.y1_empty[j % C::S1]));
+      commit(elect, smem_u32(&ctrl.y1_empty[j % C::S1]));
       if (j + C::N_DP < steps && !do_dp(j + C::N_DP)) break;
     }
   }
   // complete once everything that both threads issued has: the accumulators are
   // whole (or, after an abort, TMEM can be released)
-  mma_commit(smem_u32(&ctrl.acc_full));
+  commit(elect, smem_u32(&ctrl.acc_full));
   volatile int32_t no = 0;
   mbar_wait(smem_u32(&ctrl.acc_full), 0, &no, p.err);
 }
@@ -502,8 +536,8 @@ __device__ __forceinline__ void roles(const Params& p, Ctrl& ctrl, uint32_t base
   } else if (warp == kSoftmaxWarps) {
     if (lane == 0) producer_role<D, KEYS>(p, ctrl, base, it, entries);
   } else if (warp == kSoftmaxWarps + 1) {
-    if (lane == 0) mma_role<D, KEYS, true>(p, ctrl, base, tmem, it);
-  } else if (lane == 0) {
+    mma_role<D, KEYS, true>(p, ctrl, base, tmem, it);
+  } else {
     mma_role<D, KEYS, false>(p, ctrl, base, tmem, it);
   }
   __syncwarp();
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + Cfg<D, true>::CTRL);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool keys = static_cast<int32_t>(blockIdx.x) < p.n_key_items;
   if (base & 1023u) {       // swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(p.err, DEV_ERR_INTERNAL);
@@ -541,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctrl.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
   grid_wait();              // the rows' statistics
   const int32_t b = blockIdx.x;
   if (keys) roles<D, true>(p, ctrl, base, tmem, b, warp, lane);
