@@ -216,26 +216,28 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
     nlse = valid ? __ldg(p.nlse2 + static_cast<int64_t>(it.x) * p.Np + row) : -INFINITY;
     ndelta = valid ? __ldg(p.ndelta + static_cast<int64_t>(it.x) * p.Np + row) : 0.f;
   }
-  // the tile's descriptor, fetched one step ahead
-  int32_t desc_next = -1;
-  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
-  auto fetch = [&](int32_t j) {
+  // The tile's descriptor is loaded one step ahead, its index two, so that no load is
+  // waited for where it is issued.
+  auto index_of = [&](int32_t j) -> int32_t {
     const int32_t e = 2 * j + part;
-    desc_next = -1;
-    if (e < n) {
-      desc_next = __ldg(&entries[it.z + e]).y;
-      if (desc_next >= 0) {
-        n0 = __ldg(&descs[2 * desc_next]);
-        n1 = __ldg(&descs[2 * desc_next + 1]);
-      }
+    return e < n ? __ldg(&entries[it.z + e]).y : -1;
+  };
+  int32_t desc_next = index_of(0), desc_after = index_of(1);
+  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+  auto fetch = [&]() {
+    if (desc_next >= 0) {
+      n0 = __ldg(&descs[2 * desc_next]);
+      n1 = __ldg(&descs[2 * desc_next + 1]);
     }
   };
-  fetch(0);
+  fetch();
   bool ok = true;
   for (int32_t j = 0; j < steps; ++j) {
     const bool on = 2 * j + part < n;        // the last step may hold one tile
     const uint32_t allowed = !on ? 0u : desc_next >= 0 ? row_mask(n0, n1, r, sub) : 0xFFFFFFFFu;
-    fetch(j + 1);
+    desc_next = desc_after;
+    fetch();
+    desc_after = index_of(j + 2);
     // a warp whose rows all see nothing here (half of a tile whose other half does)
     // has no arithmetic to do, one whose rows see everything no masking
     const bool none = __all_sync(0xFFFFFFFFu, allowed == 0u);
