@@ -25,7 +25,8 @@
 // Two threads issue MMAs, because the pipe runs dry while a lone issuer waits on a
 // barrier (a step took 3,635 clocks against 2,240 of MMAs): one S and acc2, the other
 // dP and acc1.  MMAs of one thread run in issue order, so a product may overwrite
-// columns that the thread's previous product reads.
+// columns that the thread's previous product reads.  The issuers run as whole warps
+// (elect_lane, ptx.cuh): 2.55 -> 2.05 ms at 8 heads of 16,384 tokens, all blocks on.
 //
 // The 512 TMEM columns decide how far S and dP run ahead of the softmax:
 //   query items         S is free once the softmax holds it in registers; two dP
@@ -127,37 +128,6 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
       "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1));
-}
-
-// The issuers run whole warps, one lane of which issues: addresses and descriptors
-// then stay in the warp's uniform registers, where the MMA wants them.
-__device__ __forceinline__ uint32_t elect_lane() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e;
-}
-__device__ __forceinline__ void mma_ss(uint32_t elect, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t elect, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
-      : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t elect, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(elect)
-      : "memory");
 }
 
 // Allowed columns [32 sub, 32 sub + 32) of row r of a 64-wide boundary tile (grid
@@ -465,7 +435,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t o = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
-      mma_ss(elect, tmem + col, sdesc_sw128(sx + o, 16, 1024), sdesc_sw128(sy + o, 16, 1024), C::IDESC_S, kk > 0);
+      mma_bf16_ss(elect, tmem + col, sdesc_sw128(sx + o, 16, 1024), sdesc_sw128(sy + o, 16, 1024), C::IDESC_S, kk > 0);
     }
   };
   // acc[128 x D] += A (bf16, TMEM) Y over the step's rows; P and dS lie 16 columns
@@ -476,7 +446,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
       if (kk < kks)
-        mma_ts(elect, tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8,
+        mma_bf16_ts(elect, tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8,
                     sdesc_sw128(sy + kk * 16 * 128, 128 * 128, 1024), C::IDESC_A, (j > 0 || kk > 0) ? 1u : 0u);
   };
   auto y1 = [&](int32_t j) { return base + C::Y1 + (j % C::S1) * C::TILE; };
@@ -487,7 +457,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
     auto do_s = [&](int32_t j) -> bool {
       if (!wait(&ctrl.y1_full[j % C::S1], (j / C::S1) & 1)) return false;
       outer(s_col(j), base + C::X1, y1(j));
-      commit(elect, smem_u32(&ctrl.s_full[j & 1]));
+      mma_commit(elect, smem_u32(&ctrl.s_full[j & 1]));
       return true;
     };
     bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && (C::N_S == 1 || steps == 1 || do_s(1));
@@ -496,7 +466,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       if (!done(ctrl.p_full, j)) break;
       if (KEYS) {
         inner(C::A2_COL, s_col(j), y2(j), j);
-        commit(elect, smem_u32(&ctrl.y2_empty[j % C::S2]));
+        mma_commit(elect, smem_u32(&ctrl.y2_empty[j % C::S2]));
       }
       if (j + C::N_S < steps && !do_s(j + C::N_S)) break;
     }
@@ -505,8 +475,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
     auto do_dp = [&](int32_t j) -> bool {
       if (!y2_full(j)) return false;
       outer(dp_col(j), base + C::X2, y2(j));
-      commit(elect, smem_u32(&ctrl.dp_full[j & 1]));
-      commit(elect, smem_u32(&ctrl.y2_empty[j % C::S2]));
+      mma_commit(elect, smem_u32(&ctrl.dp_full[j & 1]));
+      mma_commit(elect, smem_u32(&ctrl.y2_empty[j % C::S2]));
       return true;
     };
     bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0) && (C::N_DP == 1 || steps == 1 || do_dp(1));
@@ -517,13 +487,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       if (KEYS && C::N_S == 1 && j + 1 < steps && !done(ctrl.s_full, j + 1)) break;
       // Y1 has landed: S of this step was computed from it
       inner(C::A1_COL, dp_col(j), y1(j), j);
-      commit(elect, smem_u32(&ctrl.y1_empty[j % C::S1]));
+      mma_commit(elect, smem_u32(&ctrl.y1_empty[j % C::S1]));
       if (j + C::N_DP < steps && !do_dp(j + C::N_DP)) break;
     }
   }
   // complete once everything that both threads issued has: the accumulators are
   // whole (or, after an abort, TMEM can be released)
-  commit(elect, smem_u32(&ctrl.acc_full));
+  mma_commit(elect, smem_u32(&ctrl.acc_full));
   volatile int32_t no = 0;
   mbar_wait(smem_u32(&ctrl.acc_full), 0, &no, p.err);
 }

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
   const uint32_t sQ = base;
   const uint32_t sK0 = base + C::Q_BYTES;
   const uint32_t sV0 = sK0 + STAGES * C::KV_BYTES;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
 
   if (threadIdx.x == 0) {
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctrl.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -420,17 +420,22 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    // (a whole warp with one lane acting: elect_lane, ptx.cuh)
+    {
+      const uint32_t elect = elect_lane();
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.err, p.timeout_ns));
+      };
       uint32_t item_seq = 0, kv_cnt = 0, t_cnt = 0, q_cnt = 0, o_cnt = 0;
       bool ok = true;
       // Failure-path test: wait on a barrier that is never signalled, so the
       // bounded wait expires, the CTA aborts and the error word reports it.
-      if (p.test_stall) ok = mbar_wait(smem_u32(&ctrl.never), 0, abort_flag, p.err, p.timeout_ns);
+      if (p.test_stall) ok = wait(smem_u32(&ctrl.never), 0);
       while (ok) {
         const int slot = item_seq & 1;
-        if (!mbar_wait(smem_u32(&ctrl.item_full[slot]), (item_seq >> 1) & 1, abort_flag, p.err, p.timeout_ns)) break;
-        const int32_t it = ctrl.item_slot[slot];
-        mbar_arrive(smem_u32(&ctrl.item_empty[slot]));
+        if (!wait(smem_u32(&ctrl.item_full[slot]), (item_seq >> 1) & 1)) break;
+        const int32_t it = __shfl_sync(0xFFFFFFFFu, ctrl.item_slot[slot], 0);
+        if (elect) mbar_arrive(smem_u32(&ctrl.item_empty[slot]));
         ++item_seq;
         if (it < 0) break;
         const ReqParams& rq = p.req[req_of(p, it)];
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
         // tiles written by cp.async (generic proxy) are read by the tensor core
         // (async proxy): a proxy fence follows each of their full-barrier waits
         const bool gathered = GATHER || (PERM && __ldg(&rq.items[2 * li + 1]).x != 0);
-        if (!mbar_wait(smem_u32(&ctrl.q_full), q_cnt & 1, abort_flag, p.err, p.timeout_ns)) break;
+        if (!wait(smem_u32(&ctrl.q_full), q_cnt & 1)) break;
         ++q_cnt;
         if (gathered) fence_proxy_async_smem();
         tc_fence_after();
@@ -453,20 +458,20 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
           // in issue order.  The shared-memory tile is free once they land.
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tmem_cp_128x256b(tmem + C::Q_COL + kk * 8,
+            tmem_cp_128x256b(elect, tmem + C::Q_COL + kk * 8,
                              sdesc_sw128(sQ + (kk >> 2) * C::BM * 128 + (kk & 3) * 32, 16, 1024));
-          mma_commit(smem_u32(&ctrl.q_empty));
+          mma_commit(elect, smem_u32(&ctrl.q_empty));
         }
         // O += P V for tile j of this item
         auto issue_pv = [&](int32_t j) -> bool {
           const uint32_t t = t_cnt + j, kvi = kv_cnt + j;
           const int s = kvi % STAGES;
           const uint32_t sb = t & 1;
-          if (!mbar_wait(smem_u32(&ctrl.p_full[sb]), (t >> 1) & 1, abort_flag, p.err, p.timeout_ns)) return false;
-          if (!mbar_wait(smem_u32(&ctrl.v_full[s]), (kvi / STAGES) & 1, abort_flag, p.err, p.timeout_ns)) return false;
+          if (!wait(smem_u32(&ctrl.p_full[sb]), (t >> 1) & 1)) return false;
+          if (!wait(smem_u32(&ctrl.v_full[s]), (kvi / STAGES) & 1)) return false;
           if (gathered) fence_proxy_async_smem();
           if (j == 0) {
-            if (!mbar_wait(smem_u32(&ctrl.o_empty), (o_cnt & 1) ^ 1, abort_flag, p.err, p.timeout_ns)) return false;
+            if (!wait(smem_u32(&ctrl.o_empty), (o_cnt & 1) ^ 1)) return false;
             ++o_cnt;
           }
           tc_fence_after();
@@ -474,18 +479,18 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {
             const uint64_t bdesc = sdesc_sw128(sv + kk * 16 * 128, BN * 128, 1024);
-            mma_bf16_ts(tmem + C::O_COL, tmem + sb * BN + kk * 8, bdesc, C::IDESC_PV,
+            mma_bf16_ts(elect, tmem + C::O_COL, tmem + sb * BN + kk * 8, bdesc, C::IDESC_PV,
                         (j > 0 || kk > 0) ? 1u : 0u);
           }
-          mma_commit(smem_u32(&ctrl.v_empty[s]));
-          mma_commit(smem_u32(&ctrl.pv_done));
+          mma_commit(elect, smem_u32(&ctrl.v_empty[s]));
+          mma_commit(elect, smem_u32(&ctrl.pv_done));
           return true;
         };
         for (int32_t j = 0; j < n && ok; ++j) {
           const uint32_t t = t_cnt + j, kvi = kv_cnt + j;
           const int s = kvi % STAGES;
           const uint32_t sb = t & 1;
-          if (!mbar_wait(smem_u32(&ctrl.k_full[s]), (kvi / STAGES) & 1, abort_flag, p.err, p.timeout_ns)) {
+          if (!wait(smem_u32(&ctrl.k_full[s]), (kvi / STAGES) & 1)) {
             ok = false;
             break;
           }
@@ -496,28 +501,28 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t bdesc = sdesc_sw128(sk + (kk >> 2) * BN * 128 + (kk & 3) * 32, 16, 1024);
             if constexpr (C::Q_TMEM) {
-              mma_bf16_ts(tmem + sb * BN, tmem + C::Q_COL + kk * 8, bdesc, C::IDESC_QK,
+              mma_bf16_ts(elect, tmem + sb * BN, tmem + C::Q_COL + kk * 8, bdesc, C::IDESC_QK,
                           kk > 0 ? 1u : 0u);
             } else {
               const uint64_t adesc = sdesc_sw128(sQ + (kk >> 2) * C::BM * 128 + (kk & 3) * 32, 16, 1024);
-              mma_bf16_ss(tmem + sb * BN, adesc, bdesc, C::IDESC_QK, kk > 0 ? 1u : 0u);
+              mma_bf16_ss(elect, tmem + sb * BN, adesc, bdesc, C::IDESC_QK, kk > 0 ? 1u : 0u);
             }
           }
-          mma_commit(smem_u32(&ctrl.s_full[sb]));
-          mma_commit(smem_u32(&ctrl.k_empty[s]));
-          if (!C::Q_TMEM && j == n - 1) mma_commit(smem_u32(&ctrl.q_empty));
+          mma_commit(elect, smem_u32(&ctrl.s_full[sb]));
+          mma_commit(elect, smem_u32(&ctrl.k_empty[s]));
+          if (!C::Q_TMEM && j == n - 1) mma_commit(elect, smem_u32(&ctrl.q_empty));
           // QK of tile j runs ahead of PV of tile j-1 (the other S buffer)
           if (j > 0 && !issue_pv(j - 1)) ok = false;
         }
         if (ok && !issue_pv(n - 1)) ok = false;
         // the item's output accumulator is complete once its last PV finishes
-        if (ok) mma_commit(smem_u32(&ctrl.o_full));
+        if (ok) mma_commit(elect, smem_u32(&ctrl.o_full));
         t_cnt += n;
         kv_cnt += n;
       }
-      if (p.tiles_done) atomicAdd(p.tiles_done, static_cast<unsigned long long>(t_cnt));
+      if (elect && p.tiles_done) atomicAdd(p.tiles_done, static_cast<unsigned long long>(t_cnt));
       // every MMA issued has finished before TMEM is released
-      mma_commit(smem_u32(&ctrl.final_bar));
+      mma_commit(elect, smem_u32(&ctrl.final_bar));
       volatile int32_t dummy = 0;
       mbar_wait(smem_u32(&ctrl.final_bar), 0, &dummy, p.err);
     }
