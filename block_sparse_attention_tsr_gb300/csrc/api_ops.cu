@@ -5,6 +5,7 @@
 #include <cstring>
 #include <new>
 #include <string>
+#include <utility>
 
 #include "internal.h"
 
@@ -136,6 +137,18 @@ tsr_status tsr_rope(const tsr_rope_desc* d, const tsr_rope_tensor* t, int32_t n,
       if (xs < 0 || os < d->d) return fail(TSR_ERR_INVALID_ARG, at + "strides: x >= 0, out >= d");
       if (xs > INT64_MAX / 8 / size[k] || os > INT64_MAX / 8 / size[k])
         return fail(TSR_ERR_INVALID_ARG, at + "strides too large");
+    }
+    // the output's rows must not run into each other: each dimension, in order of its
+    // stride, steps over all that the smaller ones reach
+    int order[3] = {0, 1, 2};
+    for (int a = 0; a < 2; ++a)
+      for (int b = a + 1; b < 3; ++b)
+        if (t[i].out_stride[order[b]] < t[i].out_stride[order[a]]) std::swap(order[a], order[b]);
+    int64_t reach = d->d;
+    for (int k : order) {
+      if (size[k] == 1) continue;
+      if (t[i].out_stride[k] < reach) return fail(TSR_ERR_INVALID_ARG, at + "elements of out overlap");
+      reach += t[i].out_stride[k] * (size[k] - 1);
     }
     if (t[i].x == t[i].out && !same) return fail(TSR_ERR_INVALID_ARG, at + "in place needs equal strides");
     for (int j = 0; j < i; ++j)

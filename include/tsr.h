@@ -479,9 +479,10 @@ tsr_status tsr_svg_route(const void *q, const void *k, const void *v, int32_t B,
  * int32 value, negative ones too.
  *
  * Strides are in elements, for b, h and n; d is contiguous.  x and out may be the
- * same tensor (same strides); otherwise their elements must not overlap, and no
- * two elements of out may share an address.  x strides may be 0 (a broadcast
- * input).  Any alignment of the element type; 16-byte aligned rows are fastest.
+ * same tensor (same strides); otherwise their elements must not overlap.  Rows of
+ * out must not run into each other (a dimension's stride is at least what the
+ * dimensions of smaller stride reach).  x strides may be 0 (a broadcast input);
+ * strides of dimensions of size 1 are not read.  Any alignment of the element type; 16-byte aligned rows are fastest.
  * Errors: TSR_ERR_INVALID_ARG for bad shapes, axes, pointers or strides,
  * TSR_ERR_UNSUPPORTED for B above 65535 or N above 2^24.  Asynchronous on `stream`.
  */

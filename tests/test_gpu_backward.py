@@ -186,6 +186,32 @@ def test_a_layer_together():
     plan.device_status()
 
 
+def test_a_failed_update_is_refused_until_one_succeeds():
+    spec = uniform(1, 1, 640, 64, 64, 0.4, 1, diag=True)
+    x = inputs(spec, 64, 2)
+    q, k, v, do = x
+    plan = tsr.tsr_backward_plan(gpu_mask(spec, 64))
+    out, lse = tsr.tsr_bsa_forward(q, k, v, tsr.tsr_plan(gpu_mask(spec, 64)))
+    with pytest.raises(tsr.TsrError) as e:
+        plan.update(gpu_mask(uniform(1, 1, 640, 64, 17, 0.3, 7), 64))     # the key side is too fine
+    assert e.value.status == 2
+    with pytest.raises(tsr.TsrError) as e:
+        tsr.tsr_bsa_backward(q, k, v, out, lse, do, plan)
+    assert e.value.status == 1
+    plan.update(gpu_mask(spec, 64))
+    compare(spec, x, tsr.tsr_bsa_backward(q, k, v, out, lse, do, plan))
+
+
+def test_same_tensor_for_several_inputs():
+    """Q, K, V (and dO) may be one tensor."""
+    spec = uniform(1, 2, 500, 64, 64, 0.5, 6, diag=True)
+    q = inputs(spec, 128, 8)[0]
+    mask = gpu_mask(spec, 128)
+    out, lse = tsr.tsr_bsa_forward(q, q, q, tsr.tsr_plan(mask))
+    g = tsr.tsr_bsa_backward(q, q, q, out, lse, q, tsr.tsr_backward_plan(mask))
+    compare(spec, (q, q, q, q), g)
+
+
 def test_refusals():
     svg = W.svg_mask(1, 2, n_frames=4, frame_size=32)
     keys = W.random_keylist(1, 1, 2, 128, slice_m=64)

@@ -61,6 +61,7 @@ def test_rope_refuses_bad_shapes(L, kw, code):
     (0, {}), (5, {}), (1, dict(x=0)), (1, dict(out=0)), (1, dict(x=4097)), (1, dict(out=8193)),
     (1, dict(H=0)), (1, dict(x_stride=[8192, -1, 64])), (1, dict(out_stride=[8192, 4096, 32])),
     (1, dict(out_stride=[8192, 0, 64])), (1, dict(out=4096, out_stride=[8192, 64, 128])),
+    (1, dict(out_stride=[8192, 64, 64])), (1, dict(out_stride=[8192, 4032, 64])),
     (1, dict(x_stride=[8192, 4096, 1 << 60])), (2, dict(out=4096 * 3)), (2, dict(out=4096 * 4)),
 ])
 def test_rope_refuses_bad_tensors(L, n, kw):
