@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -83,6 +84,15 @@ class _RopeTensor(ctypes.Structure):
 
 class _SelectDesc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in ("B", "H", "N", "d", "bq", "bk", "keep", "first", "diagonal")]
+
+
+# The same layouts as packed bytes, which the calls below pass (filling a ctypes
+# structure field by field takes longer than the kernels of a small call).
+_ROPE_DESC = struct.Struct("@5i4i2idPi4i4x")
+_ROPE_TENSOR = struct.Struct("@PPi3q3q")
+_SELECT_DESC = struct.Struct("@9i")
+for _packed, _fields in ((_ROPE_DESC, _RopeDesc), (_ROPE_TENSOR, _RopeTensor), (_SELECT_DESC, _SelectDesc)):
+    assert _packed.size == ctypes.sizeof(_fields)
 
 
 class _Request(ctypes.Structure):
@@ -324,7 +334,7 @@ def tsr_bsa_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: Pla
     """Attention over `plan`: returns (out bf16 [B,H,N,d], lse fp32 [B,H,N])."""
     shape = (plan.B, plan.H, plan.N, plan.d)
     for t in (q, k, v):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
+        if t.dtype != torch.bfloat16 or t.shape != shape:
             raise ValueError(f"q, k, v must be bf16 of shape {shape}")
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
@@ -393,9 +403,9 @@ def tsr_bsa_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: tor
     least plan.workspace_bytes; default: one allocated for the call."""
     shape = (plan.B, plan.H, plan.N, plan.d)
     for t in (q, k, v, out, dout, dq, dk, dv):
-        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != shape):
             raise ValueError(f"q, k, v, out, dout and the gradients must be bf16 of shape {shape}")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != shape[:3]:
+    if lse.dtype != torch.float32 or lse.shape != shape[:3]:
         raise ValueError(f"lse must be fp32 of shape {shape[:3]}")
     _on_device(q, k, v, out, lse, dout, dq, dk, dv, workspace)
     if dq is None or dk is None or dv is None or workspace is None:
@@ -466,7 +476,6 @@ def tsr_svg_route(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_frames: i
 
 
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_ROPE_ARRAYS = tuple(_RopeTensor * n for n in range(1, 5))
 
 
 def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = None,
@@ -486,53 +495,51 @@ def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = Non
         raise ValueError("one to four tensors per call")
     if (grid is None) == (positions is None):
         raise ValueError("give grid or positions")
-    if any(t.dim() != 4 for t in xs):
+    first = xs[0]
+    if first.dim() != 4:
         raise ValueError("the tensors are [B, H, N, d]")
-    B, _, N, d = xs[0].shape
-    dtype = xs[0].dtype
-    dims = [int(a) for a in axis_dims]
-    if not 1 <= len(dims) <= 4:
-        raise ValueError("one to four axes")
-    if dtype not in _ROPE_DTYPES:
+    B, _, N, d = first.shape
+    dtype = first.dtype
+    code = _ROPE_DTYPES.get(dtype)
+    if code is None:
         raise ValueError("the tensors are bf16, fp16 or fp32")
-    if out is not None:
+    dims = [int(a) for a in axis_dims]
+    axes = len(dims)
+    if not 1 <= axes <= 4:
+        raise ValueError("one to four axes")
+    for t in xs:
+        if t.dim() != 4 or t.dtype != dtype or t.shape[::2] != (B, N) or t.shape[3] != d:
+            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
+    if out is None:
+        _on_device(*xs, positions)
+        with _allocating_on(stream):
+            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
+    else:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(outs) != len(xs):
             raise ValueError("as many outputs as tensors")
         _on_device(*xs, *outs, positions)
-    else:
-        _on_device(*xs, positions)
-        with _allocating_on(stream):
-            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
-    arr = _ROPE_ARRAYS[len(xs) - 1]()
-    for i, (t, o) in enumerate(zip(xs, outs)):
-        b, h, n, width = t.shape
-        if b != B or n != N or width != d or t.dtype != dtype:
-            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
-        sb, sh, sn, last = t.stride()
-        if out is None:
-            at = (h * N * d, N * d, d)
-        else:
-            if o.shape != t.shape or o.dtype != dtype:
-                raise ValueError("out must have x's shape and dtype")
-            *at, out_last = o.stride()
-            last = max(last, out_last)
-        if last != 1:
+    tensors = b""
+    for t, o in zip(xs, outs):
+        xb, xh, xn, x_last = t.stride()
+        ob, oh, on, o_last = o.stride()
+        if out is not None and (o.shape != t.shape or o.dtype != dtype):
+            raise ValueError("out must have x's shape and dtype")
+        if x_last != 1 or o_last != 1:
             raise ValueError("the last dimension must be contiguous")
-        arr[i] = (t.data_ptr(), o.data_ptr(), h, (sb, sh, sn), tuple(at))
-    pad = (0,) * (4 - len(dims))
+        tensors += _ROPE_TENSOR.pack(t.data_ptr(), o.data_ptr(), t.shape[1], xb, xh, xn, ob, oh, on)
+    pad = (0,) * (4 - axes)
     if positions is not None:
-        if positions.dtype != torch.int32 or tuple(positions.shape) not in ((N, len(dims)), (B, N, len(dims))):
+        if positions.dtype != torch.int32 or positions.shape not in ((N, axes), (B, N, axes)):
             raise ValueError("positions must be int32 [N, axes] or [B, N, axes]")
-        where = (_dptr(positions), int(positions.dim() == 3), (0, 0, 0, 0))
+        where = (_dptr(positions), positions.dim() == 3, 0, 0, 0, 0)
     else:
         cells = [int(g) for g in grid]
-        if len(cells) != len(dims):
+        if len(cells) != axes:
             raise ValueError("grid needs one size per axis")
-        where = (None, 0, (*cells, *pad))
-    desc = _RopeDesc(B, N, d, _ROPE_DTYPES[dtype], len(dims), (*dims, *pad), int(bool(halves)),
-                     int(bool(inverse)), float(theta), *where)
-    _check(lib().tsr_rope(ctypes.byref(desc), arr, len(xs), _stream_ptr(stream)))
+        where = (0, 0, *cells, *pad)
+    desc = _ROPE_DESC.pack(B, N, d, code, axes, *dims, *pad, bool(halves), bool(inverse), theta, *where)
+    _check(lib().tsr_rope(desc, tensors, len(xs), _stream_ptr(stream)))
     return outs[0] if one else list(outs)
 
 
@@ -553,20 +560,21 @@ def tsr_block_select(q: torch.Tensor, k: torch.Tensor, keep: int, *, bq: int = 6
         raise ValueError("q, k must be bf16 [B, H, N, d] alike")
     _on_device(q, k, out, workspace)
     B, H, N, d = q.shape
-    desc = _SelectDesc(B, H, N, d, int(bq), int(bk), int(keep), int(first), int(bool(diagonal)))
+    bq, bk = int(bq), int(bk)
+    desc = _SELECT_DESC.pack(B, H, N, d, bq, bk, int(keep), int(first), bool(diagonal))
     L = lib()
     need = ctypes.c_size_t(0)
-    _check(L.tsr_block_select_workspace(ctypes.byref(desc), ctypes.byref(need)))
-    shape = (B, H, -(-N // desc.bq), -(-N // desc.bk))
+    _check(L.tsr_block_select_workspace(desc, ctypes.byref(need)))
+    shape = (B, H, -(-N // bq), -(-N // bk))
     if out is None or workspace is None:
         with _allocating_on(stream):
             if out is None:
                 out = torch.empty(shape, dtype=torch.uint8, device=q.device)
             if workspace is None:
                 workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    if tuple(out.shape) != shape or out.dtype != torch.uint8:
+    if out.shape != shape or out.dtype != torch.uint8:
         raise ValueError(f"out must be uint8 of shape {shape}")
-    _check(L.tsr_block_select(ctypes.byref(desc), _dptr(q), _dptr(k), _dptr(out), _dptr(workspace),
+    _check(L.tsr_block_select(desc, _dptr(q), _dptr(k), _dptr(out), _dptr(workspace),
                               workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
     return out
 
