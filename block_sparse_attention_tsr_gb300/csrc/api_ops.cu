@@ -72,10 +72,6 @@ tsr_status check_backward_kind(const tsr_mask* mask) {
   return TSR_OK;
 }
 
-size_t backward_workspace(const tsr_plan_s* p) {
-  return static_cast<size_t>(2) * p->B * p->H * ((static_cast<size_t>(p->N) + 63) / 64 * 64) * sizeof(float);
-}
-
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 tsr_status check_select(const tsr_select_desc* s) {
@@ -219,7 +215,8 @@ tsr_status tsr_backward_plan_device_status(tsr_backward_plan_t plan, void* strea
 tsr_status tsr_bsa_backward_workspace(tsr_backward_plan_t plan, size_t* bytes) {
   set_error("");
   if (!plan || !bytes) return fail(TSR_ERR_INVALID_ARG, "plan / bytes is NULL");
-  *bytes = backward_workspace(plan->q);
+  if (!plan->k) return fail(TSR_ERR_INVALID_ARG, "the plan's last update failed");
+  *bytes = backward_workspace(plan->q, plan->k);
   return TSR_OK;
 }
 
@@ -245,7 +242,7 @@ tsr_status tsr_bsa_backward(const void* q, const void* k, const void* v, const v
   }
   if (!workspace || !aligned(workspace, 256))
     return fail(TSR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  if (workspace_bytes < backward_workspace(plan->q)) return fail(TSR_ERR_INVALID_ARG, "workspace too small");
+  if (workspace_bytes < backward_workspace(plan->q, plan->k)) return fail(TSR_ERR_INVALID_ARG, "workspace too small");
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
   if (dev != plan->q->device) return fail(TSR_ERR_INVALID_ARG, "plan was made on another device");

@@ -37,6 +37,9 @@
 //                       softmax.  (Half-wide S products cost as much as whole ones;
 //                       a whole S waits out the softmax, and half-wide dP as well
 //                       cost more than it gained.)
+// Few items with long lists (short sequences of few heads): each list is cut in two
+// parts with a CTA each, whose fp32 accumulators go to the workspace; the part that
+// finishes last adds them up, in the parts' order.
 // Warps: 16 softmax (row = TMEM lane, 32 columns each), which also store the
 // gradients, a producer (TMA tiles, the rows' statistics) and the two issuers.  Every
 // wait is bounded: on expiry the error word is set and the kernel winds down.
@@ -66,7 +69,9 @@ struct Params {
   const float* ndelta;             // [B*H][Np] -delta
   __nv_bfloat16 *dq, *dk, *dv;
   uint32_t* err;
-  int32_t n_key_items, N, Np;
+  float4* part;                    // split items: [item * split + part][acc (2)][d / 4][128 rows]
+  int32_t* arrived;                // split items: parts finished, [key items, query items]
+  int32_t n_key_items, N, Np, split;
   float scale_log2, scale;
 };
 
@@ -100,6 +105,7 @@ struct alignas(8) Ctrl {
   uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2], acc_full;
   uint32_t tmem_base;
   int32_t abort_flag;
+  int32_t last;                // split items: this CTA's part was the last of its item
 };
 static_assert(sizeof(Ctrl) <= 512, "Ctrl");
 
@@ -308,7 +314,29 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
   }
   // ---- epilogue: a quarter of the columns of each accumulator
   constexpr int W = D / 4;
-  if (ok && n > 0) {
+  if (p.split > 1) {
+    if (ok && (n == 0 || mbar_wait(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err))) {
+      tc_fence_after();
+#pragma unroll
+      for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
+        const uint32_t col = tmem + lanes + (w ? C::A2_COL : C::A1_COL) + grp * W;
+        float4* dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + w) * (D / 4) * 128 + grp * (W / 4) * 128 + r;
+#pragma unroll
+        for (int c = 0; c < W; c += 16) {
+          uint32_t a[16] = {};
+          if (n > 0) {
+            tmem_ld16(col + c, a);
+            tc_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[(c / 4 + i) * 128] = make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
+                                                 __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]));
+        }
+      }
+      __threadfence();
+    }
+  } else if (ok && n > 0) {
     if (mbar_wait(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err)) {
       tc_fence_after();
 #pragma unroll
@@ -498,10 +526,50 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
   mbar_wait(smem_u32(&ctrl.acc_full), 0, &no, p.err);
 }
 
+// The sum of a split item's parts, by the warps that store the accumulators.
 template <int D, bool KEYS>
-__device__ __forceinline__ void roles(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int32_t item,
+__device__ __forceinline__ void merge_parts(const Params& p, int4 it, int64_t unit0, int warp, int lane) {
+  constexpr int W = D / 4;
+  const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+  const int64_t row = static_cast<int64_t>(it.y) * 128 + r;
+  if (row >= p.N) return;
+#pragma unroll
+  for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
+    __nv_bfloat16* out = KEYS ? (w ? p.dv : p.dk) : p.dq;
+    const float f = w ? 1.f : p.scale;
+    uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(it.x) * p.N + row) * D + grp * W);
+#pragma unroll
+    for (int c = 0; c < W / 8; ++c) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      for (int q = 0; q < p.split; ++q) {
+        const float4* src = p.part + ((unit0 + q) * 2 + w) * (D / 4) * 128 + (grp * (W / 4) + 2 * c) * 128 + r;
+        const float4 x = __ldcg(src), y = __ldcg(src + 128);
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+        b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+      }
+      dst[c] = make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f),
+                          pack_bf16x2(b.x * f, b.y * f), pack_bf16x2(b.z * f, b.w * f));
+    }
+  }
+}
+
+// A work item, or its part `part` of p.split: whole steps, in near-equal shares.
+template <bool KEYS>
+__device__ __forceinline__ int4 item_of(const Params& p, int32_t item, int32_t part) {
+  int4 it = __ldg((KEYS ? p.items_k : p.items_q) + 2 * static_cast<int64_t>(item));
+  if (p.split > 1) {
+    const int32_t n = it.w - it.z, steps = (n + 1) / 2;
+    const int32_t a = static_cast<int32_t>(static_cast<int64_t>(steps) * part / p.split);
+    const int32_t b = static_cast<int32_t>(static_cast<int64_t>(steps) * (part + 1) / p.split);
+    it.w = it.z + min(n, 2 * b);
+    it.z += 2 * a;
+  }
+  return it;
+}
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void roles(const Params& p, Ctrl& ctrl, uint32_t base, uint32_t tmem, int4 it,
                                       int warp, int lane) {
-  const int4 it = __ldg((KEYS ? p.items_k : p.items_q) + 2 * static_cast<int64_t>(item));
   const int2* entries = KEYS ? p.entries_k : p.entries_q;
   if (warp < kSoftmaxWarps) {
     softmax_role<D, KEYS>(p, ctrl, base, tmem, it, entries, KEYS ? p.descs_k : p.descs_q, warp, lane);
@@ -521,7 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   const uint32_t base = smem_u32(smem);
   Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + Cfg<D, true>::CTRL);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const bool keys = static_cast<int32_t>(blockIdx.x) < p.n_key_items;
+  const int32_t part = p.split > 1 ? blockIdx.x % p.split : 0, item = p.split > 1 ? blockIdx.x / p.split : blockIdx.x;
+  const bool keys = item < p.n_key_items;
   if (base & 1023u) {       // swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) atomicOr(p.err, DEV_ERR_INTERNAL);
     return;
@@ -549,28 +618,42 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
   grid_wait();              // the rows' statistics
-  const int32_t b = blockIdx.x;
-  if (keys) roles<D, true>(p, ctrl, base, tmem, b, warp, lane);
-  else roles<D, false>(p, ctrl, base, tmem, b - p.n_key_items, warp, lane);
+  const int4 it = keys ? item_of<true>(p, item, part) : item_of<false>(p, item - p.n_key_items, part);
+  if (keys) roles<D, true>(p, ctrl, base, tmem, it, warp, lane);
+  else roles<D, false>(p, ctrl, base, tmem, it, warp, lane);
   tc_fence_before();
   __syncthreads();
   if (warp == kSoftmaxWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (p.split > 1) {
+    // every warp's part is written (and fenced): count it; the last CTA adds them up
+    if (threadIdx.x == 0) ctrl.last = !ctrl.abort_flag && atomicAdd(p.arrived + item, 1) == p.split - 1;
+    __syncthreads();
+    if (ctrl.last && warp < kSoftmaxWarps) {
+      __threadfence();
+      const int64_t unit0 = static_cast<int64_t>(item) * p.split;
+      if (keys) merge_parts<D, true>(p, it, unit0, warp, lane);
+      else merge_parts<D, false>(p, it, unit0, warp, lane);
+    }
+  }
 }
 
 // Per query row: -lse in base 2 and -delta, delta = sum dO o O (fp32), one row per D / 8
-// lanes; rows past N of the padded arrays get P = 0.  HBM-bound: reads O and dO.
+// lanes; rows past N of the padded arrays get P = 0.  Also clears the counters of
+// split items.  HBM-bound: reads O and dO.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_stats_kernel(const uint4* __restrict__ o, const uint4* __restrict__ g,
                                                         const float* __restrict__ lse, float* __restrict__ nlse2,
                                                         float* __restrict__ ndelta, int64_t rows_p, int32_t N,
-                                                        int32_t Np) {
+                                                        int32_t Np, int32_t* __restrict__ arrived, int32_t n_arrived) {
   constexpr int VR = D / 8;
   const int64_t row = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / VR;
   const int v = threadIdx.x % VR;
   grid_launch_dependents();
+  if (blockIdx.x == 0)
+    for (int k = threadIdx.x; k < n_arrived; k += blockDim.x) arrived[k] = 0;
   if (row >= rows_p) return;       // whole groups of VR lanes leave together
   const int64_t bh = row / Np;
   const int32_t i = static_cast<int32_t>(row - bh * Np);
@@ -641,6 +724,36 @@ tsr_status launch_transpose_blocks(const uint8_t* src, uint8_t* dst, int64_t hea
   return TSR_OK;
 }
 
+namespace {
+
+// Parts per item that the workspace has room for: two where that still leaves an SM
+// for each.
+int32_t max_split(const tsr_plan_impl* Q, const tsr_plan_impl* K) {
+  return (Q->n_items + K->n_items) * 2 <= num_sms(Q->device) ? 2 : 1;
+}
+
+struct BwdLayout {
+  size_t stats, arrived, part, total;
+  int32_t split;
+};
+BwdLayout backward_layout(const tsr_plan_impl* Q, const tsr_plan_impl* K) {
+  BwdLayout l;
+  const int64_t items = Q->n_items + K->n_items;
+  l.split = max_split(Q, K);
+  auto round = [](size_t b) { return (b + 255) / 256 * 256; };
+  l.stats = 0;
+  l.arrived = round(static_cast<size_t>(2) * Q->B * Q->H * ((Q->N + 63) / 64 * 64) * sizeof(float));
+  l.part = l.arrived + (l.split > 1 ? round(sizeof(int32_t) * items) : 0);
+  l.total = l.part + (l.split > 1 ? static_cast<size_t>(items) * l.split * 2 * 128 * Q->d * sizeof(float) : 0);
+  return l;
+}
+
+}  // namespace
+
+size_t backward_workspace(const tsr_plan_impl* plan_q, const tsr_plan_impl* plan_k) {
+  return backward_layout(plan_q, plan_k).total;
+}
+
 tsr_status launch_backward(const BwdArgs& a, cudaStream_t st) {
   const tsr_plan_impl *Q = a.plan_q, *K = a.plan_k;
   const int32_t N = Q->N, D = Q->d, Np = (N + 63) / 64 * 64;
@@ -670,14 +783,25 @@ tsr_status launch_backward(const BwdArgs& a, cudaStream_t st) {
   p.Np = Np;
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
-  const int64_t rows = BH * Np, ctas = K->n_items + Q->n_items;
+  // Items are cut in two where the longest list leaves 16 tiles to a part.  One head,
+  // d = 128, density 0.3: 4,096 tokens 42 -> 36 us; with 11 tiles to a part (2,048
+  // tokens) 26 -> 27 us, the partial sums costing what the shorter lists save.
+  const BwdLayout l = backward_layout(Q, K);
+  p.split = std::max(Q->max_item_len, K->max_item_len) >= 16 * l.split ? l.split : 1;
+  p.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + l.part);
+  p.arrived = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + l.arrived);
+  const int64_t items = K->n_items + Q->n_items, ctas = items * p.split;
+  const int32_t n_arrived = p.split > 1 ? static_cast<int32_t>(items) : 0;
+  const int64_t rows = BH * Np;
   const int64_t stat_blocks = (rows * (D / 8) + 255) / 256;
   if (stat_blocks >= (int64_t{1} << 31)) return fail(TSR_ERR_UNSUPPORTED, "too many rows");
   const uint4 *o = static_cast<const uint4*>(a.out), *g = static_cast<const uint4*>(a.dout);
   if (D == 64)
-    bwd::bwd_stats_kernel<64><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np);
+    bwd::bwd_stats_kernel<64><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np, p.arrived,
+                                                                               n_arrived);
   else
-    bwd::bwd_stats_kernel<128><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np);
+    bwd::bwd_stats_kernel<128><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np, p.arrived,
+                                                                               n_arrived);
   TSR_CUDA(cudaGetLastError());
   return D == 64 ? bwd::launch<64>(p, ctas, Q->device, st) : bwd::launch<128>(p, ctas, Q->device, st);
 }

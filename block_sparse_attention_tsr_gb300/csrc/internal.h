@@ -195,10 +195,11 @@ struct BwdArgs {
   const float* lse;
   const void* dout;
   void *dq, *dk, *dv;
-  void* workspace;              // lse in base 2 and delta, fp32 [2][B*H][N rounded up to 64]
+  void* workspace;              // backward_workspace() bytes
   const tsr_plan_impl *plan_q, *plan_k;
 };
 tsr_status launch_backward(const BwdArgs& a, cudaStream_t stream);
+size_t backward_workspace(const tsr_plan_impl* plan_q, const tsr_plan_impl* plan_k);
 // blocks uint8 [heads][nq][nk] -> [heads][nk][nq]
 tsr_status launch_transpose_blocks(const uint8_t* src, uint8_t* dst, int64_t heads, int32_t nq, int32_t nk,
                                    cudaStream_t stream);

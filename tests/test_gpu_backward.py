@@ -123,6 +123,20 @@ def test_many_items_and_same_bits():
     assert all(torch.equal(a, b) for a, b in zip(keep, (*x, out, lse)))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,p", [(1030, 0.5), (2100, 1.1), (4200, 0.5), (4200, 0.02)])
+def test_few_items_in_parts(N, p, d):
+    """One head: items with long lists (the second and third case) are cut in two
+    parts that the later one adds up, in order: the same bits every time, from any
+    workspace."""
+    spec = uniform(1, 1, N, 64, 64, p, 12, zero_rows=1, zero_cols=1)
+    x, out, lse, plan, g = run(spec, d, 29)
+    ws = torch.full((plan.workspace_bytes,), 7, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        again = tsr.tsr_bsa_backward(*x[:3], out, lse, x[3], plan, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(g, again))
+
+
 def test_update_streams_and_overlapping_calls():
     a, b = uniform(1, 3, 900, 64, 64, 0.2, 1, zero_rows=1), uniform(1, 3, 900, 32, 128, 0.6, 2, zero_cols=1)
     x = inputs(a, 64, 3)
