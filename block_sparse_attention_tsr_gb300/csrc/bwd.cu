@@ -180,6 +180,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
                                              const int2* entries, const uint4* descs, int warp, int lane) {
   using C = Cfg<D, KEYS>;
   volatile int32_t* abort_flag = &ctrl.abort_flag;
+  grid_wait();                             // the rows' statistics; the first tiles load meanwhile
   const int grp = warp >> 2;               // columns [32 grp, +32) of the step
   const int part = grp >> 1, sub = grp & 1;
   const int r = (warp & 3) * 32 + lane;
@@ -412,6 +413,7 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
     if (KEYS) {
       const uint32_t bar = smem_u32(&ctrl.st_full[j & 1]), dst = base + C::ST + (j & 1) * C::STAT;
       if (!mbar_wait(smem_u32(&ctrl.st_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag, p.err)) break;
+      if (j == 0) grid_wait();
       mbar_arrive_expect_tx(bar, parts * 512);
       const int64_t o = static_cast<int64_t>(bh) * p.Np;
       bulk_load(dst, p.nlse2 + o + k0, 256, bar);
@@ -617,7 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
-  grid_wait();              // the rows' statistics
   const int4 it = keys ? item_of<true>(p, item, part) : item_of<false>(p, item - p.n_key_items, part);
   if (keys) roles<D, true>(p, ctrl, base, tmem, it, warp, lane);
   else roles<D, false>(p, ctrl, base, tmem, it, warp, lane);
