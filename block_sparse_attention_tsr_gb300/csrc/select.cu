@@ -99,14 +99,10 @@ __device__ __forceinline__ void two_sum(uint64_t& s, uint64_t& e, uint64_t x) {
 // rows) the four warps of a CTA.  D / 8 lanes across a row, eight loads of 16 bytes
 // in flight per lane, no barrier between blocks.  Everything is fp32 pairs: fp64
 // sums, at two lanes a clock per SM, took 320 us for a 480p layer, one CTA per block
-// (whose loads wait out its barriers) 104 us.
+// (whose loads wait out its barriers) 104 us, a warp per block 65.
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_constant__ PoolParams p) {
+__device__ __forceinline__ void pool_block(const PoolParams& p, int64_t unit, int warp, int lane) {
   constexpr int VR = D / 8, RPW = 32 / VR, WARPS = kPoolThreads / 32;   // RPW rows per warp load
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit = SHARED ? blockIdx.x : blockIdx.x * static_cast<int64_t>(WARPS) + warp;
-  grid_launch_dependents();      // select_kernel's blocks take the room of the last of these
-  if (unit >= p.n_units) return;
   const int w = unit >= p.first_k ? 1 : 0;
   const int64_t u = unit - (w ? p.first_k : 0);
   const int64_t bh = u / p.n_blocks[w];
@@ -233,6 +229,14 @@ __global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_cons
     const float f = m * 1.0001f;
     p.norm[w][u] = make_float4(sqrtf(n2) * f, sqrtf(l2) * f, sqrtf(r2) * f, 0.f);
   }
+}
+
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_constant__ PoolParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t unit = SHARED ? blockIdx.x : blockIdx.x * static_cast<int64_t>(kPoolThreads / 32) + warp;
+  grid_launch_dependents();      // select_kernel's blocks take the room of the last of these
+  if (unit < p.n_units) pool_block<D, SHARED>(p, unit, warp, lane);
 }
 
 struct SelParams {
@@ -458,18 +462,18 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   };
   // the sure ones' bytes, and the number of the near ones
   int n_sure = 0, n_near = 0;
-  uint32_t near_bits = 0u;                      // KPL > 0: bit m
+  uint64_t near_bits = 0;                       // KPL > 0: bit m
 #pragma unroll
   for (int m = 0; m < chunks; ++m) {
     const int j = m * 32 + lane;
     const float x = val(m);
     const bool in = sure(x), nr = near(m, x);
     n_sure += in ? 1 : 0;
-    if (KPL > 0) near_bits |= nr ? 1u << (m & 31) : 0u;
+    if (KPL > 0) near_bits |= nr ? 1ull << (m & 63) : 0ull;
     else n_near += nr ? 1 : 0;
     if (j < p.nk) out[j] = in ? 1 : 0;
   }
-  if (KPL > 0) n_near = __popc(near_bits);
+  if (KPL > 0) n_near = __popcll(near_bits);
   // lanes store the bytes of their own j, so a forced block's 1 comes after its 0
   for (int j = lane; j < first; j += 32) out[j] = 1;
   for (int j = d_lo + ((lane - d_lo) & 31); j < d_hi; j += 32) out[j] = 1;
@@ -478,7 +482,7 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   const int left = want - n_sure;               // of the near ones, 1 <= left <= n_near
   if (left == n_near) {
     if (KPL > 0) {
-      for (; near_bits; near_bits &= near_bits - 1) out[(__ffs(near_bits) - 1) * 32 + lane] = 1;
+      for (; near_bits; near_bits &= near_bits - 1) out[(__ffsll(near_bits) - 1) * 32 + lane] = 1;
     } else {
       for (int m = 0; m < chunks; ++m)
         if (near(m, val(m))) out[m * 32 + lane] = 1;
@@ -501,7 +505,8 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
       }
     };
     if (KPL > 0) {
-      list(0, near_bits);
+      list(0, static_cast<uint32_t>(near_bits));
+      if (KPL > 32) list(32, static_cast<uint32_t>(near_bits >> 32));
     } else {
       for (int m0 = 0; m0 < chunks; m0 += 32) {
         uint32_t bits = 0u;
@@ -575,16 +580,14 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
   }
 }
 
-// One CTA: a strip of kStrip query blocks of one head.
+// A CTA's strip of kStrip query blocks of one head.
 template <int D, int KPL>
-__global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(const __grid_constant__ SelParams p) {
-  extern __shared__ float smem[];
+__device__ __forceinline__ void select_strip(const SelParams& p, int64_t strip, float* smem) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t bh = blockIdx.x / p.strips;
-  const int i0 = static_cast<int>(blockIdx.x - bh * p.strips) * kStrip;
-  float* sc = p.scores ? p.scores + static_cast<int64_t>(blockIdx.x) * kStrip * p.pitch : smem;
+  const int64_t bh = strip / p.strips;
+  const int i0 = static_cast<int>(strip - bh * p.strips) * kStrip;
+  float* sc = p.scores ? p.scores + strip * kStrip * p.pitch : smem;
   __shared__ float3 k_max_w[kSelThreads / 32];
-  grid_wait();
 
   // the head's largest norms of the key blocks' parts (NaN counts as infinite)
   float3 km = make_float3(0.f, 0.f, 0.f);
@@ -654,8 +657,15 @@ __global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(c
     select_row<D, KPL>(p, bh, i0 + rr, sc + rr * p.pitch, k_max, lane);
 }
 
+template <int D, int KPL>
+__global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(const __grid_constant__ SelParams p) {
+  extern __shared__ float smem[];
+  grid_wait();
+  select_strip<D, KPL>(p, blockIdx.x, smem);
+}
+
 // Scores per lane that the variants of select_kernel hold in registers.
-constexpr int kRowRegs[] = {2, 8, 16, 20, 32};
+constexpr int kRowRegs[] = {2, 8, 16, 20, 40};
 
 struct Layout {
   int32_t nq, nk, strips, pitch;
@@ -699,17 +709,31 @@ Layout layout_of(const tsr_select_desc& s) {
   return l;
 }
 
-template <int D, int KPL>
-tsr_status launch_strips(const SelParams& sp, unsigned ctas, size_t smem, cudaStream_t st) {
-  auto kern = select_kernel<D, KPL>;
+template <typename Kern>
+tsr_status allow_smem(Kern kern, bool (&set)[64]) {
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  static bool attr_set[64] = {false};
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+  if (dev < 0 || dev >= 64 || !set[dev]) {
     TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripBytes));
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  TSR_CUDA(launch_dependent(kern, ctas, kSelThreads, smem, st, sp));
+  return TSR_OK;
+}
+
+template <int D, int KPL>
+tsr_status launch_variant(const PoolParams& pp, const SelParams& sp, int64_t heads, size_t smem, bool big_blocks,
+                          cudaStream_t st) {
+  constexpr int kWarps = kPoolThreads / 32;
+  // a CTA per block where a block holds more rows than a warp should read alone
+  // (256 rows are 64 kB at d = 128), or where there are too few blocks to fill the GPU
+  if (big_blocks || pp.n_units < 2048)
+    pool_kernel<D, true><<<static_cast<unsigned>(pp.n_units), kPoolThreads, 0, st>>>(pp);
+  else
+    pool_kernel<D, false><<<static_cast<unsigned>((pp.n_units + kWarps - 1) / kWarps), kPoolThreads, 0, st>>>(pp);
+  TSR_CUDA(cudaGetLastError());
+  static bool set[64] = {false};
+  if (tsr_status e = allow_smem(select_kernel<D, KPL>, set)) return e;
+  TSR_CUDA(launch_dependent(select_kernel<D, KPL>, static_cast<unsigned>(heads * sp.strips), kSelThreads, smem, st, sp));
   return TSR_OK;
 }
 
@@ -762,28 +786,25 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   sp.first = s.first;
   sp.diagonal = s.diagonal;
   const size_t smem = l.in_smem ? static_cast<size_t>(kStrip) * l.pitch * 4 : 0;
-  // a CTA per block where a block holds more rows than a warp should read alone
-  // (256 rows are 64 kB at d = 128), or where there are too few blocks to fill the GPU
-  constexpr int kWarps = kPoolThreads / 32;
-  if (std::max(s.bq, s.bk) > 256 || pp.n_units < 2048)
-    pool_kernel<D, true><<<static_cast<unsigned>(pp.n_units), kPoolThreads, 0, st>>>(pp);
-  else
-    pool_kernel<D, false><<<static_cast<unsigned>((pp.n_units + kWarps - 1) / kWarps), kPoolThreads, 0, st>>>(pp);
-  TSR_CUDA(cudaGetLastError());
-  // scores per lane held in registers: as many as a row has, up to 32
-  const unsigned ctas = static_cast<unsigned>(BH * l.strips);
-  if (l.nk <= 64) return launch_strips<D, 2>(sp, ctas, smem, st);
-  if (l.nk <= 256) return launch_strips<D, 8>(sp, ctas, smem, st);
-  if (l.nk <= 512) return launch_strips<D, 16>(sp, ctas, smem, st);
-  if (l.nk <= 640) return launch_strips<D, 20>(sp, ctas, smem, st);
-  if (l.nk <= 1024) return launch_strips<D, 32>(sp, ctas, smem, st);
-  return launch_strips<D, 0>(sp, ctas, smem, st);
+  const bool big = std::max(s.bq, s.bk) > 256;
+  // scores per lane held in registers: as many as a row has, up to 40
+  if (l.nk <= 64) return launch_variant<D, 2>(pp, sp, BH, smem, big, st);
+  if (l.nk <= 256) return launch_variant<D, 8>(pp, sp, BH, smem, big, st);
+  if (l.nk <= 512) return launch_variant<D, 16>(pp, sp, BH, smem, big, st);
+  if (l.nk <= 640) return launch_variant<D, 20>(pp, sp, BH, smem, big, st);
+  if (l.nk <= 1280) return launch_variant<D, 40>(pp, sp, BH, smem, big, st);
+  return launch_variant<D, 0>(pp, sp, BH, smem, big, st);
 }
 
 }  // namespace
 
 size_t select_workspace(const tsr_select_desc& s) { return layout_of(s).total; }
 
+// (Running one part of the heads' selection beside the next part's means, as stages
+// of a chain of dependent launches, measured 125 -> 144 us with two parts and 163
+// with four at 480p: a strip takes some 50 us in company, and each stage waits for
+// the last strips of the one before.)
+//
 // The arguments have been checked (api_ops.cu).
 tsr_status launch_select(const tsr_select_desc& s, const void* q, const void* k, uint8_t* blocks, void* ws,
                          cudaStream_t st) {

@@ -73,7 +73,11 @@ def qk(B, H, N, d, seed=0):
     (1, 1, 65, 64, 64, 16, 2),             # a block of one token
     (2, 1, 300, 64, 4096, 100, 2),         # one query block
     (1, 1, 300, 64, 100, 4096, 1),         # one key block
-    (1, 1, 14500, 64, 512, 16, 77),        # rows longer than shared memory holds
+    (1, 1, 20000, 64, 512, 16, 200),       # 1,250 blocks a row: the most that registers hold
+    (1, 1, 21000, 128, 300, 16, 77),       # more
+    (1, 1, 30000, 64, 512, 16, 700),       # rows longer than shared memory holds
+    (2, 3, 40000, 64, 64, 48, 31),         # long calls: means and selection of several
+    (1, 9, 32001, 128, 64, 64, 60),        # heads at once, uneven chunks of heads
 ])
 def test_against_exact_scores(B, H, N, d, bq, bk, keep):
     q, k = qk(B, H, N, d, seed=N + keep)
