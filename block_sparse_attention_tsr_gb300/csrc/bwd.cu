@@ -31,12 +31,12 @@
 // The 512 TMEM columns decide how far S and dP run ahead of the softmax:
 //   query items         S is free once the softmax holds it in registers; two dP
 //   key items, d = 64   two S (acc2 has to read P before an S may overwrite it), one dP
-//   key items, d = 128  the accumulators leave 256: one dP, and S in two halves of 64
-//                       columns, one per tile, each with its own eight softmax warps,
-//                       so that one half's acc2 and next S run during the other's
-//                       softmax.  (Half-wide S products cost as much as whole ones;
-//                       a whole S waits out the softmax, and half-wide dP as well
-//                       cost more than it gained.)
+//   key items, d = 128  the accumulators leave 256: one S, one dP
+// Where there is one of each, acc1 and the next dP wait for the next S: issued as they
+// come, the two threads' products fall together and then wait for the softmax
+// together (3,600 clocks a step, 3,460 in turn; 2,460 with whole-warp issuers).  S and
+// dP in 64-wide slots, or S alone in two halves, did not pay: a 64-wide product moves
+// 6 KB through shared memory where a 128-wide one moves 8.
 // Few items with long lists (short sequences of few heads): each list is cut in two
 // parts with a CTA each, whose fp32 accumulators go to the workspace; the part that
 // finishes last adds them up, in the parts' order.
@@ -798,11 +798,11 @@ tsr_status launch_backward(const BwdArgs& a, cudaStream_t st) {
   if (stat_blocks >= (int64_t{1} << 31)) return fail(TSR_ERR_UNSUPPORTED, "too many rows");
   const uint4 *o = static_cast<const uint4*>(a.out), *g = static_cast<const uint4*>(a.dout);
   if (D == 64)
-    bwd::bwd_stats_kernel<64><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np, p.arrived,
-                                                                               n_arrived);
+    bwd::bwd_stats_kernel<64><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np,
+                                                                           p.arrived, n_arrived);
   else
-    bwd::bwd_stats_kernel<128><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np, p.arrived,
-                                                                               n_arrived);
+    bwd::bwd_stats_kernel<128><<<static_cast<unsigned>(stat_blocks), 256, 0, st>>>(o, g, a.lse, nlse2, ndelta, rows, N, Np,
+                                                                           p.arrived, n_arrived);
   TSR_CUDA(cudaGetLastError());
   return D == 64 ? bwd::launch<64>(p, ctas, Q->device, st) : bwd::launch<128>(p, ctas, Q->device, st);
 }
