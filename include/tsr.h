@@ -287,7 +287,9 @@ tsr_status tsr_bsa_forward_batch(const tsr_request *reqs, int32_t n, void *strea
  * TSR_MASK_UNIFORM and TSR_MASK_SEGMENTS masks.  Other kinds, and masks whose
  * blocks are so small that 128 tokens overlap more than 8 of them (on the query or
  * the key side; blocks of 17 and 18 tokens can), give TSR_ERR_UNSUPPORTED when the
- * backward plan is made.
+ * backward plan is made.  (An SVG spatial head is a UNIFORM mask of frame_size
+ * blocks; a temporal head of radius 0 one of n_frames blocks, n_frames >= 16, over
+ * tensors in temporal-major order, tsr_temporal_permute.)
  *
  * With P = exp(q.k / sqrt(d) - lse) on the allowed pairs, dP = dO V^T and
  * delta = rowsum(dO o O):  dS = P o (dP - delta) / sqrt(d),

@@ -200,6 +200,32 @@ def test_a_layer_together():
     plan.device_status()
 
 
+def test_svg_heads_as_block_masks():
+    """An SVG layer's gradients through UNIFORM masks: spatial heads by frame, temporal
+    heads of radius 0 in temporal-major order by spatial position."""
+    F, S, d = 18, 40, 64
+    N = F * S
+    svg = W.svg_mask(1, 2, n_frames=F, frame_size=S, kinds=np.array([0, 1], np.int8))
+    x = inputs(svg, d, 41)
+    q, k, v, do = x
+    out, lse = tsr.tsr_bsa_forward(q, k, v, tsr.tsr_plan(gpu_mask(svg, d)))
+    by_frame = np.zeros((1, 1, F, F), np.uint8)
+    by_frame[0, 0, np.arange(F), np.arange(F)] = by_frame[0, 0, :, 0] = 1
+    by_place = np.eye(S, dtype=np.uint8)[None, None]
+    for h, (blocks, b) in enumerate(((by_frame, S), (by_place, F))):
+        spec = W.MaskSpec(W.MASK_UNIFORM, 1, 1, N, bq=b, bk=b, blocks=blocks)
+        one = [t[:, h:h + 1].contiguous() for t in (q, k, v, out, do)]
+        if h == 1:
+            one = [tsr.tsr_temporal_permute(t, torch.empty_like(t), F, S) for t in one]
+        o, l = tsr.tsr_bsa_forward(*one[:3], tsr.tsr_plan(gpu_mask(spec, d)))
+        lse_h = lse[:, h:h + 1].contiguous()
+        if h == 1:
+            lse_h = lse_h.view(1, 1, F, S).transpose(2, 3).reshape(1, 1, N).contiguous()
+        assert (o.float() - one[3].float()).abs().max() <= 2e-2 and (l - lse_h).abs().max() <= 1e-3 * l.abs().max()
+        g = tsr.tsr_bsa_backward(*one[:3], one[3], lse_h, one[4], tsr.tsr_backward_plan(gpu_mask(spec, d)))
+        compare(spec, (*one[:3], one[4]), g)
+
+
 def test_a_failed_update_is_refused_until_one_succeeds():
     spec = uniform(1, 1, 640, 64, 64, 0.4, 1, diag=True)
     x = inputs(spec, 64, 2)

@@ -73,6 +73,7 @@ def qk(B, H, N, d, seed=0):
     (1, 1, 65, 64, 64, 16, 2),             # a block of one token
     (2, 1, 300, 64, 4096, 100, 2),         # one query block
     (1, 1, 300, 64, 100, 4096, 1),         # one key block
+    (1, 1, 300, 64, 2 ** 31 - 1, 2 ** 31 - 1, 1),
     (1, 1, 20000, 64, 512, 16, 200),       # 1,250 blocks a row: the most that registers hold
     (1, 1, 21000, 128, 300, 16, 77),       # more
     (1, 1, 30000, 64, 512, 16, 700),       # rows longer than shared memory holds

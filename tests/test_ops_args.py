@@ -109,6 +109,8 @@ def test_select_refuses_bad_pointers(L):
     assert call(4096, 8192, 12288, 16384, n.value - 1) == INVALID
     assert b"too small" in L.tsr_last_error()
     assert L.tsr_block_select_workspace(None, ctypes.byref(n)) == INVALID
+    big, m = _select(bq=2 ** 31 - 1, bk=2 ** 31 - 1), ctypes.c_size_t(0)
+    assert L.tsr_block_select_workspace(ctypes.byref(big), ctypes.byref(m)) == 0 and 0 < m.value < n.value
     assert L.tsr_block_select_workspace(ctypes.byref(d), None) == INVALID
 
 
