@@ -657,6 +657,8 @@ __device__ __forceinline__ void select_strip(const SelParams& p, int64_t strip, 
     select_row<D, KPL>(p, bh, i0 + rr, sc + rr * p.pitch, k_max, lane);
 }
 
+// CTAs per SM (registers against warps to hide latency): with both kernels, 24 heads
+// at 480p, 64 x 64, and 720p, 128 x 128: two 135 / 219 us, three 129 / 211, four 133 / 216.
 template <int D, int KPL>
 __global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(const __grid_constant__ SelParams p) {
   extern __shared__ float smem[];
