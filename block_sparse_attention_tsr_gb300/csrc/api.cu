@@ -719,8 +719,7 @@ tsr_status tsr_attention_host(const tsr_mask* mask, const tsr_plan_opts* opts, c
     const int64_t nqb = (mask->kind == TSR_MASK_KEYLIST) ? (mask->N + mask->slice_m - 1) / mask->slice_m : 0;
     if (mask->kind == TSR_MASK_UNIFORM || mask->kind == TSR_MASK_SEGMENTS) {
       const int64_t per_head = (mask->kind == TSR_MASK_UNIFORM)
-                                   ? static_cast<int64_t>((mask->N + mask->bq - 1) / mask->bq) *
-                                         ((mask->N + mask->bk - 1) / mask->bk)
+                                   ? static_cast<int64_t>(n_blocks(mask->N, mask->bq)) * n_blocks(mask->N, mask->bk)
                                    : static_cast<int64_t>(mask->n_qseg) * mask->n_kseg;
       void* db;
       if (tsr_status s = hc.get(5, BH * per_head, &db)) return s;

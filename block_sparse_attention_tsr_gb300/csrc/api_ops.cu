@@ -42,8 +42,8 @@ tsr_status fill_backward(tsr_backward_plan_s* p, const tsr_mask* mask, cudaStrea
   tsr_mask t = *mask;
   int64_t nq, nk;
   if (mask->kind == TSR_MASK_UNIFORM) {
-    nq = (static_cast<int64_t>(mask->N) + mask->bq - 1) / mask->bq;
-    nk = (static_cast<int64_t>(mask->N) + mask->bk - 1) / mask->bk;
+    nq = n_blocks(mask->N, mask->bq);
+    nk = n_blocks(mask->N, mask->bk);
     t.bq = mask->bk;
     t.bk = mask->bq;
   } else {

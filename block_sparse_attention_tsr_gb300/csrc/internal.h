@@ -39,6 +39,14 @@ struct MaskDev {
   const int32_t* indices;
 };
 
+// Blocks of b tokens in N (N + b - 1 may pass 2^31).
+__host__ __device__ constexpr int32_t n_blocks(int32_t N, int32_t b) { return (N - 1) / b + 1; }
+
+// A UNIFORM mask's block size as MaskDev holds it: a block of 2^24 tokens holds any
+// sequence (N <= 2^24), and the planner's products of block sizes and indices (up to
+// 8 past the last block) stay in 32 bits.
+constexpr int32_t planned_block(int32_t b) { return b < (1 << 24) ? b : (1 << 24); }
+
 struct Regime {
   int32_t bn, stages, ctas, id;
   int32_t orient = TSR_ORIENT_ROWS;   // TSR_ORIENT_ROWS or TSR_ORIENT_KEYS

@@ -168,8 +168,8 @@ extern "C" tsr_status tsr_attention_noalloc(const tsr_mask* mask, const void* q,
   m.B = B;
   m.H = H;
   m.N = N;
-  m.bq = mask->bq;
-  m.bk = mask->bk;
+  m.bq = planned_block(mask->bq);
+  m.bk = planned_block(mask->bk);
   m.n_qseg = mask->n_qseg;
   m.n_kseg = mask->n_kseg;
   m.q_bounds = mask->q_bounds;
@@ -177,7 +177,7 @@ extern "C" tsr_status tsr_attention_noalloc(const tsr_mask* mask, const void* q,
   m.blocks = mask->blocks;
   const int64_t n_grid =
       (m.kind == TSR_MASK_UNIFORM)
-          ? static_cast<int64_t>(B) * H * ((N + m.bq - 1) / m.bq) * ((N + m.bk - 1) / m.bk)
+          ? static_cast<int64_t>(B) * H * n_blocks(N, m.bq) * n_blocks(N, m.bk)
           : static_cast<int64_t>(B) * H * m.n_qseg * m.n_kseg;
   if (tsr_status s = plan_count_into(m, nqt, cnt, tot, err, n_grid, st)) return s;
   unsigned long long host_tot[8];
@@ -195,7 +195,7 @@ extern "C" tsr_status tsr_attention_noalloc(const tsr_mask* mask, const void* q,
   tsr_plan_opts rows_only{};
   rows_only.orient = TSR_ORIENT_ROWS;
   Regime rg;
-  if (tsr_status s = resolve_regime(regime_lookup(m.kind, m.bq, m.bk, N, density, mask->d),
+  if (tsr_status s = resolve_regime(regime_lookup(m.kind, mask->bq, mask->bk, N, density, mask->d),
                                     &rows_only, mask->d, false, &rg))
     return s;
   const int which = (rg.bn == 64) ? 0 : 1;

@@ -214,8 +214,8 @@ __device__ KeyWindow key_window(const MaskDev& m, int h, int q0, int q1, int w) 
 
 __device__ void grid_dims(const MaskDev& m, int64_t* nqs, int64_t* nks) {
   if (m.kind == TSR_MASK_UNIFORM) {
-    *nqs = (m.N + m.bq - 1) / m.bq;
-    *nks = (m.N + m.bk - 1) / m.bk;
+    *nqs = n_blocks(m.N, m.bq);
+    *nks = n_blocks(m.N, m.bk);
   } else if (m.kind == TSR_MASK_SEGMENTS) {
     *nqs = m.n_qseg;
     *nks = m.n_kseg;
@@ -715,8 +715,8 @@ tsr_status plan_build(const tsr_mask* mask, const tsr_plan_opts* opts, tsr_plan_
   m.B = B;
   m.H = H;
   m.N = N;
-  m.bq = mask->bq;
-  m.bk = mask->bk;
+  m.bq = planned_block(mask->bq);
+  m.bk = planned_block(mask->bk);
   m.n_qseg = mask->n_qseg;
   m.n_kseg = mask->n_kseg;
   m.q_bounds = mask->q_bounds;
@@ -738,7 +738,7 @@ tsr_status plan_build(const tsr_mask* mask, const tsr_plan_opts* opts, tsr_plan_
   // GPU; SVG from the head kinds, whose host copy was queued by the caller)
   int64_t n_grid = 0;
   if (m.kind == TSR_MASK_UNIFORM) {
-    n_grid = static_cast<int64_t>(B) * H * ((N + m.bq - 1) / m.bq) * ((N + m.bk - 1) / m.bk);
+    n_grid = static_cast<int64_t>(B) * H * n_blocks(N, m.bq) * n_blocks(N, m.bk);
   } else if (m.kind == TSR_MASK_SEGMENTS) {
     n_grid = static_cast<int64_t>(B) * H * m.n_qseg * m.n_kseg;
   }
@@ -802,7 +802,7 @@ tsr_status plan_build(const tsr_mask* mask, const tsr_plan_opts* opts, tsr_plan_
 
   // 2. the regime: tile orientation (query rows per tile), width, pipeline
   Regime rg;
-  if (tsr_status s = resolve_regime(regime_lookup(m.kind, m.bq, m.bk, N, density, P->d), opts,
+  if (tsr_status s = resolve_regime(regime_lookup(m.kind, mask->bq, mask->bk, N, density, P->d), opts,
                                     P->d, false, &rg))
     return s;
   P->bn = rg.bn;

@@ -678,8 +678,8 @@ struct Layout {
 
 Layout layout_of(const tsr_select_desc& s) {
   Layout l;
-  l.nq = (s.N - 1) / s.bq + 1;                // N + bq - 1 may pass 2^31
-  l.nk = (s.N - 1) / s.bk + 1;
+  l.nq = n_blocks(s.N, s.bq);
+  l.nk = n_blocks(s.N, s.bk);
   l.strips = (l.nq + kStrip - 1) / kStrip;
   l.pitch = (l.nk + 31) / 32 * 32;           // whole chunks of 32,
   for (int kpl : kRowRegs)                   // as many as the kernel takes,
