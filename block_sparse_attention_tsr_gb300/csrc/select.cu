@@ -95,6 +95,12 @@ __device__ __forceinline__ void two_sum(uint64_t& s, uint64_t& e, uint64_t x) {
   s = t;
 }
 
+__device__ __forceinline__ void two_sum1(float& s, float& e, float x) {
+  const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+  s = t;
+}
+
 // Block means: one warp per block of rows of one head, or (SHARED: blocks of many
 // rows) the four warps of a CTA.  D / 8 lanes across a row, eight loads of 16 bytes
 // in flight per lane, no barrier between blocks.  Everything is fp32 pairs: fp64
@@ -172,6 +178,11 @@ __device__ __forceinline__ void pool_block(const PoolParams& p, int64_t unit, in
         ts = lane2(s[(k * CH + c) / 2], (k * CH + c) & 1);
         te = lane2(e[(k * CH + c) / 2], (k * CH + c) & 1);
       }
+    // the pair made unique (ts the sum rounded, te the rest): how the sum was split
+    // between them depends on the rows' order, and equal sums have to give equal means
+    const float rest = te;
+    te = 0.f;
+    two_sum1(ts, te, rest);
     float q, q2;
     if (exact) {                 // a power of two: exact
       q = ts * inv;
@@ -279,12 +290,6 @@ __device__ __forceinline__ float scale_of(float norm, double& back) {
   const int e = min(max(static_cast<int>((__float_as_uint(norm) >> 23) & 255u), 1), 253);
   back = __longlong_as_double(static_cast<int64_t>(e - 127 + 1023) << 52);
   return __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-}
-
-__device__ __forceinline__ void two_sum1(float& s, float& e, float x) {
-  const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
-  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
-  s = t;
 }
 
 // The order keys of four scores from the 48-bit means, by one warp: lanes 8 c .. 8 c

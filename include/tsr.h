@@ -525,9 +525,11 @@ tsr_status tsr_rope(const tsr_rope_desc *desc, const tsr_rope_tensor *tensors, i
  *     blocks[b][h][i][j] = 1 iff j is forced, or among the keep - |forced(i)|
  *                 highest s_ij of the others (ties: the lowest j), else 0.
  * A row so holds max(keep, |forced|) blocks (all when there are fewer).  The
- * selection is that of exact scores (48-bit means, fp64 where a fast bound does
- * not decide), so it does not depend on summation order.  Sums of bf16 values
- * must stay inside the fp32 range.
+ * order is that of scores computed, where a fast bound does not decide, from
+ * 48-bit means in pairs of fp32: within about 2^-46 |qm_i| |km_j| of the exact
+ * score.  Key blocks with equal sums have equal scores, in whatever order their
+ * rows are, as long as a block's sum fits 48 bits (from its largest partial sum
+ * to its smallest value).  Sums of bf16 values must stay inside the fp32 range.
  *
  * q, k: device bf16 [B][H][N][d], d in {64, 128}, 16-byte aligned.  blocks:
  * device uint8 [B][H][ceil(N/bq)][ceil(N/bk)], a TSR_MASK_UNIFORM mask's `blocks`.
