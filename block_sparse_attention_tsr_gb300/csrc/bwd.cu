@@ -225,9 +225,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
     const uint32_t dp_col = tmem + lanes + C::DP_COL + 32 * grp + (C::N_DP == 2 ? 128 * (j & 1) : 0);
     const uint32_t st = base + C::ST + (j & 1) * C::STAT + grp * 128;   // [-lse2 128][-delta 128]
     if (KEYS) {
-      if (!mbar_wait(smem_u32(&ctrl.st_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
+      if (!mbar_wait_warp(smem_u32(&ctrl.st_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
     }
-    if (!mbar_wait(smem_u32(&ctrl.s_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
+    if (!mbar_wait_warp(smem_u32(&ctrl.s_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
     tc_fence_after();
     uint32_t x[32];                          // S, then P, as float bits
     if (!none) {
@@ -270,7 +270,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full[ab]));
     }
-    if (!mbar_wait(smem_u32(&ctrl.dp_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
+    if (!mbar_wait_warp(smem_u32(&ctrl.dp_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
     tc_fence_after();
     if (on) {
       uint32_t pk[16];
@@ -316,7 +316,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
   // ---- epilogue: a quarter of the columns of each accumulator
   constexpr int W = D / 4;
   if (p.split > 1) {
-    if (ok && (n == 0 || mbar_wait(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err))) {
+    if (ok && (n == 0 || mbar_wait_warp(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err))) {
       tc_fence_after();
 #pragma unroll
       for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
@@ -338,7 +338,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       __threadfence();
     }
   } else if (ok && n > 0) {
-    if (mbar_wait(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err)) {
+    if (mbar_wait_warp(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err)) {
       tc_fence_after();
 #pragma unroll
       for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
@@ -455,7 +455,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
   const int32_t n = it.w - it.z, steps = (n + 1) / 2;
   const uint32_t elect = elect_lane();
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity, abort_flag, p.err));
+    return mbar_wait_warp(smem_u32(bar), parity, abort_flag, p.err);
   };
   // barriers of step j alternate, so that no phase runs two ahead of a waiter
   auto done = [&](uint64_t (&b)[2], int32_t j) { return wait(&b[j & 1], (j >> 1) & 1); };

@@ -88,6 +88,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same by a whole warp, whose lanes all leave alike: where one lane has given up
+// and another has not, the warp-wide instructions behind the wait (votes, tcgen05.ld,
+// __syncwarp) would be met by a part of the warp.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               uint32_t* err, uint64_t timeout_ns = kWaitTimeoutNs) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) return false;
+    if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > timeout_ns)) {
+      *abort_flag = 1;
+      atomicOr(err, DEV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

@@ -1,0 +1,39 @@
+"""Rules of the kernels that a run shows only when it goes wrong (a hang, a stale
+read), checked on their source."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_attention_tsr_gb300",
+                    "csrc")
+
+
+def source(name):
+    """A file's text without comments."""
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", open(os.path.join(CSRC, name)).read(), flags=re.S)
+
+
+def body(text, start):
+    """The braces that follow `start`."""
+    i = text.index("{", text.index(start))
+    depth = 0
+    for j in range(i, len(text)):
+        depth += (text[j] == "{") - (text[j] == "}")
+        if depth == 0:
+            return text[i:j + 1]
+    raise AssertionError(start)
+
+
+def test_backward_warps_leave_their_waits_together():
+    """The softmax warps use warp-wide instructions (votes, tcgen05.ld / st) behind
+    bounded waits that may give up: a wait decides for the whole warp."""
+    text = source("bwd.cu")
+    softmax = body(text, "void softmax_role(")
+    assert "mbar_wait_warp(" in softmax and not re.search(r"\bmbar_wait\(", softmax)
+    # the issuers too, but for the last wait, behind which a warp only ends
+    issuer = body(text, "void mma_role(")
+    assert len(re.findall(r"\bmbar_wait\(", issuer)) == 1
+    wait = body(source("ptx.cuh"), "bool mbar_wait_warp(")
+    for cond in re.findall(r"if \((.*)\)", wait):
+        assert re.match(r"__(all|any)_sync\(0xFFFFFFFFu, ", cond)
