@@ -128,6 +128,7 @@ EXPORTS = ("tsr_abi_version", "tsr_status_string", "tsr_last_error", "tsr_plan",
            "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope",
            "tsr_block_select_workspace", "tsr_block_select", "tsr_backward_plan",
            "tsr_backward_plan_update", "tsr_backward_plan_destroy", "tsr_backward_plan_device_status",
+           "tsr_backward_plan_test_stall",
            "tsr_bsa_backward_workspace", "tsr_bsa_backward", "tsr_attention_host",
            "tsr_release_host_buffers", "tsr_regime_load", "tsr_regime_lookup")
 
@@ -172,6 +173,7 @@ def lib():
         "tsr_backward_plan_update": ([P, P, P], ctypes.c_int),
         "tsr_backward_plan_destroy": ([P], ctypes.c_int),
         "tsr_backward_plan_device_status": ([P, P], ctypes.c_int),
+        "tsr_backward_plan_test_stall": ([P, I32], ctypes.c_int),
         "tsr_bsa_backward_workspace": ([P, P], ctypes.c_int),
         "tsr_bsa_backward": ([P] * 11 + [ctypes.c_size_t, P], ctypes.c_int),
         "tsr_attention_host": ([P, P, P, P, P, P, P], ctypes.c_int),
@@ -368,6 +370,10 @@ class BackwardPlan:
 
     def device_status(self, stream=None) -> None:
         _check(lib().tsr_backward_plan_device_status(self.handle, _stream_ptr(stream)))
+
+    def test_stall(self, where: int) -> None:
+        """Test only: see tsr_backward_plan_test_stall in include/tsr.h."""
+        _check(lib().tsr_backward_plan_test_stall(self.handle, int(where)))
 
     def destroy(self) -> None:
         if self.handle:

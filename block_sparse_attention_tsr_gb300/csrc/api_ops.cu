@@ -17,6 +17,7 @@ struct tsr_backward_plan_s {
   tsr_plan_t q = nullptr, k = nullptr;
   DevBuf blocks_t;
   bool ready = false;
+  int32_t stall = 0;            // test only
 };
 
 namespace {
@@ -212,6 +213,14 @@ tsr_status tsr_backward_plan_device_status(tsr_backward_plan_t plan, void* strea
   return tsr_plan_device_status(plan->q, stream);
 }
 
+tsr_status tsr_backward_plan_test_stall(tsr_backward_plan_t plan, int32_t where) {
+  set_error("");
+  if (!plan) return fail(TSR_ERR_INVALID_ARG, "plan is NULL");
+  if (where < 0 || where > 15) return fail(TSR_ERR_INVALID_ARG, "where must be TSR_BACKWARD_STALL_* bits");
+  plan->stall = where;
+  return TSR_OK;
+}
+
 tsr_status tsr_bsa_backward_workspace(tsr_backward_plan_t plan, size_t* bytes) {
   set_error("");
   if (!plan || !bytes) return fail(TSR_ERR_INVALID_ARG, "plan / bytes is NULL");
@@ -257,6 +266,7 @@ tsr_status tsr_bsa_backward(const void* q, const void* k, const void* v, const v
   a.dk = dk;
   a.dv = dv;
   a.workspace = workspace;
+  a.stall = plan->stall;
   a.plan_q = plan->q;
   a.plan_k = plan->k;
   return launch_backward(a, static_cast<cudaStream_t>(stream));

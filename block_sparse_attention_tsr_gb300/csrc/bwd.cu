@@ -73,6 +73,8 @@ struct Params {
   int32_t* arrived;                // split items: parts finished, [key items, query items]
   int32_t n_key_items, N, Np, split;
   float scale_log2, scale;
+  int32_t stall;                   // test only: TSR_BACKWARD_STALL_* bits
+  uint64_t timeout_ns;             // bound of every wait
 };
 
 // Shared memory and TMEM of an item.
@@ -103,6 +105,7 @@ struct alignas(8) Ctrl {
   uint64_t y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
   uint64_t st_full[2], st_empty[2];
   uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2], acc_full;
+  uint64_t never;              // never signalled (stall test)
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t last;                // split items: this CTA's part was the last of its item
@@ -225,9 +228,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
     const uint32_t dp_col = tmem + lanes + C::DP_COL + 32 * grp + (C::N_DP == 2 ? 128 * (j & 1) : 0);
     const uint32_t st = base + C::ST + (j & 1) * C::STAT + grp * 128;   // [-lse2 128][-delta 128]
     if (KEYS) {
-      if (!mbar_wait_warp(smem_u32(&ctrl.st_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
+      if (!mbar_wait_warp(smem_u32(&ctrl.st_full[ab]), phase, abort_flag, p.err, p.timeout_ns)) { ok = false; break; }
     }
-    if (!mbar_wait_warp(smem_u32(&ctrl.s_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
+    if (!mbar_wait_warp(smem_u32(&ctrl.s_full[ab]), phase, abort_flag, p.err, p.timeout_ns)) { ok = false; break; }
     tc_fence_after();
     uint32_t x[32];                          // S, then P, as float bits
     if (!none) {
@@ -270,7 +273,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full[ab]));
     }
-    if (!mbar_wait_warp(smem_u32(&ctrl.dp_full[ab]), phase, abort_flag, p.err)) { ok = false; break; }
+    if (!mbar_wait_warp(smem_u32(&ctrl.dp_full[ab]), phase, abort_flag, p.err, p.timeout_ns)) { ok = false; break; }
     tc_fence_after();
     if (on) {
       uint32_t pk[16];
@@ -316,7 +319,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
   // ---- epilogue: a quarter of the columns of each accumulator
   constexpr int W = D / 4;
   if (p.split > 1) {
-    if (ok && (n == 0 || mbar_wait_warp(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err))) {
+    if (ok && (n == 0 || mbar_wait_warp(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err, p.timeout_ns))) {
       tc_fence_after();
 #pragma unroll
       for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
@@ -338,7 +341,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
       __threadfence();
     }
   } else if (ok && n > 0) {
-    if (mbar_wait_warp(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err)) {
+    if (mbar_wait_warp(smem_u32(&ctrl.acc_full), 0, abort_flag, p.err, p.timeout_ns)) {
       tc_fence_after();
 #pragma unroll
       for (int w = 0; w < (KEYS ? 2 : 1); ++w) {
@@ -407,12 +410,12 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
       tile(map, dst, 0, k0, smem_u32(bar));
       if (parts == 2) tile(map, dst, 1, k1, smem_u32(bar));
     };
-    if (!mbar_wait(smem_u32(&ctrl.y1_empty[a]), ((j / C::S1) & 1) ^ 1, abort_flag, p.err)) break;
+    if (!mbar_wait(smem_u32(&ctrl.y1_empty[a]), ((j / C::S1) & 1) ^ 1, abort_flag, p.err, p.timeout_ns)) break;
     stream(y1, base + C::Y1 + a * C::TILE, &ctrl.y1_full[a]);
     ++i1;
     if (KEYS) {
       const uint32_t bar = smem_u32(&ctrl.st_full[j & 1]), dst = base + C::ST + (j & 1) * C::STAT;
-      if (!mbar_wait(smem_u32(&ctrl.st_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag, p.err)) break;
+      if (!mbar_wait(smem_u32(&ctrl.st_empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag, p.err, p.timeout_ns)) break;
       if (j == 0) grid_wait();
       mbar_arrive_expect_tx(bar, parts * 512);
       const int64_t o = static_cast<int64_t>(bh) * p.Np;
@@ -428,7 +431,7 @@ __device__ __forceinline__ void producer_role(const Params& p, Ctrl& ctrl, uint3
       stationary(x2, base + C::X2, &ctrl.x2_full);
       x2_issued = true;
     }
-    if (!mbar_wait(smem_u32(&ctrl.y2_empty[b]), ((j / C::S2) & 1) ^ 1, abort_flag, p.err)) break;
+    if (!mbar_wait(smem_u32(&ctrl.y2_empty[b]), ((j / C::S2) & 1) ^ 1, abort_flag, p.err, p.timeout_ns)) break;
     stream(y2, base + C::Y2 + b * C::TILE, &ctrl.y2_full[b]);
     ++i2;
   }
@@ -454,8 +457,10 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
   volatile int32_t* abort_flag = &ctrl.abort_flag;
   const int32_t n = it.w - it.z, steps = (n + 1) / 2;
   const uint32_t elect = elect_lane();
+  // test only: the step at which this issuer waits for a barrier that nobody signals
+  const int32_t stall = (p.stall & (FIRST ? 1 : 2) << (KEYS ? 0 : 2)) ? 1 : -1;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return mbar_wait_warp(smem_u32(bar), parity, abort_flag, p.err);
+    return mbar_wait_warp(smem_u32(bar), parity, abort_flag, p.err, p.timeout_ns);
   };
   // barriers of step j alternate, so that no phase runs two ahead of a waiter
   auto done = [&](uint64_t (&b)[2], int32_t j) { return wait(&b[j & 1], (j >> 1) & 1); };
@@ -492,6 +497,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
     };
     bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && (C::N_S == 1 || steps == 1 || do_s(1));
     for (int32_t j = 0; ok && j < steps; ++j) {
+      if (j == stall && !wait(&ctrl.never, 0)) break;
       if (KEYS && !y2_full(j)) break;
       if (!done(ctrl.p_full, j)) break;
       if (KEYS) {
@@ -511,6 +517,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
     };
     bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0) && (C::N_DP == 1 || steps == 1 || do_dp(1));
     for (int32_t j = 0; ok && j < steps; ++j) {
+      if (j == stall && !wait(&ctrl.never, 0)) break;
       if (!done(ctrl.ds_full, j)) break;
       // one S and one dP: acc1 and dP(j+1) wait for S(j+1), so that the pipe works on
       // them while the softmax has S(j+1) to work on, and on acc2 and S while it has dP
@@ -600,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   if (threadIdx.x == 0) {
     for (uint64_t* b : {&ctrl.x1_full, &ctrl.x2_full}) mbar_init(smem_u32(b), 1);
     mbar_init(smem_u32(&ctrl.acc_full), 2);
+    mbar_init(smem_u32(&ctrl.never), 1);
     for (int i = 0; i < 4; ++i) {
       for (uint64_t* b : {&ctrl.y1_full[i], &ctrl.y1_empty[i], &ctrl.y2_full[i]}) mbar_init(smem_u32(b), 1);
       mbar_init(smem_u32(&ctrl.y2_empty[i]), keys ? 2 : 1);     // dP, and acc2 of key items
@@ -788,6 +796,8 @@ tsr_status launch_backward(const BwdArgs& a, cudaStream_t st) {
   // d = 128, density 0.3: 4,096 tokens 42 -> 36 us; with 11 tiles to a part (2,048
   // tokens) 26 -> 27 us, the partial sums costing what the shorter lists save.
   const BwdLayout l = backward_layout(Q, K);
+  p.stall = a.stall;
+  p.timeout_ns = a.stall ? 100000000ull : kWaitTimeoutNs;
   p.split = std::max(Q->max_item_len, K->max_item_len) >= 16 * l.split ? l.split : 1;
   p.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + l.part);
   p.arrived = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + l.arrived);

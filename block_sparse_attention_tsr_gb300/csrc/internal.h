@@ -204,6 +204,7 @@ struct BwdArgs {
   const void* dout;
   void *dq, *dk, *dv;
   void* workspace;              // backward_workspace() bytes
+  int32_t stall;                // test only: TSR_BACKWARD_STALL_* bits
   const tsr_plan_impl *plan_q, *plan_k;
 };
 tsr_status launch_backward(const BwdArgs& a, cudaStream_t stream);

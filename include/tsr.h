@@ -324,6 +324,18 @@ tsr_status tsr_backward_plan_destroy(tsr_backward_plan_t plan);
 
 tsr_status tsr_backward_plan_device_status(tsr_backward_plan_t plan, void *stream);
 
+/* TEST ONLY (compare TSR_PLAN_TEST_STALL): in the plan's next calls an MMA issuer of
+   every key or query item (128-row tiles of keys or queries) that holds more than two
+   tiles waits, at its second step, on a barrier that is never signalled.  Every wait is
+   then bounded by 0.1 s: the items give up, free their resources and leave their
+   gradients unwritten, tsr_backward_plan_device_status returns TSR_ERR_TIMEOUT, and the
+   context stays usable.  where: these bits, 0 for normal calls. */
+#define TSR_BACKWARD_STALL_KEY_S 1     /* key items, the issuer of S and dV             */
+#define TSR_BACKWARD_STALL_KEY_DP 2    /* key items, the issuer of dP and dK            */
+#define TSR_BACKWARD_STALL_QUERY_S 4   /* query items, the issuer of S                  */
+#define TSR_BACKWARD_STALL_QUERY_DP 8  /* query items, the issuer of dP and dQ          */
+tsr_status tsr_backward_plan_test_stall(tsr_backward_plan_t plan, int32_t where);
+
 tsr_status tsr_bsa_backward_workspace(tsr_backward_plan_t plan, size_t *bytes /* HOST */);
 
 tsr_status tsr_bsa_backward(const void *q, const void *k, const void *v, const void *out, const float *lse,
