@@ -104,7 +104,7 @@ struct alignas(8) Ctrl {
   uint64_t x1_full, x2_full;
   uint64_t y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
   uint64_t st_full[2], st_empty[2];
-  uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2], acc_full;
+  uint64_t s_full[2], p_full[2], dp_full[2], ds_full[2], acc_full, final_bar;
   uint64_t never;              // never signalled (stall test)
   uint32_t tmem_base;
   int32_t abort_flag;
@@ -457,8 +457,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
   volatile int32_t* abort_flag = &ctrl.abort_flag;
   const int32_t n = it.w - it.z, steps = (n + 1) / 2;
   const uint32_t elect = elect_lane();
-  // test only: the step at which this issuer waits for a barrier that nobody signals
-  const int32_t stall = (p.stall & (FIRST ? 1 : 2) << (KEYS ? 0 : 2)) ? 1 : -1;
+  // test only: this issuer does one step, then waits for a barrier that nobody signals
+  const int32_t last = (p.stall & (FIRST ? 1 : 2) << (KEYS ? 0 : 2)) ? min(steps, 1) : steps;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_wait_warp(smem_u32(bar), parity, abort_flag, p.err, p.timeout_ns);
   };
@@ -487,6 +487,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
   auto y1 = [&](int32_t j) { return base + C::Y1 + (j % C::S1) * C::TILE; };
   auto y2 = [&](int32_t j) { return base + C::Y2 + (j % C::S2) * C::TILE; };
   auto y2_full = [&](int32_t j) { return wait(&ctrl.y2_full[j % C::S2], (j / C::S2) & 1); };
+  int32_t j = 0;                               // steps whose products are issued
   if constexpr (FIRST) {
     auto s_col = [&](int32_t j) { return static_cast<uint32_t>(C::S_COL + (C::N_S == 2 ? 128 * (j & 1) : 0)); };
     auto do_s = [&](int32_t j) -> bool {
@@ -495,9 +496,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       mma_commit(elect, smem_u32(&ctrl.s_full[j & 1]));
       return true;
     };
-    bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && (C::N_S == 1 || steps == 1 || do_s(1));
-    for (int32_t j = 0; ok && j < steps; ++j) {
-      if (j == stall && !wait(&ctrl.never, 0)) break;
+    const bool ok = steps > 0 && wait(&ctrl.x1_full, 0) && do_s(0) && (C::N_S == 1 || steps == 1 || do_s(1));
+    for (; ok && j < last; ++j) {
       if (KEYS && !y2_full(j)) break;
       if (!done(ctrl.p_full, j)) break;
       if (KEYS) {
@@ -515,9 +515,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       mma_commit(elect, smem_u32(&ctrl.y2_empty[j % C::S2]));
       return true;
     };
-    bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0) && (C::N_DP == 1 || steps == 1 || do_dp(1));
-    for (int32_t j = 0; ok && j < steps; ++j) {
-      if (j == stall && !wait(&ctrl.never, 0)) break;
+    const bool ok = steps > 0 && wait(&ctrl.x2_full, 0) && do_dp(0) && (C::N_DP == 1 || steps == 1 || do_dp(1));
+    for (; ok && j < last; ++j) {
       if (!done(ctrl.ds_full, j)) break;
       // one S and one dP: acc1 and dP(j+1) wait for S(j+1), so that the pipe works on
       // them while the softmax has S(j+1) to work on, and on acc2 and S while it has dP
@@ -528,11 +527,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Ctrl& ctrl, uint32_t b
       if (j + C::N_DP < steps && !do_dp(j + C::N_DP)) break;
     }
   }
-  // complete once everything that both threads issued has: the accumulators are
-  // whole (or, after an abort, TMEM can be released)
-  mma_commit(elect, smem_u32(&ctrl.acc_full));
+  // the accumulators are whole once all that both threads issued has completed; after
+  // an abort they are not, and only TMEM can be released
+  if (last < steps) wait(&ctrl.never, 0);
+  if (j == steps) mma_commit(elect, smem_u32(&ctrl.acc_full));
+  mma_commit(elect, smem_u32(&ctrl.final_bar));
   volatile int32_t no = 0;
-  mbar_wait(smem_u32(&ctrl.acc_full), 0, &no, p.err);
+  mbar_wait(smem_u32(&ctrl.final_bar), 0, &no, p.err);
 }
 
 // The sum of a split item's parts, by the warps that store the accumulators.
@@ -607,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_bwd_kernel(const __grid_const
   if (threadIdx.x == 0) {
     for (uint64_t* b : {&ctrl.x1_full, &ctrl.x2_full}) mbar_init(smem_u32(b), 1);
     mbar_init(smem_u32(&ctrl.acc_full), 2);
+    mbar_init(smem_u32(&ctrl.final_bar), 2);
     mbar_init(smem_u32(&ctrl.never), 1);
     for (int i = 0; i < 4; ++i) {
       for (uint64_t* b : {&ctrl.y1_full[i], &ctrl.y1_empty[i], &ctrl.y2_full[i]}) mbar_init(smem_u32(b), 1);

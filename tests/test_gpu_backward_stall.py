@@ -22,6 +22,17 @@ def _lib():
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("H,N", [(2, 700), (1, 2100)])       # the second: items in two parts
 def test_bounded_wait_reports_timeout_and_context_survives(H, N, d, where):
+    stall_and_recover(H, N, d, where)
+
+
+@pytest.mark.parametrize("where", [KEY_S, KEY_DP, QUERY_S, QUERY_DP])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_that_lack_the_last_step_are_not_stored(d, where):
+    """Lists of two steps: the softmax is through both when the issuer gives up."""
+    stall_and_recover(2, 250, d, where)
+
+
+def stall_and_recover(H, N, d, where):
     n = W.cdiv(N, 64)
     mask = tsr.make_mask(tsr.UNIFORM, 1, H, N, d, bq=64, bk=64,
                          blocks=torch.ones((1, H, n, n), dtype=torch.uint8, device="cuda"))
