@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
       }
     };
     auto wait_free = [&](uint32_t bar, uint32_t parity) -> bool {
-      return mbar_wait(bar, parity, abort_flag, p.err, p.timeout_ns);
+      return mbar_wait_warp(bar, parity, abort_flag, p.err, p.timeout_ns);
     };
     while (ok) {
       int32_t it = 0;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
       it = __shfl_sync(0xFFFFFFFFu, it, 0);
       const bool done = it >= p.n_items;
       const int slot = item_seq & 1;
-      if (!mbar_wait(smem_u32(&ctrl.item_empty[slot]), ((item_seq >> 1) & 1) ^ 1, abort_flag, p.err, p.timeout_ns)) break;
+      if (!mbar_wait_warp(smem_u32(&ctrl.item_empty[slot]), ((item_seq >> 1) & 1) ^ 1, abort_flag, p.err, p.timeout_ns)) break;
       if (lane == 0) {
         ctrl.item_slot[slot] = done ? -1 : it;
         mbar_arrive(smem_u32(&ctrl.item_full[slot]));
@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
     if (WHOLE_WARP || lane == 0) {
       const uint32_t elect = WHOLE_WARP ? elect_lane() : 1u;
       auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait(bar, parity, abort_flag, p.err, p.timeout_ns);
-        return WHOLE_WARP ? __all_sync(0xFFFFFFFFu, ok) != 0 : ok;
+        return WHOLE_WARP ? mbar_wait_warp(bar, parity, abort_flag, p.err, p.timeout_ns)
+                          : mbar_wait(bar, parity, abort_flag, p.err, p.timeout_ns);
       };
       uint32_t item_seq = 0, kv_cnt = 0, t_cnt = 0, q_cnt = 0, o_cnt = 0;
       bool ok = true;
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
     bool ok = true;
     while (ok) {
       const int slot = item_seq & 1;
-      if (!mbar_wait(smem_u32(&ctrl.item_full[slot]), (item_seq >> 1) & 1, abort_flag, p.err, p.timeout_ns)) break;
+      if (!mbar_wait_warp(smem_u32(&ctrl.item_full[slot]), (item_seq >> 1) & 1, abort_flag, p.err, p.timeout_ns)) break;
       const int32_t it = ctrl.item_slot[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.item_empty[slot]));
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
             dn1 = __ldg(&rq.descs[2 * desc_next + 1]);
           }
         }
-        if (!mbar_wait(smem_u32(&ctrl.s_full[sb]), (t >> 1) & 1, abort_flag, p.err, p.timeout_ns)) {
+        if (!mbar_wait_warp(smem_u32(&ctrl.s_full[sb]), (t >> 1) & 1, abort_flag, p.err, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
         // Rows that had no finite maximum before hold O = 0 and need nothing.
         const bool fix_o = fix && j > 0;
         if (__any_sync(0xFFFFFFFFu, fix_o)) {
-          if (!mbar_wait(smem_u32(&ctrl.pv_done), (t - 1) & 1, abort_flag, p.err, p.timeout_ns)) {
+          if (!mbar_wait_warp(smem_u32(&ctrl.pv_done), (t - 1) & 1, abort_flag, p.err, p.timeout_ns)) {
             ok = false;
             break;
           }
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
         // layout [unit][d / 4][row] of float4: a warp's rows are adjacent
         float4* po = reinterpret_cast<float4*>(rq.part_o + unit * kBM * D) + r;
         if (n > 0) {
-          if (!mbar_wait(smem_u32(&ctrl.o_full), o_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
+          if (!mbar_wait_warp(smem_u32(&ctrl.o_full), o_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
           ++o_seq;
           tc_fence_after();
 #pragma unroll
@@ -797,12 +797,12 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
         // every row of the part is written: count the part
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctrl.split_bar));
-        if (!mbar_wait(smem_u32(&ctrl.split_bar), split_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
+        if (!mbar_wait_warp(smem_u32(&ctrl.split_bar), split_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
         ++split_seq;
         if (r == 0) ctrl.split_last = (atomicAdd(rq.part_cnt + i1.y, 1) == i1.z - 1) ? 1 : 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctrl.split_bar));
-        if (!mbar_wait(smem_u32(&ctrl.split_bar), split_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
+        if (!mbar_wait_warp(smem_u32(&ctrl.split_bar), split_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
         ++split_seq;
         if (ctrl.split_last && valid) {
           __threadfence();
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(192, CTAS) bsa_fwd_kernel(const __grid_constan
       if (n > 0) {
         // o_full completes once per non-empty item, after its last PV; the next
         // item's first PV waits for o_empty, so the phases cannot run ahead.
-        if (!mbar_wait(smem_u32(&ctrl.o_full), o_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
+        if (!mbar_wait_warp(smem_u32(&ctrl.o_full), o_seq & 1, abort_flag, p.err, p.timeout_ns)) break;
         ++o_seq;
         tc_fence_after();
 #pragma unroll

@@ -372,17 +372,29 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_fwd_t_kernel(const __grid_con
   const uint32_t tmem = ctrl.tmem_base;
   // Bounded wait on an mbarrier phase; the wait that times out first records
   // its site (bit 8 + site of the error word) next to DEV_ERR_TIMEOUT.
+  auto timed_out = [&](int site) -> bool {
+    *abort_flag = 1;
+    atomicOr(p.err, DEV_ERR_TIMEOUT | (1u << (8 + site)));
+    return false;
+  };
+  // By a whole warp, whose lanes leave alike (mbar_wait_warp, ptx.cuh).
   auto wait = [&](uint32_t bar, uint32_t parity, int site) -> bool {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) return false;
+      if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > p.timeout_ns)) return timed_out(site);
+    }
+  };
+  // By one thread.
+  auto wait_one = [&](uint32_t bar, uint32_t parity, int site) -> bool {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
       if (mbar_try_wait(bar, parity)) return true;
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > p.timeout_ns) {
-        *abort_flag = 1;
-        atomicOr(p.err, DEV_ERR_TIMEOUT | (1u << (8 + site)));
-        return false;
-      }
+      if (globaltimer_ns() - t0 > p.timeout_ns) return timed_out(site);
     }
   };
 
@@ -487,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_fwd_t_kernel(const __grid_con
       uint32_t gq = 0, gp = 0;                            // QKs / PVs issued for the group
       int64_t tiles = 0;
       bool ok = true;
-      if (p.test_stall) ok = wait(smem_u32(&ctrl.never), 0, 4);
+      if (p.test_stall) ok = wait_one(smem_u32(&ctrl.never), 0, 4);
       while (ok) {
         const int slot = seq & 1;
-        if (!wait(smem_u32(&ctrl.item_full[slot]), (seq >> 1) & 1, 5)) break;
+        if (!wait_one(smem_u32(&ctrl.item_full[slot]), (seq >> 1) & 1, 5)) break;
         const int32_t it = ctrl.item_slot[slot];
         mbar_arrive(smem_u32(&ctrl.item_empty[slot]));
         ++seq;
@@ -504,13 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_fwd_t_kernel(const __grid_con
         if (ns == 0) continue;
         const bool gath = GATHER || (PERM && i1.x != 0);
         const int32_t nt = (ns - g + 1) >> 1;             // this group's steps in the item
-        if (!wait(smem_u32(&ctrl.q_full), qc & 1, 6)) break;
+        if (!wait_one(smem_u32(&ctrl.q_full), qc & 1, 6)) break;
         ++qc;
         if (nt == 0) {
           // a one-step item leaves group 1 without work: it releases the query
           // tile and takes the item's O^T phases without MMAs
           mbar_arrive(smem_u32(&ctrl.q_empty));
-          if (!wait(smem_u32(&ctrl.o_empty), (oc & 1) ^ 1, 10)) break;
+          if (!wait_one(smem_u32(&ctrl.o_empty), (oc & 1) ^ 1, 10)) break;
           ++oc;
           mbar_arrive(smem_u32(&ctrl.o_full));
           continue;
@@ -519,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_fwd_t_kernel(const __grid_con
         for (int32_t t = 0; t <= nt && ok; ++t) {
           if (t < nt) {
             // S^T = K Q^T for group step t (K slot g)
-            if (!wait(smem_u32(&ctrl.k_full[g]), kc & 1, 7)) { ok = false; break; }
+            if (!wait_one(smem_u32(&ctrl.k_full[g]), kc & 1, 7)) { ok = false; break; }
             ++kc;
             if (gath) fence_proxy_async_smem();
             tc_fence_after();
@@ -540,13 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_fwd_t_kernel(const __grid_con
             // O^T += V^T P^T for group step t - 1 (V slot g)
             const int32_t tt = t - 1;
             const uint32_t pb = gp & 1;                   // the group's P^T buffer of this step
-            if (!wait(smem_u32(&ctrl.p_full[g][pb]), (gp >> 1) & 1, 8)) { ok = false; break; }
-            if (!wait(smem_u32(&ctrl.v_full[g]), vc & 1, 9)) { ok = false; break; }
+            if (!wait_one(smem_u32(&ctrl.p_full[g][pb]), (gp >> 1) & 1, 8)) { ok = false; break; }
+            if (!wait_one(smem_u32(&ctrl.v_full[g]), vc & 1, 9)) { ok = false; break; }
             ++vc;
             if (gath) fence_proxy_async_smem();
             if (tt == 0) {
               // the previous item's epilogue has read both groups' O^T
-              if (!wait(smem_u32(&ctrl.o_empty), (oc & 1) ^ 1, 10)) { ok = false; break; }
+              if (!wait_one(smem_u32(&ctrl.o_empty), (oc & 1) ^ 1, 10)) { ok = false; break; }
               ++oc;
             }
             tc_fence_after();

@@ -37,3 +37,18 @@ def test_backward_warps_leave_their_waits_together():
     wait = body(source("ptx.cuh"), "bool mbar_wait_warp(")
     for cond in re.findall(r"if \((.*)\)", wait):
         assert re.match(r"__(all|any)_sync\(0xFFFFFFFFu, ", cond)
+
+
+def test_forward_warps_leave_their_waits_together():
+    """The same in the forward kernels.  A wait by single lanes is left where one lane
+    acts (the issuers) and at a warp's end (`dummy`: no abort flag, nothing behind it)."""
+    text = source("fwd_kernel.cuh")
+    single = [l for l in text.splitlines() if re.search(r"\bmbar_wait\(", l) and "dummy" not in l]
+    assert len(single) == 1 and ": mbar_wait(bar, parity" in single[0]      # a single issuing lane's
+    text = source("fwd_t_kernel.cuh")
+    assert all("dummy" in l for l in text.splitlines() if re.search(r"\bmbar_wait\(", l))
+    for cond in re.findall(r"if \((.*)\) return", body(text, "auto wait = [&]")):
+        assert re.match(r"__(all|any)_sync\(0xFFFFFFFFu, ", cond)
+    issuers = body(text, "if (warp == 1 || warp == 11)")
+    one_lane = body(issuers, "if (lane == 0)")
+    assert not re.search(r"\bwait\(", issuers) and one_lane.count("wait_one(") == text.count("wait_one(")
