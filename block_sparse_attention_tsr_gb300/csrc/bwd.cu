@@ -193,8 +193,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Ctrl& ctrl, uint32
   const bool valid = row < p.N;
   float nlse = 0.f, ndelta = 0.f;
   if (!KEYS) {
-    nlse = valid ? __ldg(p.nlse2 + static_cast<int64_t>(it.x) * p.Np + row) : -INFINITY;
-    ndelta = valid ? __ldg(p.ndelta + static_cast<int64_t>(it.x) * p.Np + row) : 0.f;
+    // plain loads: this kernel is resident while bwd_stats_kernel writes them, and
+    // __ldg is for data that stays as it is for a kernel's whole life
+    nlse = valid ? p.nlse2[static_cast<int64_t>(it.x) * p.Np + row] : -INFINITY;
+    ndelta = valid ? p.ndelta[static_cast<int64_t>(it.x) * p.Np + row] : 0.f;
   }
   // The tile's descriptor is loaded one step ahead, its index two, so that no load is
   // waited for where it is issued.

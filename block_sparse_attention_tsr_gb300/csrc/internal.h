@@ -229,7 +229,8 @@ int num_sms(int device);
 
 // Launch a kernel that may start while the stream's previous kernel finishes
 // (programmatic dependent launch): it has to call grid_wait() before it touches
-// anything that kernel reads or writes.
+// anything that kernel reads or writes, and then reads what that kernel wrote with
+// plain loads (__ldg may be moved above the wait).
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
                              A&&... args) {

@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(kPoolThreads, 8) pool_kernel(const __grid_cons
   if (unit < p.n_units) pool_block<D, SHARED>(p, unit, warp, lane);
 }
 
+// What pool_kernel writes is read with plain loads: select_kernel is resident while it
+// still writes, and __ldg is for data that stays as it is for a kernel's whole life.
 struct SelParams {
   const float *q_hi, *q_lo, *k_hi, *k_lo;
   const float4 *q_norm, *k_norm;
@@ -303,14 +305,14 @@ __device__ __forceinline__ uint64_t exact_keys(const float* qh, const float* ql,
   double q_back, k_back;
   const bool on = j >= 0;
   const int64_t o = static_cast<int64_t>(on ? j : 0);
-  const float q_scale = scale_of(q_norm, q_back), k_scale = scale_of(__ldg(&k_norm[o].x), k_back);
+  const float q_scale = scale_of(q_norm, q_back), k_scale = scale_of(k_norm[o].x, k_back);
   float s = 0.f, e = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const int c = i * 8 + (lane & 7);           // float4 of channels
-    const float4 a = __ldg(reinterpret_cast<const float4*>(qh) + c), b = __ldg(reinterpret_cast<const float4*>(ql) + c);
-    const float4 x = __ldg(reinterpret_cast<const float4*>(kh + o * D) + c);
-    const float4 y = __ldg(reinterpret_cast<const float4*>(kl + o * D) + c);
+    const float4 a = reinterpret_cast<const float4*>(qh)[c], b = reinterpret_cast<const float4*>(ql)[c];
+    const float4 x = reinterpret_cast<const float4*>(kh + o * D)[c];
+    const float4 y = reinterpret_cast<const float4*>(kl + o * D)[c];
     const float ah[4] = {a.x, a.y, a.z, a.w}, al[4] = {b.x, b.y, b.z, b.w};
     const float xh[4] = {x.x, x.y, x.z, x.w}, xl[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -376,7 +378,7 @@ __device__ __forceinline__ void select_row(const SelParams& p, int64_t bh, int i
     return;
   }
   // the last two terms cover values that the bf16 terms or their products flush
-  const float4 qn = __ldg(p.q_norm + bh * p.nq + i);
+  const float4 qn = p.q_norm[bh * p.nq + i];
   const float q_norm = qn.x;
   const float err2 = 2.002f * (kSumErr * (q_norm * k_max.x) + qn.z * k_max.x + q_norm * k_max.z + qn.y * k_max.y +
                                4e-37f * (q_norm + k_max.x) + 1e-36f);
@@ -597,7 +599,7 @@ __device__ __forceinline__ void select_strip(const SelParams& p, int64_t strip, 
   // the head's largest norms of the key blocks' parts (NaN counts as infinite)
   float3 km = make_float3(0.f, 0.f, 0.f);
   for (int j = threadIdx.x; j < p.nk; j += kSelThreads) {
-    const float4 x = __ldg(p.k_norm + bh * p.nk + j);
+    const float4 x = p.k_norm[bh * p.nk + j];
     km.x = x.x <= FLT_MAX ? fmaxf(km.x, x.x) : INFINITY;
     if (km.x > FLT_MAX) break;
     km.y = fmaxf(km.y, x.y);
@@ -621,7 +623,7 @@ __device__ __forceinline__ void select_strip(const SelParams& p, int64_t strip, 
     for (int x = threadIdx.x; x < 2 * KK * 32; x += kSelThreads) {
       const int group = i0 / 8 + x / (KK * 32);
       frag[x / (KK * 32)][x / 32 % KK][lane] =
-          group < p.q_frag_rows / 8 ? __ldg(p.q_frag + (bh * (p.q_frag_rows / 8) + group) * KK * 32 + x % (KK * 32))
+          group < p.q_frag_rows / 8 ? p.q_frag[(bh * (p.q_frag_rows / 8) + group) * KK * 32 + x % (KK * 32)]
                                     : make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
@@ -632,7 +634,7 @@ __device__ __forceinline__ void select_strip(const SelParams& p, int64_t strip, 
       float c0[2][4] = {}, c1[2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
-        const uint4 b0 = __ldg(kf + (j * KK + kk) * 32), b1 = __ldg(kf + (j1 * KK + kk) * 32);
+        const uint4 b0 = kf[(j * KK + kk) * 32], b1 = kf[(j1 * KK + kk) * 32];
         const uint4 a0 = frag[0][kk][lane], a1 = frag[1][kk][lane];
         const uint4 ah = make_uint4(a0.x, a1.x, a0.z, a1.z), al = make_uint4(a0.y, a1.y, a0.w, a1.w);
         mma_16816(c0[0], ah, b0.x, b0.z);

@@ -52,3 +52,21 @@ def test_forward_warps_leave_their_waits_together():
     issuers = body(text, "if (warp == 1 || warp == 11)")
     one_lane = body(issuers, "if (lane == 0)")
     assert not re.search(r"\bwait\(", issuers) and one_lane.count("wait_one(") == text.count("wait_one(")
+
+
+@pytest.mark.parametrize("name,first,second", [("select.cu", "struct PoolParams", "struct SelParams"),
+                                               ("bwd.cu", None, "struct Params")])
+def test_dependent_kernels_read_their_predecessor_with_plain_loads(name, first, second):
+    """A kernel started by launch_dependent is resident while the one before it still
+    writes; the read-only path (__ldg, const __restrict__) is not for that data."""
+    text = source(name)
+    assert "launch_dependent(" in text
+    fields = re.sub(r"\s+", " ", body(text, second))
+    assert "__restrict__" not in fields
+    if name == "select.cu":
+        # everything behind its parameters reads pool_kernel's output only
+        dependent = text[text.index(second):]
+    else:
+        dependent = "\n".join(l for l in text.splitlines() if re.search(r"p\.(nlse2|ndelta|part|arrived)\b", l))
+        assert "p.nlse2[" in dependent
+    assert "__ldg" not in dependent and "ld.global.nc" not in dependent
