@@ -5,8 +5,9 @@
 //   kept(i) = forced(i) + the highest s_ij of the others, ties to the lowest j
 //
 // Two kernels.  pool_kernel reads Q and K once (the bound: HBM) and writes the
-// block means; select_kernel computes a strip of scores and picks from it, the
-// scores never leaving shared memory.
+// block means; select_kernel computes the scores of a strip of 16 query blocks and
+// picks from them.  The scores stay in shared memory, for rows of more than 1,628
+// blocks in a slot per CTA of the workspace.
 //
 // Exactness.  Which block is kept last turns on differences between scores that
 // fp32 sums do not resolve, so the selection is made exact in two steps.  The
@@ -43,7 +44,12 @@ constexpr float kSumErr = 2e-5f;
 constexpr int kPoolThreads = 128;
 constexpr int kSelThreads = 256;
 constexpr int kStrip = 16;            // query blocks per CTA of select_kernel
-constexpr int kStripBytes = 112 * 1024;   // a strip's scores, two CTAs per SM
+// A strip's scores in shared memory: two CTAs per SM, each with the 8 KB of fragments,
+// the largest norms and 1 KB of the system's beside them (1,628 blocks a row).
+constexpr int kStripBytes = 104 * 1024;
+// Strips of longer rows have their scores in the workspace, one slot per CTA that is
+// resident (152 SMs x 3); each CTA takes strip after strip.
+constexpr int kScoreSlots = 456;
 
 struct PoolParams {
   const uint4* x[2];            // Q and K
@@ -257,8 +263,9 @@ struct SelParams {
   const float4 *q_norm, *k_norm;
   const uint4 *q_frag, *k_frag;
   int32_t q_frag_rows, k_frag_rows;
-  float* scores;        // [CTA][kStrip][pitch] when the strip does not fit shared memory
+  float* scores;        // [CTA][kStrip][pitch] where a strip does not fit shared memory
   uint8_t* blocks;
+  int64_t n_strips;     // of all heads
   int32_t N, bq, bk, nq, nk, strips, pitch;
   int32_t keep, first, diagonal;
 };
@@ -593,7 +600,7 @@ __device__ __forceinline__ void select_strip(const SelParams& p, int64_t strip, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t bh = strip / p.strips;
   const int i0 = static_cast<int>(strip - bh * p.strips) * kStrip;
-  float* sc = p.scores ? p.scores + strip * kStrip * p.pitch : smem;
+  float* sc = KPL == 0 && p.scores ? p.scores + static_cast<int64_t>(blockIdx.x) * kStrip * p.pitch : smem;
   __shared__ float3 k_max_w[kSelThreads / 32];
 
   // the head's largest norms of the key blocks' parts (NaN counts as infinite)
@@ -670,7 +677,14 @@ template <int D, int KPL>
 __global__ void __launch_bounds__(kSelThreads, KPL > 20 ? 2 : 3) select_kernel(const __grid_constant__ SelParams p) {
   extern __shared__ float smem[];
   grid_wait();
-  select_strip<D, KPL>(p, blockIdx.x, smem);
+  if constexpr (KPL > 0) {
+    select_strip<D, KPL>(p, blockIdx.x, smem);
+  } else {
+    for (int64_t strip = blockIdx.x; strip < p.n_strips; strip += gridDim.x) {
+      select_strip<D, KPL>(p, strip, smem);
+      __syncthreads();                          // before its scores and fragments are overwritten
+    }
+  }
 }
 
 // Scores per lane that the variants of select_kernel hold in registers.
@@ -713,7 +727,7 @@ Layout layout_of(const tsr_select_desc& s) {
   l.k_frag_rows = (l.nk + 7) / 8 * 8;
   l.q_frag = take(BH * l.q_frag_rows * s.d);
   l.k_frag = take(BH * l.k_frag_rows * s.d);
-  l.scores = take(l.in_smem ? 0 : BH * l.strips * kStrip * l.pitch);
+  l.scores = take(l.in_smem ? 0 : std::min<size_t>(kScoreSlots, BH * l.strips) * kStrip * l.pitch);
   l.total = at;
   return l;
 }
@@ -730,8 +744,7 @@ tsr_status allow_smem(Kern kern, bool (&set)[64]) {
 }
 
 template <int D, int KPL>
-tsr_status launch_variant(const PoolParams& pp, const SelParams& sp, int64_t heads, size_t smem, bool big_blocks,
-                          cudaStream_t st) {
+tsr_status launch_variant(const PoolParams& pp, const SelParams& sp, size_t smem, bool big_blocks, cudaStream_t st) {
   constexpr int kWarps = kPoolThreads / 32;
   // a CTA per block where a block holds more rows than a warp should read alone
   // (256 rows are 64 kB at d = 128), or where there are too few blocks to fill the GPU
@@ -740,9 +753,11 @@ tsr_status launch_variant(const PoolParams& pp, const SelParams& sp, int64_t hea
   else
     pool_kernel<D, false><<<static_cast<unsigned>((pp.n_units + kWarps - 1) / kWarps), kPoolThreads, 0, st>>>(pp);
   TSR_CUDA(cudaGetLastError());
+  const unsigned ctas =
+      static_cast<unsigned>(sp.scores ? std::min<int64_t>(kScoreSlots, sp.n_strips) : sp.n_strips);
   static bool set[64] = {false};
   if (tsr_status e = allow_smem(select_kernel<D, KPL>, set)) return e;
-  TSR_CUDA(launch_dependent(select_kernel<D, KPL>, static_cast<unsigned>(heads * sp.strips), kSelThreads, smem, st, sp));
+  TSR_CUDA(launch_dependent(select_kernel<D, KPL>, ctas, kSelThreads, smem, st, sp));
   return TSR_OK;
 }
 
@@ -790,6 +805,7 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   sp.nq = l.nq;
   sp.nk = l.nk;
   sp.strips = l.strips;
+  sp.n_strips = BH * l.strips;
   sp.pitch = l.pitch;
   sp.keep = s.keep;
   sp.first = s.first;
@@ -797,12 +813,12 @@ tsr_status launch(const tsr_select_desc& s, const Layout& l, const void* q, cons
   const size_t smem = l.in_smem ? static_cast<size_t>(kStrip) * l.pitch * 4 : 0;
   const bool big = std::max(s.bq, s.bk) > 256;
   // scores per lane held in registers: as many as a row has, up to 40
-  if (l.nk <= 64) return launch_variant<D, 2>(pp, sp, BH, smem, big, st);
-  if (l.nk <= 256) return launch_variant<D, 8>(pp, sp, BH, smem, big, st);
-  if (l.nk <= 512) return launch_variant<D, 16>(pp, sp, BH, smem, big, st);
-  if (l.nk <= 640) return launch_variant<D, 20>(pp, sp, BH, smem, big, st);
-  if (l.nk <= 1280) return launch_variant<D, 40>(pp, sp, BH, smem, big, st);
-  return launch_variant<D, 0>(pp, sp, BH, smem, big, st);
+  if (l.nk <= 64) return launch_variant<D, 2>(pp, sp, smem, big, st);
+  if (l.nk <= 256) return launch_variant<D, 8>(pp, sp, smem, big, st);
+  if (l.nk <= 512) return launch_variant<D, 16>(pp, sp, smem, big, st);
+  if (l.nk <= 640) return launch_variant<D, 20>(pp, sp, smem, big, st);
+  if (l.nk <= 1280) return launch_variant<D, 40>(pp, sp, smem, big, st);
+  return launch_variant<D, 0>(pp, sp, smem, big, st);
 }
 
 }  // namespace
