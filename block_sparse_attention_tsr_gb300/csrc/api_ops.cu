@@ -83,7 +83,10 @@ tsr_status check_select(const tsr_select_desc* s) {
   if (s->keep < 1) return fail(TSR_ERR_INVALID_ARG, "keep must be >= 1");
   if (s->first < 0) return fail(TSR_ERR_INVALID_ARG, "first must be >= 0");
   if (s->N > (1 << 24)) return fail(TSR_ERR_UNSUPPORTED, "N above 2^24");
-  if (static_cast<int64_t>(s->B) * s->H > (1 << 20)) return fail(TSR_ERR_UNSUPPORTED, "B*H above 2^20");
+  const int64_t heads = static_cast<int64_t>(s->B) * s->H;
+  if (heads > (1 << 20)) return fail(TSR_ERR_UNSUPPORTED, "B*H above 2^20");
+  if (heads * (static_cast<int64_t>(n_blocks(s->N, s->bq)) + n_blocks(s->N, s->bk)) >= (int64_t{1} << 31))
+    return fail(TSR_ERR_UNSUPPORTED, "more than 2^31 blocks");
   return TSR_OK;
 }
 

@@ -834,9 +834,6 @@ size_t select_workspace(const tsr_select_desc& s) { return layout_of(s).total; }
 tsr_status launch_select(const tsr_select_desc& s, const void* q, const void* k, uint8_t* blocks, void* ws,
                          cudaStream_t st) {
   const Layout l = layout_of(s);
-  const int64_t BH = static_cast<int64_t>(s.B) * s.H;
-  if (BH * (static_cast<int64_t>(l.nq) + l.nk) >= (int64_t{1} << 31))
-    return fail(TSR_ERR_UNSUPPORTED, "more than 2^31 blocks");
   if (s.d == 64) return launch<64>(s, l, q, k, blocks, static_cast<uint8_t*>(ws), st);
   return launch<128>(s, l, q, k, blocks, static_cast<uint8_t*>(ws), st);
 }

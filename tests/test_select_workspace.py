@@ -37,3 +37,14 @@ def test_a_million_tokens(L):
     """24 heads of 2^20 tokens: means, norms and fragments 1.2 GB, one strip of scores
     for each resident CTA 0.5 GB (the whole score matrix would be 26 GB)."""
     assert size(L, N=1 << 20) < 2 << 30
+
+
+def test_too_many_blocks_are_refused_before_the_workspace_is_made(L):
+    """2^31 blocks: the query says so, instead of a size that no device holds."""
+    d, n = tsr._SelectDesc(), ctypes.c_size_t(0)
+    d.B, d.H, d.N, d.d, d.bq, d.bk, d.keep = 1, 1 << 10, 1 << 24, 64, 16, 16, 1
+    assert L.tsr_block_select_workspace(ctypes.byref(d), ctypes.byref(n)) == 2
+    assert b"2^31" in L.tsr_last_error()
+    assert L.tsr_block_select(ctypes.byref(d), 4096, 8192, 12288, 16384, 1 << 62, None) == 2
+    d.N = (1 << 24) - 16                                     # 2^31 - 2^11 blocks
+    assert L.tsr_block_select_workspace(ctypes.byref(d), ctypes.byref(n)) == 0 and n.value > 0
