@@ -116,6 +116,9 @@ tsr_status tsr_rope(const tsr_rope_desc* d, const tsr_rope_tensor* t, int32_t n,
   if (width > d->d) return fail(TSR_ERR_INVALID_ARG, "axis_dim sums to more than d");
   if (!d->positions && cells != d->N) return fail(TSR_ERR_INVALID_ARG, "grid does not hold N tokens");
   if (!(d->theta > 0.0) || !std::isfinite(d->theta)) return fail(TSR_ERR_INVALID_ARG, "theta must be > 0");
+  for (int a = 0; a < d->n_axes; ++a)      // theta^(-2 j / axis_dim) of the last pair
+    if (!std::isfinite(std::pow(d->theta, -(d->axis_dim[a] - 2.0) / d->axis_dim[a])))
+      return fail(TSR_ERR_INVALID_ARG, "theta is so small that a frequency is not finite");
   if (d->N > (1 << 24)) return fail(TSR_ERR_UNSUPPORTED, "N above 2^24");
   if (d->B > 65535) return fail(TSR_ERR_UNSUPPORTED, "B above 65535");
   if (d->positions && !aligned(d->positions, 4)) return fail(TSR_ERR_INVALID_ARG, "positions must be 4-byte aligned");

@@ -8,9 +8,11 @@
 //
 // Angles.  A frequency is held in turns as a 64-bit fixed-point fraction
 // F = round(2^64 * theta^(-2 j / D_x) / 2 pi); p * F mod 2^64 is then the angle's
-// place on the circle, exact in integer arithmetic up to p * 2^-64 of a turn, and
-// its top bits go to sincospi as a float in [-1, 1).  (p * freq in fp32 would be
-// off by 2^-24 of the whole angle, 0.006 rad at position 100,000.)
+// place on the circle, exact in integer arithmetic but for F itself, which comes from
+// doubles: off by a few 2^-54 of the frequency (at most 1 / 2 pi of a turn for theta
+// >= 1), so about p * 2^-55 of a turn: 4e-7 rad at position 2^31, 2e-11 at 100,000.  Its top
+// bits go to sincospi as a float in [-1, 1).  (p * freq in fp32 would be off by 2^-24
+// of the whole angle, 0.006 rad at position 100,000.)
 //
 // Bound: HBM, one read and one write of every element.  A thread owns one unit of
 // pairs of one token (16 bytes, or two 16-byte pieces for half-split pairs),

@@ -483,8 +483,11 @@ tsr_status tsr_svg_route(const void *q, const void *k, const void *v, int32_t B,
  * where (u, v) are channels (2j, 2j + 1) of the axis, or, with `halves`,
  * (j, j + axis_dim[x] / 2).  The rotation is orthogonal: the gradient of the input
  * is the inverse rotation of the gradient of the output.  fp32 arithmetic, one
- * rounding to the tensors' type; a far position loses nothing (angles are taken
- * on the circle in 64-bit integers).
+ * rounding to the tensors' type.  Angles are taken on the circle in 64-bit integers
+ * from frequencies of double precision: off by about p_x * 2^-55 of a turn (4e-7 rad at
+ * position 2^31).  With theta < 1 a frequency may pass one turn and its whole turns
+ * cost that many bits more; a theta so small that a frequency is not finite is
+ * refused.
  *
  * Positions: grid form (positions NULL): token n has the row-major coordinates of
  * n in grid[0] x ... x grid[n_axes - 1], whose product is N (frame, row, column of
