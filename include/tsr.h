@@ -304,11 +304,15 @@ tsr_status tsr_bsa_forward_batch(const tsr_request *reqs, int32_t n, void *strea
  *
  * A backward plan holds the mask's tiles by query and by key; it is made on
  * `stream` (tsr_plan twice: the mask and its transpose, synchronising as it does),
- * belongs to the device it was made on and may serve any number of calls, at the
- * same time too, on any streams.  tsr_backward_plan_update re-plans a new mask of
- * the same B, H, N and d into the same storage; no queued call may be using the
- * plan on another stream, and a plan whose update failed is refused until one
- * succeeds.  workspace: device, 256-byte aligned, tsr_bsa_backward_workspace()
+ * whose last kernels may still be queued when the call returns: calls on other
+ * streams have to be ordered behind them (an event, or the stream synchronised).
+ * It belongs to the device it was made on and may then serve any number of calls,
+ * at the same time too, on any streams.  tsr_backward_plan_update re-plans a new
+ * mask of the same B, H, N and d into the same storage, which may move if the new
+ * mask needs more; no queued call may be using the plan on another stream, a graph
+ * that captured a call of the plan must not be replayed after an update (it holds
+ * the old tiles' addresses and counts) or after the plan's end, and a plan whose
+ * update failed is refused until one succeeds.  workspace: device, 256-byte aligned, tsr_bsa_backward_workspace()
  * bytes, contents not kept; calls that may run at the same time need one each.
  * tsr_bsa_backward is asynchronous, allocates nothing and may be captured into a
  * CUDA graph.  A bounded device wait that gave up is reported by
