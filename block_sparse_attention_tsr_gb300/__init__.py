@@ -26,7 +26,7 @@ __all__ = [
     "TsrError", "build", "lib", "make_mask", "Mask", "Plan", "tsr_plan", "tsr_plan_update",
     "tsr_bsa_forward",
     "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_temporal_permute", "tsr_svg_route",
-    "tsr_rope", "tsr_rope_backward", "tsr_block_select",
+    "tsr_rope", "tsr_rope_backward", "tsr_norm_rope", "tsr_norm_rope_backward", "tsr_block_select",
     "BackwardPlan", "tsr_backward_plan", "tsr_backward_plan_update", "tsr_bsa_backward",
     "tsr_attention_host",
     "tsr_regime_load",
@@ -82,6 +82,13 @@ class _RopeTensor(ctypes.Structure):
                 ("x_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
 
 
+class _NormRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("dout", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("dweight", ctypes.c_void_p), ("H", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64 * 3),
+                ("dout_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
+
 class _SelectDesc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in ("B", "H", "N", "d", "bq", "bk", "keep", "first", "diagonal")]
 
@@ -90,8 +97,10 @@ class _SelectDesc(ctypes.Structure):
 # structure field by field takes longer than the kernels of a small call).
 _ROPE_DESC = struct.Struct("@5i4i2idPi4i4x")
 _ROPE_TENSOR = struct.Struct("@PPi3q3q")
+_NORM_ROPE_TENSOR = struct.Struct("@PPPPP2i3q3q3q")
 _SELECT_DESC = struct.Struct("@9i")
-for _packed, _fields in ((_ROPE_DESC, _RopeDesc), (_ROPE_TENSOR, _RopeTensor), (_SELECT_DESC, _SelectDesc)):
+for _packed, _fields in ((_ROPE_DESC, _RopeDesc), (_ROPE_TENSOR, _RopeTensor), (_SELECT_DESC, _SelectDesc),
+                         (_NORM_ROPE_TENSOR, _NormRopeTensor)):
     assert _packed.size == ctypes.sizeof(_fields)
 
 
@@ -125,7 +134,8 @@ class _Regime(ctypes.Structure):
 _LIB = None
 EXPORTS = ("tsr_abi_version", "tsr_status_string", "tsr_last_error", "tsr_plan", "tsr_plan_update",
            "tsr_bsa_forward", "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_plan_destroy", "tsr_plan_get_stats",
-           "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope",
+           "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope", "tsr_norm_rope",
+           "tsr_norm_rope_backward_workspace", "tsr_norm_rope_backward",
            "tsr_block_select_workspace", "tsr_block_select", "tsr_backward_plan",
            "tsr_backward_plan_update", "tsr_backward_plan_destroy", "tsr_backward_plan_device_status",
            "tsr_backward_plan_test_stall",
@@ -167,6 +177,9 @@ def lib():
         "tsr_temporal_permute": ([P, P, I32, I32, I32, I32, I32, P, I32, P], ctypes.c_int),
         "tsr_svg_route": ([P, P, P, I32, I32, I32, I32, I32, I32, P, I32, P, P, P], ctypes.c_int),
         "tsr_rope": ([P, P, I32, P], ctypes.c_int),
+        "tsr_norm_rope": ([P, ctypes.c_double, P, I32, P], ctypes.c_int),
+        "tsr_norm_rope_backward_workspace": ([P, I32, P], ctypes.c_int),
+        "tsr_norm_rope_backward": ([P, ctypes.c_double, P, I32, P, ctypes.c_size_t, P], ctypes.c_int),
         "tsr_block_select_workspace": ([P, P], ctypes.c_int),
         "tsr_block_select": ([P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "tsr_backward_plan": ([P, P, P], ctypes.c_int),
@@ -484,6 +497,44 @@ def tsr_svg_route(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_frames: i
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _rope_heads(xs, dims, grid, positions) -> torch.dtype:
+    """The type of one to four [B, H, N, d] tensors that a call rotates."""
+    if not 1 <= len(xs) <= 4:
+        raise ValueError("one to four tensors per call")
+    if (grid is None) == (positions is None):
+        raise ValueError("give grid or positions")
+    first = xs[0]
+    if first.dim() != 4:
+        raise ValueError("the tensors are [B, H, N, d]")
+    B, _, N, d = first.shape
+    dtype = first.dtype
+    if dtype not in _ROPE_DTYPES:
+        raise ValueError("the tensors are bf16, fp16 or fp32")
+    if not 1 <= len(dims) <= 4:
+        raise ValueError("one to four axes")
+    for t in xs:
+        if t.dim() != 4 or t.dtype != dtype or t.shape[::2] != (B, N) or t.shape[3] != d:
+            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
+    return dtype
+
+
+def _rope_desc(first, dims, grid, positions, theta, halves, inverse) -> bytes:
+    """The packed tsr_rope_desc of tensors like ``first``."""
+    B, _, N, d = first.shape
+    axes = len(dims)
+    pad = (0,) * (4 - axes)
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.shape not in ((N, axes), (B, N, axes)):
+            raise ValueError("positions must be int32 [N, axes] or [B, N, axes]")
+        where = (_dptr(positions), positions.dim() == 3, 0, 0, 0, 0)
+    else:
+        cells = [int(g) for g in grid]
+        if len(cells) != axes:
+            raise ValueError("grid needs one size per axis")
+        where = (0, 0, *cells, *pad)
+    return _ROPE_DESC.pack(B, N, d, _ROPE_DTYPES[first.dtype], axes, *dims, *pad, bool(halves), bool(inverse), theta, *where)
+
+
 def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = None,
              theta: float = 10000.0, halves: bool = False, inverse: bool = False, out=None,
              stream=None):
@@ -497,25 +548,9 @@ def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = Non
     (x itself: in place); default contiguous [B, H, N, d].  Returns out."""
     one = isinstance(x, torch.Tensor)
     xs = (x,) if one else tuple(x)
-    if not 1 <= len(xs) <= 4:
-        raise ValueError("one to four tensors per call")
-    if (grid is None) == (positions is None):
-        raise ValueError("give grid or positions")
-    first = xs[0]
-    if first.dim() != 4:
-        raise ValueError("the tensors are [B, H, N, d]")
-    B, _, N, d = first.shape
-    dtype = first.dtype
-    code = _ROPE_DTYPES.get(dtype)
-    if code is None:
-        raise ValueError("the tensors are bf16, fp16 or fp32")
     dims = [int(a) for a in axis_dims]
-    axes = len(dims)
-    if not 1 <= axes <= 4:
-        raise ValueError("one to four axes")
-    for t in xs:
-        if t.dim() != 4 or t.dtype != dtype or t.shape[::2] != (B, N) or t.shape[3] != d:
-            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
+    dtype = _rope_heads(xs, dims, grid, positions)
+    first = xs[0]
     if out is None:
         _on_device(*xs, positions)
         with _allocating_on(stream):
@@ -534,17 +569,7 @@ def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = Non
         if x_last != 1 or o_last != 1:
             raise ValueError("the last dimension must be contiguous")
         tensors += _ROPE_TENSOR.pack(t.data_ptr(), o.data_ptr(), t.shape[1], xb, xh, xn, ob, oh, on)
-    pad = (0,) * (4 - axes)
-    if positions is not None:
-        if positions.dtype != torch.int32 or positions.shape not in ((N, axes), (B, N, axes)):
-            raise ValueError("positions must be int32 [N, axes] or [B, N, axes]")
-        where = (_dptr(positions), positions.dim() == 3, 0, 0, 0, 0)
-    else:
-        cells = [int(g) for g in grid]
-        if len(cells) != axes:
-            raise ValueError("grid needs one size per axis")
-        where = (0, 0, *cells, *pad)
-    desc = _ROPE_DESC.pack(B, N, d, code, axes, *dims, *pad, bool(halves), bool(inverse), theta, *where)
+    desc = _rope_desc(first, dims, grid, positions, theta, halves, inverse)
     _check(lib().tsr_rope(desc, tensors, len(xs), _stream_ptr(stream)))
     return outs[0] if one else list(outs)
 
@@ -553,6 +578,112 @@ def tsr_rope_backward(dout, axis_dims, **kw):
     """The gradient of tsr_rope's input from its output's: the inverse rotation,
     same arguments (``out``: where the gradient goes)."""
     return tsr_rope(dout, axis_dims, inverse=not kw.pop("inverse", False), **kw)
+
+
+def _heads_list(x):
+    return (x,) if isinstance(x, torch.Tensor) else tuple(x)
+
+
+def _weights(weight, xs):
+    """One weight (or None) per tensor, and their type's code."""
+    ws = tuple(weight) if isinstance(weight, (list, tuple)) else (weight,) * len(xs)
+    if len(ws) != len(xs):
+        raise ValueError("one weight (or None) for each tensor")
+    dtype = None
+    for w in ws:
+        if w is None:
+            continue
+        if w.shape != xs[0].shape[3:] or w.dtype not in (xs[0].dtype, torch.float32) or w.dtype != (dtype or w.dtype):
+            raise ValueError("the weights are [d], all of the tensors' type or all fp32")
+        dtype = w.dtype
+    return ws, _ROPE_DTYPES[dtype or xs[0].dtype]
+
+
+def tsr_norm_rope(x, weight, axis_dims, *, eps: float = 1e-6, grid=None,
+                  positions: Optional[torch.Tensor] = None, theta: float = 10000.0, halves: bool = False,
+                  out=None, stream=None):
+    """RMS norm over each head's d channels, then tsr_rope, in one pass (see
+    tsr_norm_rope in include/tsr.h).  ``x``, ``out`` and the positions as for tsr_rope;
+    ``weight``: [d] of x's type or fp32, or None (ones); for several tensors a sequence of
+    as many (one tensor alone is shared by all).  Returns out."""
+    xs = _heads_list(x)
+    dims = [int(a) for a in axis_dims]
+    dtype = _rope_heads(xs, dims, grid, positions)
+    ws, code = _weights(weight, xs)
+    if out is None:
+        _on_device(*xs, *ws, positions)
+        with _allocating_on(stream):
+            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
+    else:
+        outs = _heads_list(out)
+        if len(outs) != len(xs):
+            raise ValueError("as many outputs as tensors")
+        _on_device(*xs, *ws, *outs, positions)
+    tensors = b""
+    for t, w, o in zip(xs, ws, outs):
+        xb, xh, xn, x_last = t.stride()
+        ob, oh, on, o_last = o.stride()
+        if out is not None and (o.shape != t.shape or o.dtype != dtype):
+            raise ValueError("out must have x's shape and dtype")
+        if x_last != 1 or o_last != 1:
+            raise ValueError("the last dimension must be contiguous")
+        tensors += _NORM_ROPE_TENSOR.pack(t.data_ptr(), _dptr(w), 0, o.data_ptr(), 0, t.shape[1], code,
+                                          xb, xh, xn, 0, 0, 0, ob, oh, on)
+    desc = _rope_desc(xs[0], dims, grid, positions, theta, halves, False)
+    _check(lib().tsr_norm_rope(desc, eps, tensors, len(xs), _stream_ptr(stream)))
+    return outs[0] if isinstance(x, torch.Tensor) else list(outs)
+
+
+def tsr_norm_rope_backward(dout, x, weight, axis_dims, *, eps: float = 1e-6, grid=None,
+                           positions: Optional[torch.Tensor] = None, theta: float = 10000.0,
+                           halves: bool = False, out=None, dweight=None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of tsr_norm_rope: returns (dx, dweight), lists of them for several
+    tensors; dweight is None where the weight is.  ``out``: where dx goes (any strides);
+    ``workspace``: uint8, at least tsr_norm_rope_backward_workspace() bytes; default: one
+    allocated for the call."""
+    xs, gs = _heads_list(x), _heads_list(dout)
+    one = isinstance(x, torch.Tensor)
+    dims = [int(a) for a in axis_dims]
+    dtype = _rope_heads(xs, dims, grid, positions)
+    ws, code = _weights(weight, xs)
+    if len(set(id(w) for w in ws if w is not None)) != sum(w is not None for w in ws):
+        raise ValueError("a shared weight's gradient needs a call for each tensor")
+    if len(gs) != len(xs) or any(g.shape != t.shape or g.dtype != dtype for g, t in zip(gs, xs)):
+        raise ValueError("dout must have x's shapes and dtype")
+    outs = None if out is None else _heads_list(out)
+    dws = None if dweight is None else _heads_list(dweight)
+    for given in (outs, dws):
+        if given is not None and len(given) != len(xs):
+            raise ValueError("as many outputs as tensors")
+    _on_device(*xs, *gs, *ws, positions, workspace, *(outs or ()), *(dws or ()))
+    desc = _rope_desc(xs[0], dims, grid, positions, theta, halves, False)
+    L = lib()
+    need = ctypes.c_size_t(0)
+    _check(L.tsr_norm_rope_backward_workspace(desc, len(xs), ctypes.byref(need)))
+    with _allocating_on(stream):
+        if outs is None:
+            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
+        if dws is None:
+            dws = [None if w is None else torch.empty_like(w) for w in ws]
+        if workspace is None:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=xs[0].device)
+    tensors = b""
+    for t, g, w, o, dw in zip(xs, gs, ws, outs, dws):
+        xb, xh, xn, x_last = t.stride()
+        gb, gh, gn, g_last = g.stride()
+        ob, oh, on, o_last = o.stride()
+        if o.shape != t.shape or o.dtype != dtype:
+            raise ValueError("out must have x's shape and dtype")
+        if x_last != 1 or g_last != 1 or o_last != 1:
+            raise ValueError("the last dimension must be contiguous")
+        if (dw is None) != (w is None) or (dw is not None and (dw.shape != w.shape or dw.dtype != w.dtype)):
+            raise ValueError("dweight must have the weight's shape and dtype")
+        tensors += _NORM_ROPE_TENSOR.pack(t.data_ptr(), _dptr(w), g.data_ptr(), o.data_ptr(), _dptr(dw), t.shape[1],
+                                          code, xb, xh, xn, gb, gh, gn, ob, oh, on)
+    _check(L.tsr_norm_rope_backward(desc, eps, tensors, len(xs), _dptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+    return (outs[0], dws[0]) if one else (list(outs), list(dws))
 
 
 def tsr_block_select(q: torch.Tensor, k: torch.Tensor, keep: int, *, bq: int = 64, bk: int = 64,

@@ -73,8 +73,6 @@ tsr_status check_backward_kind(const tsr_mask* mask) {
   return TSR_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 tsr_status check_select(const tsr_select_desc* s) {
   if (!s) return fail(TSR_ERR_INVALID_ARG, "desc is NULL");
   if (s->B <= 0 || s->H <= 0 || s->N <= 0) return fail(TSR_ERR_INVALID_ARG, "B, H, N must be > 0");
@@ -92,12 +90,11 @@ tsr_status check_select(const tsr_select_desc* s) {
 
 }  // namespace
 
-extern "C" {
+namespace tsr {
 
-tsr_status tsr_rope(const tsr_rope_desc* d, const tsr_rope_tensor* t, int32_t n, void* stream) {
-  set_error("");
-  if (!d || !t) return fail(TSR_ERR_INVALID_ARG, "desc / tensors is NULL");
-  if (n < 1 || n > 4) return fail(TSR_ERR_INVALID_ARG, "1 to 4 tensors per call");
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+tsr_status check_rope_desc(const tsr_rope_desc* d) {
   if (d->B <= 0 || d->N <= 0) return fail(TSR_ERR_INVALID_ARG, "B, N must be > 0");
   if (d->d < 2 || d->d > 256 || d->d % 2) return fail(TSR_ERR_INVALID_ARG, "d must be even, 2 to 256");
   if (d->dtype < TSR_DTYPE_BF16 || d->dtype > TSR_DTYPE_F32) return fail(TSR_ERR_INVALID_ARG, "unknown dtype");
@@ -122,6 +119,46 @@ tsr_status tsr_rope(const tsr_rope_desc* d, const tsr_rope_tensor* t, int32_t n,
   if (d->N > (1 << 24)) return fail(TSR_ERR_UNSUPPORTED, "N above 2^24");
   if (d->B > 65535) return fail(TSR_ERR_UNSUPPORTED, "B above 65535");
   if (d->positions && !aligned(d->positions, 4)) return fail(TSR_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  return TSR_OK;
+}
+
+// Strides of one tensor's input and output rows; *same: the two agree.
+tsr_status check_rope_strides(const tsr_rope_desc& d, int32_t H, const int64_t* x_stride, const int64_t* out_stride,
+                              const std::string& at, bool* same) {
+  *same = true;
+  const int64_t size[3] = {d.B, H, d.N};
+  for (int k = 0; k < 3; ++k) {
+    const int64_t xs = x_stride[k], os = out_stride[k];
+    if (size[k] == 1) continue;
+    *same = *same && xs == os;
+    if (xs < 0 || os < d.d) return fail(TSR_ERR_INVALID_ARG, at + "strides: x >= 0, out >= d");
+    if (xs > INT64_MAX / 8 / size[k] || os > INT64_MAX / 8 / size[k])
+      return fail(TSR_ERR_INVALID_ARG, at + "strides too large");
+  }
+  // the output's rows must not run into each other: each dimension, in order of its
+  // stride, steps over all that the smaller ones reach
+  int order[3] = {0, 1, 2};
+  for (int a = 0; a < 2; ++a)
+    for (int b = a + 1; b < 3; ++b)
+      if (out_stride[order[b]] < out_stride[order[a]]) std::swap(order[a], order[b]);
+  int64_t reach = d.d;
+  for (int k : order) {
+    if (size[k] == 1) continue;
+    if (out_stride[k] < reach) return fail(TSR_ERR_INVALID_ARG, at + "elements of out overlap");
+    reach += out_stride[k] * (size[k] - 1);
+  }
+  return TSR_OK;
+}
+
+}  // namespace tsr
+
+extern "C" {
+
+tsr_status tsr_rope(const tsr_rope_desc* d, const tsr_rope_tensor* t, int32_t n, void* stream) {
+  set_error("");
+  if (!d || !t) return fail(TSR_ERR_INVALID_ARG, "desc / tensors is NULL");
+  if (n < 1 || n > 4) return fail(TSR_ERR_INVALID_ARG, "1 to 4 tensors per call");
+  if (tsr_status e = check_rope_desc(d)) return e;
   const size_t es = d->dtype == TSR_DTYPE_F32 ? 4 : 2;
   int64_t heads = 0;
   for (int i = 0; i < n; ++i) {
@@ -131,28 +168,8 @@ tsr_status tsr_rope(const tsr_rope_desc* d, const tsr_rope_tensor* t, int32_t n,
       return fail(TSR_ERR_INVALID_ARG, at + "pointers must be aligned to the element type");
     if (t[i].H <= 0) return fail(TSR_ERR_INVALID_ARG, at + "H must be > 0");
     heads += t[i].H;
-    const int64_t size[3] = {d->B, t[i].H, d->N};
     bool same = true;
-    for (int k = 0; k < 3; ++k) {
-      const int64_t xs = t[i].x_stride[k], os = t[i].out_stride[k];
-      if (size[k] == 1) continue;
-      same = same && xs == os;
-      if (xs < 0 || os < d->d) return fail(TSR_ERR_INVALID_ARG, at + "strides: x >= 0, out >= d");
-      if (xs > INT64_MAX / 8 / size[k] || os > INT64_MAX / 8 / size[k])
-        return fail(TSR_ERR_INVALID_ARG, at + "strides too large");
-    }
-    // the output's rows must not run into each other: each dimension, in order of its
-    // stride, steps over all that the smaller ones reach
-    int order[3] = {0, 1, 2};
-    for (int a = 0; a < 2; ++a)
-      for (int b = a + 1; b < 3; ++b)
-        if (t[i].out_stride[order[b]] < t[i].out_stride[order[a]]) std::swap(order[a], order[b]);
-    int64_t reach = d->d;
-    for (int k : order) {
-      if (size[k] == 1) continue;
-      if (t[i].out_stride[k] < reach) return fail(TSR_ERR_INVALID_ARG, at + "elements of out overlap");
-      reach += t[i].out_stride[k] * (size[k] - 1);
-    }
+    if (tsr_status e = check_rope_strides(*d, t[i].H, t[i].x_stride, t[i].out_stride, at, &same)) return e;
     if (t[i].x == t[i].out && !same) return fail(TSR_ERR_INVALID_ARG, at + "in place needs equal strides");
     for (int j = 0; j < i; ++j)
       if (t[i].out == t[j].out || t[i].x == t[j].out || t[i].out == t[j].x)

@@ -188,8 +188,21 @@ tsr_status launch_svg_temporal(const void* q, const void* k, const void* v, void
                                const int8_t* head_kind, int64_t bh_lo, int64_t bh_hi,
                                cudaStream_t stream);
 
+// argument checks that several operators share (api_ops.cu)
+bool aligned(const void* p, size_t a);
+tsr_status check_rope_desc(const tsr_rope_desc* d);
+tsr_status check_rope_strides(const tsr_rope_desc& d, int32_t H, const int64_t* x_stride, const int64_t* out_stride,
+                              const std::string& at, bool* same);
+
 // multi-axis rotary positions (rope.cu)
 tsr_status launch_rope(const tsr_rope_desc& d, const tsr_rope_tensor* t, int32_t n, cudaStream_t stream);
+
+// norm of every head's row and rotation (norm_rope.cu)
+tsr_status launch_norm_rope(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int32_t n,
+                            cudaStream_t st);
+size_t norm_rope_workspace(const tsr_rope_desc& d, int32_t n);
+tsr_status launch_norm_rope_backward(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int32_t n,
+                                     void* ws, cudaStream_t st);
 
 // block selection (select.cu)
 size_t select_workspace(const tsr_select_desc& s);

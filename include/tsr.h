@@ -532,6 +532,51 @@ tsr_status tsr_rope(const tsr_rope_desc *desc, const tsr_rope_tensor *tensors, i
                     void *stream);
 
 /*
+ * tsr_norm_rope -- the RMS norm of every head's row and the rotation of tsr_rope in one
+ * pass (Q and K of a layer whose queries and keys are normed before the attention), and
+ * tsr_norm_rope_backward, the gradients of that.
+ *
+ * For a row x of d channels, r = 1 / sqrt(mean_c x_c^2 + eps) and the rotation R of the
+ * row's token (desc, as for tsr_rope):
+ *     y = R (weight o x r)
+ * and for a gradient dout of y, with g = R^T dout and S = sum_c g_c weight_c x_c:
+ *     dx = r (g o weight - x r^2 S / d),      dweight = sum of g o x r over b, h and n.
+ * The norm runs over all d channels, rotated or not.  weight: [d], shared by the heads of
+ * its tensor, of the tensors' type or fp32 (weight_dtype, the same for all tensors of a
+ * call); NULL: all ones.  fp32 arithmetic, one rounding to the output's type; a row's sum
+ * of squares has to stay inside the fp32 range.  dweight is summed in fp32 in a fixed
+ * order (the same bits every run), of weight_dtype; NULL where it is not needed.
+ * The backward reads x again and keeps nothing from the forward.
+ *
+ * Strides, positions, grids and limits as for tsr_rope.  out (y, or dx) may be x, or dout,
+ * itself with equal strides; otherwise it must not overlap an input.  An input of stride 0
+ * (broadcast) is read as such: dx has an element for each of its uses.
+ * workspace (backward): device, 256-byte aligned, tsr_norm_rope_backward_workspace()
+ * bytes; not needed (NULL) when every dweight is NULL.  Calls that may run at the same
+ * time need one each.  Asynchronous on `stream`; nothing is allocated.
+ * Errors: TSR_ERR_INVALID_ARG, TSR_ERR_UNSUPPORTED as for tsr_rope; eps must be > 0 as fp32.
+ */
+typedef struct {
+  const void *x;
+  const void *weight;           /* [d] or NULL */
+  const void *dout;             /* backward */
+  void *out;                    /* y, or dx */
+  void *dweight;                /* backward, [d] or NULL */
+  int32_t H;
+  int32_t weight_dtype;         /* the tensors' dtype or TSR_DTYPE_F32 */
+  int64_t x_stride[3], dout_stride[3], out_stride[3];   /* b, h, n */
+} tsr_norm_rope_tensor;
+
+tsr_status tsr_norm_rope(const tsr_rope_desc *desc, double eps, const tsr_norm_rope_tensor *tensors,
+                         int32_t n_tensors, void *stream);
+
+tsr_status tsr_norm_rope_backward_workspace(const tsr_rope_desc *desc, int32_t n_tensors,
+                                            size_t *bytes /* HOST */);
+
+tsr_status tsr_norm_rope_backward(const tsr_rope_desc *desc, double eps, const tsr_norm_rope_tensor *tensors,
+                                  int32_t n_tensors, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * tsr_block_select -- a block mask for tsr_plan from a cheap score per block pair
  * (the step before the path, for callers without a mask; compare tsr_svg_route,
  * which routes whole heads).

@@ -41,3 +41,28 @@ def select(q, k, keep, bq, bk, first=0, diagonal=False):
     out = np.zeros(s.shape, np.uint8)
     np.put_along_axis(out, order, np.broadcast_to(kept, s.shape).astype(np.uint8), -1)
     return out
+
+
+def norm_rotate(x, w, pos, dims, eps, theta=1e4, halves=False):
+    """Heads' rows x [..., N, d] normed to a mean square of 1, weighted by w [d] and turned,
+    and the sum |a| + |b| of each element's pair before the turn (|a| alone past the axes)."""
+    z = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * w
+    y, size = rotate(z, pos, dims, theta, halves)
+    size[..., sum(dims):] = np.abs(z[..., sum(dims):])
+    return y, size
+
+
+def norm_rotate_gradients(dy, x, w, pos, dims, eps, theta=1e4, halves=False):
+    """dx and dw of norm_rotate, by the chain rule, and the sizes that their errors scale
+    with: for dx r (|g| |w| + |x| r^2 / d sum |g| |w| |x|), for dw the sum of |g| |x| r, with
+    |g| the sum |a| + |b| of dy's pair."""
+    d = x.shape[-1]
+    g, size = rotate(dy, pos, dims, theta, halves, inverse=True)
+    size[..., sum(dims):] = np.abs(dy[..., sum(dims):])
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    a = g * w
+    dx = r * a - x * r ** 3 * (a * x).sum(-1, keepdims=True) / d
+    sa = size * np.abs(w)
+    rows = tuple(range(x.ndim - 1))
+    dx_size = r * sa + np.abs(x) * r ** 3 * (sa * np.abs(x)).sum(-1, keepdims=True) / d
+    return dx, (g * x * r).sum(rows), dx_size, (size * np.abs(x) * r).sum(rows)
