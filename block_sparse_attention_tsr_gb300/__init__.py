@@ -27,6 +27,7 @@ __all__ = [
     "tsr_bsa_forward",
     "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_temporal_permute", "tsr_svg_route",
     "tsr_rope", "tsr_rope_backward", "tsr_norm_rope", "tsr_norm_rope_backward", "tsr_block_select",
+    "tsr_linear", "tsr_linear_backward", "tsr_linear_device_status",
     "BackwardPlan", "tsr_backward_plan", "tsr_backward_plan_update", "tsr_bsa_backward",
     "tsr_attention_host",
     "tsr_regime_load",
@@ -89,6 +90,21 @@ class _NormRopeTensor(ctypes.Structure):
                 ("dout_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
 
 
+class _LinearDesc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("B", "N", "in_heads", "in_dim", "out_heads", "out_dim", "dtype",
+                                              "activation")]
+
+
+class _LinearArgs(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("x", "weight", "bias", "residual", "out", "pre")]
+                + [(f + "_stride", ctypes.c_int64 * 3) for f in ("x", "residual", "out", "pre")])
+
+
+class _LinearGrads(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("dout", "x", "weight", "pre", "dx", "dweight", "dbias")]
+                + [(f + "_stride", ctypes.c_int64 * 3) for f in ("dout", "x", "pre", "dx")])
+
+
 class _SelectDesc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in ("B", "H", "N", "d", "bq", "bk", "keep", "first", "diagonal")]
 
@@ -98,9 +114,13 @@ class _SelectDesc(ctypes.Structure):
 _ROPE_DESC = struct.Struct("@5i4i2idPi4i4x")
 _ROPE_TENSOR = struct.Struct("@PPi3q3q")
 _NORM_ROPE_TENSOR = struct.Struct("@PPPPP2i3q3q3q")
+_LINEAR_DESC = struct.Struct("@8i")
+_LINEAR_ARGS = struct.Struct("@6P12q")
+_LINEAR_GRADS = struct.Struct("@7P12q")
 _SELECT_DESC = struct.Struct("@9i")
 for _packed, _fields in ((_ROPE_DESC, _RopeDesc), (_ROPE_TENSOR, _RopeTensor), (_SELECT_DESC, _SelectDesc),
-                         (_NORM_ROPE_TENSOR, _NormRopeTensor)):
+                         (_NORM_ROPE_TENSOR, _NormRopeTensor), (_LINEAR_DESC, _LinearDesc),
+                         (_LINEAR_ARGS, _LinearArgs), (_LINEAR_GRADS, _LinearGrads)):
     assert _packed.size == ctypes.sizeof(_fields)
 
 
@@ -135,7 +155,8 @@ _LIB = None
 EXPORTS = ("tsr_abi_version", "tsr_status_string", "tsr_last_error", "tsr_plan", "tsr_plan_update",
            "tsr_bsa_forward", "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_plan_destroy", "tsr_plan_get_stats",
            "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope", "tsr_norm_rope",
-           "tsr_norm_rope_backward_workspace", "tsr_norm_rope_backward",
+           "tsr_norm_rope_backward_workspace", "tsr_norm_rope_backward", "tsr_linear_workspace", "tsr_linear",
+           "tsr_linear_backward_workspace", "tsr_linear_backward", "tsr_linear_device_status",
            "tsr_block_select_workspace", "tsr_block_select", "tsr_backward_plan",
            "tsr_backward_plan_update", "tsr_backward_plan_destroy", "tsr_backward_plan_device_status",
            "tsr_backward_plan_test_stall",
@@ -180,6 +201,11 @@ def lib():
         "tsr_norm_rope": ([P, ctypes.c_double, P, I32, P], ctypes.c_int),
         "tsr_norm_rope_backward_workspace": ([P, I32, P], ctypes.c_int),
         "tsr_norm_rope_backward": ([P, ctypes.c_double, P, I32, P, ctypes.c_size_t, P], ctypes.c_int),
+        "tsr_linear_workspace": ([P, P], ctypes.c_int),
+        "tsr_linear": ([P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "tsr_linear_backward_workspace": ([P, P], ctypes.c_int),
+        "tsr_linear_backward": ([P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "tsr_linear_device_status": ([P], ctypes.c_int),
         "tsr_block_select_workspace": ([P, P], ctypes.c_int),
         "tsr_block_select": ([P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "tsr_backward_plan": ([P, P, P], ctypes.c_int),
@@ -684,6 +710,137 @@ def tsr_norm_rope_backward(dout, x, weight, axis_dims, *, eps: float = 1e-6, gri
     _check(L.tsr_norm_rope_backward(desc, eps, tensors, len(xs), _dptr(workspace),
                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
     return (outs[0], dws[0]) if one else (list(outs), list(dws))
+
+
+_ACTIVATIONS = {None: 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
+
+
+def _token_rows(t):
+    """B, heads, N, channels per head and the b, h, n strides of [B, N, features],
+    [N, features] or head-major [B, heads, N, dim]; channels contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        rows = (shape[0], 1, shape[1], shape[2]), (stride[0], 0, stride[1])
+    elif len(shape) == 4:
+        rows = tuple(shape), stride[:3]
+    elif len(shape) == 2:
+        rows = (1, 1, shape[0], shape[1]), (0, 0, stride[0])
+    else:
+        raise ValueError("token rows are [N, features], [B, N, features] or [B, heads, N, dim]")
+    if stride[-1] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return rows
+
+
+def _linear_desc(x_rows, weight, out_heads, dtype, activation) -> bytes:
+    B, in_heads, N, in_dim = x_rows
+    code = _ROPE_DTYPES.get(dtype)
+    if code not in (0, 1):
+        raise ValueError("the tensors are bf16 or fp16")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation: one of {list(_ACTIVATIONS)}")
+    if weight.dim() != 2 or weight.dtype != dtype or weight.shape[1] != in_heads * in_dim:
+        raise ValueError("weight must be [out features, in features] of x's type")
+    M = weight.shape[0]
+    if out_heads < 1 or M % out_heads:
+        raise ValueError("heads must divide the out features")
+    return _LINEAR_DESC.pack(B, N, in_heads, in_dim, out_heads, M // out_heads, code, _ACTIVATIONS[activation])
+
+
+def _workspace(need_of, desc, workspace, device):
+    need = ctypes.c_size_t(0)
+    _check(need_of(desc, ctypes.byref(need)))
+    if workspace is None and need.value:
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def tsr_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+               activation: Optional[str] = None, residual: Optional[torch.Tensor] = None, heads: int = 0,
+               pre=None, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None):
+    """activation(x weight^T + bias) + residual (see tsr_linear in include/tsr.h).
+
+    ``x``: [N, K], [B, N, K] or the attention's head-major [B, H, N, d] with K = H d, any
+    strides that are multiples of 8; ``weight``: [M, K].  ``heads``: 0 for an output
+    [B, N, M] ([N, M]), or the heads of a head-major output [B, heads, N, M / heads].
+    ``activation``: None, "gelu", "gelu_tanh" or "silu".  ``residual``, ``out``: like the
+    output.  ``pre``: True, or a tensor like the output: the values before the activation,
+    for tsr_linear_backward.  ``workspace``: uint8, at least tsr_linear_workspace() bytes;
+    default: one allocated for the call.  Returns out, or (out, pre)."""
+    rows, x_stride = _token_rows(x)
+    dtype, M = x.dtype, weight.shape[0]
+    out_heads = heads or 1
+    desc = _linear_desc(rows, weight, out_heads, dtype, activation)
+    B, _, N, _ = rows
+    if heads:
+        shape = (B, heads, N, M // heads)
+    else:
+        shape = (N, M) if x.dim() == 2 else (B, N, M)
+    if bias is not None and (bias.dtype != dtype or bias.shape != (M,)):
+        raise ValueError("bias must be [out features] of x's type")
+    keep = pre is not None and pre is not False
+    given = pre if isinstance(pre, torch.Tensor) else None
+    for t in (residual, out, given):
+        if t is not None and (t.shape != shape or t.dtype != dtype):
+            raise ValueError(f"residual, out and pre must be {dtype} of shape {tuple(shape)}")
+    _on_device(x, weight, bias, residual, out, given, workspace)
+    L = lib()
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=x.device)
+        if keep and given is None:
+            given = torch.empty(shape, dtype=dtype, device=x.device)
+        workspace, size = _workspace(L.tsr_linear_workspace, desc, workspace, x.device)
+    none = (0, 0, 0)
+    args = _LINEAR_ARGS.pack(x.data_ptr(), _dptr(weight), _dptr(bias), 0 if residual is None else residual.data_ptr(),
+                             out.data_ptr(), given.data_ptr() if keep else 0, *x_stride,
+                             *(none if residual is None else _token_rows(residual)[1]), *_token_rows(out)[1],
+                             *(_token_rows(given)[1] if keep else none))
+    _check(L.tsr_linear(desc, args, _dptr(workspace), size, _stream_ptr(stream)))
+    return (out, given) if keep else out
+
+
+def tsr_linear_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *,
+                        activation: Optional[str] = None, pre: Optional[torch.Tensor] = None,
+                        need=(True, True, True), dx: Optional[torch.Tensor] = None,
+                        dweight: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of tsr_linear from ``dout``, like its output (head-major if that was):
+    returns (dx, dweight, dbias), None where ``need`` is false.  ``pre``: what the forward
+    kept, for an activation.  ``dx``, ``dweight``, ``dbias``: where they go."""
+    rows, x_stride = _token_rows(x)
+    out_rows, g_stride = _token_rows(dout)
+    dtype, M = x.dtype, weight.shape[0]
+    if dout.dtype != dtype or out_rows[::2] != rows[::2] or out_rows[1] * out_rows[3] != M:
+        raise ValueError("dout must be like the layer's output")
+    desc = _linear_desc(rows, weight, out_rows[1], dtype, activation)
+    if activation is not None and (pre is None or pre.shape != dout.shape or pre.dtype != dtype):
+        raise ValueError("pre must be like the layer's output")
+    if len(need) != 3:
+        raise ValueError("need: whether dx, dweight and dbias are needed")
+    for t, like, name in ((dx, x.shape, "dx"), (dweight, weight.shape, "dweight"), (dbias, (M,), "dbias")):
+        if t is not None and (t.shape != like or t.dtype != dtype):
+            raise ValueError(f"{name} must be {dtype} of shape {tuple(like)}")
+    _on_device(dout, x, weight, pre, dx, dweight, dbias, workspace)
+    L = lib()
+    with _allocating_on(stream):
+        new = lambda t, shape, wanted: (None if not wanted else t if t is not None
+                                        else torch.empty(shape, dtype=dtype, device=x.device))
+        dx, dweight, dbias = new(dx, x.shape, need[0]), new(dweight, weight.shape, need[1]), new(dbias, (M,), need[2])
+        workspace, size = _workspace(L.tsr_linear_backward_workspace, desc, workspace, x.device)
+    none = (0, 0, 0)
+    args = _LINEAR_GRADS.pack(dout.data_ptr(), x.data_ptr(), _dptr(weight), 0 if activation is None else pre.data_ptr(),
+                              0 if dx is None else dx.data_ptr(), _dptr(dweight), _dptr(dbias), *g_stride, *x_stride,
+                              *(none if activation is None else _token_rows(pre)[1]),
+                              *(none if dx is None else _token_rows(dx)[1]))
+    _check(L.tsr_linear_backward(desc, args, _dptr(workspace), size, _stream_ptr(stream)))
+    return dx, dweight, dbias
+
+
+def tsr_linear_device_status(stream=None) -> None:
+    """Raises if a wait in a linear layer's product gave up (see include/tsr.h)."""
+    _check(lib().tsr_linear_device_status(_stream_ptr(stream)))
 
 
 def tsr_block_select(q: torch.Tensor, k: torch.Tensor, keep: int, *, bq: int = 64, bk: int = 64,

@@ -204,6 +204,13 @@ size_t norm_rope_workspace(const tsr_rope_desc& d, int32_t n);
 tsr_status launch_norm_rope_backward(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int32_t n,
                                      void* ws, cudaStream_t st);
 
+// linear layers (linear.cu)
+size_t linear_workspace(const tsr_linear_desc& d);
+size_t linear_backward_workspace(const tsr_linear_desc& d);
+tsr_status launch_linear(const tsr_linear_desc& d, const tsr_linear_args& a, void* ws, cudaStream_t st);
+tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_grads& a, void* ws, cudaStream_t st);
+tsr_status linear_device_status(cudaStream_t st);
+
 // block selection (select.cu)
 size_t select_workspace(const tsr_select_desc& s);
 tsr_status launch_select(const tsr_select_desc& s, const void* q, const void* k, uint8_t* blocks, void* ws,

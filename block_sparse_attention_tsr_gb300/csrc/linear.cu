@@ -1,0 +1,448 @@
+// linear.cu -- linear layers y = act(x W^T + b) + residual and their gradients: the host
+// side of the products (linear_gemm.cuh), the sum of a split product's parts, and the pass
+// over the output's gradient that comes before the products of the backward,
+//     dz = dout o act'(pre),   dbias = sum of dz over the tokens.
+// dz is rounded to the tensors' type, an operand of both products; dbias is summed in fp32
+// from the unrounded dz, in a fixed order.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "internal.h"
+#include "linear_gemm.cuh"
+
+namespace tsr {
+
+namespace linear {
+
+namespace {
+
+constexpr int kSms = 152;              // what the choice of tiles is made for
+constexpr uint64_t kTimeoutNs = kWaitTimeoutNs;
+
+// D's values from the parts of a split product.  HBM/L2-bound.
+__global__ void __launch_bounds__(256) linear_finish_kernel(const float* part, int32_t splits, int64_t total_rows,
+                                                            int32_t n_rows, int32_t cols,
+                                                            const __grid_constant__ Epilogue e) {
+  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  const int32_t vecs = cols / 8;
+  grid_wait();
+  if (i >= total_rows * vecs) return;
+  const int64_t row = i / vecs;
+  const int32_t f = static_cast<int32_t>(i - row * vecs) * 8;
+  const int64_t b = row / n_rows;
+  float v[8] = {};
+  for (int32_t s = 0; s < splits; ++s) {
+    const float4* src = reinterpret_cast<const float4*>(part + (s * total_rows + row) * cols + f);
+    const float4 x = src[0], y = src[1];
+    v[0] += x.x;
+    v[1] += x.y;
+    v[2] += x.z;
+    v[3] += x.w;
+    v[4] += y.x;
+    v[5] += y.y;
+    v[6] += y.z;
+    v[7] += y.w;
+  }
+  finish8(e, v, b, row - b * n_rows, f);
+}
+
+struct DzParams {
+  const uint16_t *dout, *pre;          // pre: null without activation
+  uint16_t* dz;                        // [rows][cols], null: dout itself is the operand
+  float* part;                         // [row blocks][cols], null: no dbias
+  View vdout, vpre;
+  int64_t rows;
+  int32_t n_rows, cols, rows_per_block, act, f16;
+};
+
+// 32 lanes of 8 columns, 8 rows at a time.
+__global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ DzParams p) {
+  __shared__ float red[8][32][8];
+  const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int32_t f = (blockIdx.x * 32 + lane) * 8;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_block;
+  const int64_t r1 = min(r0 + p.rows_per_block, p.rows);
+  grid_launch_dependents();
+  float sum[8] = {};
+  if (f < p.cols) {
+#pragma unroll 4
+    for (int64_t r = r0 + ty; r < r1; r += 8) {
+      const int64_t b = r / p.n_rows, n = r - b * p.n_rows;
+      float g[8];
+      unpack8(*reinterpret_cast<const uint4*>(p.dout + at(p.vdout, b, n, f)), p.f16, g);
+      if (p.pre) {
+        float z[8];
+        unpack8(*reinterpret_cast<const uint4*>(p.pre + at(p.vpre, b, n, f)), p.f16, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] *= slope(z[i], p.act);
+      }
+      if (p.dz) *reinterpret_cast<uint4*>(p.dz + r * p.cols + f) = pack8(g, p.f16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += g[i];
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[ty][lane][i] = sum[i];
+  __syncthreads();
+  const int c = threadIdx.x;           // 256 columns of the block
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += red[k][c >> 3][c & 7];
+  const int32_t col = blockIdx.x * 256 + c;
+  if (col < p.cols) p.part[static_cast<int64_t>(blockIdx.y) * p.cols + col] = s;
+}
+
+// Column sums of the row blocks' sums: 32 columns a CTA, 32 rows at a time.
+__global__ void __launch_bounds__(1024) linear_bias_kernel(const float* part, int32_t blocks, int32_t cols, void* out,
+                                                           int32_t f16) {
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  grid_wait();
+  float s = 0.f;
+  if (c < cols)
+    for (int i = slice; i < blocks; i += 32) s += part[static_cast<int64_t>(i) * cols + c];
+  red[slice][lane] = s;
+  __syncthreads();
+  if (slice == 0 && c < cols) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += red[i][lane];
+    if (f16) static_cast<__half*>(out)[c] = __float2half_rn(s);
+    else static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(s);
+  }
+}
+
+size_t round256(size_t x) { return (x + 255) & ~size_t{255}; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ----------------------------------------------------------- choice of tiles
+enum Kind { FORWARD, DX, DWEIGHT };
+enum Variant { PAIR_256, PAIR_128, SWAP_32, SWAP_128 };
+
+struct Choice {
+  Variant variant;
+  int32_t splits;
+};
+
+// Rows, columns and k of a product: D is [batches x n_rows][cols].
+struct Product {
+  int64_t batches, n_rows, cols, k_steps;
+  Kind kind;
+};
+
+bool parts(const Choice& c) { return c.splits > 1 || c.variant >= SWAP_32; }
+
+// The fastest by a model in clocks: waves of units, each its k steps, a fill and an
+// epilogue; parts cost a write, a read and a launch.  A step is bound by the MMAs or by what
+// an SM takes from L2 (59 bytes a clock).
+Choice choose(const Product& q) {
+  Choice best{PAIR_256, 1};
+  double least = 1e30;
+  for (int v = PAIR_256; v <= SWAP_128; ++v) {
+    if (v >= SWAP_32 && q.kind == DWEIGHT) continue;
+    const bool swap = v >= SWAP_32;
+    const int64_t tok = v == PAIR_256 || v == PAIR_128 ? 256 : v == SWAP_32 ? 32 : 128;
+    const int64_t feat = v == PAIR_256 ? 256 : 128;
+    const int64_t tiles = q.batches * cdiv(q.n_rows, tok) * cdiv(q.cols, feat);
+    const int64_t slots = swap ? kSms : kSms / 2;
+    const double step = v == PAIR_256 ? 560 : v == PAIR_128 ? 420 : v == SWAP_32 ? 350 : 560;
+    for (int64_t s = 1; s <= 16 && s <= q.k_steps; ++s) {
+      const int64_t waves = cdiv(tiles * s, slots);
+      double t = waves * (cdiv(q.k_steps, s) * step + 600) + 3000;
+      if (s > 1 || swap) t += 4000 + 8.0 * s * q.batches * q.n_rows * q.cols / 3000;
+      if (t < least) {
+        least = t;
+        best = {static_cast<Variant>(v), static_cast<int32_t>(s)};
+      }
+    }
+  }
+  return best;
+}
+
+size_t part_bytes(const Product& q) {
+  const Choice c = choose(q);
+  return parts(c) ? static_cast<size_t>(c.splits) * q.batches * q.n_rows * q.cols * 4 : 0;
+}
+
+// ---------------------------------------------------------------- the layer
+struct Layer {
+  int64_t B, N, K, M;                  // tokens B x N, in and out features
+  int32_t in_heads, in_dim, out_heads, out_dim;
+  bool f16;
+};
+Layer layer_of(const tsr_linear_desc& d) {
+  return {d.B, d.N, static_cast<int64_t>(d.in_heads) * d.in_dim, static_cast<int64_t>(d.out_heads) * d.out_dim,
+          d.in_heads, d.in_dim, d.out_heads, d.out_dim, d.dtype == TSR_DTYPE_F16};
+}
+Product product(const Layer& y, Kind kind) {
+  if (kind == DWEIGHT) return {1, y.M, y.K, y.B * cdiv(y.N, BK), kind};
+  return {y.B, y.N, kind == FORWARD ? y.M : y.K, cdiv(kind == FORWARD ? y.K : y.M, BK), kind};
+}
+// Tokens of all batches as one row of tokens, where every tensor of the call allows it.
+bool flat(const Layer& y, const View& v) { return y.B == 1 || y.N == 1 || v.sb == y.N * v.sn; }
+void flatten(Layer& y, View* const* views, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!flat(y, *views[i])) return;
+  for (int i = 0; i < n; ++i)
+    if (y.N == 1) views[i]->sn = views[i]->sb;
+  y.N *= y.B;
+  y.B = 1;
+}
+size_t most_parts(const tsr_linear_desc& d, Kind kind) {
+  Layer y = layer_of(d);
+  const size_t a = part_bytes(product(y, kind));
+  y.N *= y.B;
+  y.B = 1;
+  return std::max(a, part_bytes(product(y, kind)));
+}
+
+View view(const int64_t* stride, int32_t dim) { return {stride[0], stride[1], stride[2], dim}; }
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// {channel, token, head, batch} boxes of 64 channels x `rows` tokens.
+tsr_status encode(CUtensorMap* m, const void* p, const View& v, int64_t heads, int64_t n, int64_t b, int rows, bool f16) {
+  if (!encoder()) return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled is missing");
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(v.dim), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(b)};
+  auto bytes = [](int64_t size, int64_t s) { return static_cast<cuuint64_t>(size > 1 ? 2 * s : 16); };
+  cuuint64_t strides[3] = {bytes(n, v.sn), bytes(heads, v.sh), bytes(b, v.sb)};
+  cuuint32_t box[4] = {BK, static_cast<cuuint32_t>(rows), 1, 1}, es[4] = {1, 1, 1, 1};
+  const CUresult r = encoder()(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                               const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  return TSR_OK;
+}
+
+template <int CG, int BN, bool A_MN, bool B_MN, bool SWAP>
+tsr_status launch_variant(const GemmParams& p, cudaStream_t st) {
+  using C = Cfg<CG, BN, SWAP>;
+  auto kern = linear_gemm_kernel<CG, BN, A_MN, B_MN, SWAP>;
+  int dev = 0;
+  TSR_CUDA(cudaGetDevice(&dev));
+  // once per device: the attribute is the function's there
+  static bool set[64] = {};
+  if (dev >= 64 || !set[dev]) {
+    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    if (dev < 64) set[dev] = true;
+  }
+  const int64_t units = static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CG;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, num_sms(dev) / CG) * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  TSR_CUDA(cudaLaunchKernelEx(&cfg, kern, p));
+  return TSR_OK;
+}
+
+template <bool A_MN, bool B_MN, bool SWAPS>
+tsr_status launch_kind(Variant v, const GemmParams& p, cudaStream_t st) {
+  if (v == PAIR_256) return launch_variant<2, 256, A_MN, B_MN, false>(p, st);
+  if (v == PAIR_128) return launch_variant<2, 128, A_MN, B_MN, false>(p, st);
+  if constexpr (SWAPS) {
+    // the weight is A there: B's orientation here
+    if (v == SWAP_32) return launch_variant<1, 32, B_MN, A_MN, true>(p, st);
+    return launch_variant<1, 128, B_MN, A_MN, true>(p, st);
+  }
+  return fail(TSR_ERR_INTERNAL, "no kernel for this product");
+}
+
+// One product with its epilogue.  `tok`: the tensor whose rows are tokens (x or dz),
+// `other`: the weight, or x for the weight's gradient.
+tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int64_t tok_heads, const void* other,
+               const View& vother, int64_t other_heads, const Epilogue& e, float* ws, cudaStream_t st) {
+  const Product q = product(y, kind);
+  const Choice c = choose(q);
+  const bool swap = c.variant >= SWAP_32;
+  GemmParams p;
+  memset(&p, 0, sizeof p);
+  p.epi = e;
+  p.part = parts(c) ? ws : nullptr;
+  p.total_rows = q.batches * q.n_rows;
+  p.n_rows = static_cast<int32_t>(q.n_rows);
+  p.batches = static_cast<int32_t>(q.batches);
+  p.cols = static_cast<int32_t>(q.cols);
+  p.splits = c.splits;
+  p.k_steps = static_cast<int32_t>(q.k_steps);
+  p.k_steps_per_batch = static_cast<int32_t>(cdiv(y.N, BK));
+  p.group = 8;
+  p.timeout_ns = kTimeoutNs;
+  const int bn = c.variant == PAIR_256 ? 256 : c.variant == SWAP_32 ? 32 : 128;
+  const int tile = swap ? bn : 256;                       // tokens (dweight: out features) of a tile
+  p.tiles_per_batch = static_cast<int32_t>(cdiv(q.n_rows, tile));
+  p.row_tiles = p.tiles_per_batch * p.batches;
+  p.col_tiles = static_cast<int32_t>(cdiv(q.cols, swap ? 128 : bn));
+  if (swap) std::swap(p.row_tiles, p.col_tiles);
+  CUtensorMap *mt = &p.ta, *mo = &p.tb;
+  int32_t *dt = &p.a_dim, *dother = &p.b_dim;
+  if (swap) {
+    std::swap(mt, mo);
+    std::swap(dt, dother);
+  }
+  *dt = vtok.dim;
+  *dother = vother.dim;
+  const bool tok_mn = kind == DWEIGHT, other_mn = kind != FORWARD;
+  const int tok_rows = tok_mn ? BK : swap ? bn : 128, other_rows = other_mn ? BK : swap ? 128 : bn / 2;
+  if (tsr_status s = encode(mt, tok, vtok, tok_heads, y.N, y.B, tok_rows, y.f16)) return s;
+  const int64_t on = kind == DWEIGHT ? y.N : y.M, ob = kind == DWEIGHT ? y.B : 1;
+  if (tsr_status s = encode(mo, other, vother, other_heads, on, ob, other_rows, y.f16)) return s;
+  p.idesc = idesc_16bit(y.f16, swap ? 128 : 256, bn, swap ? other_mn : tok_mn, swap ? tok_mn : other_mn);
+  tsr_status s;
+  if (kind == FORWARD) s = launch_kind<false, false, true>(c.variant, p, st);
+  else if (kind == DX) s = launch_kind<false, true, true>(c.variant, p, st);
+  else s = launch_kind<true, true, false>(c.variant, p, st);
+  if (s || !p.part) return s;
+  const int64_t vecs = p.total_rows * (q.cols / 8);
+  TSR_CUDA(launch_dependent(linear_finish_kernel, static_cast<unsigned>(cdiv(vecs, 256)), 256u, 0, st,
+                            static_cast<const float*>(p.part), p.splits, p.total_rows, p.n_rows, p.cols, e));
+  return TSR_OK;
+}
+
+// Blocks of rows of the pass over dz.
+int64_t dz_blocks(int64_t T, int64_t M) { return std::max<int64_t>(1, std::min(cdiv(T, 32), kSms * 8 / cdiv(M, 256) + 1)); }
+
+struct BackwardSpace {
+  size_t dz, sums, parts, total;
+};
+BackwardSpace backward_space(const tsr_linear_desc& d) {
+  const Layer y = layer_of(d);
+  BackwardSpace s;
+  s.dz = 0;
+  s.sums = s.dz + (d.activation ? round256(static_cast<size_t>(y.B * y.N * y.M) * 2) : 0);
+  s.parts = s.sums + round256(static_cast<size_t>(dz_blocks(y.B * y.N, y.M) * y.M) * 4);
+  s.total = s.parts + round256(std::max(most_parts(d, DX), most_parts(d, DWEIGHT)));
+  return s;
+}
+
+}  // namespace
+
+}  // namespace linear
+
+using namespace linear;
+
+size_t linear_workspace(const tsr_linear_desc& d) { return round256(most_parts(d, FORWARD)); }
+size_t linear_backward_workspace(const tsr_linear_desc& d) { return backward_space(d).total; }
+
+// The arguments of both have been checked (api_layer.cu).
+tsr_status launch_linear(const tsr_linear_desc& d, const tsr_linear_args& a, void* ws, cudaStream_t st) {
+  Layer y = layer_of(d);
+  View vx = view(a.x_stride, y.in_dim);
+  Epilogue e;
+  memset(&e, 0, sizeof e);
+  e.bias = a.bias;
+  e.res = a.residual;
+  e.out = a.out;
+  e.pre = a.pre;
+  e.vout = view(a.out_stride, y.out_dim);
+  e.vres = view(a.residual_stride, y.out_dim);
+  e.vpre = view(a.pre_stride, y.out_dim);
+  e.act = d.activation;
+  e.f16 = y.f16;
+  View* views[4] = {&vx, &e.vout};
+  int n = 2;
+  if (a.residual) views[n++] = &e.vres;
+  if (a.pre) views[n++] = &e.vpre;
+  flatten(y, views, n);
+  const View vw{0, 0, y.K, static_cast<int32_t>(y.K)};
+  return run(y, FORWARD, a.x, vx, y.in_heads, a.weight, vw, 1, e, static_cast<float*>(ws), st);
+}
+
+tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_grads& a, void* ws, cudaStream_t st) {
+  Layer y = layer_of(d);
+  const BackwardSpace space = backward_space(d);
+  char* base = static_cast<char*>(ws);
+  View vx = view(a.x_stride, y.in_dim), vdx = view(a.dx_stride, y.in_dim);
+  View vdout = view(a.dout_stride, y.out_dim), vpre = view(a.pre_stride, y.out_dim);
+  View* views[4] = {&vdout};
+  int n = 1;
+  if (a.dweight) views[n++] = &vx;
+  if (a.dx) views[n++] = &vdx;
+  if (d.activation) views[n++] = &vpre;
+  flatten(y, views, n);
+  const void* dz = a.dout;
+  View vdz = vdout;
+  int64_t dz_heads = y.out_heads;
+  const bool operands = a.dx || a.dweight;
+  if ((d.activation && operands) || a.dbias) {
+    DzParams p;
+    memset(&p, 0, sizeof p);
+    p.dout = static_cast<const uint16_t*>(a.dout);
+    p.pre = d.activation ? static_cast<const uint16_t*>(a.pre) : nullptr;
+    p.dz = d.activation && operands ? reinterpret_cast<uint16_t*>(base + space.dz) : nullptr;
+    p.part = a.dbias ? reinterpret_cast<float*>(base + space.sums) : nullptr;
+    p.vdout = vdout;
+    p.vpre = vpre;
+    p.rows = y.B * y.N;
+    p.n_rows = static_cast<int32_t>(y.N);
+    p.cols = static_cast<int32_t>(y.M);
+    p.act = d.activation;
+    p.f16 = y.f16;
+    int64_t blocks = dz_blocks(p.rows, y.M);
+    p.rows_per_block = static_cast<int32_t>(cdiv(p.rows, blocks));
+    blocks = cdiv(p.rows, p.rows_per_block);
+    linear_dz_kernel<<<dim3(static_cast<unsigned>(cdiv(y.M, 256)), static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
+    TSR_CUDA(cudaGetLastError());
+    if (a.dbias)
+      TSR_CUDA(launch_dependent(linear_bias_kernel, static_cast<unsigned>(cdiv(y.M, 32)), 1024u, 0, st,
+                                static_cast<const float*>(p.part), static_cast<int32_t>(blocks), p.cols, a.dbias,
+                                p.f16));
+    if (p.dz) {
+      dz = p.dz;
+      vdz = View{y.N * y.M, 0, y.M, static_cast<int32_t>(y.M)};
+      dz_heads = 1;
+    }
+  }
+  float* part = reinterpret_cast<float*>(base + space.parts);
+  Epilogue e;
+  memset(&e, 0, sizeof e);
+  e.f16 = y.f16;
+  if (a.dx) {
+    e.out = a.dx;
+    e.vout = vdx;
+    const View vw{0, 0, y.K, static_cast<int32_t>(y.K)};
+    if (tsr_status s = run(y, DX, dz, vdz, dz_heads, a.weight, vw, 1, e, part, st)) return s;
+  }
+  if (a.dweight) {
+    e.out = a.dweight;
+    e.vout = View{0, 0, y.K, static_cast<int32_t>(y.K)};
+    return run(y, DWEIGHT, dz, vdz, dz_heads, a.x, vx, y.in_heads, e, part, st);
+  }
+  return TSR_OK;
+}
+
+tsr_status linear_device_status(cudaStream_t st) {
+  uint32_t word = 0;
+  void* at = nullptr;
+  TSR_CUDA(cudaGetSymbolAddress(&at, g_err));
+  TSR_CUDA(cudaMemcpyAsync(&word, at, sizeof word, cudaMemcpyDeviceToHost, st));
+  TSR_CUDA(cudaMemsetAsync(at, 0, sizeof word, st));
+  TSR_CUDA(cudaStreamSynchronize(st));
+  if (word & DEV_ERR_TIMEOUT) return fail(TSR_ERR_TIMEOUT, "a wait in a linear layer's product gave up");
+  if (word) return fail(TSR_ERR_INTERNAL, "a linear layer's product found its memory misaligned");
+  return TSR_OK;
+}
+
+}  // namespace tsr

@@ -1,0 +1,425 @@
+// linear_gemm.cuh -- the matrix products of a linear layer on tcgen05 tensor cores:
+//     D[r][c] = sum_k A(r, k) B(c, k)
+// with A and B 16-bit (bf16 or fp16), D in fp32 in TMEM and an epilogue on its way out.
+//
+//   forward   A = x (rows: tokens),           B = weight (rows: out features), k: in features
+//   dx        A = dz (rows: tokens),          B = weight^T (rows: in features), k: out features
+//   dweight   A = dz^T (rows: out features),  B = x^T (rows: in features),     k: tokens
+//
+// An operand whose k is contiguous in memory is K-major, one whose rows are contiguous
+// MN-major; the tensor cores take both, so nothing is transposed.  Every tensor is seen by
+// TMA as {channel, token, head, batch} with free strides: the attention's head-major
+// [B][H][N][d] is read and written in place.
+//
+// Bound: the tensor pipe for many tokens.  Two CTAs (a pair, cta_group::2) compute a tile
+// of 256 rows x BN columns; each loads half of A's and half of B's rows, so a step of 64 k
+// is 32 KB per SM for 512 clocks of MMAs at BN = 256, 64 bytes a clock, about what an SM
+// takes from L2 (a tile of 128 x 256 of one CTA would need 96).  The accumulator has two
+// buffers in TMEM: the epilogue of a tile runs beside the MMAs of the next.
+// For few tokens the weight's bytes bound it; then the features lie on the 128 rows and
+// the tokens on BN columns (SWAP), one CTA a tile, k split over CTAs.
+//
+// Persistent: a CTA (pair) takes every n-th work unit.  Units with a part of k only
+// (split) store fp32 parts that linear_finish_kernel adds in their order.
+// Warps: TMA producer, MMA issuer (of the pair's first CTA), 8 epilogue warps.  Every wait
+// is bounded: on expiry the error word is set and the kernel winds down.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace tsr {
+
+namespace linear {
+
+constexpr int kEpiWarps = 8, kThreads = (kEpiWarps + 2) * 32;
+constexpr int BK = 64;                 // k per step: 128 bytes, the swizzle's row
+
+// A tensor's addressing: element strides of batch, head and token; channels contiguous.
+struct View {
+  int64_t sb, sh, sn;
+  int32_t dim;                         // channels per head
+};
+
+// What happens to a value of D on its way out.
+struct Epilogue {
+  const void *bias, *res;              // null: none
+  void *out, *pre;                     // pre: the value before the activation, null: not kept
+  View vout, vres, vpre;
+  int32_t act, f16;
+};
+
+struct GemmParams {
+  CUtensorMap ta, tb;
+  Epilogue epi;
+  float* part;                         // [split][rows][cols] of D (SWAP: of D^T), null: epilogue here
+  int64_t total_rows;                  // of D (tokens in all batches, or features)
+  int32_t n_rows, batches;             // rows per batch
+  int32_t cols;
+  int32_t row_tiles, col_tiles;        // row tiles of all batches (SWAP: column tiles are)
+  int32_t tiles_per_batch;             // of the token axis
+  int32_t splits, k_steps;             // k steps of a whole product
+  int32_t k_steps_per_batch;           // dweight: steps of one batch's tokens
+  int32_t a_dim, b_dim;                // channels per head of A's and B's tensors
+  int32_t group;                       // row tiles that share their columns' loads in L2
+  uint32_t idesc;
+  uint64_t timeout_ns;
+};
+
+// Waits that gave up (tsr_linear_device_status): of the device, not of a call.
+static __device__ uint32_t g_err;
+
+// ------------------------------------------------------------- the epilogue
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool f16) {
+  if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
+  if (f16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ void unpack8(uint4 w, bool f16, float (&v)[8]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack16(x[i], f16);
+    v[2 * i] = p.x;
+    v[2 * i + 1] = p.y;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8], bool f16) {
+  return make_uint4(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16), pack16(v[4], v[5], f16),
+                    pack16(v[6], v[7], f16));
+}
+
+constexpr float kGelu0 = 0.7978845608028654f, kGelu1 = 0.044715f;   // sqrt(2 / pi)
+
+// The tanh form is z times the logistic function of 2u, u = kGelu0 (z + kGelu1 z^3): no
+// cancellation for negative z.  The exponential is within about |2u| 2^-23 of its value,
+// far inside a 16-bit rounding.
+__device__ __forceinline__ float activate(float z, int act) {
+  if (act == TSR_ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * kGelu0 * fmaf(kGelu1 * z * z, z, z)));
+  if (act == TSR_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+  if (act == TSR_ACT_GELU) return z * normcdff(z);
+  return z;
+}
+// The activation's derivative.  It is 0 or 1 in fp32 past |z| = 30 (SiLU: 90); z is taken
+// there so that no 0 * inf arises.
+__device__ __forceinline__ float slope(float z, int act) {
+  if (z != z) return z;
+  if (act == TSR_ACT_SILU) {
+    const float x = fminf(fmaxf(z, -80.f), 80.f);
+    const float s = __fdividef(1.f, 1.f + __expf(-x));
+    return s * fmaf(x, 1.f - s, 1.f);
+  }
+  const float x = fminf(fmaxf(z, -30.f), 30.f);
+  if (act == TSR_ACT_GELU_TANH) {
+    const float s = __fdividef(1.f, 1.f + __expf(-2.f * kGelu0 * fmaf(kGelu1 * x * x, x, x)));
+    return fmaf(x * s * (1.f - s), 2.f * kGelu0 * fmaf(3.f * kGelu1, x * x, 1.f), s);
+  }
+  if (act == TSR_ACT_GELU) return fmaf(x * 0.3989422804014327f, __expf(-0.5f * x * x), normcdff(x));
+  return 1.f;
+}
+
+__device__ __forceinline__ int64_t at(const View& v, int64_t b, int64_t n, int32_t f) {
+  const int32_t h = f / v.dim;
+  return b * v.sb + h * v.sh + n * v.sn + (f - h * v.dim);
+}
+
+// Eight neighbouring features [f, f + 8) of token (b, n), from D's values to the output.
+__device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_t b, int64_t n, int32_t f) {
+  if (e.bias) {
+    float t[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(e.bias) + f / 8), e.f16, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  if (e.pre) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.pre) + at(e.vpre, b, n, f)) = pack8(v, e.f16);
+  if (e.act) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], e.act);
+  }
+  if (e.res) {
+    float t[8];
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + at(e.vres, b, n, f)), e.f16, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at(e.vout, b, n, f)) = pack8(v, e.f16);
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int CG, int BN, bool SWAP>
+struct Cfg {
+  static constexpr int TM = 128 * CG;                     // rows of a tile
+  static constexpr int A_BYTES = 128 * BK * 2, B_ROWS = BN / CG, B_BYTES = B_ROWS * BK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = (200 * 1024 / STAGE) < 8 ? (200 * 1024 / STAGE) : 8;
+  static constexpr int CTRL = STAGES * STAGE, SMEM = CTRL + 512;
+  static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;  // two accumulators
+  static_assert(SMEM > 114 * 1024, "one CTA per SM");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(TMEM <= 512 && (TMEM & (TMEM - 1)) == 0, "TMEM");
+};
+
+struct alignas(8) Ctrl {
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], final_bar;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+static_assert(sizeof(Ctrl) <= 512, "Ctrl");
+
+// A work unit: a tile and its part of k.
+struct Unit {
+  int32_t row_tile, col_tile, split, k0, k1;
+};
+__device__ __forceinline__ Unit unit_of(const GemmParams& p, int64_t u) {
+  Unit w;
+  const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.col_tiles;
+  w.split = static_cast<int32_t>(u / tiles);
+  const int64_t t = u - w.split * tiles;
+  // `group` row tiles at a time, their columns one after another: the CTAs that run
+  // together share rows and columns in L2
+  const int64_t per = static_cast<int64_t>(p.group) * p.col_tiles;
+  const int32_t g = static_cast<int32_t>(t / per);
+  const int32_t rows = min(p.group, p.row_tiles - g * p.group);
+  const int32_t in = static_cast<int32_t>(t - g * per);
+  w.col_tile = in / rows;
+  w.row_tile = g * p.group + in % rows;
+  w.k0 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * w.split / p.splits);
+  w.k1 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * (w.split + 1) / p.splits);
+  return w;
+}
+
+template <int CG, int BN, bool A_MN, bool B_MN, bool SWAP>
+__global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmParams p) {
+  using C = Cfg<CG, BN, SWAP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + C::CTRL);
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  volatile int32_t* abort_flag = &ctrl.abort_flag;
+  if (threadIdx.x == 0) {
+    if (base & 1023u) atomicOr(&g_err, DEV_ERR_INTERNAL);   // swizzled tiles need 1024-byte alignment
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(smem_u32(&ctrl.full[i]), 1);
+      mbar_init(smem_u32(&ctrl.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctrl.acc_full[i]), 1);
+      mbar_init(smem_u32(&ctrl.acc_empty[i]), kEpiWarps * CG);
+    }
+    mbar_init(smem_u32(&ctrl.final_bar), 1);
+    ctrl.abort_flag = (base & 1023u) ? 1 : 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(smem_u32(&ctrl.tmem_base), C::TMEM);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&ctrl.tmem_base), C::TMEM);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
+  const int64_t units = static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits;
+  const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&p.ta);
+      tma_prefetch_desc(&p.tb);
+      int64_t issued = 0;                                 // steps
+      int st = 0;
+      uint32_t parity = 1u;                               // of the wait for an empty stage
+      bool ok = true;
+      for (int64_t u = first; ok && u < units; u += stride) {
+        const Unit w = unit_of(p, u);
+        // the token axis: rows of A (SWAP: rows of B), tiles of each batch by themselves
+        const int32_t tok_tile = SWAP ? w.col_tile : w.row_tile;
+        const int32_t tb = A_MN && !SWAP ? 0 : tok_tile / p.tiles_per_batch;
+        const int32_t tn = (tok_tile - tb * p.tiles_per_batch) * (SWAP ? BN : C::TM);
+        const int32_t row0 = (A_MN && !SWAP ? w.row_tile * C::TM : SWAP ? w.row_tile * 128 : tn) + rank * 128;
+        const int32_t col0 = (SWAP ? tn : w.col_tile * BN) + rank * C::B_ROWS;
+        for (int32_t s = w.k0; s < w.k1; ++s) {
+          if (!mbar_wait(smem_u32(&ctrl.empty[st]), parity, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
+          const uint32_t a = base + st * C::STAGE, b = a + C::A_BYTES;
+          uint32_t bar = smem_u32(&ctrl.full[st]);
+          if (rank == 0) mbar_arrive_expect_tx(bar, CG * C::STAGE);
+          if constexpr (CG == 2) bar = cluster_addr(bar, 0);
+          auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t f, int32_t dim, int32_t n, int32_t bt) {
+            const int32_t h = f / dim;
+            if constexpr (CG == 2) tma_load_4d_pair(dst, m, bar, f - h * dim, n, h, bt);
+            else tma_load_4d(dst, m, bar, f - h * dim, n, h, bt);
+          };
+          // k of this step as channels (K-major operands) or as tokens / weight rows
+          const int32_t kc = s * BK;
+          const int32_t kb = A_MN && !SWAP ? s / p.k_steps_per_batch : 0;
+          const int32_t kn = A_MN && !SWAP ? (s - kb * p.k_steps_per_batch) * BK : kc;
+          if constexpr (A_MN) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) load(a + g * 64 * 128, &p.ta, row0 + g * 64, p.a_dim, kn, kb);
+          } else {
+            load(a, &p.ta, kc, p.a_dim, row0, SWAP ? 0 : tb);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int g = 0; g < C::B_ROWS / 64; ++g) load(b + g * 64 * 128, &p.tb, col0 + g * 64, p.b_dim, kn, kb);
+          } else {
+            load(b, &p.tb, kc, p.b_dim, col0, SWAP ? tb : 0);
+          }
+          ++issued;
+          if (++st == C::STAGES) {
+            st = 0;
+            parity ^= 1u;
+          }
+        }
+      }
+      if (rank == 0) {
+        // every copy has landed before the CTA ends; normally they all have been waited for
+        volatile int32_t no = 0;
+        for (int64_t k = issued > C::STAGES ? issued - C::STAGES : 0; k < issued; ++k)
+          mbar_wait(smem_u32(&ctrl.full[k % C::STAGES]), static_cast<uint32_t>(k / C::STAGES) & 1u, &no, &g_err,
+                    p.timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t elect = elect_lane();
+      int st = 0;
+      uint32_t parity = 0u;
+      int32_t tile = 0;
+      bool ok = true;
+      for (int64_t u = first; ok && u < units; u += stride, ++tile) {
+        const Unit w = unit_of(p, u);
+        const int buf = tile & 1;
+        if (!mbar_wait_warp(smem_u32(&ctrl.acc_empty[buf]), ((tile >> 1) & 1) ^ 1, abort_flag, &g_err, p.timeout_ns)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + buf * BN;
+        for (int32_t s = w.k0; s < w.k1; ++s) {
+          if (!mbar_wait_warp(smem_u32(&ctrl.full[st]), parity, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a = base + st * C::STAGE, b = a + C::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k) {
+            const uint64_t da = A_MN ? sdesc_sw128(a + k * 2048, 64 * 128, 1024) : sdesc_sw128(a + k * 32, 16, 1024);
+            const uint64_t db = B_MN ? sdesc_sw128(b + k * 2048, 64 * 128, 1024) : sdesc_sw128(b + k * 32, 16, 1024);
+            const uint32_t more = s > w.k0 || k > 0;
+            if constexpr (CG == 2) mma_f16_ss_pair(elect, acc, da, db, p.idesc, more);
+            else mma_bf16_ss(elect, acc, da, db, p.idesc, more);
+          }
+          if constexpr (CG == 2) mma_commit_pair(elect, smem_u32(&ctrl.empty[st]));
+          else mma_commit(elect, smem_u32(&ctrl.empty[st]));
+          if (++st == C::STAGES) {
+            st = 0;
+            parity ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if constexpr (CG == 2) mma_commit_pair(elect, smem_u32(&ctrl.acc_full[buf]));
+        else mma_commit(elect, smem_u32(&ctrl.acc_full[buf]));
+      }
+      if (*abort_flag) {
+        // the products in flight end before TMEM is freed
+        if constexpr (CG == 2) mma_commit_pair(elect, smem_u32(&ctrl.final_bar));
+        else mma_commit(elect, smem_u32(&ctrl.final_bar));
+        volatile int32_t no = 0;
+        mbar_wait_warp(smem_u32(&ctrl.final_bar), 0, &no, &g_err, p.timeout_ns);
+      }
+    }
+  } else {
+    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;   // TMEM lanes 32 * quarter of this warp
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    int32_t tile = 0;
+    for (int64_t u = first; u < units; u += stride, ++tile) {
+      const Unit w = unit_of(p, u);
+      const int buf = tile & 1;
+      if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + lanes + buf * BN;
+      const int32_t r = quarter * 32 + lane + rank * 128;          // row in the tile
+      if constexpr (SWAP) {
+        // rows are features, columns tokens: the warp stores 32 neighbouring features of a token
+        const int32_t f = w.row_tile * 128 + r;
+        const int32_t b = w.col_tile / p.tiles_per_batch, n0 = (w.col_tile - b * p.tiles_per_batch) * BN;
+        float* dst = p.part + (static_cast<int64_t>(w.split) * p.batches + b) * p.n_rows * p.cols + f;
+#pragma unroll 1
+        for (int c = half * 16; c < BN; c += 32) {
+          if (n0 + c >= p.n_rows) break;
+          uint32_t v[16];
+          tmem_ld16(acc + c, v);
+          tc_wait_ld();
+          if (f < p.cols) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (n0 + c + i < p.n_rows) dst[static_cast<int64_t>(n0 + c + i) * p.cols] = __uint_as_float(v[i]);
+          }
+        }
+      } else {
+        const int32_t b = A_MN ? 0 : w.row_tile / p.tiles_per_batch;
+        const int64_t n = static_cast<int64_t>(w.row_tile - b * p.tiles_per_batch) * C::TM + r;
+        const bool valid = n < p.n_rows;
+        constexpr int W = BN / 2;                                   // columns of this warp
+#pragma unroll 1
+        for (int c = 0; c < W; c += 32) {
+          const int32_t f0 = w.col_tile * BN + half * W + c;
+          if (f0 >= p.cols) break;
+          uint32_t v[32];
+          tmem_ld32(acc + half * W + c, v);
+          tc_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int32_t f = f0 + 8 * g;
+              if (f >= p.cols) break;
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
+              if (p.part) {
+                float4* dst = reinterpret_cast<float4*>(
+                    p.part + (static_cast<int64_t>(w.split) * p.total_rows + static_cast<int64_t>(b) * p.n_rows + n) * p.cols + f);
+                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+              } else {
+                finish8(p.epi, x, b, n, f);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&ctrl.acc_empty[buf]);
+        if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(bar, 0));
+        else mbar_arrive(bar);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem, C::TMEM);
+    else tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+}  // namespace linear
+
+}  // namespace tsr

@@ -577,6 +577,77 @@ tsr_status tsr_norm_rope_backward(const tsr_rope_desc *desc, double eps, const t
                                   int32_t n_tensors, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * tsr_linear -- a linear layer with its epilogue in one product,
+ *     z = x weight^T + bias,      out = activation(z) + residual
+ * (the projections around the attention and a layer's feed-forward), and
+ * tsr_linear_backward, its gradients from dout, that of out:
+ *     dz = dout o activation'(pre),  dx = dz weight,  dweight = dz^T x,  dbias = sum of dz
+ * over the tokens; the residual's gradient is dout itself.
+ *
+ * Token rows (x, out, residual, pre and their gradients) are [B][heads][N][dim] by strides
+ * in elements for b, h and n, dim contiguous: heads = 1 is a token-major [B][N][features],
+ * heads > 1 the attention's head-major layout, read and written in place; feature
+ * h * dim + c of the layer is channel c of head h.  K = in_heads * in_dim, M = out_heads *
+ * out_dim.  weight: [M][K] contiguous; bias: [M] or NULL; residual: like out, or NULL (out
+ * itself with equal strides: in place); pre: like out, or NULL: z rounded to the tensors'
+ * type, which the backward of an activation needs (that of no activation reads none).
+ * All bf16 or all fp16.  Products are summed in fp32 and rounded once; the activation is
+ * taken of z before its rounding.  In the backward dz is rounded to the tensors' type as
+ * an operand of both products; dbias is summed in fp32 from dz before that.
+ * TSR_ACT_GELU is z Phi(z); TSR_ACT_GELU_TANH z / (1 + exp(-2u)) with u = sqrt(2 / pi)
+ * (z + 0.044715 z^3); TSR_ACT_SILU z / (1 + exp(-z)).
+ *
+ * dx, dweight and dbias may be NULL where they are not needed (x is read for dweight
+ * only, weight for dx only).  The same inputs give the same bits every run.
+ *
+ * Features are multiples of 8, with heads > 1 of 64 per head; pointers 16-byte aligned,
+ * strides multiples of 8 and > 0 (no broadcast inputs), strides of dimensions of size 1 not
+ * read.  Outputs must not overlap inputs but for the residual.  workspace: device, 256-byte
+ * aligned, tsr_linear_workspace() (backward: tsr_linear_backward_workspace()) bytes, NULL
+ * where that is 0; calls that may run at the same time need one each.  Asynchronous on
+ * `stream`; nothing is allocated.
+ * Errors: TSR_ERR_INVALID_ARG; TSR_ERR_UNSUPPORTED for K or M above 2^20, B * N above 2^24
+ * and strides of 2^38.
+ *
+ * tsr_linear_device_status synchronises `stream` and returns TSR_ERR_TIMEOUT if a wait in
+ * any linear layer's product on the current device has given up since the last such call
+ * (the outputs of that product are not valid), else TSR_OK.
+ */
+typedef enum { TSR_ACT_NONE = 0, TSR_ACT_GELU = 1, TSR_ACT_GELU_TANH = 2, TSR_ACT_SILU = 3 } tsr_activation;
+
+typedef struct {
+  int32_t B, N;
+  int32_t in_heads, in_dim;     /* K = in_heads * in_dim */
+  int32_t out_heads, out_dim;   /* M = out_heads * out_dim */
+  int32_t dtype;                /* TSR_DTYPE_BF16 or TSR_DTYPE_F16 */
+  int32_t activation;           /* tsr_activation */
+} tsr_linear_desc;
+
+typedef struct {
+  const void *x, *weight, *bias, *residual;
+  void *out, *pre;
+  int64_t x_stride[3], residual_stride[3], out_stride[3], pre_stride[3];   /* b, h, n */
+} tsr_linear_args;
+
+typedef struct {
+  const void *dout, *x, *weight, *pre;
+  void *dx, *dweight, *dbias;
+  int64_t dout_stride[3], x_stride[3], pre_stride[3], dx_stride[3];        /* b, h, n */
+} tsr_linear_grads;
+
+tsr_status tsr_linear_workspace(const tsr_linear_desc *desc, size_t *bytes /* HOST */);
+
+tsr_status tsr_linear(const tsr_linear_desc *desc, const tsr_linear_args *args, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+tsr_status tsr_linear_backward_workspace(const tsr_linear_desc *desc, size_t *bytes /* HOST */);
+
+tsr_status tsr_linear_backward(const tsr_linear_desc *desc, const tsr_linear_grads *args, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+tsr_status tsr_linear_device_status(void *stream);
+
+/*
  * tsr_block_select -- a block mask for tsr_plan from a cheap score per block pair
  * (the step before the path, for callers without a mask; compare tsr_svg_route,
  * which routes whole heads).
