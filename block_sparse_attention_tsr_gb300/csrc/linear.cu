@@ -214,20 +214,24 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
+// A 4-D tensor map, 128-byte swizzle; strides in elements, of dimensions 1 to 3.
+tsr_status encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int size, const int64_t (&dims)[4],
+                  const int64_t (&strides)[3], int box0, int box1) {
+  if (!encoder()) return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled is missing");
+  cuuint64_t d[4], s[3];
+  for (int i = 0; i < 4; ++i) d[i] = static_cast<cuuint64_t>(dims[i]);
+  for (int i = 0; i < 3; ++i) s[i] = static_cast<cuuint64_t>(dims[i + 1] > 1 ? size * strides[i] : 16);
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1, 1}, es[4] = {1, 1, 1, 1};
+  if (encoder()(m, type, 4, const_cast<void*>(p), d, s, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  return TSR_OK;
+}
 // {channel, token, head, batch} boxes of 64 channels x `rows` tokens.
 tsr_status encode(CUtensorMap* m, const void* p, const View& v, int64_t heads, int64_t n, int64_t b, int rows, bool f16) {
-  if (!encoder()) return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled is missing");
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(v.dim), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(heads),
-                        static_cast<cuuint64_t>(b)};
-  auto bytes = [](int64_t size, int64_t s) { return static_cast<cuuint64_t>(size > 1 ? 2 * s : 16); };
-  cuuint64_t strides[3] = {bytes(n, v.sn), bytes(heads, v.sh), bytes(b, v.sb)};
-  cuuint32_t box[4] = {BK, static_cast<cuuint32_t>(rows), 1, 1}, es[4] = {1, 1, 1, 1};
-  const CUresult r = encoder()(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                               const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-  return TSR_OK;
+  return encode(m, p, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                {v.dim, n, heads, b}, {v.sn, v.sh, v.sb}, BK, rows);
 }
 
 template <int CG, int BN, bool A_MN, bool B_MN, bool SWAP>
@@ -310,6 +314,21 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   const int64_t on = kind == DWEIGHT ? y.N : y.M, ob = kind == DWEIGHT ? y.B : 1;
   if (tsr_status s = encode(mo, other, vother, other_heads, on, ob, other_rows, y.f16)) return s;
   p.idesc = idesc_16bit(y.f16, swap ? 128 : 256, bn, swap ? other_mn : tok_mn, swap ? tok_mn : other_mn);
+  if (!swap) {
+    // out's rows: tokens, or the weight's for its gradient
+    const int64_t rows = q.n_rows, heads = q.cols / e.vout.dim;
+    if (p.part) {
+      if (tsr_status s = encode(&p.tout, p.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, {q.cols, rows, q.batches, c.splits},
+                                {q.cols, rows * q.cols, p.total_rows * q.cols}, 32, 32))
+        return s;
+    } else {
+      if (tsr_status s = encode(&p.tout, e.out, e.vout, heads, rows, q.batches, 32, y.f16)) return s;
+      if (e.pre)
+        if (tsr_status s = encode(&p.tpre, e.pre, e.vpre, heads, rows, q.batches, 32, y.f16)) return s;
+      if (e.res)
+        if (tsr_status s = encode(&p.tres, e.res, e.vres, heads, rows, q.batches, 32, y.f16)) return s;
+    }
+  }
   tsr_status s;
   if (kind == FORWARD) s = launch_kind<false, false, true>(c.variant, p, st);
   else if (kind == DX) s = launch_kind<false, true, true>(c.variant, p, st);

@@ -55,7 +55,10 @@ struct Epilogue {
 
 struct GemmParams {
   CUtensorMap ta, tb;
-  Epilogue epi;
+  // out (or the parts, fp32), pre and residual as {channel, token, head, batch} (parts:
+  // {channel, token, batch, split}) in boxes of 32 tokens x 128 bytes
+  CUtensorMap tout, tpre, tres;
+  Epilogue epi;                        // bias, activation and what is there; SWAP and parts: views
   float* part;                         // [split][rows][cols] of D (SWAP: of D^T), null: epilogue here
   int64_t total_rows;                  // of D (tokens in all batches, or features)
   int32_t n_rows, batches;             // rows per batch
@@ -110,6 +113,11 @@ __device__ __forceinline__ float activate(float z, int act) {
   if (act == TSR_ACT_GELU) return z * normcdff(z);
   return z;
 }
+__device__ __forceinline__ void activate8(float (&v)[8], int act) {
+  if (act == TSR_ACT_NONE) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = activate(v[i], act);
+}
 // The activation's derivative.  It is 0 or 1 in fp32 past |z| = 30 (SiLU: 90); z is taken
 // there so that no 0 * inf arises.
 __device__ __forceinline__ float slope(float z, int act) {
@@ -142,10 +150,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_
     for (int i = 0; i < 8; ++i) v[i] += t[i];
   }
   if (e.pre) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.pre) + at(e.vpre, b, n, f)) = pack8(v, e.f16);
-  if (e.act) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], e.act);
-  }
+  activate8(v, e.act);
   if (e.res) {
     float t[8];
     unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + at(e.vres, b, n, f)), e.f16, t);
@@ -155,14 +160,25 @@ __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at(e.vout, b, n, f)) = pack8(v, e.f16);
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int CG, int BN, bool SWAP>
 struct Cfg {
   static constexpr int TM = 128 * CG;                     // rows of a tile
   static constexpr int A_BYTES = 128 * BK * 2, B_ROWS = BN / CG, B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = (200 * 1024 / STAGE) < 8 ? (200 * 1024 / STAGE) : 8;
-  static constexpr int CTRL = STAGES * STAGE, SMEM = CTRL + 512;
+  // what leaves through shared memory: two pieces of 32 rows x 128 bytes for each epilogue warp
+  static constexpr int PIECE = 32 * 128, OUT_BYTES = SWAP ? 0 : kEpiWarps * 2 * PIECE;
+  static constexpr int FIT = (226 * 1024 - OUT_BYTES) / STAGE, STAGES = FIT < 8 ? FIT : 8;
+  static constexpr int OUT = STAGES * STAGE, CTRL = OUT + OUT_BYTES, SMEM = CTRL + 512;
   static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;  // two accumulators
   static_assert(SMEM > 114 * 1024, "one CTA per SM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -171,6 +187,7 @@ struct Cfg {
 
 struct alignas(8) Ctrl {
   uint64_t full[8], empty[8], acc_full[2], acc_empty[2], final_bar;
+  uint64_t res_full[kEpiWarps][2];     // the residual's piece has landed
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -198,6 +215,58 @@ __device__ __forceinline__ Unit unit_of(const GemmParams& p, int64_t u) {
   return w;
 }
 
+// Where an operand's copies start, step by step: 64 channels of `rows` rows (K-major, one
+// box), or G groups of 64 channels of 64 tokens or weight rows (MN-major).
+template <bool MN, int G>
+struct Walk {
+  int32_t dim, c[MN ? G : 1], h[MN ? G : 1], n, b, chunk, chunks;
+  // f0: first row (K-major) or channel (MN-major); chunks: k steps of a batch's tokens, 0:
+  // k has no batches
+  __device__ __forceinline__ Walk(int32_t dim_, int32_t f0, int32_t k0, int32_t chunks_, int32_t batch)
+      : dim(dim_), chunks(chunks_) {
+    if constexpr (MN) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        h[g] = (f0 + 64 * g) / dim;
+        c[g] = f0 + 64 * g - h[g] * dim;
+      }
+      b = chunks ? k0 / chunks : 0;
+      chunk = k0 - b * chunks;
+      n = chunk * BK;
+    } else {
+      h[0] = k0 * BK / dim;
+      c[0] = k0 * BK - h[0] * dim;
+      n = f0;
+      b = batch;
+      chunk = 0;
+    }
+  }
+  template <int CG>
+  __device__ __forceinline__ void load(uint32_t elect, uint32_t dst, const CUtensorMap* m, uint32_t bar) const {
+#pragma unroll
+    for (int g = 0; g < (MN ? G : 1); ++g) {
+      if constexpr (CG == 2) tma_load_4d_pair(elect, dst + g * 64 * 128, m, bar, c[g], n, h[g], b);
+      else tma_load_4d(elect, dst + g * 64 * 128, m, bar, c[g], n, h[g], b);
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (MN) {
+      n += BK;
+      if (chunks && ++chunk == chunks) {
+        chunk = 0;
+        n = 0;
+        ++b;
+      }
+    } else {
+      c[0] += BK;
+      if (c[0] >= dim) {
+        c[0] -= dim;
+        ++h[0];
+      }
+    }
+  }
+};
+
 template <int CG, int BN, bool A_MN, bool B_MN, bool SWAP>
 __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmParams p) {
   using C = Cfg<CG, BN, SWAP>;
@@ -218,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       mbar_init(smem_u32(&ctrl.acc_empty[i]), kEpiWarps * CG);
     }
     mbar_init(smem_u32(&ctrl.final_bar), 1);
+    for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(smem_u32(&ctrl.res_full[0][0] + i), 1);
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
     fence_mbar_init();
   }
@@ -239,64 +309,54 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (warp == 0) {
-    if (lane == 0) {
+    // The whole warp runs the loop and one lane acts, so that the copies' addresses and
+    // coordinates stay in uniform registers, and the coordinates advance by additions: a
+    // step's copies were issued in 360 ns by a single lane that divided for them, while
+    // the products of a step take 225.
+    const uint32_t elect = elect_lane();
+    if (elect) {
       tma_prefetch_desc(&p.ta);
       tma_prefetch_desc(&p.tb);
-      int64_t issued = 0;                                 // steps
-      int st = 0;
-      uint32_t parity = 1u;                               // of the wait for an empty stage
-      bool ok = true;
-      for (int64_t u = first; ok && u < units; u += stride) {
-        const Unit w = unit_of(p, u);
-        // the token axis: rows of A (SWAP: rows of B), tiles of each batch by themselves
-        const int32_t tok_tile = SWAP ? w.col_tile : w.row_tile;
-        const int32_t tb = A_MN && !SWAP ? 0 : tok_tile / p.tiles_per_batch;
-        const int32_t tn = (tok_tile - tb * p.tiles_per_batch) * (SWAP ? BN : C::TM);
-        const int32_t row0 = (A_MN && !SWAP ? w.row_tile * C::TM : SWAP ? w.row_tile * 128 : tn) + rank * 128;
-        const int32_t col0 = (SWAP ? tn : w.col_tile * BN) + rank * C::B_ROWS;
-        for (int32_t s = w.k0; s < w.k1; ++s) {
-          if (!mbar_wait(smem_u32(&ctrl.empty[st]), parity, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
-          const uint32_t a = base + st * C::STAGE, b = a + C::A_BYTES;
-          uint32_t bar = smem_u32(&ctrl.full[st]);
-          if (rank == 0) mbar_arrive_expect_tx(bar, CG * C::STAGE);
-          if constexpr (CG == 2) bar = cluster_addr(bar, 0);
-          auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t f, int32_t dim, int32_t n, int32_t bt) {
-            const int32_t h = f / dim;
-            if constexpr (CG == 2) tma_load_4d_pair(dst, m, bar, f - h * dim, n, h, bt);
-            else tma_load_4d(dst, m, bar, f - h * dim, n, h, bt);
-          };
-          // k of this step as channels (K-major operands) or as tokens / weight rows
-          const int32_t kc = s * BK;
-          const int32_t kb = A_MN && !SWAP ? s / p.k_steps_per_batch : 0;
-          const int32_t kn = A_MN && !SWAP ? (s - kb * p.k_steps_per_batch) * BK : kc;
-          if constexpr (A_MN) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) load(a + g * 64 * 128, &p.ta, row0 + g * 64, p.a_dim, kn, kb);
-          } else {
-            load(a, &p.ta, kc, p.a_dim, row0, SWAP ? 0 : tb);
-          }
-          if constexpr (B_MN) {
-#pragma unroll
-            for (int g = 0; g < C::B_ROWS / 64; ++g) load(b + g * 64 * 128, &p.tb, col0 + g * 64, p.b_dim, kn, kb);
-          } else {
-            load(b, &p.tb, kc, p.b_dim, col0, SWAP ? tb : 0);
-          }
-          ++issued;
-          if (++st == C::STAGES) {
-            st = 0;
-            parity ^= 1u;
-          }
+    }
+    constexpr bool TOK_K = A_MN && !SWAP;                 // k runs over tokens of the batches
+    int64_t issued = 0;                                   // steps
+    int st = 0;
+    uint32_t parity = 1u;                                 // of the wait for an empty stage
+    bool ok = true;
+    for (int64_t u = first; ok && u < units; u += stride) {
+      const Unit w = unit_of(p, u);
+      // the token axis: rows of A (SWAP: rows of B), tiles of each batch by themselves
+      const int32_t tok_tile = SWAP ? w.col_tile : w.row_tile;
+      const int32_t tb = TOK_K ? 0 : tok_tile / p.tiles_per_batch;
+      const int32_t tn = (tok_tile - tb * p.tiles_per_batch) * (SWAP ? BN : C::TM);
+      const int32_t row0 = (TOK_K ? w.row_tile * C::TM : SWAP ? w.row_tile * 128 : tn) + rank * 128;
+      const int32_t col0 = (SWAP ? tn : w.col_tile * BN) + rank * C::B_ROWS;
+      Walk<A_MN, 2> ca(p.a_dim, row0, w.k0, TOK_K ? p.k_steps_per_batch : 0, SWAP ? 0 : tb);
+      Walk<B_MN, (C::B_ROWS + 63) / 64> cb(p.b_dim, col0, w.k0, TOK_K ? p.k_steps_per_batch : 0, SWAP ? tb : 0);
+      for (int32_t s = w.k0; s < w.k1; ++s) {
+        if (!mbar_wait_warp(smem_u32(&ctrl.empty[st]), parity, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
+        const uint32_t a = base + st * C::STAGE, b = a + C::A_BYTES;
+        uint32_t bar = smem_u32(&ctrl.full[st]);
+        if (rank == 0) mbar_arrive_expect_tx(elect, bar, CG * C::STAGE);
+        if constexpr (CG == 2) bar = cluster_addr(bar, 0);
+        ca.template load<CG>(elect, a, &p.ta, bar);
+        cb.template load<CG>(elect, b, &p.tb, bar);
+        ca.advance();
+        cb.advance();
+        ++issued;
+        if (++st == C::STAGES) {
+          st = 0;
+          parity ^= 1u;
         }
       }
-      if (rank == 0) {
-        // every copy has landed before the CTA ends; normally they all have been waited for
-        volatile int32_t no = 0;
-        for (int64_t k = issued > C::STAGES ? issued - C::STAGES : 0; k < issued; ++k)
-          mbar_wait(smem_u32(&ctrl.full[k % C::STAGES]), static_cast<uint32_t>(k / C::STAGES) & 1u, &no, &g_err,
-                    p.timeout_ns);
-      }
     }
-    __syncwarp();
+    if (rank == 0) {
+      // every copy has landed before the CTA ends; normally they all have been waited for
+      volatile int32_t no = 0;
+      for (int64_t k = issued > C::STAGES ? issued - C::STAGES : 0; k < issued; ++k)
+        mbar_wait_warp(smem_u32(&ctrl.full[k % C::STAGES]), static_cast<uint32_t>(k / C::STAGES) & 1u, &no, &g_err,
+                       p.timeout_ns);
+    }
   } else if (warp == 1) {
     if (rank == 0) {
       const uint32_t elect = elect_lane();
@@ -344,17 +404,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   } else {
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;   // TMEM lanes 32 * quarter of this warp
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t elect = elect_lane();
+    uint32_t res_phase = 0u, res_issued = 0u;              // of the residual's two pieces
+    uint32_t turn = 0u;                                    // pieces take turns, from tile to tile
     int32_t tile = 0;
     for (int64_t u = first; u < units; u += stride, ++tile) {
       const Unit w = unit_of(p, u);
       const int buf = tile & 1;
-      if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
-      tc_fence_after();
       const uint32_t acc = tmem + lanes + buf * BN;
-      const int32_t r = quarter * 32 + lane + rank * 128;          // row in the tile
+      if (SWAP || p.part) {
+        if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
+        tc_fence_after();
+      }
       if constexpr (SWAP) {
         // rows are features, columns tokens: the warp stores 32 neighbouring features of a token
-        const int32_t f = w.row_tile * 128 + r;
+        const int32_t f = w.row_tile * 128 + quarter * 32 + lane;
         const int32_t b = w.col_tile / p.tiles_per_batch, n0 = (w.col_tile - b * p.tiles_per_batch) * BN;
         float* dst = p.part + (static_cast<int64_t>(w.split) * p.batches + b) * p.n_rows * p.cols + f;
 #pragma unroll 1
@@ -371,34 +435,121 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         }
       } else {
         const int32_t b = A_MN ? 0 : w.row_tile / p.tiles_per_batch;
-        const int64_t n = static_cast<int64_t>(w.row_tile - b * p.tiles_per_batch) * C::TM + r;
-        const bool valid = n < p.n_rows;
+        const int32_t n0 = (w.row_tile - b * p.tiles_per_batch) * C::TM + rank * 128 + quarter * 32;
         constexpr int W = BN / 2;                                   // columns of this warp
+        const int32_t f0 = w.col_tile * BN + half * W;
+        const bool inside = n0 < p.n_rows;
+        const uint32_t piece[2] = {base + C::OUT + ew * 2 * C::PIECE, base + C::OUT + (ew * 2 + 1) * C::PIECE};
+        // a lane's row of a piece, 16 bytes each, swizzled as TMA reads it
+        const uint32_t row = lane * 128;
+        auto unit_at = [&](uint32_t q, int i) { return q + row + ((i ^ (lane & 7)) << 4); };
+        if (p.part) {
 #pragma unroll 1
-        for (int c = 0; c < W; c += 32) {
-          const int32_t f0 = w.col_tile * BN + half * W + c;
-          if (f0 >= p.cols) break;
-          uint32_t v[32];
-          tmem_ld32(acc + half * W + c, v);
-          tc_wait_ld();
-          if (valid) {
+          for (int c = 0; c < W; c += 32) {
+            if (f0 + c >= p.cols || !inside) break;
+            uint32_t v[32];
+            tmem_ld32(acc + half * W + c, v);
+            const uint32_t q = piece[turn++ & 1u];
+            bulk_wait_read<1>();                                    // the piece before the last has left
+            __syncwarp();
+            tc_wait_ld();
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int32_t f = f0 + 8 * g;
-              if (f >= p.cols) break;
-              float x[8];
+            for (int i = 0; i < 8; ++i)
+              sts128(unit_at(q, i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            fence_proxy_async_smem();
+            __syncwarp();
+            tma_store_4d(elect, &p.tout, q, f0 + c, n0, b, w.split);
+            bulk_commit(elect);
+          }
+        } else {
+          const bool pre = p.epi.pre != nullptr, res = p.epi.res != nullptr, f16 = p.epi.f16 != 0;
+          const int act = p.epi.act, dim = p.epi.vout.dim;
+          // out leaves by both pieces in turn; with pre by the second, and pre by the first
+          auto load_res = [&](int c) {
+            const int k = pre ? 1 : (turn + c) & 1;
+            const int32_t f = f0 + c * 64, h = f / dim;
+            const uint32_t bar = smem_u32(&ctrl.res_full[ew][k]);
+            mbar_arrive_expect_tx(elect, bar, C::PIECE);
+            tma_load_4d(elect, piece[k], &p.tres, bar, f - h * dim, n0, h, b);
+            res_issued |= 1u << k;
+          };
+          constexpr int CHUNKS = W / 64;
+          const int chunks = !inside || f0 >= p.cols ? 0 : min(CHUNKS, (p.cols - f0 + 63) / 64);
+          if (res) {
+            bulk_wait_read<0>();
+            __syncwarp();
+            if (chunks > 0) load_res(0);
+            if (chunks > 1 && !pre) load_res(1);
+          }
+          if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
+          tc_fence_after();
+          bool ok = true;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            const int k = pre ? 1 : (turn + c) & 1;
+            if (res && pre && c > 0) {
+              bulk_wait_read<0>();
+              __syncwarp();
+              load_res(c);
+            }
+            const int32_t f = f0 + c * 64, h = f / dim;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
-              if (p.part) {
-                float4* dst = reinterpret_cast<float4*>(
-                    p.part + (static_cast<int64_t>(w.split) * p.total_rows + static_cast<int64_t>(b) * p.n_rows + n) * p.cols + f);
-                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-              } else {
-                finish8(p.epi, x, b, n, f);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t v[32];
+              tmem_ld32(acc + half * W + c * 64 + j * 32, v);
+              uint4 bias[4] = {};
+              if (p.epi.bias) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                  if (f + j * 32 + g * 8 < p.cols) bias[g] = __ldg(static_cast<const uint4*>(p.epi.bias) + (f + j * 32) / 8 + g);
+              }
+              if (j == 0) {
+                if (!res) {
+                  if (pre) bulk_wait_read<0>();
+                  else bulk_wait_read<1>();
+                  __syncwarp();
+                } else if (!mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, abort_flag, &g_err,
+                                           p.timeout_ns)) {
+                  ok = false;
+                } else {
+                  res_phase ^= 1u << k;
+                  res_issued &= ~(1u << k);
+                }
+              }
+              tc_wait_ld();
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                float x[8], t[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
+                if (p.epi.bias) {
+                  unpack8(bias[g], f16, t);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) x[i] += t[i];
+                }
+                if (pre) sts128(unit_at(piece[0], j * 4 + g), pack8(x, f16));
+                activate8(x, act);
+                const uint32_t at_out = unit_at(piece[k], j * 4 + g);
+                if (res) {
+                  unpack8(lds128(at_out), f16, t);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) x[i] += t[i];
+                }
+                sts128(at_out, pack8(x, f16));
               }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (!ok) break;
+            if (pre) {
+              tma_store_4d(elect, &p.tpre, piece[0], f - h * dim, n0, h, b);
+              bulk_commit(elect);
+            }
+            tma_store_4d(elect, &p.tout, piece[k], f - h * dim, n0, h, b);
+            bulk_commit(elect);
           }
+          if (!ok) break;
+          turn += chunks;
         }
       }
       tc_fence_before();
@@ -408,6 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(bar, 0));
         else mbar_arrive(bar);
       }
+    }
+    bulk_wait_all();                       // what was stored is written before the CTA ends
+    if (*abort_flag) {
+      // a residual's piece in flight lands before the CTA ends
+      volatile int32_t no = 0;
+      for (int k = 0; k < 2; ++k)
+        if ((res_issued >> k) & 1) mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, &no, &g_err, p.timeout_ns);
     }
   }
   tc_fence_before();
