@@ -247,17 +247,21 @@ tsr_status launch_variant(const GemmParams& p, cudaStream_t st) {
     if (dev < 64) set[dev] = true;
   }
   const int64_t units = static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CG;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  // The kernel's set-up may overlap the end of what is before it on the stream (it waits
+  // for that before it touches memory).
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, num_sms(dev) / CG) * CG));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG > 1 ? 2 : 1;
   TSR_CUDA(cudaLaunchKernelEx(&cfg, kern, p));
   return TSR_OK;
 }

@@ -145,7 +145,7 @@ __device__ __forceinline__ int64_t at(const View& v, int64_t b, int64_t n, int32
 __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_t b, int64_t n, int32_t f) {
   if (e.bias) {
     float t[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(e.bias) + f / 8), e.f16, t);
+    unpack8(reinterpret_cast<const uint4*>(e.bias)[f / 8], e.f16, t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += t[i];
   }
@@ -305,6 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
+  // what comes before may still run while this CTA sets itself up
+  grid_wait();
+  grid_launch_dependents();
   const int64_t units = static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits;
   const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
               if (p.epi.bias) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                  if (f + j * 32 + g * 8 < p.cols) bias[g] = __ldg(static_cast<const uint4*>(p.epi.bias) + (f + j * 32) / 8 + g);
+                  if (f + j * 32 + g * 8 < p.cols) bias[g] = static_cast<const uint4*>(p.epi.bias)[(f + j * 32) / 8 + g];
               }
               if (j == 0) {
                 if (!res) {
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         else mbar_arrive(bar);
       }
     }
-    bulk_wait_all();                       // what was stored is written before the CTA ends
+    bulk_wait_read<0>();                   // shared memory has been read before the CTA ends
     if (*abort_flag) {
       // a residual's piece in flight lands before the CTA ends
       volatile int32_t no = 0;

@@ -162,13 +162,11 @@ __device__ __forceinline__ void bulk_commit(uint32_t elect) {
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t@q cp.async.bulk.commit_group;\n\t}" ::"r"(elect)
                : "memory");
 }
-// Until at most N of this lane's groups have yet to read their shared memory; until all
-// have written.
+// Until at most N of this lane's groups have yet to read their shared memory.
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ----------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
