@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const float* part, i
     v[6] += y.z;
     v[7] += y.w;
   }
-  finish8(e, v, b, row - b * n_rows, f);
+  by_kind(e.f16, e.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(e, v, b, row - b * n_rows, f); });
 }
 
 struct DzParams {
@@ -66,23 +66,28 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
   const int64_t r1 = min(r0 + p.rows_per_block, p.rows);
   grid_launch_dependents();
   float sum[8] = {};
-  if (f < p.cols) {
+  if (f < p.cols)
+    by_kind(p.f16, p.act, [&](auto f16, auto act) {
 #pragma unroll 4
-    for (int64_t r = r0 + ty; r < r1; r += 8) {
-      const int64_t b = r / p.n_rows, n = r - b * p.n_rows;
-      float g[8];
-      unpack8(*reinterpret_cast<const uint4*>(p.dout + at(p.vdout, b, n, f)), p.f16, g);
-      if (p.pre) {
-        float z[8];
-        unpack8(*reinterpret_cast<const uint4*>(p.pre + at(p.vpre, b, n, f)), p.f16, z);
+      for (int64_t r = r0 + ty; r < r1; r += 8) {
+        int64_t b = 0, n = r;
+        if (p.n_rows < p.rows) {
+          b = r / p.n_rows;
+          n = r - b * p.n_rows;
+        }
+        float g[8];
+        unpack8<f16.value>(*reinterpret_cast<const uint4*>(p.dout + at(p.vdout, b, n, f)), g);
+        if constexpr (act.value != TSR_ACT_NONE) {
+          float z[8];
+          unpack8<f16.value>(*reinterpret_cast<const uint4*>(p.pre + at(p.vpre, b, n, f)), z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= slope(z[i], p.act);
+          for (int i = 0; i < 8; ++i) g[i] *= slope<act.value>(z[i]);
+        }
+        if (p.dz) *reinterpret_cast<uint4*>(p.dz + r * p.cols + f) = pack8<f16.value>(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += g[i];
       }
-      if (p.dz) *reinterpret_cast<uint4*>(p.dz + r * p.cols + f) = pack8(g, p.f16);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += g[i];
-    }
-  }
+    });
   if (!p.part) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) red[ty][lane][i] = sum[i];
@@ -217,21 +222,24 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // A 4-D tensor map, 128-byte swizzle; strides in elements, of dimensions 1 to 3.
 tsr_status encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int size, const int64_t (&dims)[4],
                   const int64_t (&strides)[3], int box0, int box1) {
+  // the box's row of 128 or 64 bytes is the swizzle's
   if (!encoder()) return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled is missing");
   cuuint64_t d[4], s[3];
   for (int i = 0; i < 4; ++i) d[i] = static_cast<cuuint64_t>(dims[i]);
   for (int i = 0; i < 3; ++i) s[i] = static_cast<cuuint64_t>(dims[i + 1] > 1 ? size * strides[i] : 16);
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1, 1}, es[4] = {1, 1, 1, 1};
   if (encoder()(m, type, 4, const_cast<void*>(p), d, s, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                box0 * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   return TSR_OK;
 }
-// {channel, token, head, batch} boxes of 64 channels x `rows` tokens.
-tsr_status encode(CUtensorMap* m, const void* p, const View& v, int64_t heads, int64_t n, int64_t b, int rows, bool f16) {
+// {channel, token, head, batch} boxes of `channels` x `rows` tokens.
+tsr_status encode(CUtensorMap* m, const void* p, const View& v, int64_t heads, int64_t n, int64_t b, int channels,
+                  int rows, bool f16) {
   return encode(m, p, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                {v.dim, n, heads, b}, {v.sn, v.sh, v.sb}, BK, rows);
+                {v.dim, n, heads, b}, {v.sn, v.sh, v.sb}, channels, rows);
 }
 
 template <int CG, int BN, bool A_MN, bool B_MN, bool SWAP>
@@ -314,9 +322,9 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   *dother = vother.dim;
   const bool tok_mn = kind == DWEIGHT, other_mn = kind != FORWARD;
   const int tok_rows = tok_mn ? BK : swap ? bn : 128, other_rows = other_mn ? BK : swap ? 128 : bn / 2;
-  if (tsr_status s = encode(mt, tok, vtok, tok_heads, y.N, y.B, tok_rows, y.f16)) return s;
+  if (tsr_status s = encode(mt, tok, vtok, tok_heads, y.N, y.B, BK, tok_rows, y.f16)) return s;
   const int64_t on = kind == DWEIGHT ? y.N : y.M, ob = kind == DWEIGHT ? y.B : 1;
-  if (tsr_status s = encode(mo, other, vother, other_heads, on, ob, other_rows, y.f16)) return s;
+  if (tsr_status s = encode(mo, other, vother, other_heads, on, ob, BK, other_rows, y.f16)) return s;
   p.idesc = idesc_16bit(y.f16, swap ? 128 : 256, bn, swap ? other_mn : tok_mn, swap ? tok_mn : other_mn);
   if (!swap) {
     // out's rows: tokens, or the weight's for its gradient
@@ -326,11 +334,11 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
                                 {q.cols, rows * q.cols, p.total_rows * q.cols}, 32, 32))
         return s;
     } else {
-      if (tsr_status s = encode(&p.tout, e.out, e.vout, heads, rows, q.batches, 32, y.f16)) return s;
+      if (tsr_status s = encode(&p.tout, e.out, e.vout, heads, rows, q.batches, 32, 32, y.f16)) return s;
       if (e.pre)
-        if (tsr_status s = encode(&p.tpre, e.pre, e.vpre, heads, rows, q.batches, 32, y.f16)) return s;
+        if (tsr_status s = encode(&p.tpre, e.pre, e.vpre, heads, rows, q.batches, 32, 32, y.f16)) return s;
       if (e.res)
-        if (tsr_status s = encode(&p.tres, e.res, e.vres, heads, rows, q.batches, 32, y.f16)) return s;
+        if (tsr_status s = encode(&p.tres, e.res, e.vres, heads, rows, q.batches, 32, 32, y.f16)) return s;
     }
   }
   tsr_status s;

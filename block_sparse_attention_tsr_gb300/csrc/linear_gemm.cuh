@@ -28,6 +28,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -56,7 +57,7 @@ struct Epilogue {
 struct GemmParams {
   CUtensorMap ta, tb;
   // out (or the parts, fp32), pre and residual as {channel, token, head, batch} (parts:
-  // {channel, token, batch, split}) in boxes of 32 tokens x 128 bytes
+  // {channel, token, batch, split}) in boxes of 32 tokens x 32 channels
   CUtensorMap tout, tpre, tres;
   Epilogue epi;                        // bias, activation and what is there; SWAP and parts: views
   float* part;                         // [split][rows][cols] of D (SWAP: of D^T), null: epilogue here
@@ -77,63 +78,87 @@ struct GemmParams {
 static __device__ uint32_t g_err;
 
 // ------------------------------------------------------------- the epilogue
-__device__ __forceinline__ float2 unpack16(uint32_t w, bool f16) {
-  if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
-  if (f16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return pack_bf16x2(lo, hi);
-}
-__device__ __forceinline__ void unpack8(uint4 w, bool f16, float (&v)[8]) {
+template <bool F16>
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack16(x[i], f16);
-    v[2 * i] = p.x;
-    v[2 * i + 1] = p.y;
+    if constexpr (F16) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+      v[2 * i] = p.x;
+      v[2 * i + 1] = p.y;
+    } else {
+      v[2 * i] = __uint_as_float(x[i] << 16);
+      v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+    }
   }
 }
-__device__ __forceinline__ uint4 pack8(const float (&v)[8], bool f16) {
-  return make_uint4(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16), pack16(v[4], v[5], f16),
-                    pack16(v[6], v[7], f16));
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F16) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      x[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 constexpr float kGelu0 = 0.7978845608028654f, kGelu1 = 0.044715f;   // sqrt(2 / pi)
 
+// 1 / (1 + e^-x).  The exponential is within about |x| 2^-23 of its value, the reciprocal
+// within 2^-23: far inside a 16-bit rounding.
+__device__ __forceinline__ float logistic(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ex2_approx(-1.4426950408889634f * x)));
+  return y;
+}
 // The tanh form is z times the logistic function of 2u, u = kGelu0 (z + kGelu1 z^3): no
-// cancellation for negative z.  The exponential is within about |2u| 2^-23 of its value,
-// far inside a 16-bit rounding.
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == TSR_ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * kGelu0 * fmaf(kGelu1 * z * z, z, z)));
-  if (act == TSR_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-  if (act == TSR_ACT_GELU) return z * normcdff(z);
+// cancellation for negative z.
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == TSR_ACT_GELU_TANH) return z * logistic(z * fmaf(2.f * kGelu0 * kGelu1, z * z, 2.f * kGelu0));
+  if constexpr (ACT == TSR_ACT_SILU) return z * logistic(z);
+  if constexpr (ACT == TSR_ACT_GELU) return z * normcdff(z);
   return z;
 }
-__device__ __forceinline__ void activate8(float (&v)[8], int act) {
-  if (act == TSR_ACT_NONE) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = activate(v[i], act);
-}
-// The activation's derivative.  It is 0 or 1 in fp32 past |z| = 30 (SiLU: 90); z is taken
+// The activation's derivative.  It is 0 or 1 in fp32 past |z| = 30 (SiLU: 80); z is taken
 // there so that no 0 * inf arises.
-__device__ __forceinline__ float slope(float z, int act) {
-  if (z != z) return z;
-  if (act == TSR_ACT_SILU) {
-    const float x = fminf(fmaxf(z, -80.f), 80.f);
-    const float s = __fdividef(1.f, 1.f + __expf(-x));
-    return s * fmaf(x, 1.f - s, 1.f);
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+  if constexpr (ACT == TSR_ACT_NONE) return 1.f;
+  const float most = ACT == TSR_ACT_SILU ? 80.f : 30.f;
+  const float x = fminf(fmaxf(z, -most), most);
+  float y;
+  if constexpr (ACT == TSR_ACT_SILU) {
+    const float s = logistic(x);
+    y = s * fmaf(x, 1.f - s, 1.f);
+  } else if constexpr (ACT == TSR_ACT_GELU_TANH) {
+    const float s = logistic(x * fmaf(2.f * kGelu0 * kGelu1, x * x, 2.f * kGelu0));
+    y = fmaf(x * s * (1.f - s), fmaf(6.f * kGelu0 * kGelu1, x * x, 2.f * kGelu0), s);
+  } else {
+    y = fmaf(x * 0.3989422804014327f, ex2_approx(-0.5f * 1.4426950408889634f * x * x), normcdff(x));
   }
-  const float x = fminf(fmaxf(z, -30.f), 30.f);
-  if (act == TSR_ACT_GELU_TANH) {
-    const float s = __fdividef(1.f, 1.f + __expf(-2.f * kGelu0 * fmaf(kGelu1 * x * x, x, x)));
-    return fmaf(x * s * (1.f - s), 2.f * kGelu0 * fmaf(3.f * kGelu1, x * x, 1.f), s);
+  return z != z ? z : y;
+}
+// f<F16, ACT>() for the call's type and activation: the elements' code has no branches on them.
+template <typename F>
+__device__ __forceinline__ void by_kind(int f16, int act, F&& f) {
+  using std::integral_constant;
+  switch (act * 2 + f16) {
+    case 0: return f(integral_constant<bool, false>(), integral_constant<int, 0>());
+    case 1: return f(integral_constant<bool, true>(), integral_constant<int, 0>());
+    case 2: return f(integral_constant<bool, false>(), integral_constant<int, 1>());
+    case 3: return f(integral_constant<bool, true>(), integral_constant<int, 1>());
+    case 4: return f(integral_constant<bool, false>(), integral_constant<int, 2>());
+    case 5: return f(integral_constant<bool, true>(), integral_constant<int, 2>());
+    case 6: return f(integral_constant<bool, false>(), integral_constant<int, 3>());
+    default: return f(integral_constant<bool, true>(), integral_constant<int, 3>());
   }
-  if (act == TSR_ACT_GELU) return fmaf(x * 0.3989422804014327f, __expf(-0.5f * x * x), normcdff(x));
-  return 1.f;
 }
 
 __device__ __forceinline__ int64_t at(const View& v, int64_t b, int64_t n, int32_t f) {
@@ -142,22 +167,23 @@ __device__ __forceinline__ int64_t at(const View& v, int64_t b, int64_t n, int32
 }
 
 // Eight neighbouring features [f, f + 8) of token (b, n), from D's values to the output.
+template <bool F16, int ACT>
 __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_t b, int64_t n, int32_t f) {
+  float t[8];
   if (e.bias) {
-    float t[8];
-    unpack8(reinterpret_cast<const uint4*>(e.bias)[f / 8], e.f16, t);
+    unpack8<F16>(static_cast<const uint4*>(e.bias)[f / 8], t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += t[i];
   }
-  if (e.pre) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.pre) + at(e.vpre, b, n, f)) = pack8(v, e.f16);
-  activate8(v, e.act);
+  if (e.pre) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.pre) + at(e.vpre, b, n, f)) = pack8<F16>(v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
   if (e.res) {
-    float t[8];
-    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + at(e.vres, b, n, f)), e.f16, t);
+    unpack8<F16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + at(e.vres, b, n, f)), t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += t[i];
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at(e.vout, b, n, f)) = pack8(v, e.f16);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at(e.vout, b, n, f)) = pack8<F16>(v);
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
@@ -175,8 +201,9 @@ struct Cfg {
   static constexpr int TM = 128 * CG;                     // rows of a tile
   static constexpr int A_BYTES = 128 * BK * 2, B_ROWS = BN / CG, B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  // what leaves through shared memory: two pieces of 32 rows x 128 bytes for each epilogue warp
-  static constexpr int PIECE = 32 * 128, OUT_BYTES = SWAP ? 0 : kEpiWarps * 2 * PIECE;
+  // what leaves through shared memory: for each epilogue warp four pieces of 32 rows x 32
+  // columns (parts, fp32: two)
+  static constexpr int PIECE = 32 * 64, OUT_BYTES = SWAP ? 0 : kEpiWarps * 4 * PIECE;
   static constexpr int FIT = (226 * 1024 - OUT_BYTES) / STAGE, STAGES = FIT < 8 ? FIT : 8;
   static constexpr int OUT = STAGES * STAGE, CTRL = OUT + OUT_BYTES, SMEM = CTRL + 512;
   static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;  // two accumulators
@@ -187,7 +214,7 @@ struct Cfg {
 
 struct alignas(8) Ctrl {
   uint64_t full[8], empty[8], acc_full[2], acc_empty[2], final_bar;
-  uint64_t res_full[kEpiWarps][2];     // the residual's piece has landed
+  uint64_t res_full[kEpiWarps][4];     // the residual's piece has landed
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -287,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       mbar_init(smem_u32(&ctrl.acc_empty[i]), kEpiWarps * CG);
     }
     mbar_init(smem_u32(&ctrl.final_bar), 1);
-    for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(smem_u32(&ctrl.res_full[0][0] + i), 1);
+    for (int i = 0; i < 4 * kEpiWarps; ++i) mbar_init(smem_u32(&ctrl.res_full[0][0] + i), 1);
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
     fence_mbar_init();
   }
@@ -408,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;   // TMEM lanes 32 * quarter of this warp
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t elect = elect_lane();
-    uint32_t res_phase = 0u, res_issued = 0u;              // of the residual's two pieces
+    uint32_t res_phase = 0u, res_issued = 0u;              // of the residual's pieces
     uint32_t turn = 0u;                                    // pieces take turns, from tile to tile
     int32_t tile = 0;
     for (int64_t u = first; u < units; u += stride, ++tile) {
@@ -442,117 +469,121 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         constexpr int W = BN / 2;                                   // columns of this warp
         const int32_t f0 = w.col_tile * BN + half * W;
         const bool inside = n0 < p.n_rows;
-        const uint32_t piece[2] = {base + C::OUT + ew * 2 * C::PIECE, base + C::OUT + (ew * 2 + 1) * C::PIECE};
-        // a lane's row of a piece, 16 bytes each, swizzled as TMA reads it
-        const uint32_t row = lane * 128;
-        auto unit_at = [&](uint32_t q, int i) { return q + row + ((i ^ (lane & 7)) << 4); };
+        const uint32_t pieces = base + C::OUT + ew * 4 * C::PIECE;
         if (p.part) {
 #pragma unroll 1
           for (int c = 0; c < W; c += 32) {
             if (f0 + c >= p.cols || !inside) break;
             uint32_t v[32];
             tmem_ld32(acc + half * W + c, v);
-            const uint32_t q = piece[turn++ & 1u];
+            const uint32_t q = pieces + (turn++ & 1u) * 2 * C::PIECE;
             bulk_wait_read<1>();                                    // the piece before the last has left
             __syncwarp();
             tc_wait_ld();
+            // a lane's row of 128 bytes, 16 each, swizzled as TMA reads it
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              sts128(unit_at(q, i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+              sts128(q + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
             fence_proxy_async_smem();
             __syncwarp();
             tma_store_4d(elect, &p.tout, q, f0 + c, n0, b, w.split);
             bulk_commit(elect);
           }
         } else {
-          const bool pre = p.epi.pre != nullptr, res = p.epi.res != nullptr, f16 = p.epi.f16 != 0;
-          const int act = p.epi.act, dim = p.epi.vout.dim;
-          // out leaves by both pieces in turn; with pre by the second, and pre by the first
-          auto load_res = [&](int c) {
-            const int k = pre ? 1 : (turn + c) & 1;
-            const int32_t f = f0 + c * 64, h = f / dim;
-            const uint32_t bar = smem_u32(&ctrl.res_full[ew][k]);
+          const bool pre = p.epi.pre != nullptr, res = p.epi.res != nullptr;
+          const int dim = p.epi.vout.dim, per = pre ? 2 : 1;
+          constexpr int STEPS = W / 32;                             // 32 columns each
+          const int steps = !inside || f0 >= p.cols ? 0 : min(STEPS, (p.cols - f0 + 31) / 32);
+          // step s takes the ring's next pieces: pre's, then out's, where the residual lands first
+          auto piece = [&](int s, int which) { return (turn + s * per + which) & 3u; };
+          auto load_res = [&](int s) {
+            const uint32_t k = piece(s, per - 1), bar = smem_u32(&ctrl.res_full[ew][k]);
+            const int32_t f = f0 + s * 32, h = f / dim;
             mbar_arrive_expect_tx(elect, bar, C::PIECE);
-            tma_load_4d(elect, piece[k], &p.tres, bar, f - h * dim, n0, h, b);
+            tma_load_4d(elect, pieces + k * C::PIECE, &p.tres, bar, f - h * dim, n0, h, b);
             res_issued |= 1u << k;
           };
-          constexpr int CHUNKS = W / 64;
-          const int chunks = !inside || f0 >= p.cols ? 0 : min(CHUNKS, (p.cols - f0 + 63) / 64);
           if (res) {
             bulk_wait_read<0>();
             __syncwarp();
-            if (chunks > 0) load_res(0);
-            if (chunks > 1 && !pre) load_res(1);
+            for (int s = 0; s < (pre ? min(steps, 2) : steps); ++s) load_res(s);
           }
           if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
           tc_fence_after();
           bool ok = true;
+          uint32_t v[32];
+          if (steps > 0) tmem_ld32(acc + half * W, v);
+          int32_t h = f0 / dim, ch = f0 - h * dim;
 #pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            const int k = pre ? 1 : (turn + c) & 1;
-            if (res && pre && c > 0) {
-              bulk_wait_read<0>();
-              __syncwarp();
-              load_res(c);
+          for (int s = 0; s < steps; ++s) {
+            const int32_t f = f0 + s * 32;
+            uint4 bias[4] = {};
+            if (p.epi.bias) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                if (f + g * 8 < p.cols) bias[g] = static_cast<const uint4*>(p.epi.bias)[f / 8 + g];
             }
-            const int32_t f = f0 + c * 64, h = f / dim;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t v[32];
-              tmem_ld32(acc + half * W + c * 64 + j * 32, v);
-              uint4 bias[4] = {};
-              if (p.epi.bias) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                  if (f + j * 32 + g * 8 < p.cols) bias[g] = static_cast<const uint4*>(p.epi.bias)[(f + j * 32) / 8 + g];
+            if (res) {
+              if (pre && s >= 2) {
+                bulk_wait_read<0>();
+                __syncwarp();
+                load_res(s);
               }
-              if (j == 0) {
-                if (!res) {
-                  if (pre) bulk_wait_read<0>();
-                  else bulk_wait_read<1>();
-                  __syncwarp();
-                } else if (!mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, abort_flag, &g_err,
-                                           p.timeout_ns)) {
-                  ok = false;
-                } else {
-                  res_phase ^= 1u << k;
-                  res_issued &= ~(1u << k);
-                }
-              }
-              tc_wait_ld();
+              const uint32_t k = piece(s, per - 1);
+              ok = mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, abort_flag, &g_err, p.timeout_ns);
+              if (!ok) break;
+              res_phase ^= 1u << k;
+              res_issued &= ~(1u << k);
+            } else {
+              // the ring's pieces of four stores (with pre two steps) ago have left
+              if (pre) bulk_wait_read<2>();
+              else bulk_wait_read<3>();
+              __syncwarp();
+            }
+            tc_wait_ld();
+            // a lane's row of 64 bytes, 16 each, swizzled as TMA reads it
+            const uint32_t row = lane * 64, turned = (lane >> 1) & 3;
+            const uint32_t q_pre = pieces + piece(s, 0) * C::PIECE, q = pieces + piece(s, per - 1) * C::PIECE;
+            by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) {
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
                 float x[8], t[8];
+                const uint32_t o = row + ((g ^ turned) << 4);
+                unpack8<f16.value>(bias[g], t);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]);
-                if (p.epi.bias) {
-                  unpack8(bias[g], f16, t);
+                for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]) + t[i];
+                if (pre) sts128(q_pre + o, pack8<f16.value>(x));
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) x[i] += t[i];
-                }
-                if (pre) sts128(unit_at(piece[0], j * 4 + g), pack8(x, f16));
-                activate8(x, act);
-                const uint32_t at_out = unit_at(piece[k], j * 4 + g);
+                for (int i = 0; i < 8; ++i) x[i] = activate<act.value>(x[i]);
                 if (res) {
-                  unpack8(lds128(at_out), f16, t);
+                  unpack8<f16.value>(lds128(q + o), t);
 #pragma unroll
                   for (int i = 0; i < 8; ++i) x[i] += t[i];
                 }
-                sts128(at_out, pack8(x, f16));
+                sts128(q + o, pack8<f16.value>(x));
               }
-            }
+            });
+            // the next step's columns are on their way while this one's leave
+            if (s + 1 < steps) tmem_ld32(acc + half * W + (s + 1) * 32, v);
             fence_proxy_async_smem();
             __syncwarp();
-            if (!ok) break;
             if (pre) {
-              tma_store_4d(elect, &p.tpre, piece[0], f - h * dim, n0, h, b);
+              tma_store_4d(elect, &p.tpre, q_pre, ch, n0, h, b);
               bulk_commit(elect);
             }
-            tma_store_4d(elect, &p.tout, piece[k], f - h * dim, n0, h, b);
+            tma_store_4d(elect, &p.tout, q, ch, n0, h, b);
             bulk_commit(elect);
+            ch += 32;
+            if (ch >= dim) {
+              ch = 0;
+              ++h;
+            }
           }
-          if (!ok) break;
-          turn += chunks;
+          if (!ok) {
+            tc_wait_ld();
+            break;
+          }
+          turn += steps * per;
         }
       }
       tc_fence_before();
@@ -567,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     if (*abort_flag) {
       // a residual's piece in flight lands before the CTA ends
       volatile int32_t no = 0;
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 4; ++k)
         if ((res_issued >> k) & 1) mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, &no, &g_err, p.timeout_ns);
     }
   }
