@@ -141,24 +141,25 @@ struct Product {
 
 bool parts(const Choice& c) { return c.splits > 1 || c.variant >= SWAP_32; }
 
-// The fastest by a model in clocks: waves of units, each its k steps, a fill and an
-// epilogue; parts cost a write, a read and a launch.  A step is bound by the MMAs or by what
-// an SM takes from L2 (59 bytes a clock).
+// The fastest by a model in microseconds, fitted to 580 timed products (forward, dx and
+// dweight, 1 to 8,000 tokens, 256 to 8,192 features; within 12% in the root mean square,
+// and its choice on average within 3% of the fastest): waves of units, each its k steps and
+// a fill and an epilogue, and for parts a launch and their traffic.  Each part has four
+// steps at least.  For example 666 x 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on 256 x
+// 256, 17 with k in three parts; 100 x 4096 -> 4096: 9.2 us with the tokens on the columns
+// and k in four parts, 13 on 256 x 128 tiles.
 Choice choose(const Product& q) {
+  constexpr double kStep[4] = {0.276, 0.169, 0.108, 0.151}, kUnit[4] = {3.1, 2.05, 0.8, 1.3};
+  constexpr int kTok[4] = {256, 256, 32, 128}, kFeat[4] = {256, 128, 128, 128};
   Choice best{PAIR_256, 1};
   double least = 1e30;
   for (int v = PAIR_256; v <= SWAP_128; ++v) {
-    if (v >= SWAP_32 && q.kind == DWEIGHT) continue;
     const bool swap = v >= SWAP_32;
-    const int64_t tok = v == PAIR_256 || v == PAIR_128 ? 256 : v == SWAP_32 ? 32 : 128;
-    const int64_t feat = v == PAIR_256 ? 256 : 128;
-    const int64_t tiles = q.batches * cdiv(q.n_rows, tok) * cdiv(q.cols, feat);
-    const int64_t slots = swap ? kSms : kSms / 2;
-    const double step = v == PAIR_256 ? 560 : v == PAIR_128 ? 420 : v == SWAP_32 ? 350 : 560;
-    for (int64_t s = 1; s <= 16 && s <= q.k_steps; ++s) {
-      const int64_t waves = cdiv(tiles * s, slots);
-      double t = waves * (cdiv(q.k_steps, s) * step + 600) + 3000;
-      if (s > 1 || swap) t += 4000 + 8.0 * s * q.batches * q.n_rows * q.cols / 3000;
+    if (swap && (q.kind == DWEIGHT || q.batches * q.n_rows > 512)) continue;   // fitted up to 300 tokens
+    const int64_t tiles = q.batches * cdiv(q.n_rows, kTok[v]) * cdiv(q.cols, kFeat[v]);
+    for (int64_t s = 1; s <= 16 && (s == 1 || q.k_steps >= 4 * s); ++s) {
+      double t = cdiv(tiles * s, swap ? kSms : kSms / 2) * (cdiv(q.k_steps, s) * kStep[v] + kUnit[v]);
+      if (s > 1 || swap) t += 2.5 + 0.6e-6 * s * q.batches * q.n_rows * q.cols;
       if (t < least) {
         least = t;
         best = {static_cast<Variant>(v), static_cast<int32_t>(s)};
