@@ -239,7 +239,7 @@ def _check(status: int) -> None:
 def _stream_ptr(stream) -> int:
     if stream is None:
         # the current stream's handle, without a Stream object for it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -255,7 +255,7 @@ def _dptr(t: Optional[torch.Tensor]) -> int:
 
 def _on_device(*tensors) -> None:
     """CUDA tensors of the current device: the library launches there."""
-    current = torch.cuda.current_device()
+    current = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != current:
             raise ValueError(f"tensor on {t.device}: arguments must be CUDA tensors of the current device, "
@@ -610,19 +610,56 @@ def _heads_list(x):
     return (x,) if isinstance(x, torch.Tensor) else tuple(x)
 
 
-def _weights(weight, xs):
+def _weights(weight, xs, dtype, d):
     """One weight (or None) per tensor, and their type's code."""
     ws = tuple(weight) if isinstance(weight, (list, tuple)) else (weight,) * len(xs)
     if len(ws) != len(xs):
         raise ValueError("one weight (or None) for each tensor")
-    dtype = None
+    kind = None
     for w in ws:
-        if w is None:
-            continue
-        if w.shape != xs[0].shape[3:] or w.dtype not in (xs[0].dtype, torch.float32) or w.dtype != (dtype or w.dtype):
-            raise ValueError("the weights are [d], all of the tensors' type or all fp32")
-        dtype = w.dtype
-    return ws, _ROPE_DTYPES[dtype or xs[0].dtype]
+        if w is not None:
+            if w.shape != (d,) or (w.dtype is not dtype and w.dtype is not torch.float32) or kind not in (None, w.dtype):
+                raise ValueError("the weights are [d], all of the tensors' type or all fp32")
+            kind = w.dtype
+    return ws, _ROPE_DTYPES[kind or dtype]
+
+
+def _heads_call(xs, axis_dims, grid, positions, theta, halves):
+    """What the calls that norm and rotate share: the tensors' type, channels, strides and
+    the packed tsr_rope_desc."""
+    if not 1 <= len(xs) <= 4:
+        raise ValueError("one to four tensors per call")
+    if (grid is None) == (positions is None):
+        raise ValueError("give grid or positions")
+    first = xs[0]
+    dtype = first.dtype
+    code = _ROPE_DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("the tensors are bf16, fp16 or fp32")
+    dims = [int(a) for a in axis_dims]
+    axes = len(dims)
+    if not 1 <= axes <= 4:
+        raise ValueError("one to four axes")
+    if first.dim() != 4:
+        raise ValueError("the tensors are [B, H, N, d]")
+    B, _, N, d = first.shape
+    rows = []
+    for t in xs:
+        shape = t.shape
+        if len(shape) != 4 or t.dtype is not dtype or shape[0] != B or shape[2] != N or shape[3] != d:
+            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
+        rows.append((t, shape, t.stride()))
+    pad = (0,) * (4 - axes)
+    if positions is not None:
+        if positions.dtype is not torch.int32 or positions.shape not in ((N, axes), (B, N, axes)):
+            raise ValueError("positions must be int32 [N, axes] or [B, N, axes]")
+        where = (_dptr(positions), positions.dim() == 3, 0, 0, 0, 0)
+    else:
+        cells = [int(g) for g in grid]
+        if len(cells) != axes:
+            raise ValueError("grid needs one size per axis")
+        where = (0, 0, *cells, *pad)
+    return dtype, d, rows, _ROPE_DESC.pack(B, N, d, code, axes, *dims, *pad, bool(halves), False, theta, *where)
 
 
 def tsr_norm_rope(x, weight, axis_dims, *, eps: float = 1e-6, grid=None,
@@ -633,29 +670,29 @@ def tsr_norm_rope(x, weight, axis_dims, *, eps: float = 1e-6, grid=None,
     ``weight``: [d] of x's type or fp32, or None (ones); for several tensors a sequence of
     as many (one tensor alone is shared by all).  Returns out."""
     xs = _heads_list(x)
-    dims = [int(a) for a in axis_dims]
-    dtype = _rope_heads(xs, dims, grid, positions)
-    ws, code = _weights(weight, xs)
+    dtype, d, rows, desc = _heads_call(xs, axis_dims, grid, positions, theta, halves)
+    ws, code = _weights(weight, xs, dtype, d)
     if out is None:
         _on_device(*xs, *ws, positions)
-        with _allocating_on(stream):
-            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
+        if stream is None:
+            outs = [t.new_empty(shape) for t, shape, _ in rows]
+        else:
+            with _allocating_on(stream):
+                outs = [t.new_empty(shape) for t, shape, _ in rows]
     else:
         outs = _heads_list(out)
         if len(outs) != len(xs):
             raise ValueError("as many outputs as tensors")
         _on_device(*xs, *ws, *outs, positions)
     tensors = b""
-    for t, w, o in zip(xs, ws, outs):
-        xb, xh, xn, x_last = t.stride()
-        ob, oh, on, o_last = o.stride()
-        if out is not None and (o.shape != t.shape or o.dtype != dtype):
+    for (t, shape, (xb, xh, xn, x_last)), w, o in zip(rows, ws, outs):
+        if out is not None and (o.shape != shape or o.dtype != dtype):
             raise ValueError("out must have x's shape and dtype")
+        ob, oh, on, o_last = o.stride()
         if x_last != 1 or o_last != 1:
             raise ValueError("the last dimension must be contiguous")
-        tensors += _NORM_ROPE_TENSOR.pack(t.data_ptr(), _dptr(w), 0, o.data_ptr(), 0, t.shape[1], code,
+        tensors += _NORM_ROPE_TENSOR.pack(t.data_ptr(), 0 if w is None else _dptr(w), 0, o.data_ptr(), 0, shape[1], code,
                                           xb, xh, xn, 0, 0, 0, ob, oh, on)
-    desc = _rope_desc(xs[0], dims, grid, positions, theta, halves, False)
     _check(lib().tsr_norm_rope(desc, eps, tensors, len(xs), _stream_ptr(stream)))
     return outs[0] if isinstance(x, torch.Tensor) else list(outs)
 
@@ -670,9 +707,8 @@ def tsr_norm_rope_backward(dout, x, weight, axis_dims, *, eps: float = 1e-6, gri
     allocated for the call."""
     xs, gs = _heads_list(x), _heads_list(dout)
     one = isinstance(x, torch.Tensor)
-    dims = [int(a) for a in axis_dims]
-    dtype = _rope_heads(xs, dims, grid, positions)
-    ws, code = _weights(weight, xs)
+    dtype, d, rows, desc = _heads_call(xs, axis_dims, grid, positions, theta, halves)
+    ws, code = _weights(weight, xs, dtype, d)
     if len(set(id(w) for w in ws if w is not None)) != sum(w is not None for w in ws):
         raise ValueError("a shared weight's gradient needs a call for each tensor")
     if len(gs) != len(xs) or any(g.shape != t.shape or g.dtype != dtype for g, t in zip(gs, xs)):
@@ -683,30 +719,28 @@ def tsr_norm_rope_backward(dout, x, weight, axis_dims, *, eps: float = 1e-6, gri
         if given is not None and len(given) != len(xs):
             raise ValueError("as many outputs as tensors")
     _on_device(*xs, *gs, *ws, positions, workspace, *(outs or ()), *(dws or ()))
-    desc = _rope_desc(xs[0], dims, grid, positions, theta, halves, False)
     L = lib()
-    need = ctypes.c_size_t(0)
-    _check(L.tsr_norm_rope_backward_workspace(desc, len(xs), ctypes.byref(need)))
     with _allocating_on(stream):
         if outs is None:
-            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
+            outs = [t.new_empty(shape) for t, shape, _ in rows]
         if dws is None:
             dws = [None if w is None else torch.empty_like(w) for w in ws]
         if workspace is None:
+            need = ctypes.c_size_t(0)
+            _check(L.tsr_norm_rope_backward_workspace(desc, len(xs), ctypes.byref(need)))
             workspace = torch.empty(need.value, dtype=torch.uint8, device=xs[0].device)
     tensors = b""
-    for t, g, w, o, dw in zip(xs, gs, ws, outs, dws):
-        xb, xh, xn, x_last = t.stride()
+    for (t, shape, (xb, xh, xn, x_last)), g, w, o, dw in zip(rows, gs, ws, outs, dws):
         gb, gh, gn, g_last = g.stride()
         ob, oh, on, o_last = o.stride()
-        if o.shape != t.shape or o.dtype != dtype:
+        if o.shape != shape or o.dtype != dtype:
             raise ValueError("out must have x's shape and dtype")
         if x_last != 1 or g_last != 1 or o_last != 1:
             raise ValueError("the last dimension must be contiguous")
         if (dw is None) != (w is None) or (dw is not None and (dw.shape != w.shape or dw.dtype != w.dtype)):
             raise ValueError("dweight must have the weight's shape and dtype")
-        tensors += _NORM_ROPE_TENSOR.pack(t.data_ptr(), _dptr(w), g.data_ptr(), o.data_ptr(), _dptr(dw), t.shape[1],
-                                          code, xb, xh, xn, gb, gh, gn, ob, oh, on)
+        tensors += _NORM_ROPE_TENSOR.pack(t.data_ptr(), _dptr(w), g.data_ptr(), o.data_ptr(), _dptr(dw), shape[1], code,
+                                          xb, xh, xn, gb, gh, gn, ob, oh, on)
     _check(L.tsr_norm_rope_backward(desc, eps, tensors, len(xs), _dptr(workspace),
                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
     return (outs[0], dws[0]) if one else (list(outs), list(dws))
@@ -747,12 +781,22 @@ def _linear_desc(x_rows, weight, out_heads, dtype, activation) -> bytes:
     return _LINEAR_DESC.pack(B, N, in_heads, in_dim, out_heads, M // out_heads, code, _ACTIVATIONS[activation])
 
 
-def _workspace(need_of, desc, workspace, device):
-    need = ctypes.c_size_t(0)
-    _check(need_of(desc, ctypes.byref(need)))
-    if workspace is None and need.value:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+_LINEAR_WORKSPACE = {}    # bytes by entry point and packed desc (sizes only)
+
+
+def _workspace(need_of, name, desc, workspace, device):
+    if workspace is None:
+        need = _LINEAR_WORKSPACE.get((name, desc))
+        if need is None:
+            n = ctypes.c_size_t(0)
+            _check(need_of(desc, ctypes.byref(n)))
+            if len(_LINEAR_WORKSPACE) >= 4096:
+                _LINEAR_WORKSPACE.clear()
+            need = _LINEAR_WORKSPACE[name, desc] = n.value
+        if need == 0:
+            return None, 0
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def tsr_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
@@ -791,7 +835,7 @@ def tsr_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
             out = torch.empty(shape, dtype=dtype, device=x.device)
         if keep and given is None:
             given = torch.empty(shape, dtype=dtype, device=x.device)
-        workspace, size = _workspace(L.tsr_linear_workspace, desc, workspace, x.device)
+        workspace, size = _workspace(L.tsr_linear_workspace, 0, desc, workspace, x.device)
     none = (0, 0, 0)
     args = _LINEAR_ARGS.pack(x.data_ptr(), _dptr(weight), _dptr(bias), 0 if residual is None else residual.data_ptr(),
                              out.data_ptr(), given.data_ptr() if keep else 0, *x_stride,
@@ -828,7 +872,7 @@ def tsr_linear_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
         new = lambda t, shape, wanted: (None if not wanted else t if t is not None
                                         else torch.empty(shape, dtype=dtype, device=x.device))
         dx, dweight, dbias = new(dx, x.shape, need[0]), new(dweight, weight.shape, need[1]), new(dbias, (M,), need[2])
-        workspace, size = _workspace(L.tsr_linear_backward_workspace, desc, workspace, x.device)
+        workspace, size = _workspace(L.tsr_linear_backward_workspace, 1, desc, workspace, x.device)
     none = (0, 0, 0)
     args = _LINEAR_GRADS.pack(dout.data_ptr(), x.data_ptr(), _dptr(weight), 0 if activation is None else pre.data_ptr(),
                               0 if dx is None else dx.data_ptr(), _dptr(dweight), _dptr(dbias), *g_stride, *x_stride,

@@ -1,0 +1,512 @@
+// norm_rope_kernel.cuh -- RMS norm of every head's row and the position rotation in one pass,
+// forward and backward, between any two strided layouts.
+//
+// With r = 1 / sqrt(mean_c x_c^2 + eps), xhat = x r and R the rotation of the row's
+// token (rope.cu):
+//     y = R (w o xhat)
+// and for a gradient dy of y, g = R^T dy, S = sum_c g_c w_c x_c:
+//     dx = r (g o w - x r^2 S / d),        dw = sum over rows of g o xhat.
+// The backward takes x, not y: r is computed again, nothing is kept by the forward.
+//
+// Bound: HBM, one read of x (and dy) and one write.  A row lies in registers across a
+// group of lanes, 16 bytes each, and its sums are butterflies in the group: a pass of its
+// own for the norm would read and write everything once more.  As in rope.cu a thread
+// keeps its unit of pairs of one token and goes over the heads of every tensor, so the
+// angles cost 1 / heads of a sincos per pair.
+//
+// The row's sums stand between its loads and its stores, so loads held in registers leave
+// the memory idle in between (480p forward 199 us, 720p backward 876).  Every thread
+// therefore has 64 bytes in each of the three stages of a ring in shared memory, which
+// cp.async fills two stages ahead, across heads and tokens, at no cost in registers; the
+// lanes that share a row need a barrier of their own only.
+//
+// dw: a thread sums its channels over all rows it meets in fp32, the CTA adds its groups
+// in shared memory and stores one partial row, and a dependent kernel adds the CTAs' rows
+// in their order: no atomics, the same bits every run.
+#pragma once
+#include "internal.h"
+#include "ptx.cuh"
+#include "rope_units.cuh"
+
+namespace tsr {
+
+namespace norm {
+
+using rope::kMaxTensors;
+using rope::Unit;
+
+constexpr int kThreads = 256;
+constexpr int kStages = 3;
+// CTAs that an SM holds, by registers
+constexpr int ctas_per_sm(bool grad, int P) { return grad || P == 1 ? 2 : 3; }
+
+struct NormParams {
+  const void* x[kMaxTensors];
+  const void* w[kMaxTensors];        // null: 1
+  const void* g[kMaxTensors];        // backward: dy
+  void* out[kMaxTensors];            // y or dx
+  int64_t xs[kMaxTensors][3], gs[kMaxTensors][3], os[kMaxTensors][3];   // element strides of b, h, n
+  int32_t H[kMaxTensors];
+  int32_t cta0[kMaxTensors + 1];     // CTAs of each tensor, one after another
+  int32_t chunk[kMaxTensors];        // heads an item takes
+  rope::Angles ang;
+  int32_t n_tensors, N, B, d, lanes_log2, w_f32;
+  float eps;
+  float* part;                       // backward: [CTA][d], null: no weight gradient
+};
+
+// Two fp32 values in a 64-bit register, for packed arithmetic: two operations an
+// instruction (480p forward 160 -> 148 us).
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The pairs of a unit as floats, first elements and second elements, two pairs a register
+// (P = 1: the other half is 0), and back.
+template <typename T, int P, bool ADJ>
+__device__ __forceinline__ void get(const Unit<T, P, ADJ>& u, F2 (&a)[(P + 1) / 2], F2 (&b)[(P + 1) / 2]) {
+  using rope::Two;
+  if constexpr (P == 1) {
+    a[0] = pack2(rope::to_f(u.e0), 0.f);
+    b[0] = pack2(rope::to_f(u.e1), 0.f);
+  } else if constexpr (ADJ) {
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      const float2 v = Two<T>::load(u.a.w[2 * i]), z = Two<T>::load(u.a.w[2 * i + 1]);
+      a[i] = pack2(v.x, z.x);
+      b[i] = pack2(v.y, z.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      const float2 v = Two<T>::load(u.a.w[i]), z = Two<T>::load(u.b.w[i]);
+      a[i] = pack2(v.x, v.y);
+      b[i] = pack2(z.x, z.y);
+    }
+  }
+}
+template <typename T, int P, bool ADJ>
+__device__ __forceinline__ void put(Unit<T, P, ADJ>& u, const F2 (&a)[(P + 1) / 2], const F2 (&b)[(P + 1) / 2]) {
+  using rope::Two;
+  if constexpr (P == 1) {
+    u.e0 = rope::from_f<T>(unpack2(a[0]).x);
+    u.e1 = rope::from_f<T>(unpack2(b[0]).x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      const float2 v = unpack2(a[i]), z = unpack2(b[i]);
+      if constexpr (ADJ) {
+        u.a.w[2 * i] = Two<T>::store(make_float2(v.x, z.x));
+        u.a.w[2 * i + 1] = Two<T>::store(make_float2(v.y, z.y));
+      } else {
+        u.a.w[i] = Two<T>::store(v);
+        u.b.w[i] = Two<T>::store(z);
+      }
+    }
+  }
+}
+
+// Channels of a unit's pair i.
+template <int P, bool ADJ>
+__device__ __forceinline__ int first_of(int ch0, int i) { return P == 1 ? ch0 : ADJ ? ch0 + 2 * i : ch0 + i; }
+template <int P, bool ADJ>
+__device__ __forceinline__ int second_of(int ch0, int ch1, int i) {
+  return P == 1 ? ch1 : ADJ ? ch0 + 2 * i + 1 : ch1 + i;
+}
+
+template <typename T>
+__device__ __forceinline__ float weight_at(const NormParams& p, int t, int c) {
+  if (!p.w[t]) return 1.f;
+  if (p.w_f32) return __ldg(static_cast<const float*>(p.w[t]) + c);
+  return rope::to_f(static_cast<const T*>(p.w[t])[c]);
+}
+
+// What a thread copies and holds of a row, and how many rows at a time.
+template <typename T, int P, bool ADJ, int K, bool GRAD>
+struct Batch {
+  static constexpr bool RING = P > 1;
+  static constexpr int Q = GRAD ? 2 : 1;                                     // rows of x, and of dy
+  static constexpr int COPIES = RING ? K * 2 * P * static_cast<int>(sizeof(T)) / 16 : 0;   // of 16 bytes of a row
+  static constexpr int R = !RING ? (GRAD ? 1 : 2) : 64 / (Q * COPIES * 16) < 1 ? 1 : 64 / (Q * COPIES * 16);
+  static constexpr int SLOT = R * Q * COPIES * 16 * kThreads;                // a stage of the CTA
+  static constexpr int RED = GRAD ? 512 * P * K * 4 : 0;                     // weight gradients of its groups
+  static constexpr int SMEM = kStages * SLOT > RED ? kStages * SLOT : RED;
+};
+
+// Where a thread is: an item (`tokens` tokens, `chunk` heads) and its next head.
+struct Place {
+  // item = rest * tiles + tile, rest = b * chunks + chunk: below 2^24 and 2^16 (one chunk) or
+  // as few as the CTAs
+  int tile, rest, n, b, h, h1;
+};
+
+// One CTA works on one tensor, on items of `tokens` tokens and `chunk` heads.  A row is
+// K units in each of 2^lanes_log2 lanes.  FULL: every lane has its K units and all their
+// pairs turn.
+template <typename T, int P, bool ADJ, int K, bool GRAD, bool FULL>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kernel(const __grid_constant__ NormParams p) {
+  using B = Batch<T, P, ADJ, K, GRAD>;
+  constexpr int R = B::R, NP = (P + 1) / 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lanes = 1 << p.lanes_log2;
+  const int group = threadIdx.x >> p.lanes_log2, lane = threadIdx.x & (lanes - 1);
+  const int tokens = kThreads >> p.lanes_log2;
+  const uint32_t mask = (lanes == 32 ? 0xFFFFFFFFu : (1u << lanes) - 1u) << ((threadIdx.x & 31) - lane);
+  int t = 0;
+  while (t + 1 < p.n_tensors && static_cast<int>(blockIdx.x) >= p.cta0[t + 1]) ++t;
+  const int tiles = (p.N + tokens - 1) / tokens;
+  const int H = p.H[t], chunk = p.chunk[t], chunks = (H + chunk - 1) / chunk;
+  const int rests = p.B * chunks, stride = p.cta0[t + 1] - p.cta0[t];
+  const float inv_d = 1.f / p.d;
+
+  int ch0[K], ch1[K];
+  bool has[K];
+  auto on = [&](int k) { return FULL || has[k]; };
+  F2 wa[K][NP], wb[K][NP];                 // weights of the first and of the second elements
+  F2 da[K][NP], db[K][NP];                 // and their gradients, over the rows of this thread
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int unit = lane + k * lanes;
+    has[k] = unit < p.ang.units;
+    ch0[k] = on(k) ? p.ang.c0[unit] : 0;
+    ch1[k] = on(k) ? p.ang.c1[unit] : 0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      auto w0 = [&](int j) { return on(k) && j < P ? weight_at<T>(p, t, first_of<P, ADJ>(ch0[k], j)) : 0.f; };
+      auto w1 = [&](int j) { return on(k) && j < P ? weight_at<T>(p, t, second_of<P, ADJ>(ch0[k], ch1[k], j)) : 0.f; };
+      wa[k][i] = pack2(w0(2 * i), w0(2 * i + 1));
+      wb[k][i] = pack2(w1(2 * i), w1(2 * i + 1));
+      da[k][i] = db[k][i] = 0;
+    }
+  }
+
+  // The place's first item, or the one `tiles` and `rests` on; false behind the last.
+  // Items whose token this group does not have are passed over.
+  const int step_tile = stride % tiles, step_rest = stride / tiles;
+  auto settle = [&](Place& q) -> bool {
+    while (q.rest < rests) {
+      q.n = q.tile * tokens + group;
+      if (q.n < p.N) {
+        q.b = chunks == 1 ? q.rest : q.rest / chunks;
+        q.h = chunks == 1 ? 0 : (q.rest - q.b * chunks) * chunk;
+        q.h1 = min(q.h + chunk, H);
+        return true;
+      }
+      q.tile += step_tile;
+      q.rest += step_rest;
+      if (q.tile >= tiles) {
+        q.tile -= tiles;
+        ++q.rest;
+      }
+    }
+    return false;
+  };
+  auto next = [&](Place& q) -> bool {
+    q.tile += step_tile;
+    q.rest += step_rest;
+    if (q.tile >= tiles) {
+      q.tile -= tiles;
+      ++q.rest;
+    }
+    return settle(q);
+  };
+  const int first = static_cast<int>(blockIdx.x) - p.cta0[t];
+  Place cur;
+  cur.rest = first / tiles;
+  cur.tile = first - cur.rest * tiles;
+  bool live = settle(cur);
+
+  const int64_t xs = p.xs[t][1], os = p.os[t][1], gs = GRAD ? p.gs[t][1] : 0;
+  auto row_of = [&](const void* base, const int64_t (&s)[3], const Place& q) {
+    return static_cast<const T*>(base) + q.b * s[0] + q.n * s[2] + q.h * s[1];
+  };
+  // A row of the ring, a group's own: its lanes copy 16 bytes each, row after row in whole
+  // lines (half-split pieces would be parts of sectors), and read their units back.
+  const int row_bytes = p.d * static_cast<int>(sizeof(T)), pitch = tokens * row_bytes;
+  const int stage_bytes = R * B::Q * pitch;
+  uint8_t* const mine = smem + group * row_bytes;
+  int filled = 0, read = 0;                // the ring's next stages to copy to and to read
+  auto advance = [&](int& at) {
+    at += stage_bytes;
+    if (at == kStages * stage_bytes) at = 0;
+  };
+  Place far = cur;                         // the next rows to copy
+  bool more = live;
+  const T *far_x = nullptr, *far_g = nullptr;
+  auto point = [&]() {
+    far_x = row_of(p.x[t], p.xs[t], far);
+    if constexpr (GRAD) far_g = row_of(p.g[t], p.gs[t], far);
+  };
+  auto fetch = [&]() {
+    if (more) {
+      const uint32_t to = smem_u32(mine + filled) + lane * 16;
+      const uint8_t* from_x = reinterpret_cast<const uint8_t*>(far_x) + lane * 16;
+      const uint8_t* from_g = reinterpret_cast<const uint8_t*>(far_g) + lane * 16;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (far.h + j < far.h1) {
+#pragma unroll
+          for (int m = 0; m < B::COPIES; ++m) {
+            const int at = m * lanes * 16;
+            if (FULL || lane * 16 + at < row_bytes) {
+              cp_async_16(to + j * B::Q * pitch + at, from_x + j * xs * static_cast<int64_t>(sizeof(T)) + at);
+              if constexpr (GRAD)
+                cp_async_16(to + (j * B::Q + 1) * pitch + at, from_g + j * gs * static_cast<int64_t>(sizeof(T)) + at);
+            }
+          }
+        }
+      far.h += R;
+      far_x += R * xs;
+      far_g += R * gs;
+      if (far.h >= far.h1) {
+        more = next(far);
+        if (more) point();
+      }
+    }
+    cp_async_commit();
+    advance(filled);
+  };
+  if constexpr (B::RING) {
+    if (more) point();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+  }
+
+  // Pair (u, v) -> (u c0 - v s0, u s1 + v c1): of the weighted row forward (the weights are
+  // in the factors), of the gradient back (c0 = c1 = cos, s0 = s1 = -sin).  Pairs that do
+  // not turn are left alone: 0 times a partner that is not finite would not be 0.
+  F2 c0[K][NP], s0[K][NP], s1[K][NP], c1[K][NP];
+  int turning[K];
+  T* dst = nullptr;
+  auto begin = [&]() {                     // an item's angles and rows
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float cs[P], sn[P];
+      turning[k] = rope::angles_of<P>(p.ang, cur.b, cur.n, on(k) ? lane + k * lanes : p.ang.units, cs, sn);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float hi = P == 1 ? 0.f : cs[(2 * i + 1) % P], ti = P == 1 ? 0.f : sn[(2 * i + 1) % P];
+        const F2 c = pack2(cs[2 * i % P], hi), s = pack2(sn[2 * i % P], ti), minus = pack2(-1.f, -1.f);
+        if constexpr (GRAD) {
+          c0[k][i] = c;
+          s0[k][i] = s;                    // u cos + v sin
+          s1[k][i] = mul2(s, minus);       // v cos - u sin
+        } else {
+          c0[k][i] = mul2(c, wa[k][i]);
+          s0[k][i] = mul2(mul2(s, minus), wb[k][i]);
+          s1[k][i] = mul2(s, wa[k][i]);
+          c1[k][i] = mul2(c, wb[k][i]);
+        }
+      }
+    }
+    dst = const_cast<T*>(row_of(p.out[t], p.os[t], cur));
+  };
+  // the first and second elements of two pairs, turned
+  auto turn = [&](int k, int i, F2 u, F2 v, F2& y, F2& z) {
+    y = fma2(v, s0[k][i], mul2(u, c0[k][i]));
+    z = fma2(u, s1[k][i], mul2(v, GRAD ? c0[k][i] : c1[k][i]));
+    if constexpr (!FULL) {
+      const F2 y0 = GRAD ? u : mul2(u, wa[k][i]), z0 = GRAD ? v : mul2(v, wb[k][i]);
+      const bool lo = 2 * i < turning[k], hi = 2 * i + 1 < turning[k];
+      y = pack2(lo ? unpack2(y).x : unpack2(y0).x, hi ? unpack2(y).y : unpack2(y0).y);
+      z = pack2(lo ? unpack2(z).x : unpack2(z0).x, hi ? unpack2(z).y : unpack2(z0).y);
+    }
+  };
+  if (live) begin();
+  while (live) {
+    Unit<T, P, ADJ> u[R][K], v[GRAD ? R : 1][K];
+    if constexpr (B::RING) {
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp(mask);                    // the group's copies, all lanes'
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const T* x = reinterpret_cast<const T*>(mine + read + j * B::Q * pitch);
+        const T* g = GRAD ? reinterpret_cast<const T*>(mine + read + (j * B::Q + 1) * pitch) : nullptr;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          u[j][k].load(x + ch0[k], x + ch1[k]);
+          if constexpr (GRAD) v[j][k].load(g + ch0[k], g + ch1[k]);
+        }
+      }
+      advance(read);
+    } else {
+      const T* src = row_of(p.x[t], p.xs[t], cur);
+      const T* grd = GRAD ? row_of(p.g[t], p.gs[t], cur) : nullptr;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (cur.h + j < cur.h1) {
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            if (on(k)) {
+              u[j][k].load(src + j * xs + ch0[k], src + j * xs + ch1[k]);
+              if constexpr (GRAD) v[j][k].load(grd + j * gs + ch0[k], grd + j * gs + ch1[k]);
+            }
+        }
+    }
+    float ss[R], sp[R];
+    F2 ga[GRAD ? R : 1][K][NP], gb[GRAD ? R : 1][K][NP];     // R^T dy
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      F2 q0 = 0, q1 = 0, t0 = 0, t1 = 0;
+      if (cur.h + j < cur.h1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (on(k)) {
+            F2 a[NP], c[NP];
+            get(u[j][k], a, c);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              q0 = fma2(a[i], a[i], q0);
+              q1 = fma2(c[i], c[i], q1);
+            }
+            if constexpr (GRAD) {
+              F2 e[NP], f[NP];
+              get(v[j][k], e, f);
+#pragma unroll
+              for (int i = 0; i < NP; ++i) {
+                turn(k, i, e[i], f[i], ga[j][k][i], gb[j][k][i]);
+                t0 = fma2(mul2(ga[j][k][i], wa[k][i]), a[i], t0);
+                t1 = fma2(mul2(gb[j][k][i], wb[k][i]), c[i], t1);
+              }
+            }
+          }
+      }
+      const float2 x0 = unpack2(q0), x1 = unpack2(q1), y0 = unpack2(t0), y1 = unpack2(t1);
+      ss[j] = (x0.x + x0.y) + (x1.x + x1.y);
+      sp[j] = (y0.x + y0.y) + (y1.x + y1.y);
+    }
+    for (int m = lanes >> 1; m; m >>= 1) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        ss[j] += __shfl_xor_sync(mask, ss[j], m);
+        if constexpr (GRAD) sp[j] += __shfl_xor_sync(mask, sp[j], m);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (cur.h + j < cur.h1) {
+        const float r = rsqrtf(fmaf(ss[j], inv_d, p.eps));
+        const float off = GRAD ? -(r * r * sp[j] * inv_d) : 0.f;
+        const F2 r2 = pack2(r, r), off2 = pack2(off, off);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (on(k)) {
+            F2 a[NP], c[NP], y[NP], z[NP];
+            get(u[j][k], a, c);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              if constexpr (GRAD) {
+                y[i] = mul2(r2, fma2(a[i], off2, mul2(ga[j][k][i], wa[k][i])));
+                z[i] = mul2(r2, fma2(c[i], off2, mul2(gb[j][k][i], wb[k][i])));
+                da[k][i] = fma2(ga[j][k][i], mul2(a[i], r2), da[k][i]);
+                db[k][i] = fma2(gb[j][k][i], mul2(c[i], r2), db[k][i]);
+              } else {
+                // normed first: a large row's products with the weights stay finite
+                turn(k, i, mul2(a[i], r2), mul2(c[i], r2), y[i], z[i]);
+              }
+            }
+            put(u[j][k], y, z);
+            u[j][k].store(dst + j * os + ch0[k], dst + j * os + ch1[k]);
+          }
+      }
+    }
+    cur.h += R;
+    dst += R * os;
+    if (cur.h >= cur.h1) {
+      live = next(cur);
+      if (live) begin();
+    }
+  }
+  if constexpr (GRAD) {
+    if (!p.part) return;
+    // the ring's memory, once every thread is through with it
+    if constexpr (B::RING) cp_async_wait_all();
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (on(k)) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float2 x = unpack2(da[k][i / 2]), y = unpack2(db[k][i / 2]);
+          red[group * p.d + first_of<P, ADJ>(ch0[k], i)] = i % 2 ? x.y : x.x;
+          red[group * p.d + second_of<P, ADJ>(ch0[k], ch1[k], i)] = i % 2 ? y.y : y.x;
+        }
+      }
+    __syncthreads();
+    grid_launch_dependents();
+    for (int c = threadIdx.x; c < p.d; c += kThreads) {
+      float s = 0.f;
+      for (int q = 0; q < tokens; ++q) s += red[q * p.d + c];
+      p.part[static_cast<int64_t>(blockIdx.x) * p.d + c] = s;
+    }
+  }
+}
+
+inline tsr_status launch_one(void (*kern)(NormParams), int smem, unsigned ctas, const NormParams& p, cudaStream_t st) {
+  if (smem > 48 * 1024) TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  kern<<<ctas, kThreads, smem, st>>>(p);
+  TSR_CUDA(cudaGetLastError());
+  return TSR_OK;
+}
+
+template <bool GRAD>
+tsr_status launch(const NormParams& p, int dtype, bool halves, int P, int K, cudaStream_t st) {
+  const unsigned ctas = static_cast<unsigned>(p.cta0[p.n_tensors]);
+  const bool full = P > 1 && p.ang.units == K << p.lanes_log2 && p.ang.n_pairs == p.ang.units * P;
+#define TSR_NORM_ONE(T, P_, ADJ_, K_, FULL_)                                                          \
+  if (P == P_ && halves != ADJ_ && K == K_ && full == FULL_)                                          \
+    return launch_one(norm_rope_kernel<T, P_, ADJ_, K_, GRAD, FULL_>, Batch<T, P_, ADJ_, K_, GRAD>::SMEM, ctas, p, st);
+#define TSR_NORM(T, P_, ADJ_, K_)         \
+  TSR_NORM_ONE(T, P_, ADJ_, K_, false)    \
+  if constexpr (P_ > 1) {                 \
+    TSR_NORM_ONE(T, P_, ADJ_, K_, true)   \
+  }
+#define TSR_NORM_16(T)      \
+  TSR_NORM(T, 4, true, 1)   \
+  TSR_NORM(T, 1, true, 4)   \
+  TSR_NORM(T, 4, false, 1)  \
+  TSR_NORM(T, 1, false, 4)
+  if (dtype == TSR_DTYPE_BF16) {
+    TSR_NORM_16(__nv_bfloat16)
+  } else if (dtype == TSR_DTYPE_F16) {
+    TSR_NORM_16(__half)
+  } else {
+    TSR_NORM(float, 2, true, 1)
+    TSR_NORM(float, 2, true, 2)
+    TSR_NORM(float, 1, true, 4)
+    TSR_NORM(float, 4, false, 1)
+    TSR_NORM(float, 1, false, 4)
+  }
+#undef TSR_NORM_16
+#undef TSR_NORM
+#undef TSR_NORM_ONE
+  return fail(TSR_ERR_INTERNAL, "no norm kernel for this layout");
+}
+
+// The forward's kernels (norm_rope.cu) and the backward's (norm_rope_bwd.cu) are compiled apart.
+extern template tsr_status launch<false>(const NormParams&, int, bool, int, int, cudaStream_t);
+extern template tsr_status launch<true>(const NormParams&, int, bool, int, int, cudaStream_t);
+
+}  // namespace norm
+
+}  // namespace tsr
