@@ -262,11 +262,14 @@ def _on_device(*tensors) -> None:
                              f"cuda:{current}")
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _allocating_on(stream):
     """Context in which new tensors belong to the stream that the call runs on, so
     that a workspace freed on return is not reused before the call's kernels end."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
@@ -674,11 +677,8 @@ def tsr_norm_rope(x, weight, axis_dims, *, eps: float = 1e-6, grid=None,
     ws, code = _weights(weight, xs, dtype, d)
     if out is None:
         _on_device(*xs, *ws, positions)
-        if stream is None:
+        with _allocating_on(stream):
             outs = [t.new_empty(shape) for t, shape, _ in rows]
-        else:
-            with _allocating_on(stream):
-                outs = [t.new_empty(shape) for t, shape, _ in rows]
     else:
         outs = _heads_list(out)
         if len(outs) != len(xs):
@@ -832,9 +832,9 @@ def tsr_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     L = lib()
     with _allocating_on(stream):
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=x.device)
+            out = x.new_empty(shape)
         if keep and given is None:
-            given = torch.empty(shape, dtype=dtype, device=x.device)
+            given = x.new_empty(shape)
         workspace, size = _workspace(L.tsr_linear_workspace, 0, desc, workspace, x.device)
     none = (0, 0, 0)
     args = _LINEAR_ARGS.pack(x.data_ptr(), _dptr(weight), _dptr(bias), 0 if residual is None else residual.data_ptr(),
@@ -869,8 +869,7 @@ def tsr_linear_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     _on_device(dout, x, weight, pre, dx, dweight, dbias, workspace)
     L = lib()
     with _allocating_on(stream):
-        new = lambda t, shape, wanted: (None if not wanted else t if t is not None
-                                        else torch.empty(shape, dtype=dtype, device=x.device))
+        new = lambda t, shape, wanted: None if not wanted else t if t is not None else x.new_empty(shape)
         dx, dweight, dbias = new(dx, x.shape, need[0]), new(dweight, weight.shape, need[1]), new(dbias, (M,), need[2])
         workspace, size = _workspace(L.tsr_linear_backward_workspace, 1, desc, workspace, x.device)
     none = (0, 0, 0)
