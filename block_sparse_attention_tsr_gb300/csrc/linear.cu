@@ -21,20 +21,22 @@ namespace {
 constexpr int kSms = 152;              // what the choice of tiles is made for
 constexpr uint64_t kTimeoutNs = kWaitTimeoutNs;
 
-// D's values from the parts of a split product.  HBM/L2-bound.
-__global__ void __launch_bounds__(256) linear_finish_kernel(const float* part, int32_t splits, int64_t total_rows,
-                                                            int32_t n_rows, int32_t cols,
-                                                            const __grid_constant__ Epilogue e) {
-  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  const int32_t vecs = cols / 8;
+// D's values of the tiles that were cut along k, from their parts.  HBM/L2-bound.
+template <int BN>
+__global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ GemmParams p) {
+  constexpr int VECS = BN / 8;
+  const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+  const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole;
+  const int64_t cut = i / (256 * VECS);
+  const int32_t row = static_cast<int32_t>(i / VECS) % 256, c = static_cast<int32_t>(i % VECS) * 8;
   grid_wait();
-  if (i >= total_rows * vecs) return;
-  const int64_t row = i / vecs;
-  const int32_t f = static_cast<int32_t>(i - row * vecs) * 8;
-  const int64_t b = row / n_rows;
+  if (cut >= rest) return;
+  const int2 rc = tile_of(p, p.whole + cut);
+  const int32_t b = rc.x / p.tiles_per_batch, n = (rc.x - b * p.tiles_per_batch) * 256 + row, f = rc.y * BN + c;
+  if (n >= p.n_rows || f >= p.cols) return;
   float v[8] = {};
-  for (int32_t s = 0; s < splits; ++s) {
-    const float4* src = reinterpret_cast<const float4*>(part + (s * total_rows + row) * cols + f);
+  for (int32_t s = 0; s < p.splits; ++s) {
+    const float4* src = reinterpret_cast<const float4*>(p.part + ((s * rest + cut) * 256 + row) * BN + c);
     const float4 x = src[0], y = src[1];
     v[0] += x.x;
     v[1] += x.y;
@@ -45,7 +47,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const float* part, i
     v[6] += y.z;
     v[7] += y.w;
   }
-  by_kind(e.f16, e.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(e, v, b, row - b * n_rows, f); });
+  by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(p.epi, v, b, n, f); });
 }
 
 struct DzParams {
@@ -126,11 +128,12 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ----------------------------------------------------------- choice of tiles
 enum Kind { FORWARD, DX, DWEIGHT };
-enum Variant { PAIR_256, PAIR_128, SWAP_32, SWAP_128 };
+enum Variant { PAIR_256, PAIR_128, FEW_32, FEW_128 };
 
 struct Choice {
   Variant variant;
   int32_t splits;
+  int64_t whole;                       // tiles that are not cut along k (pairs)
 };
 
 // Rows, columns and k of a product: D is [batches x n_rows][cols].
@@ -139,30 +142,33 @@ struct Product {
   Kind kind;
 };
 
-bool parts(const Choice& c) { return c.splits > 1 || c.variant >= SWAP_32; }
-
-// The fastest by a model in microseconds, fitted to 580 timed products (forward, dx and
-// dweight, 1 to 8,000 tokens, 256 to 8,192 features; within 12% in the root mean square,
-// and its choice on average within 3% of the fastest): waves of units, each its k steps and
-// a fill and an epilogue, and for parts a launch and their traffic.  Each part has four
-// steps at least.  For example 666 x 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on 256 x
-// 256, 17 with k in three parts; 100 x 4096 -> 4096: 9.2 us with the tokens on the columns
-// and k in four parts, 13 on 256 x 128 tiles.
+// The fastest by a model in microseconds, fitted to 468 timed products (forward, dx and
+// dweight, 1 to 8,000 tokens, 256 to 8,192 features; 13% off in the root mean square, and
+// its choice on average within 1.2% of the fastest): waves of units, each its k steps and a
+// fill and an epilogue; where pairs' tiles are cut a launch and the parts' traffic; clusters
+// of 4 and 8 CTAs leave SMs free.  Each part has four steps at least.  For example 666 x
+// 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on 256 x 256, 18 with k in three parts; 1 x
+// 4096 -> 4096: 8.5 us with the token on 32 columns and k in four parts, 21 on 256 x 128.
 Choice choose(const Product& q) {
-  constexpr double kStep[4] = {0.276, 0.169, 0.108, 0.151}, kUnit[4] = {3.1, 2.05, 0.8, 1.3};
+  constexpr double kStep[4] = {0.298, 0.18, 0.13, 0.188}, kUnit[4] = {2.06, 1.27, 3.9, 5.14};
   constexpr int kTok[4] = {256, 256, 32, 128}, kFeat[4] = {256, 128, 128, 128};
-  Choice best{PAIR_256, 1};
+  Choice best{PAIR_256, 1, 0};
   double least = 1e30;
-  for (int v = PAIR_256; v <= SWAP_128; ++v) {
-    const bool swap = v >= SWAP_32;
-    if (swap && (q.kind == DWEIGHT || q.batches * q.n_rows > 512)) continue;   // fitted up to 300 tokens
+  for (int v = PAIR_256; v <= FEW_128; ++v) {
+    const bool few = v >= FEW_32;
+    if (few && (q.kind == DWEIGHT || q.batches * q.n_rows > 512)) continue;   // fitted up to 300 tokens
     const int64_t tiles = q.batches * cdiv(q.n_rows, kTok[v]) * cdiv(q.cols, kFeat[v]);
-    for (int64_t s = 1; s <= 16 && (s == 1 || q.k_steps >= 4 * s); ++s) {
-      double t = cdiv(tiles * s, swap ? kSms : kSms / 2) * (cdiv(q.k_steps, s) * kStep[v] + kUnit[v]);
-      if (s > 1 || swap) t += 2.5 + 0.6e-6 * s * q.batches * q.n_rows * q.cols;
+    for (int64_t s = 1; s <= (few ? 8 : 16) && (s == 1 || q.k_steps >= 4 * s); s += few ? s : 1) {
+      const int64_t slots = !few ? kSms / 2 : s == 8 ? 96 : s == 4 ? 128 : 150;
+      const int64_t whole = s == 1 ? tiles : few ? 0 : tiles / slots * slots;
+      if (s > 1 && whole == tiles) continue;
+      double t = cdiv(whole, slots) * (q.k_steps * kStep[v] + kUnit[v]) +
+                 cdiv((tiles - whole) * s, slots) * (cdiv(q.k_steps, s) * kStep[v] + kUnit[v]);
+      if (few) t += 0.15 * s;
+      else t += 2.75 + (s > 1 ? 2.6 + 0.66e-6 * s * (tiles - whole) * kTok[v] * kFeat[v] : 0.0);
       if (t < least) {
         least = t;
-        best = {static_cast<Variant>(v), static_cast<int32_t>(s)};
+        best = {static_cast<Variant>(v), static_cast<int32_t>(s), whole};
       }
     }
   }
@@ -171,7 +177,9 @@ Choice choose(const Product& q) {
 
 size_t part_bytes(const Product& q) {
   const Choice c = choose(q);
-  return parts(c) ? static_cast<size_t>(c.splits) * q.batches * q.n_rows * q.cols * 4 : 0;
+  if (c.splits == 1 || c.variant >= FEW_32) return 0;
+  const int bn = c.variant == PAIR_256 ? 256 : 128;
+  return static_cast<size_t>(q.batches * cdiv(q.n_rows, 256) * cdiv(q.cols, bn) - c.whole) * c.splits * 256 * bn * 4;
 }
 
 // ---------------------------------------------------------------- the layer
@@ -243,46 +251,60 @@ tsr_status encode(CUtensorMap* m, const void* p, const View& v, int64_t heads, i
                 {v.dim, n, heads, b}, {v.sn, v.sh, v.sb}, channels, rows);
 }
 
-template <int CG, int BN, bool A_MN, bool B_MN, bool SWAP>
-tsr_status launch_variant(const GemmParams& p, cudaStream_t st) {
-  using C = Cfg<CG, BN, SWAP>;
-  auto kern = linear_gemm_kernel<CG, BN, A_MN, B_MN, SWAP>;
+// A kernel that may set itself up while what is before it on the stream ends (it waits for
+// that before it touches memory), in clusters of `cluster` CTAs.
+tsr_status launch_clusters(void (*kern)(GemmParams), bool (&set)[64], int smem, int64_t ctas, int cluster,
+                           const GemmParams& p, cudaStream_t st) {
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
   // once per device: the attribute is the function's there
-  static bool set[64] = {};
   if (dev >= 64 || !set[dev]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     if (dev < 64) set[dev] = true;
   }
-  const int64_t units = static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits;
-  // The kernel's set-up may overlap the end of what is before it on the stream (it waits
-  // for that before it touches memory).
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, num_sms(dev) / CG) * CG));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = CG > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   TSR_CUDA(cudaLaunchKernelEx(&cfg, kern, p));
   return TSR_OK;
 }
 
-template <bool A_MN, bool B_MN, bool SWAPS>
+template <int BN, bool A_MN, bool B_MN>
+tsr_status launch_pairs(const GemmParams& p, cudaStream_t st) {
+  static bool set[64] = {};
+  const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.col_tiles, rest = tiles - p.whole;
+  int dev = 0;
+  TSR_CUDA(cudaGetDevice(&dev));
+  const int64_t pairs = std::min<int64_t>(p.whole + rest * p.splits, num_sms(dev) / 2);
+  if (tsr_status e = launch_clusters(linear_gemm_kernel<BN, A_MN, B_MN>, set, Cfg<BN>::SMEM, pairs * 2, 2, p, st)) return e;
+  if (rest)
+    TSR_CUDA(launch_dependent(linear_finish_kernel<BN>, static_cast<unsigned>(rest * BN / 8), 256u, 0, st, p));
+  return TSR_OK;
+}
+template <int BN, bool W_MN>
+tsr_status launch_few(const GemmParams& p, cudaStream_t st) {
+  static bool set[64] = {};
+  return launch_clusters(linear_few_kernel<BN, W_MN>, set, FewCfg<BN>::SMEM,
+                         static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits, p.splits, p, st);
+}
+
+template <bool A_MN, bool B_MN>
 tsr_status launch_kind(Variant v, const GemmParams& p, cudaStream_t st) {
-  if (v == PAIR_256) return launch_variant<2, 256, A_MN, B_MN, false>(p, st);
-  if (v == PAIR_128) return launch_variant<2, 128, A_MN, B_MN, false>(p, st);
-  if constexpr (SWAPS) {
-    // the weight is A there: B's orientation here
-    if (v == SWAP_32) return launch_variant<1, 32, B_MN, A_MN, true>(p, st);
-    return launch_variant<1, 128, B_MN, A_MN, true>(p, st);
+  if (v == PAIR_256) return launch_pairs<256, A_MN, B_MN>(p, st);
+  if (v == PAIR_128) return launch_pairs<128, A_MN, B_MN>(p, st);
+  if constexpr (!A_MN) {
+    if (v == FEW_32) return launch_few<32, B_MN>(p, st);
+    return launch_few<128, B_MN>(p, st);
   }
   return fail(TSR_ERR_INTERNAL, "no kernel for this product");
 }
@@ -293,64 +315,53 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
                const View& vother, int64_t other_heads, const Epilogue& e, float* ws, cudaStream_t st) {
   const Product q = product(y, kind);
   const Choice c = choose(q);
-  const bool swap = c.variant >= SWAP_32;
+  const bool few = c.variant >= FEW_32;
   GemmParams p;
   memset(&p, 0, sizeof p);
   p.epi = e;
-  p.part = parts(c) ? ws : nullptr;
-  p.total_rows = q.batches * q.n_rows;
+  p.part = ws;
   p.n_rows = static_cast<int32_t>(q.n_rows);
   p.batches = static_cast<int32_t>(q.batches);
   p.cols = static_cast<int32_t>(q.cols);
   p.splits = c.splits;
+  p.whole = c.whole;
   p.k_steps = static_cast<int32_t>(q.k_steps);
   p.k_steps_per_batch = static_cast<int32_t>(cdiv(y.N, BK));
   p.group = 8;
   p.timeout_ns = kTimeoutNs;
-  const int bn = c.variant == PAIR_256 ? 256 : c.variant == SWAP_32 ? 32 : 128;
-  const int tile = swap ? bn : 256;                       // tokens (dweight: out features) of a tile
-  p.tiles_per_batch = static_cast<int32_t>(cdiv(q.n_rows, tile));
+  const int bn = c.variant == PAIR_256 ? 256 : c.variant == FEW_32 ? 32 : 128;
+  p.tiles_per_batch = static_cast<int32_t>(cdiv(q.n_rows, few ? bn : 256));
   p.row_tiles = p.tiles_per_batch * p.batches;
-  p.col_tiles = static_cast<int32_t>(cdiv(q.cols, swap ? 128 : bn));
-  if (swap) std::swap(p.row_tiles, p.col_tiles);
-  CUtensorMap *mt = &p.ta, *mo = &p.tb;
-  int32_t *dt = &p.a_dim, *dother = &p.b_dim;
-  if (swap) {
-    std::swap(mt, mo);
-    std::swap(dt, dother);
-  }
-  *dt = vtok.dim;
-  *dother = vother.dim;
+  p.col_tiles = static_cast<int32_t>(cdiv(q.cols, few ? 128 : bn));
+  if (few) std::swap(p.row_tiles, p.col_tiles);
+  CUtensorMap *mt = few ? &p.tb : &p.ta, *mo = few ? &p.ta : &p.tb;
+  (few ? p.b_dim : p.a_dim) = vtok.dim;
+  (few ? p.a_dim : p.b_dim) = vother.dim;
   const bool tok_mn = kind == DWEIGHT, other_mn = kind != FORWARD;
-  const int tok_rows = tok_mn ? BK : swap ? bn : 128, other_rows = other_mn ? BK : swap ? 128 : bn / 2;
+  const int tok_rows = tok_mn ? BK : few ? bn : 128, other_rows = other_mn ? BK : few ? 128 : bn / 2;
   if (tsr_status s = encode(mt, tok, vtok, tok_heads, y.N, y.B, BK, tok_rows, y.f16)) return s;
   const int64_t on = kind == DWEIGHT ? y.N : y.M, ob = kind == DWEIGHT ? y.B : 1;
   if (tsr_status s = encode(mo, other, vother, other_heads, on, ob, BK, other_rows, y.f16)) return s;
-  p.idesc = idesc_16bit(y.f16, swap ? 128 : 256, bn, swap ? other_mn : tok_mn, swap ? tok_mn : other_mn);
-  if (!swap) {
+  p.idesc = idesc_16bit(y.f16, few ? 128 : 256, bn, few ? other_mn : tok_mn, few ? tok_mn : other_mn);
+  if (!few) {
     // out's rows: tokens, or the weight's for its gradient
     const int64_t rows = q.n_rows, heads = q.cols / e.vout.dim;
-    if (p.part) {
-      if (tsr_status s = encode(&p.tout, p.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, {q.cols, rows, q.batches, c.splits},
-                                {q.cols, rows * q.cols, p.total_rows * q.cols}, 32, 32))
-        return s;
-    } else {
+    if (c.whole) {
       if (tsr_status s = encode(&p.tout, e.out, e.vout, heads, rows, q.batches, 32, 32, y.f16)) return s;
       if (e.pre)
         if (tsr_status s = encode(&p.tpre, e.pre, e.vpre, heads, rows, q.batches, 32, 32, y.f16)) return s;
       if (e.res)
         if (tsr_status s = encode(&p.tres, e.res, e.vres, heads, rows, q.batches, 32, 32, y.f16)) return s;
     }
+    const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - c.whole;
+    if (rest)
+      if (tsr_status s = encode(&p.tpart, p.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, {bn, 256, rest, c.splits},
+                                {bn, 256 * bn, rest * 256 * bn}, 32, 32))
+        return s;
   }
-  tsr_status s;
-  if (kind == FORWARD) s = launch_kind<false, false, true>(c.variant, p, st);
-  else if (kind == DX) s = launch_kind<false, true, true>(c.variant, p, st);
-  else s = launch_kind<true, true, false>(c.variant, p, st);
-  if (s || !p.part) return s;
-  const int64_t vecs = p.total_rows * (q.cols / 8);
-  TSR_CUDA(launch_dependent(linear_finish_kernel, static_cast<unsigned>(cdiv(vecs, 256)), 256u, 0, st,
-                            static_cast<const float*>(p.part), p.splits, p.total_rows, p.n_rows, p.cols, e));
-  return TSR_OK;
+  if (kind == FORWARD) return launch_kind<false, false>(c.variant, p, st);
+  if (kind == DX) return launch_kind<false, true>(c.variant, p, st);
+  return launch_kind<true, true>(c.variant, p, st);
 }
 
 // Blocks of rows of the pass over dz.

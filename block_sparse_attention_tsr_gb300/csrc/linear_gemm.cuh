@@ -16,13 +16,18 @@
 // is 32 KB per SM for 512 clocks of MMAs at BN = 256, 64 bytes a clock, about what an SM
 // takes from L2 (a tile of 128 x 256 of one CTA would need 96).  The accumulator has two
 // buffers in TMEM: the epilogue of a tile runs beside the MMAs of the next.
-// For few tokens the weight's bytes bound it; then the features lie on the 128 rows and
-// the tokens on BN columns (SWAP), one CTA a tile, k split over CTAs.
 //
-// Persistent: a CTA (pair) takes every n-th work unit.  Units with a part of k only
-// (split) store fp32 parts that linear_finish_kernel adds in their order.
+// Persistent: a CTA pair takes every n-th work unit, whole tiles first.  The tiles that
+// would make up a last, part-filled wave are cut along k instead (and all tiles, where
+// there are fewer than pairs): their units store fp32 parts that linear_finish_kernel adds
+// in their order.
 // Warps: TMA producer, MMA issuer (of the pair's first CTA), 8 epilogue warps.  Every wait
 // is bounded: on expiry the error word is set and the kernel winds down.
+//
+// For few tokens the weight's bytes bound it (linear_few_kernel): the features lie on the
+// 128 rows and the tokens on 32 or 128 columns, and a cluster of up to 8 CTAs shares a
+// tile's k; each leaves its sums in shared memory and adds up its share of the tile from
+// all of them.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -55,16 +60,16 @@ struct Epilogue {
 };
 
 struct GemmParams {
-  CUtensorMap ta, tb;
-  // out (or the parts, fp32), pre and residual as {channel, token, head, batch} (parts:
-  // {channel, token, batch, split}) in boxes of 32 tokens x 32 channels
-  CUtensorMap tout, tpre, tres;
-  Epilogue epi;                        // bias, activation and what is there; SWAP and parts: views
-  float* part;                         // [split][rows][cols] of D (SWAP: of D^T), null: epilogue here
-  int64_t total_rows;                  // of D (tokens in all batches, or features)
-  int32_t n_rows, batches;             // rows per batch
+  CUtensorMap ta, tb;                  // few tokens: the weight, and the tokens
+  // out, pre and residual as {channel, token, head, batch} and the parts, fp32, as {column,
+  // row, tile, part}, in boxes of 32 x 32
+  CUtensorMap tout, tpre, tres, tpart;
+  Epilogue epi;
+  float* part;                         // [splits][tiles - whole][256][BN]
+  int64_t whole;                       // tiles that are not cut along k: the first ones
+  int32_t n_rows, batches;             // rows per batch (tokens, or features)
   int32_t cols;
-  int32_t row_tiles, col_tiles;        // row tiles of all batches (SWAP: column tiles are)
+  int32_t row_tiles, col_tiles;        // row tiles of all batches
   int32_t tiles_per_batch;             // of the token axis
   int32_t splits, k_steps;             // k steps of a whole product
   int32_t k_steps_per_batch;           // dweight: steps of one batch's tokens
@@ -196,17 +201,17 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int CG, int BN, bool SWAP>
+template <int BN>
 struct Cfg {
-  static constexpr int TM = 128 * CG;                     // rows of a tile
-  static constexpr int A_BYTES = 128 * BK * 2, B_ROWS = BN / CG, B_BYTES = B_ROWS * BK * 2;
+  static constexpr int TM = 256;                          // rows of a tile, half of them in each CTA
+  static constexpr int A_BYTES = 128 * BK * 2, B_ROWS = BN / 2, B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   // what leaves through shared memory: for each epilogue warp four pieces of 32 rows x 32
   // columns (parts, fp32: two)
-  static constexpr int PIECE = 32 * 64, OUT_BYTES = SWAP ? 0 : kEpiWarps * 4 * PIECE;
+  static constexpr int PIECE = 32 * 64, OUT_BYTES = kEpiWarps * 4 * PIECE;
   static constexpr int FIT = (226 * 1024 - OUT_BYTES) / STAGE, STAGES = FIT < 8 ? FIT : 8;
   static constexpr int OUT = STAGES * STAGE, CTRL = OUT + OUT_BYTES, SMEM = CTRL + 512;
-  static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;  // two accumulators
+  static constexpr int TMEM = 2 * BN;                     // two accumulators
   static_assert(SMEM > 114 * 1024, "one CTA per SM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(TMEM <= 512 && (TMEM & (TMEM - 1)) == 0, "TMEM");
@@ -220,25 +225,40 @@ struct alignas(8) Ctrl {
 };
 static_assert(sizeof(Ctrl) <= 512, "Ctrl");
 
-// A work unit: a tile and its part of k.
-struct Unit {
-  int32_t row_tile, col_tile, split, k0, k1;
-};
-__device__ __forceinline__ Unit unit_of(const GemmParams& p, int64_t u) {
-  Unit w;
-  const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.col_tiles;
-  w.split = static_cast<int32_t>(u / tiles);
-  const int64_t t = u - w.split * tiles;
-  // `group` row tiles at a time, their columns one after another: the CTAs that run
-  // together share rows and columns in L2
+// Row and column of tile t: `group` row tiles at a time, their columns one after another,
+// so that the CTAs that run together share rows and columns in L2.
+__device__ __forceinline__ int2 tile_of(const GemmParams& p, int64_t t) {
   const int64_t per = static_cast<int64_t>(p.group) * p.col_tiles;
   const int32_t g = static_cast<int32_t>(t / per);
   const int32_t rows = min(p.group, p.row_tiles - g * p.group);
   const int32_t in = static_cast<int32_t>(t - g * per);
-  w.col_tile = in / rows;
-  w.row_tile = g * p.group + in % rows;
-  w.k0 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * w.split / p.splits);
-  w.k1 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * (w.split + 1) / p.splits);
+  return make_int2(g * p.group + in % rows, in / rows);
+}
+// A work unit: a tile and its part of k.
+struct Unit {
+  int32_t row_tile, col_tile, cut, split, k0, k1;         // cut: the tile's number among the cut ones, or -1
+};
+__device__ __forceinline__ int64_t units_of(const GemmParams& p) {
+  return p.whole + (static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole) * p.splits;
+}
+__device__ __forceinline__ Unit unit_of(const GemmParams& p, int64_t u) {
+  Unit w;
+  int64_t t = u;
+  w.cut = -1;
+  w.split = 0;
+  w.k0 = 0;
+  w.k1 = p.k_steps;
+  if (u >= p.whole) {
+    const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole;
+    w.split = static_cast<int32_t>((u - p.whole) / rest);
+    w.cut = static_cast<int32_t>(u - p.whole - w.split * rest);
+    t = p.whole + w.cut;
+    w.k0 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * w.split / p.splits);
+    w.k1 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * (w.split + 1) / p.splits);
+  }
+  const int2 rc = tile_of(p, t);
+  w.row_tile = rc.x;
+  w.col_tile = rc.y;
   return w;
 }
 
@@ -294,14 +314,14 @@ struct Walk {
   }
 };
 
-template <int CG, int BN, bool A_MN, bool B_MN, bool SWAP>
+template <int BN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmParams p) {
-  using C = Cfg<CG, BN, SWAP>;
+  using C = Cfg<BN>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + C::CTRL);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const uint32_t rank = cluster_rank();
   volatile int32_t* abort_flag = &ctrl.abort_flag;
   if (threadIdx.x == 0) {
     if (base & 1023u) atomicOr(&g_err, DEV_ERR_INTERNAL);   // swizzled tiles need 1024-byte alignment
@@ -311,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctrl.acc_full[i]), 1);
-      mbar_init(smem_u32(&ctrl.acc_empty[i]), kEpiWarps * CG);
+      mbar_init(smem_u32(&ctrl.acc_empty[i]), kEpiWarps * 2);
     }
     mbar_init(smem_u32(&ctrl.final_bar), 1);
     for (int i = 0; i < 4 * kEpiWarps; ++i) mbar_init(smem_u32(&ctrl.res_full[0][0] + i), 1);
@@ -319,24 +339,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     fence_mbar_init();
   }
   if (warp == 1) {
-    if constexpr (CG == 2) {
-      tmem_alloc_pair(smem_u32(&ctrl.tmem_base), C::TMEM);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(&ctrl.tmem_base), C::TMEM);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(smem_u32(&ctrl.tmem_base), C::TMEM);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
   // what comes before may still run while this CTA sets itself up
   grid_wait();
   grid_launch_dependents();
-  const int64_t units = static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits;
-  const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int64_t units = units_of(p), first = blockIdx.x / 2, stride = gridDim.x / 2;
 
   if (warp == 0) {
     // The whole warp runs the loop and one lane acts, so that the copies' addresses and
@@ -348,29 +362,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       tma_prefetch_desc(&p.ta);
       tma_prefetch_desc(&p.tb);
     }
-    constexpr bool TOK_K = A_MN && !SWAP;                 // k runs over tokens of the batches
     int64_t issued = 0;                                   // steps
     int st = 0;
     uint32_t parity = 1u;                                 // of the wait for an empty stage
     bool ok = true;
     for (int64_t u = first; ok && u < units; u += stride) {
       const Unit w = unit_of(p, u);
-      // the token axis: rows of A (SWAP: rows of B), tiles of each batch by themselves
-      const int32_t tok_tile = SWAP ? w.col_tile : w.row_tile;
-      const int32_t tb = TOK_K ? 0 : tok_tile / p.tiles_per_batch;
-      const int32_t tn = (tok_tile - tb * p.tiles_per_batch) * (SWAP ? BN : C::TM);
-      const int32_t row0 = (TOK_K ? w.row_tile * C::TM : SWAP ? w.row_tile * 128 : tn) + rank * 128;
-      const int32_t col0 = (SWAP ? tn : w.col_tile * BN) + rank * C::B_ROWS;
-      Walk<A_MN, 2> ca(p.a_dim, row0, w.k0, TOK_K ? p.k_steps_per_batch : 0, SWAP ? 0 : tb);
-      Walk<B_MN, (C::B_ROWS + 63) / 64> cb(p.b_dim, col0, w.k0, TOK_K ? p.k_steps_per_batch : 0, SWAP ? tb : 0);
+      // token rows: tiles of each batch by themselves (dweight: rows are features, k tokens)
+      const int32_t b = A_MN ? 0 : w.row_tile / p.tiles_per_batch;
+      const int32_t row0 = (w.row_tile - b * p.tiles_per_batch) * C::TM + rank * 128;
+      const int32_t col0 = w.col_tile * BN + rank * C::B_ROWS;
+      Walk<A_MN, 2> ca(p.a_dim, row0, w.k0, A_MN ? p.k_steps_per_batch : 0, b);
+      Walk<B_MN, C::B_ROWS / 64> cb(p.b_dim, col0, w.k0, A_MN ? p.k_steps_per_batch : 0, 0);
       for (int32_t s = w.k0; s < w.k1; ++s) {
         if (!mbar_wait_warp(smem_u32(&ctrl.empty[st]), parity, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
-        const uint32_t a = base + st * C::STAGE, b = a + C::A_BYTES;
-        uint32_t bar = smem_u32(&ctrl.full[st]);
-        if (rank == 0) mbar_arrive_expect_tx(elect, bar, CG * C::STAGE);
-        if constexpr (CG == 2) bar = cluster_addr(bar, 0);
-        ca.template load<CG>(elect, a, &p.ta, bar);
-        cb.template load<CG>(elect, b, &p.tb, bar);
+        const uint32_t a = base + st * C::STAGE;
+        if (rank == 0) mbar_arrive_expect_tx(elect, smem_u32(&ctrl.full[st]), 2 * C::STAGE);
+        const uint32_t bar = cluster_addr(smem_u32(&ctrl.full[st]), 0);
+        ca.template load<2>(elect, a, &p.ta, bar);
+        cb.template load<2>(elect, a + C::A_BYTES, &p.tb, bar);
         ca.advance();
         cb.advance();
         ++issued;
@@ -409,24 +419,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             const uint64_t da = A_MN ? sdesc_sw128(a + k * 2048, 64 * 128, 1024) : sdesc_sw128(a + k * 32, 16, 1024);
             const uint64_t db = B_MN ? sdesc_sw128(b + k * 2048, 64 * 128, 1024) : sdesc_sw128(b + k * 32, 16, 1024);
             const uint32_t more = s > w.k0 || k > 0;
-            if constexpr (CG == 2) mma_f16_ss_pair(elect, acc, da, db, p.idesc, more);
-            else mma_bf16_ss(elect, acc, da, db, p.idesc, more);
+            mma_f16_ss_pair(elect, acc, da, db, p.idesc, more);
           }
-          if constexpr (CG == 2) mma_commit_pair(elect, smem_u32(&ctrl.empty[st]));
-          else mma_commit(elect, smem_u32(&ctrl.empty[st]));
+          mma_commit_pair(elect, smem_u32(&ctrl.empty[st]));
           if (++st == C::STAGES) {
             st = 0;
             parity ^= 1u;
           }
         }
         if (!ok) break;
-        if constexpr (CG == 2) mma_commit_pair(elect, smem_u32(&ctrl.acc_full[buf]));
-        else mma_commit(elect, smem_u32(&ctrl.acc_full[buf]));
+        mma_commit_pair(elect, smem_u32(&ctrl.acc_full[buf]));
       }
       if (*abort_flag) {
         // the products in flight end before TMEM is freed
-        if constexpr (CG == 2) mma_commit_pair(elect, smem_u32(&ctrl.final_bar));
-        else mma_commit(elect, smem_u32(&ctrl.final_bar));
+        mma_commit_pair(elect, smem_u32(&ctrl.final_bar));
         volatile int32_t no = 0;
         mbar_wait_warp(smem_u32(&ctrl.final_bar), 0, &no, &g_err, p.timeout_ns);
       }
@@ -442,35 +448,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       const Unit w = unit_of(p, u);
       const int buf = tile & 1;
       const uint32_t acc = tmem + lanes + buf * BN;
-      if (SWAP || p.part) {
+      if (w.cut >= 0) {
         if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
         tc_fence_after();
       }
-      if constexpr (SWAP) {
-        // rows are features, columns tokens: the warp stores 32 neighbouring features of a token
-        const int32_t f = w.row_tile * 128 + quarter * 32 + lane;
-        const int32_t b = w.col_tile / p.tiles_per_batch, n0 = (w.col_tile - b * p.tiles_per_batch) * BN;
-        float* dst = p.part + (static_cast<int64_t>(w.split) * p.batches + b) * p.n_rows * p.cols + f;
-#pragma unroll 1
-        for (int c = half * 16; c < BN; c += 32) {
-          if (n0 + c >= p.n_rows) break;
-          uint32_t v[16];
-          tmem_ld16(acc + c, v);
-          tc_wait_ld();
-          if (f < p.cols) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (n0 + c + i < p.n_rows) dst[static_cast<int64_t>(n0 + c + i) * p.cols] = __uint_as_float(v[i]);
-          }
-        }
-      } else {
+      {
         const int32_t b = A_MN ? 0 : w.row_tile / p.tiles_per_batch;
         const int32_t n0 = (w.row_tile - b * p.tiles_per_batch) * C::TM + rank * 128 + quarter * 32;
         constexpr int W = BN / 2;                                   // columns of this warp
         const int32_t f0 = w.col_tile * BN + half * W;
         const bool inside = n0 < p.n_rows;
         const uint32_t pieces = base + C::OUT + ew * 4 * C::PIECE;
-        if (p.part) {
+        if (w.cut >= 0) {
 #pragma unroll 1
           for (int c = 0; c < W; c += 32) {
             if (f0 + c >= p.cols || !inside) break;
@@ -486,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
               sts128(q + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
             fence_proxy_async_smem();
             __syncwarp();
-            tma_store_4d(elect, &p.tout, q, f0 + c, n0, b, w.split);
+            tma_store_4d(elect, &p.tpart, q, half * W + c, rank * 128 + quarter * 32, w.cut, w.split);
             bulk_commit(elect);
           }
         } else {
@@ -590,8 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) {
         const uint32_t bar = smem_u32(&ctrl.acc_empty[buf]);
-        if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(bar, 0));
-        else mbar_arrive(bar);
+        mbar_arrive_cluster(cluster_addr(bar, 0));
       }
     }
     bulk_wait_read<0>();                   // shared memory has been read before the CTA ends
@@ -604,11 +592,155 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (CG == 2) tmem_dealloc_pair(tmem, C::TMEM);
-    else tmem_dealloc(tmem, C::TMEM);
+    tmem_dealloc_pair(tmem, C::TMEM);
+  }
+}
+
+// ---------------------------------------------------------------- few tokens
+template <int BN>
+struct FewCfg {
+  static constexpr int A_BYTES = 128 * BK * 2, STAGE = A_BYTES + BN * BK * 2;
+  static constexpr int RED = BN * 128 * 4;                // the tile's sums, [token][feature]
+  static constexpr int FIT = (226 * 1024 - RED) / STAGE, STAGES = FIT < 8 ? FIT : 8;
+  static constexpr int SUMS = STAGES * STAGE, CTRL = SUMS + RED, SMEM = CTRL + 512;
+  static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one CTA per SM");
+};
+
+// D^T: 128 features on the rows, BN tokens on the columns; the cluster's CTAs take p.splits
+// parts of k.  W_MN: the weight's rows are k (dx).
+template <int BN, bool W_MN>
+__global__ void __launch_bounds__(kThreads, 1) linear_few_kernel(const __grid_constant__ GemmParams p) {
+  using C = FewCfg<BN>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  Ctrl& ctrl = *reinterpret_cast<Ctrl*>(smem + C::CTRL);
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int32_t rank = static_cast<int32_t>(cluster_rank());
+  volatile int32_t* abort_flag = &ctrl.abort_flag;
+  if (threadIdx.x == 0) {
+    if (base & 1023u) atomicOr(&g_err, DEV_ERR_INTERNAL);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(smem_u32(&ctrl.full[i]), 1);
+      mbar_init(smem_u32(&ctrl.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctrl.acc_full[0]), 1);
+    mbar_init(smem_u32(&ctrl.final_bar), 1);
+    ctrl.abort_flag = (base & 1023u) ? 1 : 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctrl.tmem_base), BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
+  grid_wait();
+  grid_launch_dependents();
+  const int32_t tile = static_cast<int32_t>(blockIdx.x) / p.splits;
+  const int32_t f_tile = tile % p.row_tiles, t_tile = tile / p.row_tiles;
+  const int32_t b = t_tile / p.tiles_per_batch, n0 = (t_tile - b * p.tiles_per_batch) * BN;
+  const int32_t k0 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * rank / p.splits);
+  const int32_t k1 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.splits);
+  if (warp == 0) {
+    const uint32_t elect = elect_lane();
+    Walk<W_MN, 2> ca(p.a_dim, f_tile * 128, k0, 0, 0);
+    Walk<false, 1> cb(p.b_dim, n0, k0, 0, b);
+    int st = 0;
+    uint32_t parity = 1u;
+    int32_t issued = 0;
+    for (int32_t s = k0; s < k1; ++s) {
+      if (!mbar_wait_warp(smem_u32(&ctrl.empty[st]), parity, abort_flag, &g_err, p.timeout_ns)) break;
+      const uint32_t a = base + st * C::STAGE, bar = smem_u32(&ctrl.full[st]);
+      mbar_arrive_expect_tx(elect, bar, C::STAGE);
+      ca.template load<1>(elect, a, &p.ta, bar);
+      cb.template load<1>(elect, a + C::A_BYTES, &p.tb, bar);
+      ca.advance();
+      cb.advance();
+      ++issued;
+      if (++st == C::STAGES) {
+        st = 0;
+        parity ^= 1u;
+      }
+    }
+    // every copy has landed before the CTA ends; normally they all have been waited for
+    volatile int32_t no = 0;
+    for (int32_t k = max(0, issued - C::STAGES); k < issued; ++k)
+      mbar_wait_warp(smem_u32(&ctrl.full[k % C::STAGES]), static_cast<uint32_t>(k / C::STAGES) & 1u, &no, &g_err,
+                     p.timeout_ns);
+  } else if (warp == 1) {
+    const uint32_t elect = elect_lane();
+    int st = 0;
+    uint32_t parity = 0u;
+    bool ok = true;
+    for (int32_t s = k0; s < k1; ++s) {
+      if (!mbar_wait_warp(smem_u32(&ctrl.full[st]), parity, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t a = base + st * C::STAGE, t = a + C::A_BYTES;
+#pragma unroll
+      for (int k = 0; k < BK / 16; ++k) {
+        const uint64_t da = W_MN ? sdesc_sw128(a + k * 2048, 64 * 128, 1024) : sdesc_sw128(a + k * 32, 16, 1024);
+        mma_bf16_ss(elect, tmem, da, sdesc_sw128(t + k * 32, 16, 1024), p.idesc, s > k0 || k > 0);
+      }
+      mma_commit(elect, smem_u32(&ctrl.empty[st]));
+      if (++st == C::STAGES) {
+        st = 0;
+        parity ^= 1u;
+      }
+    }
+    if (ok) mma_commit(elect, smem_u32(&ctrl.acc_full[0]));
+    mma_commit(elect, smem_u32(&ctrl.final_bar));
+    // the products in flight end before TMEM is freed
+    volatile int32_t no = 0;
+    mbar_wait_warp(smem_u32(&ctrl.final_bar), 0, &no, &g_err, p.timeout_ns);
+  } else {
+    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
+    if (mbar_wait_warp(smem_u32(&ctrl.acc_full[0]), 0, abort_flag, &g_err, p.timeout_ns)) {
+      tc_fence_after();
+      float* sums = reinterpret_cast<float*>(smem + C::SUMS) + quarter * 32 + lane;
+#pragma unroll 1
+      for (int c = half * 16; c < BN; c += 32) {
+        if (n0 + c >= p.n_rows) break;
+        uint32_t v[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[(c + i) * 128] = __uint_as_float(v[i]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                          // all CTAs' sums lie in their shared memory
+  // token rank, rank + splits, ... of the tile, 8 features a thread
+  const int32_t tokens = min(BN, p.n_rows - n0);
+  for (int32_t i = threadIdx.x; i < (tokens - rank + p.splits - 1) / p.splits * 16; i += kThreads) {
+    const int32_t t = rank + i / 16 * p.splits, f = f_tile * 128 + i % 16 * 8;
+    if (f >= p.cols) continue;
+    const uint32_t src = base + C::SUMS + (t * 128 + i % 16 * 8) * 4;
+    float v[8] = {};
+    for (int32_t s = 0; s < p.splits; ++s) {
+      const uint32_t at = cluster_addr(src, static_cast<uint32_t>(s));
+      const float4 x = ld_cluster(at), y = ld_cluster(at + 16);
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
+      v[3] += x.w;
+      v[4] += y.x;
+      v[5] += y.y;
+      v[6] += y.z;
+      v[7] += y.w;
+    }
+    by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(p.epi, v, b, n0 + t, f); });
+  }
+  cluster_sync();                          // nobody leaves while its sums are read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, BN);
   }
 }
 

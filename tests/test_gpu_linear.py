@@ -111,10 +111,14 @@ def check_backward(grads, dout, x, w, activation=None, pre=None, norm=True):
             assert (rows(got[None] if got.dim() == 1 else got) - want).norm() <= U[dtype] * want.norm()
 
 
-# tokens, in features, out features: each kind of tile, whole and split products
+# batches, tokens, in features, out features: each kind of tile, in all three products, whole,
+# cut along k, and both in one launch
 SIZES = [(1, 1, 8, 8), (1, 2, 256, 2048), (1, 5, 1160, 264), (2, 33, 200, 1544), (1, 130, 72, 64),
          (1, 200, 1160, 1544), (2, 350, 264, 1544), (3, 257, 1160, 8), (1, 5001, 1160, 1544), (1, 3000, 136, 72),
-         (2, 333, 4096, 2048), (1, 4096, 512, 512), (3, 129, 64, 320), (5, 1, 512, 512)]
+         (2, 333, 4096, 2048), (1, 4096, 512, 512), (3, 129, 64, 320), (5, 1, 512, 512),
+         (1, 130, 1120, 3944), (1, 72, 1352, 3560), (1, 355, 3392, 264), (2, 1, 3192, 32), (1, 1283, 2264, 1576),
+         (1, 2593, 1176, 1712), (1, 2674, 3456, 520), (1, 6588, 3360, 8), (2, 657, 2744, 1592), (1, 329, 264, 3432),
+         (1, 65, 3744, 1392), (1, 517, 3224, 2536), (3, 526, 2704, 1320), (1, 1, 16, 2336)]
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
