@@ -678,7 +678,7 @@ def tsr_norm_rope(x, weight, axis_dims, *, eps: float = 1e-6, grid=None,
     if out is None:
         _on_device(*xs, *ws, positions)
         with _allocating_on(stream):
-            outs = [t.new_empty(shape) for t, shape, _ in rows]
+            outs = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in xs]
     else:
         outs = _heads_list(out)
         if len(outs) != len(xs):
@@ -722,7 +722,7 @@ def tsr_norm_rope_backward(dout, x, weight, axis_dims, *, eps: float = 1e-6, gri
     L = lib()
     with _allocating_on(stream):
         if outs is None:
-            outs = [t.new_empty(shape) for t, shape, _ in rows]
+            outs = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in xs]
         if dws is None:
             dws = [None if w is None else torch.empty_like(w) for w in ws]
         if workspace is None:
@@ -832,9 +832,9 @@ def tsr_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     L = lib()
     with _allocating_on(stream):
         if out is None:
-            out = x.new_empty(shape)
+            out = torch.empty(shape, dtype=dtype, device=x.device)
         if keep and given is None:
-            given = x.new_empty(shape)
+            given = torch.empty(shape, dtype=dtype, device=x.device)
         workspace, size = _workspace(L.tsr_linear_workspace, 0, desc, workspace, x.device)
     none = (0, 0, 0)
     args = _LINEAR_ARGS.pack(x.data_ptr(), _dptr(weight), _dptr(bias), 0 if residual is None else residual.data_ptr(),
@@ -869,7 +869,8 @@ def tsr_linear_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     _on_device(dout, x, weight, pre, dx, dweight, dbias, workspace)
     L = lib()
     with _allocating_on(stream):
-        new = lambda t, shape, wanted: None if not wanted else t if t is not None else x.new_empty(shape)
+        new = lambda t, shape, wanted: None if not wanted else t if t is not None else torch.empty(
+            shape, dtype=dtype, device=x.device)
         dx, dweight, dbias = new(dx, x.shape, need[0]), new(dweight, weight.shape, need[1]), new(dbias, (M,), need[2])
         workspace, size = _workspace(L.tsr_linear_backward_workspace, 1, desc, workspace, x.device)
     none = (0, 0, 0)

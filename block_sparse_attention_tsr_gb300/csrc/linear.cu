@@ -60,7 +60,7 @@ struct DzParams {
 };
 
 // 32 lanes of 8 columns, 8 rows at a time.
-__global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ DzParams p) {
+__global__ void __launch_bounds__(256, 4) linear_dz_kernel(const __grid_constant__ DzParams p) {
   __shared__ float red[8][32][8];
   const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int32_t f = (blockIdx.x * 32 + lane) * 8;
@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
   float sum[8] = {};
   if (f < p.cols)
     by_kind(p.f16, p.act, [&](auto f16, auto act) {
-#pragma unroll 4
+      constexpr int kRows = act.value == TSR_ACT_NONE ? 8 : 4;      // in flight
+#pragma unroll kRows
       for (int64_t r = r0 + ty; r < r1; r += 8) {
         int64_t b = 0, n = r;
         if (p.n_rows < p.rows) {
@@ -231,6 +232,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // A 4-D tensor map, 128-byte swizzle; strides in elements, of dimensions 1 to 3.
 tsr_status encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int size, const int64_t (&dims)[4],
                   const int64_t (&strides)[3], int box0, int box1) {
+  // no promotion of misses to longer L2 fetches: it cost up to 6% where rows are not lines
   // the box's row of 128 or 64 bytes is the swizzle's
   if (!encoder()) return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled is missing");
   cuuint64_t d[4], s[3];
@@ -239,7 +241,7 @@ tsr_status encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int s
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1, 1}, es[4] = {1, 1, 1, 1};
   if (encoder()(m, type, 4, const_cast<void*>(p), d, s, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 box0 * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return fail(TSR_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   return TSR_OK;
@@ -364,8 +366,9 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   return launch_kind<true, true>(c.variant, p, st);
 }
 
-// Blocks of rows of the pass over dz.
-int64_t dz_blocks(int64_t T, int64_t M) { return std::max<int64_t>(1, std::min(cdiv(T, 32), kSms * 8 / cdiv(M, 256) + 1)); }
+// Blocks of rows of the pass over dz: one wave of the four CTAs that an SM holds (twice as
+// many and one more took 253 us for 233 of 32,760 x 8,192).
+int64_t dz_blocks(int64_t T, int64_t M) { return std::max<int64_t>(1, std::min(cdiv(T, 32), kSms * 4 / cdiv(M, 256))); }
 
 struct BackwardSpace {
   size_t dz, sums, parts, total;

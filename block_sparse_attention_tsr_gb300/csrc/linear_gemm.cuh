@@ -113,42 +113,59 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-constexpr float kGelu0 = 0.7978845608028654f, kGelu1 = 0.044715f;   // sqrt(2 / pi)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGelu0 = 2.f * 0.7978845608028654f, kGelu1 = kGelu0 * 0.044715f;   // 2 sqrt(2 / pi)
 
-// 1 / (1 + e^-x).  The exponential is within about |x| 2^-23 of its value, the reciprocal
+// 1 / (1 + 2^-x).  The exponential is within about |x| 2^-23 of its value, the reciprocal
 // within 2^-23: far inside a 16-bit rounding.
-__device__ __forceinline__ float logistic(float x) {
+__device__ __forceinline__ float logistic2(float x) {
   float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ex2_approx(-1.4426950408889634f * x)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ex2_approx(-x)));
   return y;
 }
-// The tanh form is z times the logistic function of 2u, u = kGelu0 (z + kGelu1 z^3): no
-// cancellation for negative z.
+// The normal distribution function Phi(z) = erfc(-z / sqrt 2) / 2: with x = |z| / sqrt 2 and
+// t = 1 / (1 + x / 2), erfc(x) = t 2^(G(t) - x^2 log2 e), G a least-squares polynomial of
+// log2(erfc(x) e^(x^2) / t) at Chebyshev points of t in [0.2, 1].  Within 3e-6 of itself for
+// z > -5, 1.3e-5 for z > -11: no cancellation for negative z.
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float x = 0.70710678118654752f * fabsf(z);
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, x, 1.f)));
+  float g = -0.26132926f;
+  g = fmaf(g, t, 1.04207718f);
+  g = fmaf(g, t, -1.36707688f);
+  g = fmaf(g, t, 0.429223797f);
+  g = fmaf(g, t, -0.0146213521f);
+  g = fmaf(g, t, 0.554580669f);
+  g = fmaf(g, t, 1.44300415f);
+  g = fmaf(g, t, -1.8258592f);
+  const float tail = 0.5f * t * ex2_approx(fmaf(-kLog2e * x, x, g));
+  return z < 0.f ? tail : 1.f - tail;
+}
+// The tanh form is z times the logistic function of 2u, u = sqrt(2 / pi) (z + 0.044715
+// z^3): no cancellation there either.
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
-  if constexpr (ACT == TSR_ACT_GELU_TANH) return z * logistic(z * fmaf(2.f * kGelu0 * kGelu1, z * z, 2.f * kGelu0));
-  if constexpr (ACT == TSR_ACT_SILU) return z * logistic(z);
-  if constexpr (ACT == TSR_ACT_GELU) return z * normcdff(z);
+  if constexpr (ACT == TSR_ACT_GELU_TANH) return z * logistic2(z * fmaf(kLog2e * kGelu1, z * z, kLog2e * kGelu0));
+  if constexpr (ACT == TSR_ACT_SILU) return z * logistic2(kLog2e * z);
+  if constexpr (ACT == TSR_ACT_GELU) return z * normal_cdf(z);
   return z;
 }
-// The activation's derivative.  It is 0 or 1 in fp32 past |z| = 30 (SiLU: 80); z is taken
-// there so that no 0 * inf arises.
+// The activation's derivative.  Far out the logistic function is 0 or 1 in fp32 and s (1 - s)
+// exactly 0, and so is its product with any finite z (z^2 is cut off where it no longer
+// matters); at an infinite z the derivative is NaN, as the formula's inf * 0.
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
-  if constexpr (ACT == TSR_ACT_NONE) return 1.f;
-  const float most = ACT == TSR_ACT_SILU ? 80.f : 30.f;
-  const float x = fminf(fmaxf(z, -most), most);
-  float y;
   if constexpr (ACT == TSR_ACT_SILU) {
-    const float s = logistic(x);
-    y = s * fmaf(x, 1.f - s, 1.f);
+    const float s = logistic2(kLog2e * z);
+    return s * fmaf(z, 1.f - s, 1.f);
   } else if constexpr (ACT == TSR_ACT_GELU_TANH) {
-    const float s = logistic(x * fmaf(2.f * kGelu0 * kGelu1, x * x, 2.f * kGelu0));
-    y = fmaf(x * s * (1.f - s), fmaf(6.f * kGelu0 * kGelu1, x * x, 2.f * kGelu0), s);
-  } else {
-    y = fmaf(x * 0.3989422804014327f, ex2_approx(-0.5f * 1.4426950408889634f * x * x), normcdff(x));
+    const float q = fminf(z * z, 900.f), s = logistic2(z * fmaf(kLog2e * kGelu1, q, kLog2e * kGelu0));
+    return fmaf(z * (s * (1.f - s)), fmaf(3.f * kGelu1, q, kGelu0), s);
+  } else if constexpr (ACT == TSR_ACT_GELU) {
+    return fmaf(z * 0.3989422804014327f, ex2_approx(-0.5f * kLog2e * z * z), normal_cdf(z));
   }
-  return z != z ? z : y;
+  return 1.f;
 }
 // f<F16, ACT>() for the call's type and activation: the elements' code has no branches on them.
 template <typename F>
@@ -338,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 2) tma_prefetch_desc(lane ? &p.tb : &p.ta);
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&ctrl.tmem_base), C::TMEM);
     tmem_relinquish_pair();
@@ -358,10 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     // step's copies were issued in 360 ns by a single lane that divided for them, while
     // the products of a step take 225.
     const uint32_t elect = elect_lane();
-    if (elect) {
-      tma_prefetch_desc(&p.ta);
-      tma_prefetch_desc(&p.tb);
-    }
     int64_t issued = 0;                                   // steps
     int st = 0;
     uint32_t parity = 1u;                                 // of the wait for an empty stage
@@ -500,17 +514,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
           if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
           tc_fence_after();
           bool ok = true;
-          uint32_t v[32];
-          if (steps > 0) tmem_ld32(acc + half * W, v);
+          // two steps at a time share a fence and the waits (one where pre takes a piece too)
+          uint32_t v[2][32];
+          auto columns = [&](int s) {
+            if (s < steps) tmem_ld32(acc + half * W + s * 32, v[0]);
+            if (!pre && s + 1 < steps) tmem_ld32(acc + half * W + (s + 1) * 32, v[1]);
+          };
+          columns(0);
           int32_t h = f0 / dim, ch = f0 - h * dim;
 #pragma unroll 1
-          for (int s = 0; s < steps; ++s) {
-            const int32_t f = f0 + s * 32;
-            uint4 bias[4] = {};
+          for (int s = 0; s < steps;) {
+            const int n = pre ? 1 : min(2, steps - s);
+            uint4 bias[2][4] = {};
             if (p.epi.bias) {
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
-                if (f + g * 8 < p.cols) bias[g] = static_cast<const uint4*>(p.epi.bias)[f / 8 + g];
+              for (int g = 0; g < 8; ++g) {
+                const int32_t f = f0 + s * 32 + g * 8;
+                if (f < p.cols && g < 4 * n) bias[g >> 2][g & 3] = static_cast<const uint4*>(p.epi.bias)[f / 8];
+              }
             }
             if (res) {
               if (pre && s >= 2) {
@@ -518,55 +539,64 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                 __syncwarp();
                 load_res(s);
               }
-              const uint32_t k = piece(s, per - 1);
-              ok = mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, abort_flag, &g_err, p.timeout_ns);
+              for (int j = 0; ok && j < n; ++j) {
+                const uint32_t k = piece(s + j, per - 1);
+                ok = mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, abort_flag, &g_err, p.timeout_ns);
+                if (!ok) break;
+                res_phase ^= 1u << k;
+                res_issued &= ~(1u << k);
+              }
               if (!ok) break;
-              res_phase ^= 1u << k;
-              res_issued &= ~(1u << k);
             } else {
-              // the ring's pieces of four stores (with pre two steps) ago have left
-              if (pre) bulk_wait_read<2>();
-              else bulk_wait_read<3>();
+              bulk_wait_read<1>();                                  // all but the last iteration's pieces have left
               __syncwarp();
             }
             tc_wait_ld();
             // a lane's row of 64 bytes, 16 each, swizzled as TMA reads it
             const uint32_t row = lane * 64, turned = (lane >> 1) & 3;
-            const uint32_t q_pre = pieces + piece(s, 0) * C::PIECE, q = pieces + piece(s, per - 1) * C::PIECE;
             by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) {
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                float x[8], t[8];
-                const uint32_t o = row + ((g ^ turned) << 4);
-                unpack8<f16.value>(bias[g], t);
+              for (int j = 0; j < 2; ++j) {
+                if (j < n) {
+                  const uint32_t q_pre = pieces + piece(s + j, 0) * C::PIECE + row;
+                  const uint32_t q = pieces + piece(s + j, per - 1) * C::PIECE + row;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * g + i]) + t[i];
-                if (pre) sts128(q_pre + o, pack8<f16.value>(x));
+                  for (int g = 0; g < 4; ++g) {
+                    float x[8], t[8];
+                    const uint32_t o = (g ^ turned) << 4;
+                    unpack8<f16.value>(bias[j][g], t);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = activate<act.value>(x[i]);
-                if (res) {
-                  unpack8<f16.value>(lds128(q + o), t);
+                    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[j][8 * g + i]) + t[i];
+                    if (pre) sts128(q_pre + o, pack8<f16.value>(x));
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) x[i] += t[i];
+                    for (int i = 0; i < 8; ++i) x[i] = activate<act.value>(x[i]);
+                    if (res) {
+                      unpack8<f16.value>(lds128(q + o), t);
+#pragma unroll
+                      for (int i = 0; i < 8; ++i) x[i] += t[i];
+                    }
+                    sts128(q + o, pack8<f16.value>(x));
+                  }
                 }
-                sts128(q + o, pack8<f16.value>(x));
               }
             });
-            // the next step's columns are on their way while this one's leave
-            if (s + 1 < steps) tmem_ld32(acc + half * W + (s + 1) * 32, v);
+            columns(s + n);                                         // on their way while these leave
             fence_proxy_async_smem();
             __syncwarp();
-            if (pre) {
-              tma_store_4d(elect, &p.tpre, q_pre, ch, n0, h, b);
-              bulk_commit(elect);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (j < n) {
+                if (pre) tma_store_4d(elect, &p.tpre, pieces + piece(s + j, 0) * C::PIECE, ch, n0, h, b);
+                tma_store_4d(elect, &p.tout, pieces + piece(s + j, per - 1) * C::PIECE, ch, n0, h, b);
+                ch += 32;
+                if (ch >= dim) {
+                  ch = 0;
+                  ++h;
+                }
+              }
             }
-            tma_store_4d(elect, &p.tout, q, ch, n0, h, b);
             bulk_commit(elect);
-            ch += 32;
-            if (ch >= dim) {
-              ch = 0;
-              ++h;
-            }
+            s += n;
           }
           if (!ok) {
             tc_wait_ld();
@@ -631,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_few_kernel(const __grid_co
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 2) tma_prefetch_desc(lane ? &p.tb : &p.ta);
   if (warp == 1) {
     tmem_alloc(smem_u32(&ctrl.tmem_base), BN);
     tmem_relinquish();
