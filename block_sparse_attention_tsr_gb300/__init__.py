@@ -156,8 +156,8 @@ EXPORTS = ("tsr_abi_version", "tsr_status_string", "tsr_last_error", "tsr_plan",
            "tsr_bsa_forward", "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_plan_destroy", "tsr_plan_get_stats",
            "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope", "tsr_norm_rope",
            "tsr_norm_rope_backward_workspace", "tsr_norm_rope_backward", "tsr_linear_workspace", "tsr_linear",
-           "tsr_linear_backward_workspace", "tsr_linear_backward", "tsr_linear_device_status",
-           "tsr_block_select_workspace", "tsr_block_select", "tsr_backward_plan",
+           "tsr_linear_backward_workspace", "tsr_linear_backward", "tsr_linear_device_status", "tsr_linear_test_stall",
+           "tsr_linear_test_stall", "tsr_block_select_workspace", "tsr_block_select", "tsr_backward_plan",
            "tsr_backward_plan_update", "tsr_backward_plan_destroy", "tsr_backward_plan_device_status",
            "tsr_backward_plan_test_stall",
            "tsr_bsa_backward_workspace", "tsr_bsa_backward", "tsr_attention_host",
@@ -206,6 +206,7 @@ def lib():
         "tsr_linear_backward_workspace": ([P, P], ctypes.c_int),
         "tsr_linear_backward": ([P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "tsr_linear_device_status": ([P], ctypes.c_int),
+        "tsr_linear_test_stall": ([I32], ctypes.c_int),
         "tsr_block_select_workspace": ([P, P], ctypes.c_int),
         "tsr_block_select": ([P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "tsr_backward_plan": ([P, P, P], ctypes.c_int),

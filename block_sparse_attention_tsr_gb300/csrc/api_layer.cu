@@ -193,6 +193,13 @@ tsr_status tsr_linear_backward(const tsr_linear_desc* desc, const tsr_linear_gra
   return launch_linear_backward(d, *a, workspace, static_cast<cudaStream_t>(stream));
 }
 
+tsr_status tsr_linear_test_stall(int32_t on) {
+  set_error("");
+  if (on != 0 && on != 1) return fail(TSR_ERR_INVALID_ARG, "on must be 0 or 1");
+  linear_test_stall(on);
+  return TSR_OK;
+}
+
 tsr_status tsr_linear_device_status(void* stream) {
   set_error("");
   return linear_device_status(static_cast<cudaStream_t>(stream));

@@ -210,6 +210,7 @@ size_t linear_backward_workspace(const tsr_linear_desc& d);
 tsr_status launch_linear(const tsr_linear_desc& d, const tsr_linear_args& a, void* ws, cudaStream_t st);
 tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_grads& a, void* ws, cudaStream_t st);
 tsr_status linear_device_status(cudaStream_t st);
+void linear_test_stall(int32_t on);
 
 // block selection (select.cu)
 size_t select_workspace(const tsr_select_desc& s);

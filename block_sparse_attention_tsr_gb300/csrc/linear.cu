@@ -19,7 +19,8 @@ namespace linear {
 namespace {
 
 constexpr int kSms = 152;              // what the choice of tiles is made for
-constexpr uint64_t kTimeoutNs = kWaitTimeoutNs;
+constexpr uint64_t kStallNs = 20000000;    // bound of the waits of a stalled product (test only)
+thread_local int32_t g_stall = 0;
 
 // D's values of the tiles that were cut along k, from their parts.  HBM/L2-bound.
 template <int BN>
@@ -330,7 +331,8 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   p.k_steps = static_cast<int32_t>(q.k_steps);
   p.k_steps_per_batch = static_cast<int32_t>(cdiv(y.N, BK));
   p.group = 8;
-  p.timeout_ns = kTimeoutNs;
+  p.stall = g_stall;
+  p.timeout_ns = g_stall ? kStallNs : kWaitTimeoutNs;
   const int bn = c.variant == PAIR_256 ? 256 : c.variant == FEW_32 ? 32 : 128;
   p.tiles_per_batch = static_cast<int32_t>(cdiv(q.n_rows, few ? bn : 256));
   p.row_tiles = p.tiles_per_batch * p.batches;
@@ -478,6 +480,8 @@ tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_gra
   }
   return TSR_OK;
 }
+
+void linear_test_stall(int32_t on) { g_stall = on; }
 
 tsr_status linear_device_status(cudaStream_t st) {
   uint32_t word = 0;

@@ -76,7 +76,8 @@ struct GemmParams {
   int32_t a_dim, b_dim;                // channels per head of A's and B's tensors
   int32_t group;                       // row tiles that share their columns' loads in L2
   uint32_t idesc;
-  uint64_t timeout_ns;
+  int32_t stall;                       // test only: the issuer waits for ever after its first step
+  uint64_t timeout_ns;                 // bound of every wait
 };
 
 // Waits that gave up (tsr_linear_device_status): of the device, not of a call.
@@ -236,6 +237,7 @@ struct Cfg {
 
 struct alignas(8) Ctrl {
   uint64_t full[8], empty[8], acc_full[2], acc_empty[2], final_bar;
+  uint64_t never;                      // never signalled (stall test)
   uint64_t res_full[kEpiWarps][4];     // the residual's piece has landed
   uint32_t tmem_base;
   int32_t abort_flag;
@@ -351,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       mbar_init(smem_u32(&ctrl.acc_empty[i]), kEpiWarps * 2);
     }
     mbar_init(smem_u32(&ctrl.final_bar), 1);
+    mbar_init(smem_u32(&ctrl.never), 1);
     for (int i = 0; i < 4 * kEpiWarps; ++i) mbar_init(smem_u32(&ctrl.res_full[0][0] + i), 1);
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
     fence_mbar_init();
@@ -436,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             mma_f16_ss_pair(elect, acc, da, db, p.idesc, more);
           }
           mma_commit_pair(elect, smem_u32(&ctrl.empty[st]));
+          if (p.stall && !mbar_wait_warp(smem_u32(&ctrl.never), 0, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
           if (++st == C::STAGES) {
             st = 0;
             parity ^= 1u;
@@ -658,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_few_kernel(const __grid_co
     }
     mbar_init(smem_u32(&ctrl.acc_full[0]), 1);
     mbar_init(smem_u32(&ctrl.final_bar), 1);
+    mbar_init(smem_u32(&ctrl.never), 1);
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
     fence_mbar_init();
   }
@@ -718,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_few_kernel(const __grid_co
         mma_bf16_ss(elect, tmem, da, sdesc_sw128(t + k * 32, 16, 1024), p.idesc, s > k0 || k > 0);
       }
       mma_commit(elect, smem_u32(&ctrl.empty[st]));
+      if (p.stall && !mbar_wait_warp(smem_u32(&ctrl.never), 0, abort_flag, &g_err, p.timeout_ns)) { ok = false; break; }
       if (++st == C::STAGES) {
         st = 0;
         parity ^= 1u;

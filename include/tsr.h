@@ -647,6 +647,10 @@ tsr_status tsr_linear_backward(const tsr_linear_desc *desc, const tsr_linear_gra
 
 tsr_status tsr_linear_device_status(void *stream);
 
+/* Test only: while on, the calling thread's products stop after their first step and give
+ * up (every wait in them after 20 ms): tsr_linear_device_status reports it. */
+tsr_status tsr_linear_test_stall(int32_t on);
+
 /*
  * tsr_block_select -- a block mask for tsr_plan from a cheap score per block pair
  * (the step before the path, for callers without a mask; compare tsr_svg_route,

@@ -1,5 +1,5 @@
-"""Argument checks of a layer's operators (norm with rotation), on the host, before
-anything is launched."""
+"""Argument checks of a layer's operators (norm with rotation, linear layers), on the host,
+before anything is launched."""
 import ctypes
 
 import pytest
@@ -101,3 +101,114 @@ def test_norm_rope_refuses_bad_workspaces(L):
     assert L.tsr_norm_rope_backward_workspace(None, 1, ctypes.byref(n)) == INVALID
     assert L.tsr_norm_rope(None, 1e-6, t, 1, None) == INVALID
     assert L.tsr_norm_rope(ctypes.byref(d), 1e-6, None, 1, None) == INVALID
+
+
+def _linear(**kw):
+    d = tsr._LinearDesc()
+    base = dict(B=2, N=50, in_heads=1, in_dim=128, out_heads=2, out_dim=64, dtype=0, activation=0)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(d, k, v)
+    return d
+
+
+def _args(**kw):
+    a = tsr._LinearArgs()
+    base = dict(x=1 << 20, weight=2 << 20, bias=3 << 20, residual=4 << 20, out=5 << 20, pre=6 << 20,
+                x_stride=[50 * 128, 0, 128], residual_stride=[6400, 3200, 64], out_stride=[6400, 3200, 64],
+                pre_stride=[6400, 3200, 64])
+    base.update(kw)
+    for k, v in base.items():
+        if isinstance(v, list):
+            getattr(a, k)[:] = v
+        else:
+            setattr(a, k, v)
+    return a
+
+
+def _grads(**kw):
+    a = tsr._LinearGrads()
+    base = dict(dout=1 << 20, x=2 << 20, weight=3 << 20, pre=4 << 20, dx=5 << 20, dweight=6 << 20, dbias=7 << 20,
+                dout_stride=[6400, 3200, 64], x_stride=[50 * 128, 0, 128], pre_stride=[6400, 3200, 64],
+                dx_stride=[50 * 128, 0, 128])
+    base.update(kw)
+    for k, v in base.items():
+        if isinstance(v, list):
+            getattr(a, k)[:] = v
+        else:
+            setattr(a, k, v)
+    return a
+
+
+def _linear_both(L, d, a=None, g=None, ws=1 << 24, size=1 << 40):
+    return (L.tsr_linear(ctypes.byref(d), ctypes.byref(a or _args()), ws, size, None),
+            L.tsr_linear_backward(ctypes.byref(d), ctypes.byref(g or _grads()), ws, size, None))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0), INVALID), (dict(N=0), INVALID), (dict(N=-3), INVALID), (dict(in_heads=0), INVALID), (dict(out_heads=-1), INVALID),
+    (dict(in_dim=0), INVALID), (dict(in_dim=12), INVALID), (dict(out_dim=72), INVALID), (dict(out_heads=1, out_dim=4), INVALID),
+    (dict(dtype=2), INVALID), (dict(dtype=-1), INVALID), (dict(activation=4), INVALID), (dict(activation=-1), INVALID),
+    (dict(in_dim=(1 << 20) + 8), UNSUPPORTED), (dict(out_heads=1 << 14, out_dim=128), UNSUPPORTED),
+    (dict(B=1 << 12, N=1 << 13), UNSUPPORTED), (dict(B=(1 << 31) - 1, N=(1 << 31) - 1), UNSUPPORTED),
+])
+def test_linear_refuses_bad_shapes(L, kw, code):
+    assert _linear_both(L, _linear(**kw)) == (code, code)
+    n = ctypes.c_size_t(0)
+    for f in (L.tsr_linear_workspace, L.tsr_linear_backward_workspace):
+        assert f(ctypes.byref(_linear(**kw)), ctypes.byref(n)) == code
+    assert len(L.tsr_last_error()) > 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=0), dict(weight=0), dict(out=0), dict(x=(1 << 20) + 8), dict(weight=(2 << 20) + 2), dict(bias=(3 << 20) + 8),
+    dict(residual=(4 << 20) + 8), dict(out=(5 << 20) + 4), dict(pre=(6 << 20) + 8), dict(x_stride=[6400, 0, 0]),
+    dict(x_stride=[6400, 0, 124]), dict(x_stride=[-6400, 0, 128]), dict(out_stride=[6400, 3200, 32]),
+    dict(out_stride=[6400, 3136, 64]), dict(out_stride=[0, 3200, 64]), dict(residual_stride=[6400, 0, 64]),
+    dict(pre_stride=[6400, 64, 64]), dict(residual=5 << 20, residual_stride=[6400, 64, 128]), dict(pre=5 << 20),
+    dict(pre=4 << 20), dict(out=1 << 20), dict(out=2 << 20), dict(pre=3 << 20),
+])
+def test_linear_refuses_bad_tensors(L, kw):
+    assert _linear_both(L, _linear(), _args(**kw))[0] == INVALID
+    assert len(L.tsr_last_error()) > 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dx=0, dweight=0, dbias=0), dict(dout=0), dict(x=0), dict(weight=0), dict(pre=0), dict(dout=(1 << 20) + 8),
+    dict(dx=(5 << 20) + 8), dict(dweight=(6 << 20) + 8), dict(dbias=(7 << 20) + 8), dict(dout_stride=[6400, 3200, 0]),
+    dict(pre_stride=[6400, 3200, 4]), dict(dx_stride=[6400, 0, 64]), dict(dx=1 << 20), dict(dweight=3 << 20),
+    dict(dbias=2 << 20), dict(dx=4 << 20), dict(dweight=5 << 20),
+])
+def test_linear_backward_refuses_bad_tensors(L, kw):
+    assert _linear_both(L, _linear(activation=1), None, _grads(**kw))[1] == INVALID
+    assert len(L.tsr_last_error()) > 0
+
+
+def test_linear_refuses_strides_beyond_the_tensor_maps(L):
+    a = _args(x_stride=[1 << 38, 0, 128])
+    assert _linear_both(L, _linear(), a)[0] == UNSUPPORTED
+
+
+def test_linear_refuses_bad_workspaces(L):
+    d, n = _linear(activation=3, N=4000, in_dim=4096, out_dim=128), ctypes.c_size_t(0)
+    g = _grads(x_stride=[4000 * 4096, 0, 4096], dx_stride=[4000 * 4096, 0, 4096], dout_stride=[4000 * 256, 4000 * 128, 128],
+               pre_stride=[4000 * 256, 4000 * 128, 128])
+    assert L.tsr_linear_backward_workspace(ctypes.byref(d), ctypes.byref(n)) == 0 and n.value >= 2 * 4000 * 256 * 2
+    for ws, size in ((None, n.value), ((1 << 24) + 64, n.value), (1 << 24, n.value - 1)):
+        assert L.tsr_linear_backward(ctypes.byref(d), ctypes.byref(g), ws, size, None) == INVALID
+    assert b"too small" in L.tsr_last_error()
+    assert L.tsr_linear_workspace(None, ctypes.byref(n)) == INVALID
+    assert L.tsr_linear_workspace(ctypes.byref(d), None) == INVALID
+    assert L.tsr_linear_backward_workspace(ctypes.byref(d), None) == INVALID
+    assert L.tsr_linear(ctypes.byref(d), None, None, 0, None) == INVALID
+    assert L.tsr_linear(None, ctypes.byref(_args()), None, 0, None) == INVALID
+    assert L.tsr_linear_backward(ctypes.byref(d), None, None, 0, None) == INVALID
+
+
+def test_linear_workspaces_cover_both_ways_to_take_the_batches(L):
+    """The tokens of a batch are one row of tokens where the strides allow it, a tile of each
+    batch's own otherwise: one size serves both."""
+    a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert L.tsr_linear_workspace(ctypes.byref(_linear(B=3, N=700, in_dim=4096, out_heads=1, out_dim=8)), ctypes.byref(a)) == 0
+    assert L.tsr_linear_workspace(ctypes.byref(_linear(B=1, N=2100, in_dim=4096, out_heads=1, out_dim=8)), ctypes.byref(b)) == 0
+    assert a.value >= b.value

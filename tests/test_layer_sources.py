@@ -1,0 +1,36 @@
+"""Rules of the linear layers' and the norm's kernels that a run shows only when it goes
+wrong (a hang, a stale read), checked on their source."""
+import re
+
+from test_kernel_sources import body, source
+
+
+def test_linear_warps_leave_their_waits_together():
+    """Warp-wide instructions stand behind bounded waits that may give up: every wait
+    decides for its whole warp."""
+    text = source("linear_gemm.cuh")
+    assert text.count("mbar_wait_warp(") >= 12 and not re.search(r"\bmbar_wait\(", text)
+    assert not re.search(r"mbar_try_wait|mbar_test_wait|while \(true\)", text)
+
+
+def test_linear_kernels_read_with_plain_loads():
+    """They start while the kernel before them may still write; the read-only path is not for
+    data that it wrote.  Nothing is read before the wait for it."""
+    for name in ("linear_gemm.cuh", "linear.cu"):
+        text = source(name)
+        assert "__ldg" not in text and "ld.global.nc" not in text and "__restrict__" not in text
+    text = source("linear_gemm.cuh")
+    for kernel in ("linear_gemm_kernel(", "linear_few_kernel("):
+        code = body(text, kernel)
+        before = code[:code.index("grid_wait();")]
+        assert "tma_load" not in before and "p.epi" not in before and "p.part" not in before
+    for kernel in ("linear_finish_kernel(", "linear_bias_kernel("):
+        code = body(source("linear.cu"), kernel)
+        before = code[:code.index("grid_wait();")]
+        assert "part[" not in before and "p.part" not in before and "return" not in before
+
+
+def test_norm_weights_read_their_predecessor_with_plain_loads():
+    code = body(source("norm_rope.cu"), "norm_weight_kernel(")
+    before = code[:code.index("grid_wait();")]
+    assert "__ldg" not in code and "p.part[" not in before and "return" not in before
