@@ -18,7 +18,7 @@
 // the memory idle in between (480p forward 199 us, 720p backward 876).  Every thread
 // therefore has 64 bytes in each of the three stages of a ring in shared memory, which
 // cp.async fills two stages ahead, across heads and tokens, at no cost in registers; the
-// lanes that share a row need a barrier of their own only.
+// lanes that share a row need the warp's barrier only.
 //
 // dw: a thread sums its channels over all rows it meets in fp32, the CTA adds its groups
 // in shared memory and stores one partial row, and a dependent kernel adds the CTAs' rows
@@ -151,11 +151,13 @@ struct Batch {
   static constexpr int SMEM = kStages * SLOT > RED ? kStages * SLOT : RED;
 };
 
-// Where a thread is: an item (`tokens` tokens, `chunk` heads) and its next head.
+// Where a CTA is: an item (`tokens` tokens, `chunk` heads) and its next head.  All threads
+// are at the same place, so that its registers and branches are the warp's; a group whose
+// token is past the last one goes along without loads and stores.
 struct Place {
   // item = rest * tiles + tile, rest = b * chunks + chunk: below 2^24 and 2^16 (one chunk) or
   // as few as the CTAs
-  int tile, rest, n, b, h, h1;
+  int tile, rest, b, h, h1;
 };
 
 // One CTA works on one tensor, on items of `tokens` tokens and `chunk` heads.  A row is
@@ -169,7 +171,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   const int lanes = 1 << p.lanes_log2;
   const int group = threadIdx.x >> p.lanes_log2, lane = threadIdx.x & (lanes - 1);
   const int tokens = kThreads >> p.lanes_log2;
-  const uint32_t mask = (lanes == 32 ? 0xFFFFFFFFu : (1u << lanes) - 1u) << ((threadIdx.x & 31) - lane);
   int t = 0;
   while (t + 1 < p.n_tensors && static_cast<int>(blockIdx.x) >= p.cta0[t + 1]) ++t;
   const int tiles = (p.N + tokens - 1) / tokens;
@@ -198,26 +199,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
     }
   }
 
-  // The place's first item, or the one `tiles` and `rests` on; false behind the last.
-  // Items whose token this group does not have are passed over.
   const int step_tile = stride % tiles, step_rest = stride / tiles;
-  auto settle = [&](Place& q) -> bool {
-    while (q.rest < rests) {
-      q.n = q.tile * tokens + group;
-      if (q.n < p.N) {
-        q.b = chunks == 1 ? q.rest : q.rest / chunks;
-        q.h = chunks == 1 ? 0 : (q.rest - q.b * chunks) * chunk;
-        q.h1 = min(q.h + chunk, H);
-        return true;
-      }
-      q.tile += step_tile;
-      q.rest += step_rest;
-      if (q.tile >= tiles) {
-        q.tile -= tiles;
-        ++q.rest;
-      }
-    }
-    return false;
+  const int first = static_cast<int>(blockIdx.x) - p.cta0[t];
+  auto settle = [&](Place& q) -> bool {    // false behind the last item
+    q.b = chunks == 1 ? q.rest : q.rest / chunks;
+    q.h = chunks == 1 ? 0 : (q.rest - q.b * chunks) * chunk;
+    q.h1 = min(q.h + chunk, H);
+    return q.rest < rests;
   };
   auto next = [&](Place& q) -> bool {
     q.tile += step_tile;
@@ -228,7 +216,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
     }
     return settle(q);
   };
-  const int first = static_cast<int>(blockIdx.x) - p.cta0[t];
   Place cur;
   cur.rest = first / tiles;
   cur.tile = first - cur.rest * tiles;
@@ -236,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
 
   const int64_t xs = p.xs[t][1], os = p.os[t][1], gs = GRAD ? p.gs[t][1] : 0;
   auto row_of = [&](const void* base, const int64_t (&s)[3], const Place& q) {
-    return static_cast<const T*>(base) + q.b * s[0] + q.n * s[2] + q.h * s[1];
+    const int n = q.tile * tokens + group;
+    return static_cast<const T*>(base) + q.b * s[0] + (n < p.N ? n : 0) * s[2] + q.h * s[1];
   };
   // A row of the ring, a group's own: its lanes copy 16 bytes each, row after row in whole
   // lines (half-split pieces would be parts of sectors), and read their units back.
@@ -251,7 +239,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   Place far = cur;                         // the next rows to copy
   bool more = live;
   const T *far_x = nullptr, *far_g = nullptr;
+  bool far_ok = false;
   auto point = [&]() {
+    far_ok = far.tile * tokens + group < p.N;
     far_x = row_of(p.x[t], p.xs[t], far);
     if constexpr (GRAD) far_g = row_of(p.g[t], p.gs[t], far);
   };
@@ -266,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
 #pragma unroll
           for (int m = 0; m < B::COPIES; ++m) {
             const int at = m * lanes * 16;
-            if (FULL || lane * 16 + at < row_bytes) {
+            if (far_ok && (FULL || lane * 16 + at < row_bytes)) {
               cp_async_16(to + j * B::Q * pitch + at, from_x + j * xs * static_cast<int64_t>(sizeof(T)) + at);
               if constexpr (GRAD)
                 cp_async_16(to + (j * B::Q + 1) * pitch + at, from_g + j * gs * static_cast<int64_t>(sizeof(T)) + at);
@@ -296,11 +286,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   F2 c0[K][NP], s0[K][NP], s1[K][NP], c1[K][NP];
   int turning[K];
   T* dst = nullptr;
+  bool ok = false;
   auto begin = [&]() {                     // an item's angles and rows
+    const int n = cur.tile * tokens + group;
+    ok = n < p.N;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float cs[P], sn[P];
-      turning[k] = rope::angles_of<P>(p.ang, cur.b, cur.n, on(k) ? lane + k * lanes : p.ang.units, cs, sn);
+      turning[k] = rope::angles_of<P>(p.ang, cur.b, ok ? n : 0, on(k) ? lane + k * lanes : p.ang.units, cs, sn);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float hi = P == 1 ? 0.f : cs[(2 * i + 1) % P], ti = P == 1 ? 0.f : sn[(2 * i + 1) % P];
@@ -336,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
     if constexpr (B::RING) {
       fetch();
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncwarp(mask);                    // the group's copies, all lanes'
+      __syncwarp();                        // the copies of the lanes that share a row
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const T* x = reinterpret_cast<const T*>(mine + read + j * B::Q * pitch);
@@ -353,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
       const T* grd = GRAD ? row_of(p.g[t], p.gs[t], cur) : nullptr;
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (cur.h + j < cur.h1) {
+        if (cur.h + j < cur.h1 && ok) {
 #pragma unroll
           for (int k = 0; k < K; ++k)
             if (on(k)) {
@@ -397,13 +390,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
     for (int m = lanes >> 1; m; m >>= 1) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        ss[j] += __shfl_xor_sync(mask, ss[j], m);
-        if constexpr (GRAD) sp[j] += __shfl_xor_sync(mask, sp[j], m);
+        ss[j] += __shfl_xor_sync(0xFFFFFFFFu, ss[j], m);
+        if constexpr (GRAD) sp[j] += __shfl_xor_sync(0xFFFFFFFFu, sp[j], m);
       }
     }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      if (cur.h + j < cur.h1) {
+      if (cur.h + j < cur.h1 && ok) {
         const float r = rsqrtf(fmaf(ss[j], inv_d, p.eps));
         const float off = GRAD ? -(r * r * sp[j] * inv_d) : 0.f;
         const F2 r2 = pack2(r, r), off2 = pack2(off, off);
