@@ -144,15 +144,16 @@ struct Product {
   Kind kind;
 };
 
-// The fastest by a model in microseconds, fitted to 468 timed products (forward, dx and
+// The fastest by a model in microseconds, fitted to 490 timed products (forward, dx and
 // dweight, 1 to 8,000 tokens, 256 to 8,192 features; 13% off in the root mean square, and
-// its choice on average within 1.2% of the fastest): waves of units, each its k steps and a
-// fill and an epilogue; where pairs' tiles are cut a launch and the parts' traffic; clusters
-// of 4 and 8 CTAs leave SMs free.  Each part has four steps at least.  For example 666 x
-// 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on 256 x 256, 18 with k in three parts; 1 x
-// 4096 -> 4096: 8.5 us with the token on 32 columns and k in four parts, 21 on 256 x 128.
+// its choice on average within 1.5% of the fastest): waves of units, each its k steps and a
+// fill and an epilogue; where pairs' tiles are cut a launch and the parts' traffic.  With 32
+// tokens 70 CTAs take what the L2 gives; clusters of 4 and 8 CTAs leave SMs free.  Each part
+// has four steps at least.  For example 666 x 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on
+// 256 x 256, 18 with k in three parts; 1 x 4096 -> 4096: 8.5 us with the token on 32 columns
+// and k in four parts, 21 on 256 x 128.
 Choice choose(const Product& q) {
-  constexpr double kStep[4] = {0.298, 0.18, 0.13, 0.188}, kUnit[4] = {2.06, 1.27, 3.9, 5.14};
+  constexpr double kStep[4] = {0.298, 0.18, 0.156, 0.188}, kUnit[4] = {2.06, 1.27, 3.35, 5.14};
   constexpr int kTok[4] = {256, 256, 32, 128}, kFeat[4] = {256, 128, 128, 128};
   Choice best{PAIR_256, 1, 0};
   double least = 1e30;
@@ -161,13 +162,14 @@ Choice choose(const Product& q) {
     if (few && (q.kind == DWEIGHT || q.batches * q.n_rows > 512)) continue;   // fitted up to 300 tokens
     const int64_t tiles = q.batches * cdiv(q.n_rows, kTok[v]) * cdiv(q.cols, kFeat[v]);
     for (int64_t s = 1; s <= (few ? 8 : 16) && (s == 1 || q.k_steps >= 4 * s); s += few ? s : 1) {
-      const int64_t slots = !few ? kSms / 2 : s == 8 ? 96 : s == 4 ? 128 : 150;
-      const int64_t whole = s == 1 ? tiles : few ? 0 : tiles / slots * slots;
-      if (s > 1 && whole == tiles) continue;
-      double t = cdiv(whole, slots) * (q.k_steps * kStep[v] + kUnit[v]) +
-                 cdiv((tiles - whole) * s, slots) * (cdiv(q.k_steps, s) * kStep[v] + kUnit[v]);
-      if (few) t += 0.15 * s;
-      else t += 2.75 + (s > 1 ? 2.6 + 0.66e-6 * s * (tiles - whole) * kTok[v] * kFeat[v] : 0.0);
+      const int64_t slots = !few ? kSms / 2 : v == FEW_32 ? (s < 4 ? 300 : 256) : s == 8 ? 96 : s == 4 ? 128 : 150;
+      const int64_t whole = s == 1 ? tiles : few ? 0 : tiles / slots * slots, rest = tiles - whole;
+      if (s > 1 && !rest) continue;
+      const double crowd = v == FEW_32 ? std::max(1.0, std::min<double>(static_cast<double>(tiles * s), slots) / 70) : 1.0;
+      double t = cdiv(whole, slots) * (q.k_steps * kStep[v] * crowd + kUnit[v]) +
+                 cdiv(rest * s, slots) * (cdiv(q.k_steps, s) * kStep[v] * crowd + kUnit[v]);
+      if (few) t += 0.11 * s;
+      else t += 2.75 + (s > 1 ? 2.6 + 0.66e-6 * s * rest * kTok[v] * kFeat[v] : 0.0);
       if (t < least) {
         least = t;
         best = {static_cast<Variant>(v), static_cast<int32_t>(s), whole};
