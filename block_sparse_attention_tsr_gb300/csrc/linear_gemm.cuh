@@ -76,6 +76,7 @@ struct GemmParams {
   int32_t a_dim, b_dim;                // channels per head of A's and B's tensors
   int32_t group;                       // row tiles that share their columns' loads in L2
   uint32_t idesc;
+  int32_t late;                        // what is before on the stream is not an input: waited for at the end
   int32_t stall;                       // test only: the issuer waits for ever after its first step
   uint64_t timeout_ns;                 // bound of every wait
 };
@@ -368,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
-  // what comes before may still run while this CTA sets itself up
-  grid_wait();
+  // what comes before may still run while this CTA sets itself up; where it is no input, till
+  // this kernel's end (so that no kernel behind this one starts before it has ended)
+  if (!p.late) grid_wait();
   grid_launch_dependents();
   const int64_t units = units_of(p), first = blockIdx.x / 2, stride = gridDim.x / 2;
 
@@ -631,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::TMEM);
   }
+  if (p.late) grid_wait();
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -677,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<BN>::CTAS) linear_few_kernel(
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
-  grid_wait();
+  if (!p.late) grid_wait();
   grid_launch_dependents();
   const int32_t tile = static_cast<int32_t>(blockIdx.x) / p.splits;
   const int32_t f_tile = tile % p.row_tiles, t_tile = tile / p.row_tiles;
@@ -781,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<BN>::CTAS) linear_few_kernel(
     tc_fence_after();
     tmem_dealloc(tmem, BN);
   }
+  if (p.late) grid_wait();
 }
 
 }  // namespace linear

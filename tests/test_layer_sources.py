@@ -22,8 +22,10 @@ def test_linear_kernels_read_with_plain_loads():
     text = source("linear_gemm.cuh")
     for kernel in ("linear_gemm_kernel(", "linear_few_kernel("):
         code = body(text, kernel)
-        before = code[:code.index("grid_wait();")]
+        before = code[:code.index("if (!p.late) grid_wait();")]
         assert "tma_load" not in before and "p.epi" not in before and "p.part" not in before
+        # a product that did not wait at its start does at its end
+        assert code.rstrip("} \n").endswith("if (p.late) grid_wait();")
     for kernel in ("linear_finish_kernel(", "linear_bias_kernel("):
         code = body(source("linear.cu"), kernel)
         before = code[:code.index("grid_wait();")]
