@@ -154,7 +154,7 @@ struct Product {
 // 256 x 256, 18 with k in three parts; 1 x 4096 -> 4096: 8.5 us with the token on 32 columns
 // and k in four parts, 21 on 256 x 128.
 Choice choose(const Product& q) {
-  constexpr double kStep[4] = {0.298, 0.18, 0.156, 0.188}, kUnit[4] = {2.06, 1.27, 3.35, 5.14};
+  constexpr double kStep[4] = {0.298, 0.18, 0.156, 0.188}, kUnit[4] = {2.06, 1.27, 3.35, 4.4};
   constexpr int kTok[4] = {256, 256, 32, 128}, kFeat[4] = {256, 128, 128, 128};
   Choice best{PAIR_256, 1, 0};
   double least = 1e30;
@@ -169,7 +169,7 @@ Choice choose(const Product& q) {
       const double crowd = v == FEW_32 ? std::max(1.0, std::min<double>(static_cast<double>(tiles * s), slots) / 70) : 1.0;
       double t = cdiv(whole, slots) * (q.k_steps * kStep[v] * crowd + kUnit[v]) +
                  cdiv(rest * s, slots) * (cdiv(q.k_steps, s) * kStep[v] * crowd + kUnit[v]);
-      if (few) t += 0.11 * s;
+      if (few) t += 0.11 * s + (v == FEW_128 && s > 1 ? 2.4 : 0.0);
       else t += 2.75 + (s > 1 ? 2.6 + 0.66e-6 * s * rest * kTok[v] * kFeat[v] : 0.0);
       if (t < least) {
         least = t;
@@ -355,11 +355,12 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
     // out's rows: tokens, or the weight's for its gradient
     const int64_t rows = q.n_rows, heads = q.cols / e.vout.dim;
     if (c.whole) {
-      if (tsr_status s = encode(&p.tout, e.out, e.vout, heads, rows, q.batches, 32, 32, y.f16)) return s;
+      const int width = e.pre ? 32 : 64;
+      if (tsr_status s = encode(&p.tout, e.out, e.vout, heads, rows, q.batches, width, 32, y.f16)) return s;
       if (e.pre)
-        if (tsr_status s = encode(&p.tpre, e.pre, e.vpre, heads, rows, q.batches, 32, 32, y.f16)) return s;
+        if (tsr_status s = encode(&p.tpre, e.pre, e.vpre, heads, rows, q.batches, width, 32, y.f16)) return s;
       if (e.res)
-        if (tsr_status s = encode(&p.tres, e.res, e.vres, heads, rows, q.batches, 32, 32, y.f16)) return s;
+        if (tsr_status s = encode(&p.tres, e.res, e.vres, heads, rows, q.batches, width, 32, y.f16)) return s;
     }
     const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - c.whole;
     if (rest)

@@ -61,8 +61,8 @@ struct Epilogue {
 
 struct GemmParams {
   CUtensorMap ta, tb;                  // few tokens: the weight, and the tokens
-  // out, pre and residual as {channel, token, head, batch} and the parts, fp32, as {column,
-  // row, tile, part}, in boxes of 32 x 32
+  // out, pre and residual as {channel, token, head, batch} in boxes of 32 tokens x 64 channels
+  // (32 where pre is kept), and the parts, fp32, as {column, row, tile, part} in boxes of 32 x 32
   CUtensorMap tout, tpre, tres, tpart;
   Epilogue epi;
   float* part;                         // [splits][tiles - whole][256][BN]
@@ -225,9 +225,9 @@ struct Cfg {
   static constexpr int TM = 256;                          // rows of a tile, half of them in each CTA
   static constexpr int A_BYTES = 128 * BK * 2, B_ROWS = BN / 2, B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  // what leaves through shared memory: for each epilogue warp four pieces of 32 rows x 32
-  // columns (parts, fp32: two)
-  static constexpr int PIECE = 32 * 64, OUT_BYTES = kEpiWarps * 4 * PIECE;
+  // what leaves through shared memory: for each epilogue warp two pieces of 32 rows x 128
+  // bytes (64 columns, of parts 32)
+  static constexpr int PIECE = 32 * 128, OUT_BYTES = kEpiWarps * 2 * PIECE;
   static constexpr int FIT = (226 * 1024 - OUT_BYTES) / STAGE, STAGES = FIT < 8 ? FIT : 8;
   static constexpr int OUT = STAGES * STAGE, CTRL = OUT + OUT_BYTES, SMEM = CTRL + 512;
   static constexpr int TMEM = 2 * BN;                     // two accumulators
@@ -239,7 +239,7 @@ struct Cfg {
 struct alignas(8) Ctrl {
   uint64_t full[8], empty[8], acc_full[2], acc_empty[2], final_bar;
   uint64_t never;                      // never signalled (stall test)
-  uint64_t res_full[kEpiWarps][4];     // the residual's piece has landed
+  uint64_t res_full[kEpiWarps][2];     // the residual's piece has landed
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     }
     mbar_init(smem_u32(&ctrl.final_bar), 1);
     mbar_init(smem_u32(&ctrl.never), 1);
-    for (int i = 0; i < 4 * kEpiWarps; ++i) mbar_init(smem_u32(&ctrl.res_full[0][0] + i), 1);
+    for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(smem_u32(&ctrl.res_full[0][0] + i), 1);
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
     fence_mbar_init();
   }
@@ -478,14 +478,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         constexpr int W = BN / 2;                                   // columns of this warp
         const int32_t f0 = w.col_tile * BN + half * W;
         const bool inside = n0 < p.n_rows;
-        const uint32_t pieces = base + C::OUT + ew * 4 * C::PIECE;
+        const uint32_t pieces = base + C::OUT + ew * 2 * C::PIECE;
         if (w.cut >= 0) {
 #pragma unroll 1
           for (int c = 0; c < W; c += 32) {
             if (f0 + c >= p.cols || !inside) break;
             uint32_t v[32];
             tmem_ld32(acc + half * W + c, v);
-            const uint32_t q = pieces + (turn++ & 1u) * 2 * C::PIECE;
+            const uint32_t q = pieces + (turn++ & 1u) * C::PIECE;
             bulk_wait_read<1>();                                    // the piece before the last has left
             __syncwarp();
             tc_wait_ld();
@@ -500,76 +500,74 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
           }
         } else {
           const bool pre = p.epi.pre != nullptr, res = p.epi.res != nullptr;
-          const int dim = p.epi.vout.dim, per = pre ? 2 : 1;
-          constexpr int STEPS = W / 32;                             // 32 columns each
-          const int steps = !inside || f0 >= p.cols ? 0 : min(STEPS, (p.cols - f0 + 31) / 32);
-          // step s takes the ring's next pieces: pre's, then out's, where the residual lands first
-          auto piece = [&](int s, int which) { return (turn + s * per + which) & 3u; };
+          const int dim = p.epi.vout.dim;
+          // a step takes a piece: 64 columns, or with pre 32, pre's in its first half and out's
+          // in the second; a residual lands where out's will be
+          const int width = pre ? 32 : 64, half_piece = pre ? C::PIECE / 2 : 0;
+          const int steps = !inside || f0 >= p.cols ? 0 : (min(W, p.cols - f0) + width - 1) / width;
           auto load_res = [&](int s) {
-            const uint32_t k = piece(s, per - 1), bar = smem_u32(&ctrl.res_full[ew][k]);
-            const int32_t f = f0 + s * 32, h = f / dim;
-            mbar_arrive_expect_tx(elect, bar, C::PIECE);
-            tma_load_4d(elect, pieces + k * C::PIECE, &p.tres, bar, f - h * dim, n0, h, b);
+            const uint32_t k = (turn + s) & 1u, bar = smem_u32(&ctrl.res_full[ew][k]);
+            const int32_t f = f0 + s * width, h = f / dim;
+            mbar_arrive_expect_tx(elect, bar, width * 64);
+            tma_load_4d(elect, pieces + k * C::PIECE + half_piece, &p.tres, bar, f - h * dim, n0, h, b);
             res_issued |= 1u << k;
           };
           if (res) {
             bulk_wait_read<0>();
             __syncwarp();
-            for (int s = 0; s < (pre ? min(steps, 2) : steps); ++s) load_res(s);
+            for (int s = 0; s < min(steps, 2); ++s) load_res(s);
           }
           if (!mbar_wait_warp(smem_u32(&ctrl.acc_full[buf]), (tile >> 1) & 1, abort_flag, &g_err, p.timeout_ns)) break;
           tc_fence_after();
           bool ok = true;
-          // two steps at a time share a fence and the waits (one where pre takes a piece too)
           uint32_t v[2][32];
           auto columns = [&](int s) {
-            if (s < steps) tmem_ld32(acc + half * W + s * 32, v[0]);
-            if (!pre && s + 1 < steps) tmem_ld32(acc + half * W + (s + 1) * 32, v[1]);
+            if (s < steps) {
+              tmem_ld32(acc + half * W + s * width, v[0]);
+              if (!pre) tmem_ld32(acc + half * W + s * width + 32, v[1]);
+            }
           };
           columns(0);
           int32_t h = f0 / dim, ch = f0 - h * dim;
 #pragma unroll 1
-          for (int s = 0; s < steps;) {
-            const int n = pre ? 1 : min(2, steps - s);
+          for (int s = 0; s < steps; ++s) {
+            const int n = pre ? 1 : 2;                              // 32 columns each
+            const uint32_t k = (turn + s) & 1u;
             uint4 bias[2][4] = {};
             if (p.epi.bias) {
 #pragma unroll
               for (int g = 0; g < 8; ++g) {
-                const int32_t f = f0 + s * 32 + g * 8;
+                const int32_t f = f0 + s * width + g * 8;
                 if (f < p.cols && g < 4 * n) bias[g >> 2][g & 3] = static_cast<const uint4*>(p.epi.bias)[f / 8];
               }
             }
             if (res) {
-              if (pre && s >= 2) {
+              if (s >= 2) {
                 bulk_wait_read<0>();
                 __syncwarp();
                 load_res(s);
               }
-              for (int j = 0; ok && j < n; ++j) {
-                const uint32_t k = piece(s + j, per - 1);
-                ok = mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, abort_flag, &g_err, p.timeout_ns);
-                if (!ok) break;
-                res_phase ^= 1u << k;
-                res_issued &= ~(1u << k);
-              }
+              ok = mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, abort_flag, &g_err, p.timeout_ns);
               if (!ok) break;
+              res_phase ^= 1u << k;
+              res_issued &= ~(1u << k);
             } else {
-              bulk_wait_read<1>();                                  // all but the last iteration's pieces have left
+              bulk_wait_read<1>();                                  // all but the last step's piece have left
               __syncwarp();
             }
             tc_wait_ld();
-            // a lane's row of 64 bytes, 16 each, swizzled as TMA reads it
-            const uint32_t row = lane * 64, turned = (lane >> 1) & 3;
+            // a lane's row of the piece, 16 bytes each, swizzled as TMA reads it (rows of 128
+            // bytes, or of 64)
+            const uint32_t q_pre = pieces + k * C::PIECE, q = q_pre + half_piece;
+            const uint32_t row = lane * (pre ? 64 : 128), turned = pre ? (lane >> 1) & 3 : lane & 7;
             by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 if (j < n) {
-                  const uint32_t q_pre = pieces + piece(s + j, 0) * C::PIECE + row;
-                  const uint32_t q = pieces + piece(s + j, per - 1) * C::PIECE + row;
 #pragma unroll
                   for (int g = 0; g < 4; ++g) {
                     float x[8], t[8];
-                    const uint32_t o = (g ^ turned) << 4;
+                    const uint32_t o = row + (((j * 4 + g) ^ turned) << 4);
                     unpack8<f16.value>(bias[j][g], t);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[j][8 * g + i]) + t[i];
@@ -586,29 +584,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                 }
               }
             });
-            columns(s + n);                                         // on their way while these leave
+            columns(s + 1);                                         // on their way while these leave
             fence_proxy_async_smem();
             __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (j < n) {
-                if (pre) tma_store_4d(elect, &p.tpre, pieces + piece(s + j, 0) * C::PIECE, ch, n0, h, b);
-                tma_store_4d(elect, &p.tout, pieces + piece(s + j, per - 1) * C::PIECE, ch, n0, h, b);
-                ch += 32;
-                if (ch >= dim) {
-                  ch = 0;
-                  ++h;
-                }
-              }
-            }
+            if (pre) tma_store_4d(elect, &p.tpre, q_pre, ch, n0, h, b);
+            tma_store_4d(elect, &p.tout, q, ch, n0, h, b);
             bulk_commit(elect);
-            s += n;
+            ch += width;
+            if (ch >= dim) {
+              ch = 0;
+              ++h;
+            }
           }
           if (!ok) {
             tc_wait_ld();
             break;
           }
-          turn += steps * per;
+          turn += steps;
         }
       }
       tc_fence_before();
@@ -622,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     if (*abort_flag) {
       // a residual's piece in flight lands before the CTA ends
       volatile int32_t no = 0;
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 2; ++k)
         if ((res_issued >> k) & 1) mbar_wait_warp(smem_u32(&ctrl.res_full[ew][k]), (res_phase >> k) & 1, &no, &g_err, p.timeout_ns);
     }
   }

@@ -118,7 +118,9 @@ SIZES = [(1, 1, 8, 8), (1, 2, 256, 2048), (1, 5, 1160, 264), (2, 33, 200, 1544),
          (2, 333, 4096, 2048), (1, 4096, 512, 512), (3, 129, 64, 320), (5, 1, 512, 512),
          (1, 130, 1120, 3944), (1, 72, 1352, 3560), (1, 355, 3392, 264), (2, 1, 3192, 32), (1, 1283, 2264, 1576),
          (1, 2593, 1176, 1712), (1, 2674, 3456, 520), (1, 6588, 3360, 8), (2, 657, 2744, 1592), (1, 329, 264, 3432),
-         (1, 65, 3744, 1392), (1, 517, 3224, 2536), (3, 526, 2704, 1320), (1, 1, 16, 2336)]
+         (1, 65, 3744, 1392), (1, 517, 3224, 2536), (3, 526, 2704, 1320), (1, 1, 16, 2336),
+         (1, 65, 2456, 4128), (1, 33, 2616, 3952), (5, 65, 3584, 392), (1, 71, 4120, 2664), (3, 11, 4056, 2464),
+         (1, 354, 392, 3256)]
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
