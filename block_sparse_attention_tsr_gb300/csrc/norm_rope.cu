@@ -52,21 +52,22 @@ Shape shape_of(int units, int P) {
   return s;
 }
 
-// CTAs of each tensor: as many as run together, in proportion to the tensors' heads, or one
-// for each item where there are fewer.  An item takes all heads of its tokens (their angles
+// CTAs of each tensor: as many as run together, in proportion to the tensors' heads and four
+// more (an item's angles take about as long as four rows), or one for each item where there
+// are fewer.  An item takes all heads of its tokens (their angles
 // are computed once) unless there are too few items for the card.
 void spread(NormParams& p, int ctas) {
   const int tokens = kThreads >> p.lanes_log2;
   const int64_t tiles = (static_cast<int64_t>(p.N) + tokens - 1) / tokens * p.B;
   const int64_t want = ctas;
   int64_t rows = 0;
-  for (int i = 0; i < p.n_tensors; ++i) rows += p.H[i];
+  for (int i = 0; i < p.n_tensors; ++i) rows += p.H[i] + 4;
   p.cta0[0] = 0;
   for (int i = 0; i < p.n_tensors; ++i) {
     int64_t chunks = std::min<int64_t>(p.H[i], std::max<int64_t>(1, want / (tiles * p.n_tensors)));
     p.chunk[i] = static_cast<int32_t>((p.H[i] + chunks - 1) / chunks);
     chunks = (p.H[i] + p.chunk[i] - 1) / p.chunk[i];
-    const int64_t share = std::max<int64_t>(1, (want * p.H[i] + rows / 2) / rows);
+    const int64_t share = std::max<int64_t>(1, (want * (p.H[i] + 4) + rows / 2) / rows);
     p.cta0[i + 1] = p.cta0[i] + static_cast<int32_t>(std::min<int64_t>(tiles * chunks, share));
   }
 }

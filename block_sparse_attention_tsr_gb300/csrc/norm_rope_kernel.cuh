@@ -281,10 +281,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   }
 
   // Pair (u, v) -> (u c0 - v s0, u s1 + v c1): of the weighted row forward (the weights are
-  // in the factors), of the gradient back (c0 = c1 = cos, s0 = s1 = -sin).  Pairs that do
-  // not turn are left alone: 0 times a partner that is not finite would not be 0.
+  // in the factors), of the gradient back (c0 = c1 = cos, s0 = s1 = -sin).  Of pairs that do
+  // not turn (cos 1, sin 0) the partner is masked out: 0 times one that is not finite would
+  // not be 0.
   F2 c0[K][NP], s0[K][NP], s1[K][NP], c1[K][NP];
-  int turning[K];
+  F2 turns[FULL ? 1 : K][NP];              // all ones for pairs that turn
   T* dst = nullptr;
   bool ok = false;
   auto begin = [&]() {                     // an item's angles and rows
@@ -293,11 +294,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float cs[P], sn[P];
-      turning[k] = rope::angles_of<P>(p.ang, cur.b, ok ? n : 0, on(k) ? lane + k * lanes : p.ang.units, cs, sn);
+      const int turning = rope::angles_of<P>(p.ang, cur.b, ok ? n : 0, on(k) ? lane + k * lanes : p.ang.units, cs, sn);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float hi = P == 1 ? 0.f : cs[(2 * i + 1) % P], ti = P == 1 ? 0.f : sn[(2 * i + 1) % P];
         const F2 c = pack2(cs[2 * i % P], hi), s = pack2(sn[2 * i % P], ti), minus = pack2(-1.f, -1.f);
+        if constexpr (!FULL)
+          turns[k][i] = (2 * i < turning ? 0xFFFFFFFFull : 0ull) | (2 * i + 1 < turning ? 0xFFFFFFFFull << 32 : 0ull);
         if constexpr (GRAD) {
           c0[k][i] = c;
           s0[k][i] = s;                    // u cos + v sin
@@ -314,14 +317,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   };
   // the first and second elements of two pairs, turned
   auto turn = [&](int k, int i, F2 u, F2 v, F2& y, F2& z) {
-    y = fma2(v, s0[k][i], mul2(u, c0[k][i]));
-    z = fma2(u, s1[k][i], mul2(v, GRAD ? c0[k][i] : c1[k][i]));
-    if constexpr (!FULL) {
-      const F2 y0 = GRAD ? u : mul2(u, wa[k][i]), z0 = GRAD ? v : mul2(v, wb[k][i]);
-      const bool lo = 2 * i < turning[k], hi = 2 * i + 1 < turning[k];
-      y = pack2(lo ? unpack2(y).x : unpack2(y0).x, hi ? unpack2(y).y : unpack2(y0).y);
-      z = pack2(lo ? unpack2(z).x : unpack2(z0).x, hi ? unpack2(z).y : unpack2(z0).y);
-    }
+    const F2 u1 = FULL ? u : u & turns[k][i], v1 = FULL ? v : v & turns[k][i];
+    y = fma2(v1, s0[k][i], mul2(u, c0[k][i]));
+    z = fma2(u1, s1[k][i], mul2(v, GRAD ? c0[k][i] : c1[k][i]));
   };
   if (live) begin();
   while (live) {
