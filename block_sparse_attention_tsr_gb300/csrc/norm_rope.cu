@@ -10,7 +10,7 @@ namespace tsr {
 
 namespace norm {
 
-template tsr_status launch<false>(const NormParams&, int, bool, int, int, cudaStream_t);
+template tsr_status launch<false>(const NormParams&, int, const Shape&, cudaStream_t);
 
 namespace {
 
@@ -42,16 +42,6 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant
   }
 }
 
-// Lanes that share a row, and units each of them holds.
-struct Shape {
-  int lanes_log2, K;
-};
-Shape shape_of(int units, int P) {
-  Shape s{0, P == 1 ? 4 : units > 32 ? 2 : 1};
-  while ((1 << s.lanes_log2) < units && s.lanes_log2 < 5) ++s.lanes_log2;
-  return s;
-}
-
 // CTAs of each tensor: as many as run together, in proportion to the tensors' heads and four
 // more (an item's angles take about as long as four rows), or one for each item where there
 // are fewer.  An item takes all heads of its tokens (their angles
@@ -72,8 +62,8 @@ void spread(NormParams& p, int ctas) {
   }
 }
 
-// Parameters of a call; returns the pairs per unit.
-int fill(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int32_t n, bool grad, NormParams& p) {
+// Parameters of a call, the lanes that share a row among them.
+Shape fill(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int32_t n, bool grad, NormParams& p) {
   memset(&p, 0, sizeof p);
   const size_t es = d.dtype == TSR_DTYPE_F32 ? 4 : 2;
   p.n_tensors = n;
@@ -103,11 +93,33 @@ int fill(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int3
     }
   }
   bits |= static_cast<uint64_t>(d.d) * es;
-  // the ring copies 16 bytes; half-split pairs of 16-bit types in units of 16 bytes too, so
-  // that a row is spread over as many lanes as one of neighbouring pairs
-  if (bits & 15) bits |= es;
-  else if (d.halves && es == 2) bits |= 8;
-  return rope::fill_angles(d, bits, p.ang);
+  for (int a = 0; a < d.n_axes; ++a) p.inv_extent[a] = d.positions ? 0.f : 1.f / d.grid[a];
+  // A unit is 16 bytes of neighbouring pairs, or two pieces of 8 (fp32: 16) bytes of half-split
+  // ones, where rows start on 16 bytes and the half widths are whole pieces; else its pairs
+  // are gathered one by one, from the ring or, of rows that start elsewhere, from memory.
+  Shape s{static_cast<int>(16 / (2 * es)), NEAR, 1};
+  const bool rows = (bits & 15) == 0;
+  if (d.halves && rows) {
+    int32_t width = 0;
+    uint64_t halves = 0;
+    for (int a = 0; a < d.n_axes; ++a) {
+      halves |= static_cast<uint64_t>(d.axis_dim[a] / 2) * es;
+      width += d.axis_dim[a];
+    }
+    halves |= static_cast<uint64_t>(d.d - width) / 2 * es;
+    s.L = halves % (4 * es) ? ANY : HALVES;
+    s.P = s.L == HALVES ? 4 : s.P;
+    bits |= s.L == ANY ? es : 4 * es;
+  } else if (!rows) {
+    s.P = 1;
+    s.L = HALVES;
+    bits |= es;
+  }
+  rope::fill_angles(d, bits, p.ang);
+  p.ang.units = d.d / 2 / s.P;
+  s.K = s.P == 1 ? 4 : p.ang.units > 32 ? 2 : 1;
+  while ((1 << p.lanes_log2) < p.ang.units && p.lanes_log2 < 5) ++p.lanes_log2;
+  return s;
 }
 
 }  // namespace
@@ -120,13 +132,11 @@ using namespace norm;
 tsr_status launch_norm_rope(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int32_t n,
                             cudaStream_t st) {
   NormParams p;
-  const int P = fill(d, eps, t, n, false, p);
-  const Shape s = shape_of(p.ang.units, P);
-  p.lanes_log2 = s.lanes_log2;
+  const Shape s = fill(d, eps, t, n, false, p);
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  spread(p, num_sms(dev) * ctas_per_sm(false, P));
-  return launch<false>(p, d.dtype, d.halves != 0, P, s.K, st);
+  spread(p, num_sms(dev) * ctas_per_sm(false, s.P));
+  return launch<false>(p, d.dtype, s, st);
 }
 
 // One partial row of weight gradients per CTA that any call of this shape may use.
@@ -138,12 +148,10 @@ size_t norm_rope_workspace(const tsr_rope_desc& d, int32_t n) {
 tsr_status launch_norm_rope_backward(const tsr_rope_desc& d, double eps, const tsr_norm_rope_tensor* t, int32_t n,
                                      void* ws, cudaStream_t st) {
   NormParams p;
-  const int P = fill(d, eps, t, n, true, p);
-  const Shape s = shape_of(p.ang.units, P);
-  p.lanes_log2 = s.lanes_log2;
+  const Shape s = fill(d, eps, t, n, true, p);
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  spread(p, std::min(num_sms(dev), 256) * ctas_per_sm(true, P));
+  spread(p, std::min(num_sms(dev), 256) * ctas_per_sm(true, s.P));
   SumParams q;
   memset(&q, 0, sizeof q);
   bool any = false;
@@ -152,7 +160,7 @@ tsr_status launch_norm_rope_backward(const tsr_rope_desc& d, double eps, const t
     any = any || t[i].dweight;
   }
   p.part = any ? static_cast<float*>(ws) : nullptr;
-  if (tsr_status e = launch<true>(p, d.dtype, d.halves != 0, P, s.K, st)) return e;
+  if (tsr_status e = launch<true>(p, d.dtype, s, st)) return e;
   if (!any) return TSR_OK;
   q.part = p.part;
   memcpy(q.cta0, p.cta0, sizeof q.cta0);

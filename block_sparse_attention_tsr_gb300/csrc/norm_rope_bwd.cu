@@ -6,7 +6,7 @@ namespace tsr {
 
 namespace norm {
 
-template tsr_status launch<true>(const NormParams&, int, bool, int, int, cudaStream_t);
+template tsr_status launch<true>(const NormParams&, int, const Shape&, cudaStream_t);
 
 }  // namespace norm
 

@@ -50,6 +50,7 @@ struct NormParams {
   int32_t cta0[kMaxTensors + 1];     // CTAs of each tensor, one after another
   int32_t chunk[kMaxTensors];        // heads an item takes
   rope::Angles ang;
+  float inv_extent[4];
   int32_t n_tensors, N, B, d, lanes_log2, w_f32;
   float eps;
   float* part;                       // backward: [CTA][d], null: no weight gradient
@@ -124,12 +125,65 @@ __device__ __forceinline__ void put(Unit<T, P, ADJ>& u, const F2 (&a)[(P + 1) / 
   }
 }
 
-// Channels of a unit's pair i.
-template <int P, bool ADJ>
-__device__ __forceinline__ int first_of(int ch0, int i) { return P == 1 ? ch0 : ADJ ? ch0 + 2 * i : ch0 + i; }
-template <int P, bool ADJ>
-__device__ __forceinline__ int second_of(int ch0, int ch1, int i) {
-  return P == 1 ? ch1 : ADJ ? ch0 + 2 * i + 1 : ch1 + i;
+// How a unit's pairs lie in a row: NEAR, neighbouring channels; HALVES, two pieces of P
+// channels; ANY, pair by pair (half-split pairs whose half widths are no whole pieces), which
+// are gathered from the ring's row and put back there before it is stored.
+enum Layout { NEAR, HALVES, ANY };
+
+// Channels of a unit's pair i.  at: a unit's first channels, first and second piece; of ANY
+// each pair's, 16 bits each.
+template <int P, int L>
+struct Channels {
+  uint32_t at[L == ANY ? P : 1];
+  __device__ __forceinline__ int first(int i) const {
+    return L == ANY ? at[L == ANY ? i : 0] & 0xFFFF : (at[0] & 0xFFFF) + (P == 1 ? 0 : L == NEAR ? 2 * i : i);
+  }
+  __device__ __forceinline__ int second(int i) const {
+    return L == ANY ? at[L == ANY ? i : 0] >> 16
+                    : L == NEAR && P > 1 ? (at[0] & 0xFFFF) + 2 * i + 1 : (at[0] >> 16) + (P == 1 ? 0 : i);
+  }
+  __device__ __forceinline__ void set(const rope::Angles& a, int unit) {
+    if constexpr (L == ANY) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) at[i] = a.c0[unit * P + i] | static_cast<uint32_t>(a.c1[unit * P + i]) << 16;
+    } else {
+      at[0] = a.c0[unit] | static_cast<uint32_t>(a.c1[unit]) << 16;
+    }
+  }
+};
+// A unit in registers: ANY's pairs lie there as neighbours.
+template <typename T, int P, int L>
+using UnitOf = Unit<T, P, L != HALVES>;
+
+template <typename T, int P, int L>
+__device__ __forceinline__ void gather(UnitOf<T, P, L>& u, const T* row, const Channels<P, L>& c) {
+  if constexpr (L == ANY) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      struct alignas(2 * sizeof(T)) Both {
+        T a, b;
+      } v{row[c.first(i)], row[c.second(i)]};
+      u.a.w[i] = *reinterpret_cast<const typename rope::Two<T>::Word*>(&v);
+    }
+  } else {
+    u.load(row + c.first(0), row + c.second(0));
+  }
+}
+template <typename T, int P, int L>
+__device__ __forceinline__ void scatter(const UnitOf<T, P, L>& u, T* row, const Channels<P, L>& c) {
+  if constexpr (L == ANY) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      struct alignas(2 * sizeof(T)) Both {
+        T a, b;
+      };
+      const Both v = *reinterpret_cast<const Both*>(&u.a.w[i]);
+      row[c.first(i)] = v.a;
+      row[c.second(i)] = v.b;
+    }
+  } else {
+    u.store(row + c.first(0), row + c.second(0));
+  }
 }
 
 template <typename T>
@@ -140,7 +194,7 @@ __device__ __forceinline__ float weight_at(const NormParams& p, int t, int c) {
 }
 
 // What a thread copies and holds of a row, and how many rows at a time.
-template <typename T, int P, bool ADJ, int K, bool GRAD>
+template <typename T, int P, int K, bool GRAD>
 struct Batch {
   static constexpr bool RING = P > 1;
   static constexpr int Q = GRAD ? 2 : 1;                                     // rows of x, and of dy
@@ -148,7 +202,8 @@ struct Batch {
   static constexpr int R = !RING ? (GRAD ? 1 : 2) : 64 / (Q * COPIES * 16) < 1 ? 1 : 64 / (Q * COPIES * 16);
   static constexpr int SLOT = R * Q * COPIES * 16 * kThreads;                // a stage of the CTA
   static constexpr int RED = GRAD ? 512 * P * K * 4 : 0;                     // weight gradients of its groups
-  static constexpr int SMEM = kStages * SLOT > RED ? kStages * SLOT : RED;
+  static constexpr int TABLE = kStages * SLOT > RED ? kStages * SLOT : RED;  // frequencies, axes behind it
+  static constexpr int SMEM = TABLE + rope::kMaxPairs * 9;
 };
 
 // Where a CTA is: an item (`tokens` tokens, `chunk` heads) and its next head.  All threads
@@ -163,9 +218,9 @@ struct Place {
 // One CTA works on one tensor, on items of `tokens` tokens and `chunk` heads.  A row is
 // K units in each of 2^lanes_log2 lanes.  FULL: every lane has its K units and all their
 // pairs turn.
-template <typename T, int P, bool ADJ, int K, bool GRAD, bool FULL>
+template <typename T, int P, int L, int K, bool GRAD, bool FULL>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kernel(const __grid_constant__ NormParams p) {
-  using B = Batch<T, P, ADJ, K, GRAD>;
+  using B = Batch<T, P, K, GRAD>;
   constexpr int R = B::R, NP = (P + 1) / 2;
   extern __shared__ __align__(16) uint8_t smem[];
   const int lanes = 1 << p.lanes_log2;
@@ -178,7 +233,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   const int rests = p.B * chunks, stride = p.cta0[t + 1] - p.cta0[t];
   const float inv_d = 1.f / p.d;
 
-  int ch0[K], ch1[K];
+  // the pairs' frequencies and axes: lanes differ in them, which constant memory serves one
+  // by one
+  uint64_t* const freq = reinterpret_cast<uint64_t*>(smem + B::TABLE);
+  uint8_t* const axis = smem + B::TABLE + rope::kMaxPairs * 8;
+  for (int i = threadIdx.x; i < p.ang.n_pairs; i += kThreads) {
+    freq[i] = p.ang.freq[i];
+    axis[i] = p.ang.axis[i];
+  }
+  __syncthreads();
+
+  Channels<P, L> ch[K];
   bool has[K];
   auto on = [&](int k) { return FULL || has[k]; };
   F2 wa[K][NP], wb[K][NP];                 // weights of the first and of the second elements
@@ -187,12 +252,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   for (int k = 0; k < K; ++k) {
     const int unit = lane + k * lanes;
     has[k] = unit < p.ang.units;
-    ch0[k] = on(k) ? p.ang.c0[unit] : 0;
-    ch1[k] = on(k) ? p.ang.c1[unit] : 0;
+    ch[k].set(p.ang, on(k) ? unit : 0);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      auto w0 = [&](int j) { return on(k) && j < P ? weight_at<T>(p, t, first_of<P, ADJ>(ch0[k], j)) : 0.f; };
-      auto w1 = [&](int j) { return on(k) && j < P ? weight_at<T>(p, t, second_of<P, ADJ>(ch0[k], ch1[k], j)) : 0.f; };
+      auto w0 = [&](int j) { return on(k) && j < P ? weight_at<T>(p, t, ch[k].first(j)) : 0.f; };
+      auto w1 = [&](int j) { return on(k) && j < P ? weight_at<T>(p, t, ch[k].second(j)) : 0.f; };
       wa[k][i] = pack2(w0(2 * i), w0(2 * i + 1));
       wb[k][i] = pack2(w1(2 * i), w1(2 * i + 1));
       da[k][i] = db[k][i] = 0;
@@ -291,10 +355,46 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   auto begin = [&]() {                     // an item's angles and rows
     const int n = cur.tile * tokens + group;
     ok = n < p.N;
+    // the token's coordinates, once for all its pairs
+    int at[4] = {0, 0, 0, 0};
+    if (p.ang.positions) {
+      const int32_t* src = p.ang.positions + cur.b * p.ang.pos_batch + static_cast<int64_t>(ok ? n : 0) * p.ang.n_axes;
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+        if (a < p.ang.n_axes) at[a] = __ldg(src + a);
+    } else {
+      int rest = ok ? n : 0;
+#pragma unroll
+      for (int a = 3; a > 0; --a)
+        if (a < p.ang.n_axes) {
+          // rest < 2^24: the quotient by the reciprocal is off by one at most
+          const int e = p.ang.extent[a];
+          int q = static_cast<int>(static_cast<float>(rest) * p.inv_extent[a]);
+          q -= q * e > rest;
+          q += rest - q * e >= e;
+          at[a] = rest - q * e;
+          rest = q;
+        }
+      at[0] = rest;
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float cs[P], sn[P];
-      const int turning = rope::angles_of<P>(p.ang, cur.b, ok ? n : 0, on(k) ? lane + k * lanes : p.ang.units, cs, sn);
+      const int pair0 = (lane + k * lanes) * P;
+      const int turning = on(k) ? min(max(p.ang.n_pairs - pair0, 0), P) : 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+        if (FULL || i < turning) {
+          const int a = axis[pair0 + i];
+          const int64_t pos = a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3];
+          // the angle's place on the circle in 2^-32 of a turn (rope.cu), half turns in [-1, 1)
+          const uint64_t turn = static_cast<uint64_t>(pos) * freq[pair0 + i];
+          sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
+          if (p.ang.inverse) sn[i] = -sn[i];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float hi = P == 1 ? 0.f : cs[(2 * i + 1) % P], ti = P == 1 ? 0.f : sn[(2 * i + 1) % P];
@@ -323,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   };
   if (live) begin();
   while (live) {
-    Unit<T, P, ADJ> u[R][K], v[GRAD ? R : 1][K];
+    UnitOf<T, P, L> u[R][K], v[GRAD ? R : 1][K];
+    const int used = read;                 // the stage of these rows
     if constexpr (B::RING) {
       fetch();
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -334,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
         const T* g = GRAD ? reinterpret_cast<const T*>(mine + read + (j * B::Q + 1) * pitch) : nullptr;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          u[j][k].load(x + ch0[k], x + ch1[k]);
-          if constexpr (GRAD) v[j][k].load(g + ch0[k], g + ch1[k]);
+          gather<T, P, L>(u[j][k], x, ch[k]);
+          if constexpr (GRAD) gather<T, P, L>(v[j][k], g, ch[k]);
         }
       }
       advance(read);
@@ -348,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
 #pragma unroll
           for (int k = 0; k < K; ++k)
             if (on(k)) {
-              u[j][k].load(src + j * xs + ch0[k], src + j * xs + ch1[k]);
-              if constexpr (GRAD) v[j][k].load(grd + j * gs + ch0[k], grd + j * gs + ch1[k]);
+              gather<T, P, L>(u[j][k], src + j * xs, ch[k]);
+              if constexpr (GRAD) gather<T, P, L>(v[j][k], grd + j * gs, ch[k]);
             }
         }
     }
@@ -416,9 +517,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
               }
             }
             put(u[j][k], y, z);
-            u[j][k].store(dst + j * os + ch0[k], dst + j * os + ch1[k]);
+            scatter<T, P, L>(u[j][k], L == ANY ? reinterpret_cast<T*>(mine + used + j * B::Q * pitch) : dst + j * os, ch[k]);
           }
       }
+    }
+    if constexpr (L == ANY) {
+      // the rows lie whole in the ring again: out as they came in (a lane's next copy goes to
+      // where it has read itself)
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (cur.h + j < cur.h1 && ok) {
+#pragma unroll
+          for (int m = 0; m < B::COPIES; ++m) {
+            const int at = (lane + m * lanes) * 16;
+            if (FULL || at < row_bytes)
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst + j * os) + at) =
+                  *reinterpret_cast<const uint4*>(mine + used + j * B::Q * pitch + at);
+          }
+        }
     }
     cur.h += R;
     dst += R * os;
@@ -439,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const float2 x = unpack2(da[k][i / 2]), y = unpack2(db[k][i / 2]);
-          red[group * p.d + first_of<P, ADJ>(ch0[k], i)] = i % 2 ? x.y : x.x;
-          red[group * p.d + second_of<P, ADJ>(ch0[k], ch1[k], i)] = i % 2 ? y.y : y.x;
+          red[group * p.d + ch[k].first(i)] = i % 2 ? x.y : x.x;
+          red[group * p.d + ch[k].second(i)] = i % 2 ? y.y : y.x;
         }
       }
     __syncthreads();
@@ -453,50 +570,65 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
   }
 }
 
-inline tsr_status launch_one(void (*kern)(NormParams), int smem, unsigned ctas, const NormParams& p, cudaStream_t st) {
-  if (smem > 48 * 1024) TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+template <typename T, int P, int L, int K, bool GRAD, bool FULL>
+tsr_status launch_one(unsigned ctas, const NormParams& p, cudaStream_t st) {
+  constexpr int smem = Batch<T, P, K, GRAD>::SMEM;
+  auto kern = norm_rope_kernel<T, P, L, K, GRAD, FULL>;
+  if constexpr (smem > 48 * 1024) {
+    static bool set[64] = {};              // per device: the attribute is the function's there
+    int dev = 0;
+    TSR_CUDA(cudaGetDevice(&dev));
+    if (dev >= 64 || !set[dev]) {
+      TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      if (dev < 64) set[dev] = true;
+    }
+  }
   kern<<<ctas, kThreads, smem, st>>>(p);
   TSR_CUDA(cudaGetLastError());
   return TSR_OK;
 }
 
+// Pairs per unit, how they lie, and units of a row in each of its lanes.
+struct Shape {
+  int P, L, K;
+};
+
 template <bool GRAD>
-tsr_status launch(const NormParams& p, int dtype, bool halves, int P, int K, cudaStream_t st) {
+tsr_status launch(const NormParams& p, int dtype, const Shape& s, cudaStream_t st) {
   const unsigned ctas = static_cast<unsigned>(p.cta0[p.n_tensors]);
-  const bool full = P > 1 && p.ang.units == K << p.lanes_log2 && p.ang.n_pairs == p.ang.units * P;
-#define TSR_NORM_ONE(T, P_, ADJ_, K_, FULL_)                                                          \
-  if (P == P_ && halves != ADJ_ && K == K_ && full == FULL_)                                          \
-    return launch_one(norm_rope_kernel<T, P_, ADJ_, K_, GRAD, FULL_>, Batch<T, P_, ADJ_, K_, GRAD>::SMEM, ctas, p, st);
-#define TSR_NORM(T, P_, ADJ_, K_)         \
-  TSR_NORM_ONE(T, P_, ADJ_, K_, false)    \
-  if constexpr (P_ > 1) {                 \
-    TSR_NORM_ONE(T, P_, ADJ_, K_, true)   \
+  const bool full = s.P > 1 && p.ang.units == s.K << p.lanes_log2 && p.ang.n_pairs == p.ang.units * s.P;
+#define TSR_NORM(T, P_, L_, K_)                                                                    \
+  if (s.P == P_ && s.L == L_ && s.K == K_) {                                                       \
+    if constexpr (P_ > 1) {                                                                        \
+      if (full) return launch_one<T, P_, L_, K_, GRAD, true>(ctas, p, st);                         \
+    }                                                                                              \
+    return launch_one<T, P_, L_, K_, GRAD, false>(ctas, p, st);                                    \
   }
 #define TSR_NORM_16(T)      \
-  TSR_NORM(T, 4, true, 1)   \
-  TSR_NORM(T, 1, true, 4)   \
-  TSR_NORM(T, 4, false, 1)  \
-  TSR_NORM(T, 1, false, 4)
+  TSR_NORM(T, 4, NEAR, 1)   \
+  TSR_NORM(T, 4, HALVES, 1) \
+  TSR_NORM(T, 4, ANY, 1)    \
+  TSR_NORM(T, 1, HALVES, 4)
   if (dtype == TSR_DTYPE_BF16) {
     TSR_NORM_16(__nv_bfloat16)
   } else if (dtype == TSR_DTYPE_F16) {
     TSR_NORM_16(__half)
   } else {
-    TSR_NORM(float, 2, true, 1)
-    TSR_NORM(float, 2, true, 2)
-    TSR_NORM(float, 1, true, 4)
-    TSR_NORM(float, 4, false, 1)
-    TSR_NORM(float, 1, false, 4)
+    TSR_NORM(float, 2, NEAR, 1)
+    TSR_NORM(float, 2, NEAR, 2)
+    TSR_NORM(float, 4, HALVES, 1)
+    TSR_NORM(float, 2, ANY, 1)
+    TSR_NORM(float, 2, ANY, 2)
+    TSR_NORM(float, 1, HALVES, 4)
   }
 #undef TSR_NORM_16
 #undef TSR_NORM
-#undef TSR_NORM_ONE
   return fail(TSR_ERR_INTERNAL, "no norm kernel for this layout");
 }
 
 // The forward's kernels (norm_rope.cu) and the backward's (norm_rope_bwd.cu) are compiled apart.
-extern template tsr_status launch<false>(const NormParams&, int, bool, int, int, cudaStream_t);
-extern template tsr_status launch<true>(const NormParams&, int, bool, int, int, cudaStream_t);
+extern template tsr_status launch<false>(const NormParams&, int, const Shape&, cudaStream_t);
+extern template tsr_status launch<true>(const NormParams&, int, const Shape&, cudaStream_t);
 
 }  // namespace norm
 
