@@ -135,7 +135,7 @@ tsr_status launch_norm_rope(const tsr_rope_desc& d, double eps, const tsr_norm_r
   const Shape s = fill(d, eps, t, n, false, p);
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  spread(p, num_sms(dev) * ctas_per_sm(false, s.P));
+  spread(p, num_sms(dev) * ctas_per_sm(false, s.P, s.L));
   return launch<false>(p, d.dtype, s, st);
 }
 
@@ -151,7 +151,7 @@ tsr_status launch_norm_rope_backward(const tsr_rope_desc& d, double eps, const t
   const Shape s = fill(d, eps, t, n, true, p);
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  spread(p, std::min(num_sms(dev), 256) * ctas_per_sm(true, s.P));
+  spread(p, std::min(num_sms(dev), 256) * ctas_per_sm(true, s.P, s.L));
   SumParams q;
   memset(&q, 0, sizeof q);
   bool any = false;

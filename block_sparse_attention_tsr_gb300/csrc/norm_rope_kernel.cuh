@@ -16,9 +16,12 @@
 //
 // The row's sums stand between its loads and its stores, so loads held in registers leave
 // the memory idle in between (480p forward 199 us, 720p backward 876).  Every thread
-// therefore has 64 bytes in each of the three stages of a ring in shared memory, which
-// cp.async fills two stages ahead, across heads and tokens, at no cost in registers; the
-// lanes that share a row need the warp's barrier only.
+// therefore has 32 bytes (backward: of both rows, 64) in each of the two stages of a ring in
+// shared memory, which cp.async fills one stage ahead, across heads and tokens, at no cost in
+// registers; the lanes that share a row need the warp's barrier only.  A third stage only
+// adds instructions and rows in flight (forward 126 -> 127 us, backward 426 -> 465).
+// 32,760 tokens of 12 + 12 heads of 128, forward: 126 us, 6.4 TB/s, 94% of a copy's rate;
+// 56,700 tokens backward: 426 us, 6.5 TB/s, 97%.
 //
 // dw: a thread sums its channels over all rows it meets in fp32, the CTA adds its groups
 // in shared memory and stores one partial row, and a dependent kernel adds the CTAs' rows
@@ -36,9 +39,15 @@ using rope::kMaxTensors;
 using rope::Unit;
 
 constexpr int kThreads = 256;
-constexpr int kStages = 3;
-// CTAs that an SM holds, by registers
-constexpr int ctas_per_sm(bool grad, int P) { return grad || P == 1 ? 2 : 3; }
+constexpr int kStages = 2;
+// How a unit's pairs lie in a row: NEAR, neighbouring channels; HALVES, two pieces of P
+// channels; ANY, pair by pair (half-split pairs whose half widths are no whole pieces), which
+// are gathered from the ring's row and put back there before it is stored.
+enum Layout { NEAR, HALVES, ANY };
+
+// CTAs that an SM holds, by registers: a third one where 80 a thread are enough (forward
+// 141 -> 126 us; ANY's gathers need more, 80 -> 87)
+constexpr int ctas_per_sm(bool grad, int P, int L) { return grad || P == 1 || L == ANY ? 2 : 3; }
 
 struct NormParams {
   const void* x[kMaxTensors];
@@ -125,11 +134,6 @@ __device__ __forceinline__ void put(Unit<T, P, ADJ>& u, const F2 (&a)[(P + 1) / 
   }
 }
 
-// How a unit's pairs lie in a row: NEAR, neighbouring channels; HALVES, two pieces of P
-// channels; ANY, pair by pair (half-split pairs whose half widths are no whole pieces), which
-// are gathered from the ring's row and put back there before it is stored.
-enum Layout { NEAR, HALVES, ANY };
-
 // Channels of a unit's pair i.  at: a unit's first channels, first and second piece; of ANY
 // each pair's, 16 bits each.
 template <int P, int L>
@@ -194,12 +198,16 @@ __device__ __forceinline__ float weight_at(const NormParams& p, int t, int c) {
 }
 
 // What a thread copies and holds of a row, and how many rows at a time.
-template <typename T, int P, int K, bool GRAD>
+template <typename T, int P, int L, int K, bool GRAD>
 struct Batch {
   static constexpr bool RING = P > 1;
   static constexpr int Q = GRAD ? 2 : 1;                                     // rows of x, and of dy
   static constexpr int COPIES = RING ? K * 2 * P * static_cast<int>(sizeof(T)) / 16 : 0;   // of 16 bytes of a row
-  static constexpr int R = !RING ? (GRAD ? 1 : 2) : 64 / (Q * COPIES * 16) < 1 ? 1 : 64 / (Q * COPIES * 16);
+  // Two rows at a time in 16 bits: forward four leave registers for two CTAs only (126 -> 141
+  // us), backward one is too few (426 -> 515 us), but enough where pairs are gathered (of two
+  // 119 -> 195).
+  static constexpr int BYTES = GRAD && L != ANY ? 64 : 32;
+  static constexpr int R = !RING ? (GRAD ? 1 : 2) : BYTES < Q * COPIES * 16 ? 1 : BYTES / (Q * COPIES * 16);
   static constexpr int SLOT = R * Q * COPIES * 16 * kThreads;                // a stage of the CTA
   static constexpr int RED = GRAD ? 512 * P * K * 4 : 0;                     // weight gradients of its groups
   static constexpr int TABLE = kStages * SLOT > RED ? kStages * SLOT : RED;  // frequencies, axes behind it
@@ -219,8 +227,8 @@ struct Place {
 // K units in each of 2^lanes_log2 lanes.  FULL: every lane has its K units and all their
 // pairs turn.
 template <typename T, int P, int L, int K, bool GRAD, bool FULL>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kernel(const __grid_constant__ NormParams p) {
-  using B = Batch<T, P, K, GRAD>;
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P, L)) norm_rope_kernel(const __grid_constant__ NormParams p) {
+  using B = Batch<T, P, L, K, GRAD>;
   constexpr int R = B::R, NP = (P + 1) / 2;
   extern __shared__ __align__(16) uint8_t smem[];
   const int lanes = 1 << p.lanes_log2;
@@ -572,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P)) norm_rope_kern
 
 template <typename T, int P, int L, int K, bool GRAD, bool FULL>
 tsr_status launch_one(unsigned ctas, const NormParams& p, cudaStream_t st) {
-  constexpr int smem = Batch<T, P, K, GRAD>::SMEM;
+  constexpr int smem = Batch<T, P, L, K, GRAD>::SMEM;
   auto kern = norm_rope_kernel<T, P, L, K, GRAD, FULL>;
   if constexpr (smem > 48 * 1024) {
     static bool set[64] = {};              // per device: the attribute is the function's there
