@@ -27,13 +27,12 @@ template <int BN>
 __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ GemmParams p) {
   constexpr int VECS = BN / 8;
   const int64_t i = blockIdx.x * 256ll + threadIdx.x;
-  const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole;
-  const int64_t cut = i / (256 * VECS);
+  const int64_t rest = p.by_cut.d, cut = i / (256 * VECS);
   const int32_t row = static_cast<int32_t>(i / VECS) % 256, c = static_cast<int32_t>(i % VECS) * 8;
   grid_wait();
   if (cut >= rest) return;
-  const int2 rc = tile_of(p, p.whole + cut);
-  const int32_t b = rc.x / p.tiles_per_batch, n = (rc.x - b * p.tiles_per_batch) * 256 + row, f = rc.y * BN + c;
+  const int2 rc = tile_of(p, p.whole + static_cast<uint32_t>(cut));
+  const int32_t b = p.by_batch(rc.x), n = (rc.x - b * static_cast<int32_t>(p.by_batch.d)) * 256 + row, f = rc.y * BN + c;
   if (n >= p.n_rows || f >= p.cols) return;
   float v[8] = {};
   for (int32_t s = 0; s < p.splits; ++s) {
@@ -288,10 +287,10 @@ tsr_status launch_clusters(void (*kern)(GemmParams), bool (&set)[64], int smem, 
 template <int BN, bool A_MN, bool B_MN>
 tsr_status launch_pairs(const GemmParams& p, cudaStream_t st) {
   static bool set[64] = {};
-  const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.col_tiles, rest = tiles - p.whole;
+  const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole;
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  const int64_t pairs = std::min<int64_t>(p.whole + rest * p.splits, num_sms(dev) / 2);
+  const int64_t pairs = std::min<int64_t>(p.units, num_sms(dev) / 2);
   if (tsr_status e = launch_clusters(linear_gemm_kernel<BN, A_MN, B_MN>, set, Cfg<BN>::SMEM, pairs * 2, 2, p, st)) return e;
   if (rest)
     TSR_CUDA(launch_dependent(linear_finish_kernel<BN>, static_cast<unsigned>(rest * BN / 8), 256u, 0, st, p));
@@ -330,21 +329,33 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   p.batches = static_cast<int32_t>(q.batches);
   p.cols = static_cast<int32_t>(q.cols);
   p.splits = c.splits;
-  p.whole = c.whole;
   p.k_steps = static_cast<int32_t>(q.k_steps);
+  p.k_each = static_cast<uint32_t>(q.k_steps / c.splits);
+  p.k_more = static_cast<uint32_t>(q.k_steps % c.splits);
   p.k_steps_per_batch = static_cast<int32_t>(cdiv(y.N, BK));
-  p.group = 8;
   p.late = late;
   p.stall = g_stall;
   p.timeout_ns = g_stall ? kStallNs : kWaitTimeoutNs;
   const int bn = c.variant == PAIR_256 ? 256 : c.variant == FEW_32 ? 32 : 128;
-  p.tiles_per_batch = static_cast<int32_t>(cdiv(q.n_rows, few ? bn : 256));
-  p.row_tiles = p.tiles_per_batch * p.batches;
-  p.col_tiles = static_cast<int32_t>(cdiv(q.cols, few ? 128 : bn));
-  if (few) std::swap(p.row_tiles, p.col_tiles);
+  const int64_t per_batch = cdiv(q.n_rows, few ? bn : 256), col_tiles = cdiv(q.cols, few ? 128 : bn);
+  const int64_t tiles = per_batch * q.batches * col_tiles, rest = tiles - c.whole;
+  if (c.whole + rest * c.splits > INT32_MAX) return fail(TSR_ERR_UNSUPPORTED, "a linear layer of too many tiles");
+  p.row_tiles = static_cast<int32_t>(per_batch * q.batches);
+  p.col_tiles = static_cast<int32_t>(col_tiles);
+  p.by_batch = div_by(static_cast<uint32_t>(per_batch));
+  if (few) {
+    std::swap(p.row_tiles, p.col_tiles);
+  } else {
+    p.whole = static_cast<uint32_t>(c.whole);
+    p.units = static_cast<uint32_t>(c.whole + rest * c.splits);
+    // of one group that holds all tiles only the remainders are taken
+    p.by_group = div_by(static_cast<uint32_t>(std::min<int64_t>(kGroup * col_tiles, INT32_MAX)));
+    p.by_cut = div_by(static_cast<uint32_t>(std::max<int64_t>(rest, 1)));
+    p.out_dim = div_by(e.vout.dim);
+  }
   CUtensorMap *mt = few ? &p.tb : &p.ta, *mo = few ? &p.ta : &p.tb;
-  (few ? p.b_dim : p.a_dim) = vtok.dim;
-  (few ? p.a_dim : p.b_dim) = vother.dim;
+  (few ? p.b_dim : p.a_dim) = div_by(vtok.dim);
+  (few ? p.a_dim : p.b_dim) = div_by(vother.dim);
   const bool tok_mn = kind == DWEIGHT, other_mn = kind != FORWARD;
   const int tok_rows = tok_mn ? BK : few ? bn : 128, other_rows = other_mn ? BK : few ? 128 : bn / 2;
   if (tsr_status s = encode(mt, tok, vtok, tok_heads, y.N, y.B, BK, tok_rows, y.f16)) return s;
@@ -362,7 +373,6 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
       if (e.res)
         if (tsr_status s = encode(&p.tres, e.res, e.vres, heads, rows, q.batches, width, 32, y.f16)) return s;
     }
-    const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - c.whole;
     if (rest)
       if (tsr_status s = encode(&p.tpart, p.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, {bn, 256, rest, c.splits},
                                 {bn, 256 * bn, rest * 256 * bn}, 32, 32))

@@ -51,6 +51,19 @@ struct View {
   int32_t dim;                         // channels per head
 };
 
+// Quotients of n < 2^31 by a number that the host knows, by its reciprocal: with 2^(l-1) < d
+// <= 2^l and m = floor(2^(31+l) / d) + 1, n m / 2^(31+l) exceeds n / d by less than 1 / d.  A
+// division costs some 200 clocks; a tile of few steps waited for five, in every warp.
+struct Div {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return d == 1 ? n : __umulhi(n, mul) >> shift; }
+};
+inline Div div_by(uint32_t d) {
+  uint32_t l = 0;
+  while (1ull << l < d) ++l;
+  return {d, d == 1 ? 0u : static_cast<uint32_t>((1ull << (31 + l)) / d + 1), d == 1 ? 0u : l - 1};
+}
+
 // What happens to a value of D on its way out.
 struct Epilogue {
   const void *bias, *res;              // null: none
@@ -66,15 +79,16 @@ struct GemmParams {
   CUtensorMap tout, tpre, tres, tpart;
   Epilogue epi;
   float* part;                         // [splits][tiles - whole][256][BN]
-  int64_t whole;                       // tiles that are not cut along k: the first ones
+  uint32_t whole, units;               // tiles that are not cut along k: the first ones; all work units
   int32_t n_rows, batches;             // rows per batch (tokens, or features)
   int32_t cols;
   int32_t row_tiles, col_tiles;        // row tiles of all batches
-  int32_t tiles_per_batch;             // of the token axis
+  Div by_batch;                        // row tiles per batch
+  Div by_group, by_cut;                // tiles that take turns (tile_of); tiles that are cut
   int32_t splits, k_steps;             // k steps of a whole product
+  uint32_t k_each, k_more;             // k steps of a part; parts that have one more
   int32_t k_steps_per_batch;           // dweight: steps of one batch's tokens
-  int32_t a_dim, b_dim;                // channels per head of A's and B's tensors
-  int32_t group;                       // row tiles that share their columns' loads in L2
+  Div a_dim, b_dim, out_dim;           // channels per head of A's, B's and out's tensors
   uint32_t idesc;
   int32_t late;                        // what is before on the stream is not an input: waited for at the end
   int32_t stall;                       // test only: the issuer waits for ever after its first step
@@ -245,38 +259,36 @@ struct alignas(8) Ctrl {
 };
 static_assert(sizeof(Ctrl) <= 512, "Ctrl");
 
-// Row and column of tile t: `group` row tiles at a time, their columns one after another,
-// so that the CTAs that run together share rows and columns in L2.
-__device__ __forceinline__ int2 tile_of(const GemmParams& p, int64_t t) {
-  const int64_t per = static_cast<int64_t>(p.group) * p.col_tiles;
-  const int32_t g = static_cast<int32_t>(t / per);
-  const int32_t rows = min(p.group, p.row_tiles - g * p.group);
-  const int32_t in = static_cast<int32_t>(t - g * per);
-  return make_int2(g * p.group + in % rows, in / rows);
+// Row and column of tile t: eight row tiles at a time, their columns one after another, so
+// that the CTAs that run together share rows and columns in L2.
+constexpr uint32_t kGroup = 8;
+__device__ __forceinline__ int2 tile_of(const GemmParams& p, uint32_t t) {
+  const uint32_t g = p.by_group(t), in = t - g * p.by_group.d, row = g * kGroup, rows = p.row_tiles - row;
+  if (rows >= kGroup) return make_int2(row + in % kGroup, in / kGroup);
+  const uint32_t col = in / rows;
+  return make_int2(row + (in - col * rows), col);
 }
 // A work unit: a tile and its part of k.
 struct Unit {
   int32_t row_tile, col_tile, cut, split, k0, k1;         // cut: the tile's number among the cut ones, or -1
 };
-__device__ __forceinline__ int64_t units_of(const GemmParams& p) {
-  return p.whole + (static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole) * p.splits;
-}
-__device__ __forceinline__ Unit unit_of(const GemmParams& p, int64_t u) {
-  Unit w;
-  int64_t t = u;
+__device__ __forceinline__ void steps_of(const GemmParams& p, uint32_t u, Unit& w) {
   w.cut = -1;
   w.split = 0;
   w.k0 = 0;
   w.k1 = p.k_steps;
   if (u >= p.whole) {
-    const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole;
-    w.split = static_cast<int32_t>((u - p.whole) / rest);
-    w.cut = static_cast<int32_t>(u - p.whole - w.split * rest);
-    t = p.whole + w.cut;
-    w.k0 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * w.split / p.splits);
-    w.k1 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * (w.split + 1) / p.splits);
+    const uint32_t split = p.by_cut(u - p.whole);
+    w.split = split;
+    w.cut = u - p.whole - split * p.by_cut.d;
+    w.k0 = split * p.k_each + min(split, p.k_more);
+    w.k1 = w.k0 + p.k_each + (split < p.k_more);
   }
-  const int2 rc = tile_of(p, t);
+}
+__device__ __forceinline__ Unit unit_of(const GemmParams& p, uint32_t u) {
+  Unit w;
+  steps_of(p, u, w);
+  const int2 rc = tile_of(p, w.cut < 0 ? u : p.whole + w.cut);
   w.row_tile = rc.x;
   w.col_tile = rc.y;
   return w;
@@ -289,19 +301,19 @@ struct Walk {
   int32_t dim, c[MN ? G : 1], h[MN ? G : 1], n, b, chunk, chunks;
   // f0: first row (K-major) or channel (MN-major); chunks: k steps of a batch's tokens, 0:
   // k has no batches
-  __device__ __forceinline__ Walk(int32_t dim_, int32_t f0, int32_t k0, int32_t chunks_, int32_t batch)
-      : dim(dim_), chunks(chunks_) {
+  __device__ __forceinline__ Walk(const Div& by, int32_t f0, int32_t k0, int32_t chunks_, int32_t batch)
+      : dim(by.d), chunks(chunks_) {
     if constexpr (MN) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        h[g] = (f0 + 64 * g) / dim;
+        h[g] = by(f0 + 64 * g);
         c[g] = f0 + 64 * g - h[g] * dim;
       }
-      b = chunks ? k0 / chunks : 0;
+      b = chunks && k0 >= chunks ? k0 / chunks : 0;
       chunk = k0 - b * chunks;
       n = chunk * BK;
     } else {
-      h[0] = k0 * BK / dim;
+      h[0] = by(k0 * BK);
       c[0] = k0 * BK - h[0] * dim;
       n = f0;
       b = batch;
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   // this kernel's end (so that no kernel behind this one starts before it has ended)
   if (!p.late) grid_wait();
   grid_launch_dependents();
-  const int64_t units = units_of(p), first = blockIdx.x / 2, stride = gridDim.x / 2;
+  const uint32_t units = p.units, first = blockIdx.x / 2, stride = gridDim.x / 2;
 
   if (warp == 0) {
     // The whole warp runs the loop and one lane acts, so that the copies' addresses and
@@ -385,11 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     int st = 0;
     uint32_t parity = 1u;                                 // of the wait for an empty stage
     bool ok = true;
-    for (int64_t u = first; ok && u < units; u += stride) {
+    for (uint32_t u = first; ok && u < units; u += stride) {
       const Unit w = unit_of(p, u);
       // token rows: tiles of each batch by themselves (dweight: rows are features, k tokens)
-      const int32_t b = A_MN ? 0 : w.row_tile / p.tiles_per_batch;
-      const int32_t row0 = (w.row_tile - b * p.tiles_per_batch) * C::TM + rank * 128;
+      const int32_t b = A_MN ? 0 : p.by_batch(w.row_tile);
+      const int32_t row0 = (w.row_tile - b * static_cast<int32_t>(p.by_batch.d)) * C::TM + rank * 128;
       const int32_t col0 = w.col_tile * BN + rank * C::B_ROWS;
       Walk<A_MN, 2> ca(p.a_dim, row0, w.k0, A_MN ? p.k_steps_per_batch : 0, b);
       Walk<B_MN, C::B_ROWS / 64> cb(p.b_dim, col0, w.k0, A_MN ? p.k_steps_per_batch : 0, 0);
@@ -423,8 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       uint32_t parity = 0u;
       int32_t tile = 0;
       bool ok = true;
-      for (int64_t u = first; ok && u < units; u += stride, ++tile) {
-        const Unit w = unit_of(p, u);
+      for (uint32_t u = first; ok && u < units; u += stride, ++tile) {
+        Unit w;
+        steps_of(p, u, w);
         const int buf = tile & 1;
         if (!mbar_wait_warp(smem_u32(&ctrl.acc_empty[buf]), ((tile >> 1) & 1) ^ 1, abort_flag, &g_err, p.timeout_ns)) break;
         tc_fence_after();
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     uint32_t res_phase = 0u, res_issued = 0u;              // of the residual's pieces
     uint32_t turn = 0u;                                    // pieces take turns, from tile to tile
     int32_t tile = 0;
-    for (int64_t u = first; u < units; u += stride, ++tile) {
+    for (uint32_t u = first; u < units; u += stride, ++tile) {
       const Unit w = unit_of(p, u);
       const int buf = tile & 1;
       const uint32_t acc = tmem + lanes + buf * BN;
@@ -473,41 +486,48 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         tc_fence_after();
       }
       {
-        const int32_t b = A_MN ? 0 : w.row_tile / p.tiles_per_batch;
-        const int32_t n0 = (w.row_tile - b * p.tiles_per_batch) * C::TM + rank * 128 + quarter * 32;
+        const int32_t b = A_MN ? 0 : p.by_batch(w.row_tile);
+        const int32_t n0 = (w.row_tile - b * static_cast<int32_t>(p.by_batch.d)) * C::TM + rank * 128 + quarter * 32;
         constexpr int W = BN / 2;                                   // columns of this warp
         const int32_t f0 = w.col_tile * BN + half * W;
         const bool inside = n0 < p.n_rows;
         const uint32_t pieces = base + C::OUT + ew * 2 * C::PIECE;
         if (w.cut >= 0) {
 #pragma unroll 1
-          for (int c = 0; c < W; c += 32) {
+          for (int c = 0; c < W; c += 64) {
             if (f0 + c >= p.cols || !inside) break;
-            uint32_t v[32];
-            tmem_ld32(acc + half * W + c, v);
-            const uint32_t q = pieces + (turn++ & 1u) * C::PIECE;
-            bulk_wait_read<1>();                                    // the piece before the last has left
-            __syncwarp();
+            uint32_t v[2][32];
+            tmem_ld32(acc + half * W + c, v[0]);
+            tmem_ld32(acc + half * W + c + 32, v[1]);
             tc_wait_ld();
-            // a lane's row of 128 bytes, 16 each, swizzled as TMA reads it
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              sts128(q + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-            fence_proxy_async_smem();
-            __syncwarp();
-            tma_store_4d(elect, &p.tpart, q, half * W + c, rank * 128 + quarter * 32, w.cut, w.split);
-            bulk_commit(elect);
+            for (int j = 0; j < 2; ++j) {
+              if (f0 + c + j * 32 >= p.cols) break;
+              const uint32_t q = pieces + (turn++ & 1u) * C::PIECE;
+              bulk_wait_read<1>();                                  // the piece before the last has left
+              __syncwarp();
+              // a lane's row of 128 bytes, 16 each, swizzled as TMA reads it
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                sts128(q + lane * 128 + ((i ^ (lane & 7)) << 4),
+                       make_uint4(v[j][4 * i], v[j][4 * i + 1], v[j][4 * i + 2], v[j][4 * i + 3]));
+              fence_proxy_async_smem();
+              __syncwarp();
+              tma_store_4d(elect, &p.tpart, q, half * W + c + j * 32, rank * 128 + quarter * 32, w.cut, w.split);
+              bulk_commit(elect);
+            }
           }
         } else {
-          const bool pre = p.epi.pre != nullptr, res = p.epi.res != nullptr;
-          const int dim = p.epi.vout.dim;
+          const bool pre = p.epi.pre != nullptr, res = p.epi.res != nullptr, plain = !pre && !res && !p.epi.bias;
+          const int dim = p.out_dim.d;
+          int32_t h = p.out_dim(f0), ch = f0 - h * dim;
           // a step takes a piece: 64 columns, or with pre 32, pre's in its first half and out's
           // in the second; a residual lands where out's will be
           const int width = pre ? 32 : 64, half_piece = pre ? C::PIECE / 2 : 0;
           const int steps = !inside || f0 >= p.cols ? 0 : (min(W, p.cols - f0) + width - 1) / width;
           auto load_res = [&](int s) {
             const uint32_t k = (turn + s) & 1u, bar = smem_u32(&ctrl.res_full[ew][k]);
-            const int32_t f = f0 + s * width, h = f / dim;
+            const int32_t f = f0 + s * width, h = p.out_dim(f);
             mbar_arrive_expect_tx(elect, bar, width * 64);
             tma_load_4d(elect, pieces + k * C::PIECE + half_piece, &p.tres, bar, f - h * dim, n0, h, b);
             res_issued |= 1u << k;
@@ -528,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             }
           };
           columns(0);
-          int32_t h = f0 / dim, ch = f0 - h * dim;
 #pragma unroll 1
           for (int s = 0; s < steps; ++s) {
             const int n = pre ? 1 : 2;                              // 32 columns each
@@ -561,6 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             const uint32_t q_pre = pieces + k * C::PIECE, q = q_pre + half_piece;
             const uint32_t row = lane * (pre ? 64 : 128), turned = pre ? (lane >> 1) & 3 : lane & 7;
             by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) {
+              if constexpr (act.value == TSR_ACT_NONE) {
+                if (plain) {
+#pragma unroll
+                  for (int g = 0; g < 8; ++g) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[g >> 2][8 * (g & 3) + i]);
+                    sts128(q + row + ((g ^ turned) << 4), pack8<f16.value>(x));
+                  }
+                  return;
+                }
+              }
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 if (j < n) {
@@ -676,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<BN>::CTAS) linear_few_kernel(
   grid_launch_dependents();
   const int32_t tile = static_cast<int32_t>(blockIdx.x) / p.splits;
   const int32_t f_tile = tile % p.row_tiles, t_tile = tile / p.row_tiles;
-  const int32_t b = t_tile / p.tiles_per_batch, n0 = (t_tile - b * p.tiles_per_batch) * BN;
+  const int32_t b = p.by_batch(t_tile), n0 = (t_tile - b * static_cast<int32_t>(p.by_batch.d)) * BN;
   const int32_t k0 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * rank / p.splits);
   const int32_t k1 = static_cast<int32_t>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.splits);
   if (warp == 0) {
