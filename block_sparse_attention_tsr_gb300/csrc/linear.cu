@@ -22,32 +22,49 @@ constexpr int kSms = 152;              // what the choice of tiles is made for
 constexpr uint64_t kStallNs = 20000000;    // bound of the waits of a stalled product (test only)
 thread_local int32_t g_stall = 0;
 
-// D's values of the tiles that were cut along k, from their parts.  HBM/L2-bound.
-template <int BN>
+// D's values of the tiles that were cut along k, from their parts, in their order.  L2-bound;
+// of eight parts and more, eight groups of threads add up an eighth each (a loop over 76 of
+// them alone took 10 us of 20, 128 x 128 from 32,760 tokens; 14 in all now).
+constexpr int kGroupedParts = 8;
+template <int BN, int G>
 __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ GemmParams p) {
-  constexpr int VECS = BN / 8;
-  const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+  constexpr int VECS = BN / 8, EACH = 256 / G;
+  __shared__ float red[G > 1 ? G : 1][G > 1 ? EACH : 1][8];
+  const int at = threadIdx.x % EACH, g = threadIdx.x / EACH;
+  const int64_t i = blockIdx.x * static_cast<int64_t>(EACH) + at;
   const int64_t rest = p.by_cut.d, cut = i / (256 * VECS);
   const int32_t row = static_cast<int32_t>(i / VECS) % 256, c = static_cast<int32_t>(i % VECS) * 8;
   grid_wait();
-  if (cut >= rest) return;
-  const int2 rc = tile_of(p, p.whole + static_cast<uint32_t>(cut));
+  const int2 rc = tile_of(p, p.whole + static_cast<uint32_t>(min(cut, rest - 1)));
   const int32_t b = p.by_batch(rc.x), n = (rc.x - b * static_cast<int32_t>(p.by_batch.d)) * 256 + row, f = rc.y * BN + c;
-  if (n >= p.n_rows || f >= p.cols) return;
+  const bool on = cut < rest && n < p.n_rows && f < p.cols;
   float v[8] = {};
-  for (int32_t s = 0; s < p.splits; ++s) {
-    const float4* src = reinterpret_cast<const float4*>(p.part + ((s * rest + cut) * 256 + row) * BN + c);
-    const float4 x = src[0], y = src[1];
-    v[0] += x.x;
-    v[1] += x.y;
-    v[2] += x.z;
-    v[3] += x.w;
-    v[4] += y.x;
-    v[5] += y.y;
-    v[6] += y.z;
-    v[7] += y.w;
+  if (on) {
+    const int32_t s1 = p.splits * (g + 1) / G;
+#pragma unroll 4
+    for (int32_t s = p.splits * g / G; s < s1; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(p.part + ((s * rest + cut) * 256 + row) * BN + c);
+      const float4 x = src[0], y = src[1];
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
+      v[3] += x.w;
+      v[4] += y.x;
+      v[5] += y.y;
+      v[6] += y.z;
+      v[7] += y.w;
+    }
   }
-  by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(p.epi, v, b, n, f); });
+  if constexpr (G > 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) red[g][at][k] = v[k];
+    __syncthreads();
+    if (g) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      for (int h = 1; h < G; ++h) v[k] += red[h][at][k];
+  }
+  if (on) by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(p.epi, v, b, n, f); });
 }
 
 struct DzParams {
@@ -161,7 +178,9 @@ Choice choose(const Product& q) {
     const bool few = v >= FEW_32;
     if (few && (q.kind == DWEIGHT || q.batches * q.n_rows > 512)) continue;   // fitted up to 300 tokens
     const int64_t tiles = q.batches * cdiv(q.n_rows, kTok[v]) * cdiv(q.cols, kFeat[v]);
-    for (int64_t s = 1; s <= (few ? 8 : 16) && (s == 1 || q.k_steps >= 4 * s); s += few ? s : 1) {
+    // more than 16 parts only of tiles that are too few for the pairs
+    for (int64_t s = 1; s <= (few ? 8 : std::max<int64_t>(16, kSms / 2 / tiles)) && (s == 1 || q.k_steps >= 4 * s);
+         s += few ? s : 1) {
       const int64_t slots = !few ? kSms / 2 : v == FEW_32 ? (s < 4 ? 300 : 256) : s == 8 ? 96 : s == 4 ? 128 : 150;
       const int64_t whole = s == 1 ? tiles : few ? 0 : tiles / slots * slots, rest = tiles - whole;
       if (s > 1 && !rest) continue;
@@ -213,6 +232,7 @@ void flatten(Layer& y, View* const* views, int n) {
 size_t most_parts(const tsr_linear_desc& d, Kind kind) {
   Layer y = layer_of(d);
   const size_t a = part_bytes(product(y, kind));
+  if (y.B == 1) return a;
   y.N *= y.B;
   y.B = 1;
   return std::max(a, part_bytes(product(y, kind)));
@@ -292,8 +312,11 @@ tsr_status launch_pairs(const GemmParams& p, cudaStream_t st) {
   TSR_CUDA(cudaGetDevice(&dev));
   const int64_t pairs = std::min<int64_t>(p.units, num_sms(dev) / 2);
   if (tsr_status e = launch_clusters(linear_gemm_kernel<BN, A_MN, B_MN>, set, Cfg<BN>::SMEM, pairs * 2, 2, p, st)) return e;
-  if (rest)
-    TSR_CUDA(launch_dependent(linear_finish_kernel<BN>, static_cast<unsigned>(rest * BN / 8), 256u, 0, st, p));
+  if (rest) {
+    const bool many = p.splits >= kGroupedParts;
+    TSR_CUDA(launch_dependent(many ? linear_finish_kernel<BN, 8> : linear_finish_kernel<BN, 1>,
+                              static_cast<unsigned>(rest * BN / 8 * (many ? 8 : 1)), 256u, 0, st, p));
+  }
   return TSR_OK;
 }
 template <int BN, bool W_MN>
