@@ -73,14 +73,15 @@ struct DzParams {
   float* part;                         // [row blocks][cols], null: no dbias
   View vdout, vpre;
   int64_t rows;
-  int32_t n_rows, cols, rows_per_block, act, f16;
+  int32_t n_rows, cols, rows_per_block, lanes_log2, act, f16;
 };
 
-// 32 lanes of 8 columns, 8 rows at a time.
+// 8, 16 or 32 lanes of 8 columns, 32, 16 or 8 rows at a time.
 __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const __grid_constant__ DzParams p) {
-  __shared__ float red[8][32][8];
-  const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int32_t f = (blockIdx.x * 32 + lane) * 8;
+  __shared__ float red[256][8];
+  const int lanes = 1 << p.lanes_log2, rows = 256 >> p.lanes_log2;
+  const int lane = threadIdx.x & (lanes - 1), ty = threadIdx.x >> p.lanes_log2;
+  const int32_t f = (blockIdx.x * lanes + lane) * 8;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_block;
   const int64_t r1 = min(r0 + p.rows_per_block, p.rows);
   grid_launch_dependents();
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const __grid_constant
     by_kind(p.f16, p.act, [&](auto f16, auto act) {
       constexpr int kRows = act.value == TSR_ACT_NONE ? 8 : 4;      // in flight
 #pragma unroll kRows
-      for (int64_t r = r0 + ty; r < r1; r += 8) {
+      for (int64_t r = r0 + ty; r < r1; r += rows) {
         int64_t b = 0, n = r;
         if (p.n_rows < p.rows) {
           b = r / p.n_rows;
@@ -110,14 +111,14 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const __grid_constant
     });
   if (!p.part) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[ty][lane][i] = sum[i];
+  for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = sum[i];
   __syncthreads();
-  const int c = threadIdx.x;           // 256 columns of the block
+  const int c = threadIdx.x;           // a column of the block's
+  const int32_t col = blockIdx.x * lanes * 8 + c;
   float s = 0.f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) s += red[k][c >> 3][c & 7];
-  const int32_t col = blockIdx.x * 256 + c;
-  if (col < p.cols) p.part[static_cast<int64_t>(blockIdx.y) * p.cols + col] = s;
+  if (c >= lanes * 8 || col >= p.cols) return;
+  for (int k = 0; k < rows; ++k) s += red[k * lanes + (c >> 3)][c & 7];
+  p.part[static_cast<int64_t>(blockIdx.y) * p.cols + col] = s;
 }
 
 // Column sums of the row blocks' sums: 32 columns a CTA, 32 rows at a time.
@@ -406,9 +407,18 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   return launch_kind<true, true>(c.variant, p, st);
 }
 
-// Blocks of rows of the pass over dz: one wave of the four CTAs that an SM holds (twice as
-// many and one more took 253 us for 233 of 32,760 x 8,192).
-int64_t dz_blocks(int64_t T, int64_t M) { return std::max<int64_t>(1, std::min(cdiv(T, 32), kSms * 4 / cdiv(M, 256))); }
+// Lanes of a row in the pass over dz: as many as leave the fewest idle.
+int dz_lanes_log2(int64_t M) {
+  int best = 5;
+  for (int l = 4; l >= 3; --l)
+    if (cdiv(M, 8 << l) << l < cdiv(M, 8 << best) << best) best = l;
+  return best;
+}
+// Blocks of rows of it: one wave of the four CTAs that an SM holds (twice as many and one
+// more took 253 us for 233 of 32,760 x 8,192).
+int64_t dz_blocks(int64_t T, int64_t M) {
+  return std::max<int64_t>(1, std::min(cdiv(T, 32), kSms * 4 / cdiv(M, 8 << dz_lanes_log2(M))));
+}
 
 struct BackwardSpace {
   size_t dz, sums, parts, total;
@@ -487,9 +497,10 @@ tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_gra
     p.act = d.activation;
     p.f16 = y.f16;
     int64_t blocks = dz_blocks(p.rows, y.M);
+    p.lanes_log2 = dz_lanes_log2(y.M);
     p.rows_per_block = static_cast<int32_t>(cdiv(p.rows, blocks));
     blocks = cdiv(p.rows, p.rows_per_block);
-    linear_dz_kernel<<<dim3(static_cast<unsigned>(cdiv(y.M, 256)), static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
+    linear_dz_kernel<<<dim3(static_cast<unsigned>(cdiv(y.M, 8 << p.lanes_log2)), static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
     TSR_CUDA(cudaGetLastError());
     if (a.dbias)
       TSR_CUDA(launch_dependent(linear_bias_kernel, static_cast<unsigned>(cdiv(y.M, 32)), 1024u, 0, st,
