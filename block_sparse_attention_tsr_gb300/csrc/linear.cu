@@ -164,14 +164,14 @@ struct Product {
 
 // The fastest by a model in microseconds, fitted to 490 timed products (forward, dx and
 // dweight, 1 to 8,000 tokens, 256 to 8,192 features; 13% off in the root mean square, and
-// its choice on average within 1.5% of the fastest): waves of units, each its k steps and a
+// its choice on average within 1% of the fastest, of 44 other layers too): waves of units, each its k steps and a
 // fill and an epilogue; where pairs' tiles are cut a launch and the parts' traffic.  With 32
 // tokens 70 CTAs take what the L2 gives; clusters of 4 and 8 CTAs leave SMs free.  Each part
 // has four steps at least.  For example 666 x 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on
 // 256 x 256, 18 with k in three parts; 1 x 4096 -> 4096: 8.5 us with the token on 32 columns
 // and k in four parts, 21 on 256 x 128.
 Choice choose(const Product& q) {
-  constexpr double kStep[4] = {0.298, 0.18, 0.156, 0.188}, kUnit[4] = {2.06, 1.27, 3.35, 4.4};
+  constexpr double kStep[4] = {0.298, 0.18, 0.156, 0.188}, kUnit[4] = {1.5, 1.27, 3.35, 4.4};
   constexpr int kTok[4] = {256, 256, 32, 128}, kFeat[4] = {256, 128, 128, 128};
   Choice best{PAIR_256, 1, 0};
   double least = 1e30;
