@@ -311,3 +311,16 @@ def test_binding_refusals():
             tsr.tsr_linear_backward(**{**dict(dout=y, x=x, weight=w), **bad})
     with pytest.raises(tsr.TsrError):
         tsr.tsr_linear_backward(y, x, w, need=(False, False, False))
+
+
+@pytest.mark.parametrize("activation", [None, "silu"])
+@pytest.mark.parametrize("B,N,K,M", [(1, 20011, 64, 64), (1, 19999, 264, 8), (2, 9001, 136, 96), (1, 12345, 8, 544),
+                                     (3, 4700, 320, 264)])
+def test_narrow_weight_gradients_of_many_tokens(B, N, K, M, activation):
+    # one to four tiles cut into up to 76 parts; rows of 1 to 68 pieces of eight columns
+    x, w = make((B, N, K), BF, 1), make((M, K), BF, 2, K ** -0.5)
+    dout, pre = make((B, N, M), BF, 3), make((B, N, M), BF, 4) if activation else None
+    grads = tsr.tsr_linear_backward(dout, x, w, activation=activation, pre=pre)
+    check_backward(grads, dout, x, w, activation, pre)
+    again = tsr.tsr_linear_backward(dout, x, w, activation=activation, pre=pre)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
