@@ -29,7 +29,7 @@ constexpr int kGroupedParts = 8;
 template <int BN, int G>
 __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ GemmParams p) {
   constexpr int VECS = BN / 8, EACH = 256 / G;
-  __shared__ float red[G > 1 ? G : 1][G > 1 ? EACH : 1][8];
+  __shared__ F2 red[G > 1 ? G : 1][G > 1 ? EACH : 1][4];
   const int at = threadIdx.x % EACH, g = threadIdx.x / EACH;
   const int64_t i = blockIdx.x * static_cast<int64_t>(EACH) + at;
   const int64_t rest = p.by_cut.d, cut = i / (256 * VECS);
@@ -38,31 +38,27 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
   const int2 rc = tile_of(p, p.whole + static_cast<uint32_t>(min(cut, rest - 1)));
   const int32_t b = p.by_batch(rc.x), n = (rc.x - b * static_cast<int32_t>(p.by_batch.d)) * 256 + row, f = rc.y * BN + c;
   const bool on = cut < rest && n < p.n_rows && f < p.cols;
-  float v[8] = {};
+  F2 v[4] = {};
   if (on) {
     const int32_t s1 = p.splits * (g + 1) / G;
 #pragma unroll 4
     for (int32_t s = p.splits * g / G; s < s1; ++s) {
       const float4* src = reinterpret_cast<const float4*>(p.part + ((s * rest + cut) * 256 + row) * BN + c);
       const float4 x = src[0], y = src[1];
-      v[0] += x.x;
-      v[1] += x.y;
-      v[2] += x.z;
-      v[3] += x.w;
-      v[4] += y.x;
-      v[5] += y.y;
-      v[6] += y.z;
-      v[7] += y.w;
+      v[0] = add2(v[0], pack2(x.x, x.y));
+      v[1] = add2(v[1], pack2(x.z, x.w));
+      v[2] = add2(v[2], pack2(y.x, y.y));
+      v[3] = add2(v[3], pack2(y.z, y.w));
     }
   }
   if constexpr (G > 1) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) red[g][at][k] = v[k];
+    for (int k = 0; k < 4; ++k) red[g][at][k] = v[k];
     __syncthreads();
     if (g) return;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      for (int h = 1; h < G; ++h) v[k] += red[h][at][k];
+    for (int k = 0; k < 4; ++k)
+      for (int h = 1; h < G; ++h) v[k] = add2(v[k], red[h][at][k]);
   }
   if (on) by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(p.epi, v, b, n, f); });
 }
@@ -85,7 +81,7 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const __grid_constant
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_block;
   const int64_t r1 = min(r0 + p.rows_per_block, p.rows);
   grid_launch_dependents();
-  float sum[8] = {};
+  F2 sum[4] = {};
   if (f < p.cols)
     by_kind(p.f16, p.act, [&](auto f16, auto act) {
       constexpr int kRows = act.value == TSR_ACT_NONE ? 8 : 4;      // in flight
@@ -96,22 +92,26 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const __grid_constant
           b = r / p.n_rows;
           n = r - b * p.n_rows;
         }
-        float g[8];
+        F2 g[4];
         unpack8<f16.value>(*reinterpret_cast<const uint4*>(p.dout + at(p.vdout, b, n, f)), g);
         if constexpr (act.value != TSR_ACT_NONE) {
-          float z[8];
+          F2 z[4];
           unpack8<f16.value>(*reinterpret_cast<const uint4*>(p.pre + at(p.vpre, b, n, f)), z);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] *= slope<act.value>(z[i]);
+          for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], slope<act.value>(z[i]));
         }
         if (p.dz) *reinterpret_cast<uint4*>(p.dz + r * p.cols + f) = pack8<f16.value>(g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += g[i];
+        for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], g[i]);
       }
     });
   if (!p.part) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = sum[i];
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2(sum[i]);
+    red[threadIdx.x][2 * i] = x.x;
+    red[threadIdx.x][2 * i + 1] = x.y;
+  }
   __syncthreads();
   const int c = threadIdx.x;           // a column of the block's
   const int32_t col = blockIdx.x * lanes * 8 + c;

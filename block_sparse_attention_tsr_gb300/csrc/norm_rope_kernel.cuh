@@ -65,30 +65,6 @@ struct NormParams {
   float* part;                       // backward: [CTA][d], null: no weight gradient
 };
 
-// Two fp32 values in a 64-bit register, for packed arithmetic: two operations an
-// instruction (480p forward 160 -> 148 us).
-using F2 = uint64_t;
-__device__ __forceinline__ F2 pack2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(F2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // The pairs of a unit as floats, first elements and second elements, two pairs a register
 // (P = 1: the other half is 0), and back.
 template <typename T, int P, bool ADJ>
