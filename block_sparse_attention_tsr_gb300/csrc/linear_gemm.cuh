@@ -84,7 +84,8 @@ struct GemmParams {
   int32_t cols;
   int32_t row_tiles, col_tiles;        // row tiles of all batches
   Div by_batch;                        // row tiles per batch
-  Div by_group, by_cut;                // tiles that take turns (tile_of); tiles that are cut
+  Div by_group, by_cut;                // tiles of a group of row tiles (tile_of); tiles that are cut
+  uint32_t group_log2;                 // row tiles of a group
   int32_t splits, k_steps;             // k steps of a whole product
   uint32_t k_each, k_more;             // k steps of a part; parts that have one more
   int32_t k_steps_per_batch;           // dweight: steps of one batch's tokens
@@ -272,12 +273,11 @@ struct alignas(8) Ctrl {
 };
 static_assert(sizeof(Ctrl) <= 512, "Ctrl");
 
-// Row and column of tile t: eight row tiles at a time, their columns one after another, so
-// that the CTAs that run together share rows and columns in L2.
-constexpr uint32_t kGroup = 8;
+// Row and column of tile t: a group of row tiles at a time, their columns one after another,
+// so that the CTAs that run together share rows and columns in L2.
 __device__ __forceinline__ int2 tile_of(const GemmParams& p, uint32_t t) {
-  const uint32_t g = p.by_group(t), in = t - g * p.by_group.d, row = g * kGroup, rows = p.row_tiles - row;
-  if (rows >= kGroup) return make_int2(row + in % kGroup, in / kGroup);
+  const uint32_t g = p.by_group(t), in = t - g * p.by_group.d, row = g << p.group_log2, rows = p.row_tiles - row;
+  if (rows >> p.group_log2) return make_int2(row + (in & ((1u << p.group_log2) - 1)), in >> p.group_log2);
   const uint32_t col = in / rows;
   return make_int2(row + (in - col * rows), col);
 }
