@@ -201,24 +201,12 @@ Choice choose(const Product& q) {
 
 // Row tiles of a group.  A B that stays in L2 is read again at no cost: two, so that A's rows
 // are through soonest (2048 -> 6144, 32,760 tokens: 482 us, of eight 490; its dx 490 for 505).
-// Else the fewest rows and columns among the tiles that run together: 8192 -> 2048, dweight,
-// 8 x 32 tiles: of eight 654 us, of two 695; 2048 -> 8192, 32 x 8 tiles: of two 654, of eight
-// 672; 5120 -> 5120, 9,000 tokens: of eight 291, of two 294.
-uint32_t group_log2(const Product& q, int bn) {
-  if (q.cols * q.k_steps * BK * 2 <= 40 << 20) return 1;
-  const int64_t pairs = kSms / 2, cols = cdiv(q.cols, bn);
-  uint32_t best = 1;
-  int64_t least = INT64_MAX;
-  for (uint32_t l = 1; l <= 4; ++l) {
-    const int64_t per = cols << l;
-    const int64_t rows_at_once = per >= pairs ? 1 << l : cdiv(pairs, per) << l;
-    const int64_t reach = rows_at_once * 256 + std::min(cols, cdiv(pairs, int64_t{1} << l)) * bn;
-    if (reach < least) {
-      least = reach;
-      best = l;
-    }
-  }
-  return best;
+// Else eight by some nine columns run together on 76 pairs, the fewest rows and columns of
+// all shapes (8192 -> 2048, dweight, 8 x 32 tiles: of eight 654 us, of two 695; 5120 -> 5120,
+// 9,000 tokens: 291, of two 294); two where there are no more columns than that anyway (2048
+// -> 8192, dweight, 32 x 8 tiles: of two 654, of eight 672).
+uint32_t group_log2(const Product& q, int64_t col_tiles) {
+  return q.cols * q.k_steps * BK * 2 <= 40 << 20 || col_tiles < 10 ? 1 : 3;
 }
 
 size_t part_bytes(const Product& q) {
@@ -394,7 +382,7 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   } else {
     p.whole = static_cast<uint32_t>(c.whole);
     p.units = static_cast<uint32_t>(c.whole + rest * c.splits);
-    p.group_log2 = group_log2(q, bn);
+    p.group_log2 = group_log2(q, col_tiles);
     // of one group that holds all tiles only the remainders are taken
     p.by_group = div_by(static_cast<uint32_t>(std::min<int64_t>(col_tiles << p.group_log2, INT32_MAX)));
     p.by_cut = div_by(static_cast<uint32_t>(std::max<int64_t>(rest, 1)));

@@ -324,3 +324,12 @@ def test_narrow_weight_gradients_of_many_tokens(B, N, K, M, activation):
     check_backward(grads, dout, x, w, activation, pre)
     again = tsr.tsr_linear_backward(dout, x, w, activation=activation, pre=pre)
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+@pytest.mark.parametrize("N,K,M", [(1300, 4608, 5000), (4300, 4608, 5000), (30001, 776, 1032), (700, 6600, 4104)])
+def test_groups_of_row_tiles(N, K, M):
+    # operands past the size that two row tiles at a time are taken for; groups that are not full
+    x, w = make((1, N, K), BF, 1), make((M, K), BF, 2, K ** -0.5)
+    check_forward(tsr.tsr_linear(x, w), x, w)
+    dout = make((1, N, M), BF, 3)
+    check_backward(tsr.tsr_linear_backward(dout, x, w), dout, x, w)
