@@ -481,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(GRAD, P, L)) norm_rope_k
     for (int j = 0; j < R; ++j) {
       if (cur.h + j < cur.h1 && ok) {
         const float r = rsqrtf(fmaf(ss[j], inv_d, p.eps));
-        const float off = GRAD ? -(r * r * sp[j] * inv_d) : 0.f;
+        // r one factor at a time: r^2 alone is beyond fp32 where a row's mean square and eps are
+        // small, r S / d is of the size of g o w
+        const float off = GRAD ? -(r * sp[j] * inv_d * r) : 0.f;
         const F2 r2 = pack2(r, r), off2 = pack2(off, off);
 #pragma unroll
         for (int k = 0; k < K; ++k)

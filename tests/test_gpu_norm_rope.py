@@ -257,3 +257,26 @@ def test_binding_refusals():
             tsr.tsr_norm_rope_backward(axis_dims=(8, 8), grid=(3, 4), **args)
     with pytest.raises(tsr.TsrError):
         tsr.tsr_norm_rope_backward(dy, x, w, (8, 8), grid=(3, 4), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("halves,d,dims", [(False, 64, (16, 24, 24)), (True, 64, (16, 24, 24)), (False, 6, (2, 2))])
+@pytest.mark.parametrize("eps", [2.0 ** -149, 2.0 ** -140, 2.0 ** -126, 2.0 ** -100])
+def test_gradient_at_the_smallest_eps(eps, halves, d, dims, dtype):
+    """Any eps > 0 of fp32 is taken: a row of zeros has r = eps^-1/2, up to 2^74.5, and the
+    gradient r (g o w), finite in these types; rows beside it of 2^-55 to 2^55 (their squares
+    stay inside fp32's normal range)."""
+    grid, H = (2, 3, 2)[:len(dims)], 5
+    N, pos = int(np.prod(grid)), layer.coordinates(grid)
+    x, dy, w = make((1, H, N, d), dtype, 1), make((1, H, N, d), dtype, 2), make((d,), torch.float32, 3)
+    x[0, :, 0] = 0
+    x[0, 2] = 0
+    x[0, 3] = torch.sign(x[0, 3]) * 2.0 ** -55
+    x[0, 4] *= 2.0 ** 55
+    kw = dict(eps=eps, grid=grid, halves=halves)
+    y = tsr.tsr_norm_rope(x, w, dims, **kw)
+    assert torch.all(y[0, :, 0] == 0) and torch.all(y[0, 2] == 0)
+    check_forward(x, w, y, pos, dims, halves=halves, eps=eps)
+    dx, dw = tsr.tsr_norm_rope_backward(dy, x, w, dims, **kw)
+    assert torch.isfinite(dx).all()
+    check_backward(dy, x, w, dx, dw, pos, dims, halves=halves, eps=eps)
