@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(1024) linear_bias_kernel(const float* part, in
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   grid_wait();
+  grid_pass_on();                      // dz, to the products, which do not wait for this grid
   grid_launch_dependents();
   float s = 0.f;
   if (c < cols)
@@ -351,7 +352,8 @@ tsr_status launch_kind(Variant v, const GemmParams& p, cudaStream_t st) {
 // One product with its epilogue.  `tok`: the tensor whose rows are tokens (x or dz),
 // `other`: the weight, or x for the weight's gradient.
 tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int64_t tok_heads, const void* other,
-               const View& vother, int64_t other_heads, const Epilogue& e, float* ws, bool late, cudaStream_t st) {
+               const View& vother, int64_t other_heads, const Epilogue& e, float* ws, bool late, bool pass_on,
+               cudaStream_t st) {
   const Product q = product(y, kind);
   const Choice c = choose(q);
   const bool few = c.variant >= FEW_32;
@@ -368,6 +370,7 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   p.k_more = static_cast<uint32_t>(q.k_steps % c.splits);
   p.k_steps_per_batch = static_cast<int32_t>(cdiv(y.N, BK));
   p.late = late;
+  p.pass_on = pass_on;
   p.stall = g_stall;
   p.timeout_ns = g_stall ? kStallNs : kWaitTimeoutNs;
   const int bn = c.variant == PAIR_256 ? 256 : c.variant == FEW_32 ? 32 : 128;
@@ -474,7 +477,7 @@ tsr_status launch_linear(const tsr_linear_desc& d, const tsr_linear_args& a, voi
   if (a.pre) views[n++] = &e.vpre;
   flatten(y, views, n);
   const View vw{0, 0, y.K, static_cast<int32_t>(y.K)};
-  return run(y, FORWARD, a.x, vx, y.in_heads, a.weight, vw, 1, e, static_cast<float*>(ws), false, st);
+  return run(y, FORWARD, a.x, vx, y.in_heads, a.weight, vw, 1, e, static_cast<float*>(ws), false, false, st);
 }
 
 tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_grads& a, void* ws, cudaStream_t st) {
@@ -528,21 +531,23 @@ tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_gra
   memset(&e, 0, sizeof e);
   e.f16 = y.f16;
   // A product's CTAs may start as those of the kernel before leave, where that kernel has
-  // waited for the products' inputs and writes nothing that the product touches: behind the
-  // sum of dbias, and dweight behind a dx whose tiles are not cut (its parts would share
-  // their memory).
+  // waited for the products' inputs, passed them on (grid_pass_on) and writes nothing that the
+  // product touches: behind the sum of dbias, and dweight behind a dx whose tiles are not cut
+  // (its parts would share their memory).
   bool late = a.dbias != nullptr;
   if (a.dx) {
     e.out = a.dx;
     e.vout = vdx;
     const View vw{0, 0, y.K, static_cast<int32_t>(y.K)};
-    if (tsr_status s = run(y, DX, dz, vdz, dz_heads, a.weight, vw, 1, e, part, late, st)) return s;
-    late = part_bytes(product(y, DX)) == 0;
+    const bool uncut = part_bytes(product(y, DX)) == 0;
+    if (tsr_status s = run(y, DX, dz, vdz, dz_heads, a.weight, vw, 1, e, part, late, late || (a.dweight && uncut), st))
+      return s;
+    late = uncut;
   }
   if (a.dweight) {
     e.out = a.dweight;
     e.vout = View{0, 0, y.K, static_cast<int32_t>(y.K)};
-    return run(y, DWEIGHT, dz, vdz, dz_heads, a.x, vx, y.in_heads, e, part, late, st);
+    return run(y, DWEIGHT, dz, vdz, dz_heads, a.x, vx, y.in_heads, e, part, late, late, st);
   }
   return TSR_OK;
 }

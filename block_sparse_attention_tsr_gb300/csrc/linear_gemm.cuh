@@ -92,6 +92,7 @@ struct GemmParams {
   Div a_dim, b_dim, out_dim;           // channels per head of A's, B's and out's tensors
   uint32_t idesc;
   int32_t late;                        // what is before on the stream is not an input: waited for at the end
+  int32_t pass_on;                     // late, or a late product behind this one reads inputs that this one was shown
   int32_t stall;                       // test only: the issuer waits for ever after its first step
   uint64_t timeout_ns;                 // bound of every wait
 };
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   // what comes before may still run while this CTA sets itself up; where it is no input, till
   // this kernel's end (so that no kernel behind this one starts before it has ended)
   if (!p.late) grid_wait();
+  if (p.pass_on) grid_pass_on();
   grid_launch_dependents();
   const uint32_t units = p.units, first = blockIdx.x / 2, stride = gridDim.x / 2;
 
@@ -718,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<BN>::CTAS) linear_few_kernel(
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
   if (!p.late) grid_wait();
+  if (p.pass_on) grid_pass_on();
   grid_launch_dependents();
   const int32_t tile = static_cast<int32_t>(blockIdx.x) / p.splits;
   const int32_t f_tile = tile % p.row_tiles, t_tile = tile / p.row_tiles;

@@ -29,6 +29,13 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // completed and their writes are visible; let the dependent kernel's blocks start.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Before grid_launch_dependents, where a grid that it lets start reads what this one has been
+// shown (by its grid_wait, or passed on to it) without a grid_wait of its own: letting it start
+// orders no memory by itself.  Plain accesses and the copies of the async proxy.
+__device__ __forceinline__ void grid_pass_on() {
+  __threadfence();
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 
 // ----------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

@@ -36,3 +36,21 @@ def test_norm_weights_read_their_predecessor_with_plain_loads():
     code = body(source("norm_rope.cu"), "norm_weight_kernel(")
     before = code[:code.index("grid_wait();")]
     assert "__ldg" not in code and "p.part[" not in before and "return" not in before
+
+
+def test_what_a_late_product_reads_is_passed_on_to_it():
+    """A product that does not wait at its start reads what the grid before it has been shown;
+    every such grid waits (or was passed it), fences for plain accesses and for the copies, and
+    only then lets the next one start."""
+    fences = body(source("ptx.cuh"), "void grid_pass_on()")
+    assert re.search(r"__threadfence\(\);.*fence\.proxy\.async\.global;", fences, re.S)
+    bias = re.sub(r"\s+", " ", body(source("linear.cu"), "linear_bias_kernel("))
+    assert "grid_wait(); grid_pass_on(); grid_launch_dependents();" in bias
+    for kernel in ("linear_gemm_kernel(", "linear_few_kernel("):
+        code = re.sub(r"\s+", " ", body(source("linear_gemm.cuh"), kernel))
+        assert "if (!p.late) grid_wait(); if (p.pass_on) grid_pass_on(); grid_launch_dependents();" in code
+        assert code.count("grid_launch_dependents") == 1
+    calls = re.sub(r"\s+", " ", body(source("linear.cu"), "tsr_status launch_linear_backward("))
+    # the products: late only behind the sum of dbias, or dweight behind a dx that is not cut
+    assert "bool late = a.dbias != nullptr;" in calls and "late = uncut;" in calls
+    assert "late, late || (a.dweight && uncut), st)" in calls and "late, late, st)" in calls
