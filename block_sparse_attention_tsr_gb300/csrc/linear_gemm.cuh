@@ -436,8 +436,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         }
       }
     }
-    if (rank == 0) {
-      // every copy has landed before the CTA ends; normally they all have been waited for
+    // the issuer's arrivals on this CTA's empty barriers come before the CTA ends (those of the
+    // last steps nobody else waits for; the peer's CTA may be through with its part before)
+    for (int64_t k = issued > C::STAGES ? issued - C::STAGES : 0; ok && k < issued; ++k)
+      ok = mbar_wait_warp(smem_u32(&ctrl.empty[k % C::STAGES]), static_cast<uint32_t>(k / C::STAGES) & 1u, abort_flag,
+                          &g_err, p.timeout_ns);
+    if (rank == 0 && !ok) {
+      // given up: every copy lands before the CTA ends
       volatile int32_t no = 0;
       for (int64_t k = issued > C::STAGES ? issued - C::STAGES : 0; k < issued; ++k)
         mbar_wait_warp(smem_u32(&ctrl.full[k % C::STAGES]), static_cast<uint32_t>(k / C::STAGES) & 1u, &no, &g_err,

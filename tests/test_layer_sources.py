@@ -54,3 +54,19 @@ def test_what_a_late_product_reads_is_passed_on_to_it():
     # the products: late only behind the sum of dbias, or dweight behind a dx that is not cut
     assert "bool late = a.dbias != nullptr;" in calls and "late = uncut;" in calls
     assert "late, late || (a.dweight && uncut), st)" in calls and "late, late, st)" in calls
+
+
+def test_arrivals_on_the_peer_come_before_its_end():
+    """The issuer of a pair arrives on barriers of both CTAs; a CTA must not end before the last
+    of them: the producer of either CTA waits for each stage that it has filled last."""
+    code = re.sub(r"\s+", " ", body(source("linear_gemm.cuh"), "linear_gemm_kernel("))
+    producer = code[code.index("if (warp == 0) {"):code.index("} else if (warp == 1)")]
+    tail = producer[producer.index("++issued;"):]
+    wait = tail.index("ok = mbar_wait_warp(smem_u32(&ctrl.empty[k % C::STAGES])")
+    assert "rank" not in tail[:wait]
+    # copies in flight are waited for where that was given up
+    assert "if (rank == 0 && !ok)" in tail[wait:] and "ctrl.full[k % C::STAGES]" in tail[wait:]
+    # the other commits of the pair are waited for by the epilogue of both and by the issuer
+    assert code.count("mma_commit_pair(") == 3
+    for bar in ("empty[st]", "acc_full[buf]", "final_bar"):
+        assert code.count("mma_commit_pair(elect, smem_u32(&ctrl.%s));" % bar) == 1
