@@ -38,6 +38,9 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
   const int2 rc = tile_of(p, p.whole + static_cast<uint32_t>(min(cut, rest - 1)));
   const int32_t b = p.by_batch(rc.x), n = (rc.x - b * static_cast<int32_t>(p.by_batch.d)) * 256 + row, f = rc.y * BN + c;
   const bool on = cut < rest && n < p.n_rows && f < p.cols;
+  // a CTA that gave up has not stored its parts: nothing is added then
+  static_assert(kMostCtas == 32 * sizeof(uint2), "a warp reads them");
+  const uint2 gave_up = reinterpret_cast<const uint2*>(p.gave_up)[threadIdx.x & 31];
   F2 v[4] = {};
   if (on) {
     const int32_t s1 = p.splits * (g + 1) / G;
@@ -60,6 +63,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
     for (int k = 0; k < 4; ++k)
       for (int h = 1; h < G; ++h) v[k] = add2(v[k], red[h][at][k]);
   }
+  if (__any_sync(0xFFFFFFFFu, gave_up.x | gave_up.y)) return;
   if (on) by_kind(p.epi.f16, p.epi.act, [&](auto f16, auto act) { finish8<f16.value, act.value>(p.epi, v, b, n, f); });
 }
 
@@ -210,11 +214,15 @@ uint32_t group_log2(const Product& q, int64_t col_tiles) {
   return q.cols * q.k_steps * BK * 2 <= 40 << 20 || col_tiles < 10 ? 1 : 3;
 }
 
-size_t part_bytes(const Product& q) {
-  const Choice c = choose(q);
+// The parts of a product, and behind them a byte for each CTA.
+size_t part_bytes(const Product& q, const Choice& c) {
   if (c.splits == 1 || c.variant >= FEW_32) return 0;
   const int bn = c.variant == PAIR_256 ? 256 : 128;
   return static_cast<size_t>(q.batches * cdiv(q.n_rows, 256) * cdiv(q.cols, bn) - c.whole) * c.splits * 256 * bn * 4;
+}
+size_t part_space(const Product& q) {
+  const size_t parts = part_bytes(q, choose(q));
+  return parts ? parts + kMostCtas : 0;
 }
 
 // ---------------------------------------------------------------- the layer
@@ -243,11 +251,11 @@ void flatten(Layer& y, View* const* views, int n) {
 }
 size_t most_parts(const tsr_linear_desc& d, Kind kind) {
   Layer y = layer_of(d);
-  const size_t a = part_bytes(product(y, kind));
+  const size_t a = part_space(product(y, kind));
   if (y.B == 1) return a;
   y.N *= y.B;
   y.B = 1;
-  return std::max(a, part_bytes(product(y, kind)));
+  return std::max(a, part_space(product(y, kind)));
 }
 
 View view(const int64_t* stride, int32_t dim) { return {stride[0], stride[1], stride[2], dim}; }
@@ -320,10 +328,7 @@ template <int BN, bool A_MN, bool B_MN>
 tsr_status launch_pairs(const GemmParams& p, cudaStream_t st) {
   static bool set[64] = {};
   const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole;
-  int dev = 0;
-  TSR_CUDA(cudaGetDevice(&dev));
-  const int64_t pairs = std::min<int64_t>(p.units, num_sms(dev) / 2);
-  if (tsr_status e = launch_clusters(linear_gemm_kernel<BN, A_MN, B_MN>, set, Cfg<BN>::SMEM, pairs * 2, 2, p, st)) return e;
+  if (tsr_status e = launch_clusters(linear_gemm_kernel<BN, A_MN, B_MN>, set, Cfg<BN>::SMEM, p.ctas, 2, p, st)) return e;
   if (rest) {
     const bool many = p.splits >= kGroupedParts;
     TSR_CUDA(launch_dependent(many ? linear_finish_kernel<BN, 8> : linear_finish_kernel<BN, 1>,
@@ -390,6 +395,10 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
     p.by_group = div_by(static_cast<uint32_t>(std::min<int64_t>(col_tiles << p.group_log2, INT32_MAX)));
     p.by_cut = div_by(static_cast<uint32_t>(std::max<int64_t>(rest, 1)));
     p.out_dim = div_by(e.vout.dim);
+    int dev = 0;
+    TSR_CUDA(cudaGetDevice(&dev));
+    p.ctas = 2 * std::min<uint32_t>(p.units, std::min(num_sms(dev), kMostCtas) / 2);
+    if (rest) p.gave_up = reinterpret_cast<uint8_t*>(ws) + part_bytes(q, c);
   }
   CUtensorMap *mt = few ? &p.tb : &p.ta, *mo = few ? &p.ta : &p.tb;
   (few ? p.b_dim : p.a_dim) = div_by(vtok.dim);
@@ -539,7 +548,7 @@ tsr_status launch_linear_backward(const tsr_linear_desc& d, const tsr_linear_gra
     e.out = a.dx;
     e.vout = vdx;
     const View vw{0, 0, y.K, static_cast<int32_t>(y.K)};
-    const bool uncut = part_bytes(product(y, DX)) == 0;
+    const bool uncut = part_space(product(y, DX)) == 0;
     if (tsr_status s = run(y, DX, dz, vdz, dz_heads, a.weight, vw, 1, e, part, late, late || (a.dweight && uncut), st))
       return s;
     late = uncut;

@@ -22,7 +22,8 @@
 // there are fewer than pairs): their units store fp32 parts that linear_finish_kernel adds
 // in their order.
 // Warps: TMA producer, MMA issuer (of the pair's first CTA), 8 epilogue warps.  Every wait
-// is bounded: on expiry the error word is set and the kernel winds down.
+// is bounded: on expiry the error word is set and the kernel winds down; what has not been
+// computed is not stored.
 //
 // For few tokens the weight's bytes bound it (linear_few_kernel): the features lie on the
 // 128 rows and the tokens on 32 or 128 columns, and a cluster of up to 8 CTAs shares a
@@ -43,6 +44,7 @@ namespace tsr {
 namespace linear {
 
 constexpr int kEpiWarps = 8, kThreads = (kEpiWarps + 2) * 32;
+constexpr int kMostCtas = 256;         // of a product by pairs
 constexpr int BK = 64;                 // k per step: 128 bytes, the swizzle's row
 
 // A tensor's addressing: element strides of batch, head and token; channels contiguous.
@@ -79,6 +81,8 @@ struct GemmParams {
   CUtensorMap tout, tpre, tres, tpart;
   Epilogue epi;
   float* part;                         // [splits][tiles - whole][256][BN]
+  uint8_t* gave_up;                    // [kMostCtas] behind the parts: 1 of a CTA that gave up
+  uint32_t ctas;
   uint32_t whole, units;               // tiles that are not cut along k: the first ones; all work units
   int32_t n_rows, batches;             // rows per batch (tokens, or features)
   int32_t cols;
@@ -271,6 +275,7 @@ struct alignas(8) Ctrl {
   uint64_t res_full[kEpiWarps][2];     // the residual's piece has landed
   uint32_t tmem_base;
   int32_t abort_flag;
+  uint32_t gave_up;                    // few tokens: a CTA of the cluster has given up
 };
 static_assert(sizeof(Ctrl) <= 512, "Ctrl");
 
@@ -401,6 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   if (p.pass_on) grid_pass_on();
   grid_launch_dependents();
   const uint32_t units = p.units, first = blockIdx.x / 2, stride = gridDim.x / 2;
+  // each CTA clears its own, the first those of none (a word of each, stored at the end: 22.6 ->
+  // 23.6 us for 2,593 x 1176 -> 1712)
+  if (p.gave_up && warp == 2) {
+    if (lane == 0) p.gave_up[blockIdx.x] = 0;
+    if (blockIdx.x == 0)
+      for (uint32_t k = gridDim.x + lane; k < kMostCtas; k += 32) p.gave_up[k] = 0;
+  }
 
   if (warp == 0) {
     // The whole warp runs the loop and one lane acts, so that the copies' addresses and
@@ -673,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   cluster_sync();
+  if (p.gave_up && *abort_flag && threadIdx.x == 0) p.gave_up[blockIdx.x] = 1;
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::TMEM);
@@ -713,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<BN>::CTAS) linear_few_kernel(
     mbar_init(smem_u32(&ctrl.final_bar), 1);
     mbar_init(smem_u32(&ctrl.never), 1);
     ctrl.abort_flag = (base & 1023u) ? 1 : 0;
+    ctrl.gave_up = 0u;
     fence_mbar_init();
   }
   if (warp == 0 && lane < 2) tma_prefetch_desc(lane ? &p.tb : &p.ta);
@@ -722,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<BN>::CTAS) linear_few_kernel(
   }
   tc_fence_before();
   __syncthreads();
+  cluster_arrive();                        // this CTA's control block is set up (waited for at the end)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl.tmem_base, 0);
   if (!p.late) grid_wait();
@@ -802,9 +817,13 @@ __global__ void __launch_bounds__(kThreads, FewCfg<BN>::CTAS) linear_few_kernel(
   }
   tc_fence_before();
   __syncthreads();
+  cluster_wait();
+  // a CTA that gave up tells the others, and nobody stores (their flags read by all: 5.2 -> 5.7
+  // us for 32 x 1024 -> 1024)
+  if (*abort_flag && threadIdx.x < p.splits) st_cluster(cluster_addr(smem_u32(&ctrl.gave_up), threadIdx.x), 1u);
   cluster_sync();                          // all CTAs' sums lie in their shared memory
   // token rank, rank + splits, ... of the tile, 8 features a thread
-  const int32_t tokens = min(BN, p.n_rows - n0);
+  const int32_t tokens = ctrl.gave_up ? 0 : min(BN, p.n_rows - n0);
   for (int32_t i = threadIdx.x; i < (tokens - rank + p.splits - 1) / p.splits * 16; i += kThreads) {
     const int32_t t = rank + i / 16 * p.splits, f = f_tile * 128 + i % 16 * 8;
     if (f >= p.cols) continue;

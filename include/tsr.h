@@ -611,7 +611,7 @@ tsr_status tsr_norm_rope_backward(const tsr_rope_desc *desc, double eps, const t
  *
  * tsr_linear_device_status synchronises `stream` and returns TSR_ERR_TIMEOUT if a wait in
  * any linear layer's product on the current device has given up since the last such call
- * (the outputs of that product are not valid), else TSR_OK.
+ * (its outputs are not valid: what it has not computed is not stored), else TSR_OK.
  */
 typedef enum { TSR_ACT_NONE = 0, TSR_ACT_GELU = 1, TSR_ACT_GELU_TANH = 2, TSR_ACT_SILU = 3 } tsr_activation;
 
