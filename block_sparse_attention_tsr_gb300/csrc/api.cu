@@ -38,12 +38,12 @@ tsr_status cuda_fail(cudaError_t e, const char* what) {
 }
 
 int num_sms(int device) {
-  static int cache[64] = {0};
-  if (device >= 0 && device < 64 && cache[device]) return cache[device];
-  int n = 0;
+  static std::atomic<int> cache[64] = {};
+  int n = device >= 0 && device < 64 ? cache[device].load(std::memory_order_relaxed) : 0;
+  if (n) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0)
     n = 1;
-  if (device >= 0 && device < 64) cache[device] = n;
+  if (device >= 0 && device < 64) cache[device].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -717,11 +717,8 @@ __global__ void transpose_blocks_kernel(const uint8_t* __restrict__ src, uint8_t
 template <int D>
 tsr_status launch(const Params& prm, int64_t ctas, int device, cudaStream_t st) {
   auto kern = bsa_bwd_kernel<D>;
-  static bool attr_set[64] = {false};
-  if (device < 0 || device >= 64 || !attr_set[device]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, true>::SMEM));
-    if (device >= 0 && device < 64) attr_set[device] = true;
-  }
+  static OncePerDevice once;
+  if (tsr_status e = allow_smem(kern, Cfg<D, true>::SMEM, device, once)) return e;
   TSR_CUDA(launch_dependent(kern, static_cast<unsigned>(ctas), kThreads, Cfg<D, true>::SMEM, st, prm));
   return TSR_OK;
 }

@@ -902,11 +902,8 @@ template <int D, int BN, int STAGES, int CTAS, int MODE, int MAXR>
 tsr_status launch_variant(const FwdParamsT<MAXR>& prm, int n_items, int device, cudaStream_t stream) {
   using C = Cfg<D, BN, STAGES, CTAS>;
   auto kern = bsa_fwd_kernel<D, BN, STAGES, CTAS, MODE, MAXR>;
-  static bool attr_set[64] = {false};
-  if (device < 0 || device >= 64 || !attr_set[device]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-    if (device >= 0 && device < 64) attr_set[device] = true;
-  }
+  static OncePerDevice once;
+  if (tsr_status e = allow_smem(kern, C::SMEM, device, once)) return e;
   const int grid = std::min(n_items, num_sms(device) * CTAS);
   if (grid <= 0) return TSR_OK;
   kern<<<grid, 192, C::SMEM, stream>>>(prm);

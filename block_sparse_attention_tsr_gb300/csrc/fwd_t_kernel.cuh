@@ -1075,11 +1075,8 @@ __global__ void __launch_bounds__(kThreads, 1) bsa_fwd_t_kernel(const __grid_con
 template <int MODE, int MAXR>
 tsr_status launch_t(const FwdParamsT<MAXR>& prm, int n_items, int device, cudaStream_t stream) {
   auto kern = bsa_fwd_t_kernel<MODE, MAXR>;
-  static bool attr_set[64] = {false};
-  if (device < 0 || device >= 64 || !attr_set[device]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
-    if (device >= 0 && device < 64) attr_set[device] = true;
-  }
+  static OncePerDevice once;
+  if (tsr_status e = allow_smem(kern, SMEM_BYTES, device, once)) return e;
   const int grid = std::min(n_items, num_sms(device));
   if (grid <= 0) return TSR_OK;
   kern<<<grid, kThreads, SMEM_BYTES, stream>>>(prm);

@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 #include <string>
 #include <vector>
@@ -247,6 +248,28 @@ bool encode_tmap_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t r
                     uint64_t outer, uint32_t box_inner, uint32_t box_rows);
 
 int num_sms(int device);
+
+// What has been done on each device (an attribute of a function is its own on each).  Calls
+// of several threads may both find it undone: it is done twice then, to the same end.
+class OncePerDevice {
+ public:
+  bool done(int device) const { return device >= 0 && device < 64 && done_[device].load(std::memory_order_acquire); }
+  void mark(int device) {
+    if (device >= 0 && device < 64) done_[device].store(true, std::memory_order_release);
+  }
+
+ private:
+  std::atomic<bool> done_[64] = {};
+};
+
+// The limit of a kernel's dynamic shared memory; `once`: the kernel's own.
+template <typename Kern>
+tsr_status allow_smem(Kern kern, size_t bytes, int device, OncePerDevice& once) {
+  if (once.done(device)) return TSR_OK;
+  TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
+  once.mark(device);
+  return TSR_OK;
+}
 
 // Launch a kernel that may start while the stream's previous kernel finishes
 // (programmatic dependent launch): it has to call grid_wait() before it touches

@@ -298,15 +298,11 @@ tsr_status encode(CUtensorMap* m, const void* p, const View& v, int64_t heads, i
 
 // A kernel that may set itself up while what is before it on the stream ends (it waits for
 // that before it touches memory), in clusters of `cluster` CTAs.
-tsr_status launch_clusters(void (*kern)(GemmParams), bool (&set)[64], int smem, int64_t ctas, int cluster,
+tsr_status launch_clusters(void (*kern)(GemmParams), OncePerDevice& once, int smem, int64_t ctas, int cluster,
                            const GemmParams& p, cudaStream_t st) {
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  // once per device: the attribute is the function's there
-  if (dev >= 64 || !set[dev]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    if (dev < 64) set[dev] = true;
-  }
+  if (tsr_status e = allow_smem(kern, smem, dev, once)) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -326,9 +322,9 @@ tsr_status launch_clusters(void (*kern)(GemmParams), bool (&set)[64], int smem, 
 
 template <int BN, bool A_MN, bool B_MN>
 tsr_status launch_pairs(const GemmParams& p, cudaStream_t st) {
-  static bool set[64] = {};
+  static OncePerDevice once;
   const int64_t rest = static_cast<int64_t>(p.row_tiles) * p.col_tiles - p.whole;
-  if (tsr_status e = launch_clusters(linear_gemm_kernel<BN, A_MN, B_MN>, set, Cfg<BN>::SMEM, p.ctas, 2, p, st)) return e;
+  if (tsr_status e = launch_clusters(linear_gemm_kernel<BN, A_MN, B_MN>, once, Cfg<BN>::SMEM, p.ctas, 2, p, st)) return e;
   if (rest) {
     const bool many = p.splits >= kGroupedParts;
     TSR_CUDA(launch_dependent(many ? linear_finish_kernel<BN, 8> : linear_finish_kernel<BN, 1>,
@@ -338,8 +334,8 @@ tsr_status launch_pairs(const GemmParams& p, cudaStream_t st) {
 }
 template <int BN, bool W_MN>
 tsr_status launch_few(const GemmParams& p, cudaStream_t st) {
-  static bool set[64] = {};
-  return launch_clusters(linear_few_kernel<BN, W_MN>, set, FewCfg<BN>::SMEM,
+  static OncePerDevice once;
+  return launch_clusters(linear_few_kernel<BN, W_MN>, once, FewCfg<BN>::SMEM,
                          static_cast<int64_t>(p.row_tiles) * p.col_tiles * p.splits, p.splits, p, st);
 }
 

@@ -561,13 +561,10 @@ tsr_status launch_one(unsigned ctas, const NormParams& p, cudaStream_t st) {
   constexpr int smem = Batch<T, P, L, K, GRAD>::SMEM;
   auto kern = norm_rope_kernel<T, P, L, K, GRAD, FULL>;
   if constexpr (smem > 48 * 1024) {
-    static bool set[64] = {};              // per device: the attribute is the function's there
+    static OncePerDevice once;
     int dev = 0;
     TSR_CUDA(cudaGetDevice(&dev));
-    if (dev >= 64 || !set[dev]) {
-      TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-      if (dev < 64) set[dev] = true;
-    }
+    if (tsr_status e = allow_smem(kern, smem, dev, once)) return e;
   }
   kern<<<ctas, kThreads, smem, st>>>(p);
   TSR_CUDA(cudaGetLastError());

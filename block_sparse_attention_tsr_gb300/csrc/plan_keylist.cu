@@ -664,16 +664,11 @@ tsr_status plan_build_keylist(const tsr_mask* mask, const tsr_plan_opts* opts, t
   const bool bitmap = N <= kBitmapMaxN;
   if (bitmap) {
     // validation runs inside the count kernel
-    static bool attr_done[64] = {false};
-    if (P->device < 0 || P->device >= 64 || !attr_done[P->device]) {
-      TSR_CUDA(cudaFuncSetAttribute(keylist_count_bitmap_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(2 * 4 * bitmap_words16(kBitmapMaxN))));
-      TSR_CUDA(cudaFuncSetAttribute(keylist_emit_bitmap_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(4 * emit_bitmap_words(kBitmapMaxN))));
-      if (P->device >= 0 && P->device < 64) attr_done[P->device] = true;
-    }
+    static OncePerDevice count, emit;
+    if (tsr_status s = allow_smem(keylist_count_bitmap_kernel, 2 * 4 * bitmap_words16(kBitmapMaxN), P->device, count))
+      return s;
+    if (tsr_status s = allow_smem(keylist_emit_bitmap_kernel, 4 * emit_bitmap_words(kBitmapMaxN), P->device, emit))
+      return s;
     if (n_items > 0) {
       keylist_count_bitmap_kernel<<<static_cast<unsigned>(n_items), 256,
                                     2 * 4 * static_cast<size_t>(bitmap_words16(N)), stream>>>(

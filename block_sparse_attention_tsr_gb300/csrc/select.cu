@@ -735,17 +735,6 @@ Layout layout_of(const tsr_select_desc& s) {
   return l;
 }
 
-template <typename Kern>
-tsr_status allow_smem(Kern kern, bool (&set)[64]) {
-  int dev = 0;
-  TSR_CUDA(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= 64 || !set[dev]) {
-    TSR_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripBytes));
-    if (dev >= 0 && dev < 64) set[dev] = true;
-  }
-  return TSR_OK;
-}
-
 template <int D, int KPL>
 tsr_status launch_variant(const PoolParams& pp, const SelParams& sp, size_t smem, bool big_blocks, cudaStream_t st) {
   constexpr int kWarps = kPoolThreads / 32;
@@ -758,8 +747,10 @@ tsr_status launch_variant(const PoolParams& pp, const SelParams& sp, size_t smem
   TSR_CUDA(cudaGetLastError());
   const unsigned ctas =
       static_cast<unsigned>(sp.scores ? std::min<int64_t>(kScoreSlots, sp.n_strips) : sp.n_strips);
-  static bool set[64] = {false};
-  if (tsr_status e = allow_smem(select_kernel<D, KPL>, set)) return e;
+  static OncePerDevice once;
+  int dev = 0;
+  TSR_CUDA(cudaGetDevice(&dev));
+  if (tsr_status e = allow_smem(select_kernel<D, KPL>, kStripBytes, dev, once)) return e;
   TSR_CUDA(launch_dependent(select_kernel<D, KPL>, ctas, kSelThreads, smem, st, sp));
   return TSR_OK;
 }

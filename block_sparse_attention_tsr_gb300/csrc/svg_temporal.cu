@@ -229,14 +229,10 @@ tsr_status launch_d(const void* q, const void* k, const void* v, void* out, floa
                     int32_t N, int32_t F, int32_t S, const int8_t* head_kind, int64_t bh_lo,
                     int64_t bh_hi, cudaStream_t stream) {
   // the dynamic shared memory limit, once per device (sized for F = 32)
-  static bool attr_done[64] = {false};
+  static OncePerDevice once;
   int dev = 0;
   TSR_CUDA(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    TSR_CUDA(cudaFuncSetAttribute(svg_temporal_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(smem_bytes<D>(kMaxF))));
-    if (dev >= 0 && dev < 64) attr_done[dev] = true;
-  }
+  if (tsr_status e = allow_smem(svg_temporal_kernel<D>, smem_bytes<D>(kMaxF), dev, once)) return e;
   const float scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
   for (int64_t b0 = bh_lo; b0 < bh_hi; b0 += 65535) {       // grid.y <= 65535
     const int64_t b1 = b0 + 65535 < bh_hi ? b0 + 65535 : bh_hi;

@@ -1,8 +1,9 @@
 """Rules of the linear layers' and the norm's kernels that a run shows only when it goes
 wrong (a hang, a stale read), checked on their source."""
+import os
 import re
 
-from test_kernel_sources import body, source
+from test_kernel_sources import CSRC, body, source
 
 
 def test_linear_warps_leave_their_waits_together():
@@ -70,3 +71,11 @@ def test_arrivals_on_the_peer_come_before_its_end():
     assert code.count("mma_commit_pair(") == 3
     for bar in ("empty[st]", "acc_full[buf]", "final_bar"):
         assert code.count("mma_commit_pair(elect, smem_u32(&ctrl.%s));" % bar) == 1
+
+
+def test_what_first_calls_note_is_atomic():
+    """First calls may come from several threads at once: the flags and numbers that they leave
+    behind for the next ones are atomic."""
+    for name in sorted(n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh", ".h"))):
+        assert not re.search(r"\bstatic (bool|int|int32_t|int64_t|size_t) \w+(\[\d+\])? *(=|;)", source(name)), name
+    assert "std::atomic<bool> done_[64]" in body(source("internal.h"), "class OncePerDevice")
