@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 from test_gpu_linear import check_backward, check_forward
+from test_gpu_norm_rope import check_backward as norm_backward
 from test_gpu_norm_rope import check_forward as norm_forward
 
 import block_sparse_attention_tsr_gb300 as tsr
@@ -60,3 +61,22 @@ def test_linear_past_2_31():
     rest = torch.ones(T, dtype=torch.bool, device="cuda")
     rest[at.cuda()] = False
     assert not dx[rest].any()
+
+
+def test_norm_rope_gradients_past_2_31():
+    """Against the formulas: rows of gradients around 2^31 elements and at both ends, all other
+    rows zero, so that dweight is the sum of theirs alone and dx zero everywhere else."""
+    B, H, N, d, dims = 2, 5, 1 << 21, 128, (44, 42, 42)
+    grid = (128, 128, 128)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((B, H, N, d), generator=g, device="cuda", dtype=BF)
+    w = torch.randn((d,), generator=g, device="cuda")
+    rows = torch.tensor([0, 1, 2 ** 20 - 1, 2 ** 20, 2 ** 21 - 2, 2 ** 21 - 1])
+    at = rows.cuda()
+    dy = torch.zeros_like(x)
+    dy[:, :, at] = torch.randn((B, H, len(rows), d), generator=g, device="cuda", dtype=BF)
+    pos = np.stack(np.unravel_index(rows.numpy(), grid), 1)
+    dx, dw = tsr.tsr_norm_rope_backward(dy, x, w, dims, grid=grid)
+    norm_backward(dy[:, :, at], x[:, :, at], w, dx[:, :, at], dw, pos, dims)
+    dx[:, :, at] = 0
+    assert not dx.any()

@@ -333,3 +333,76 @@ def test_groups_of_row_tiles(N, K, M):
     check_forward(tsr.tsr_linear(x, w), x, w)
     dout = make((1, N, M), BF, 3)
     check_backward(tsr.tsr_linear_backward(dout, x, w), dout, x, w)
+
+
+@pytest.mark.parametrize("activation", ["gelu", "silu"])
+@pytest.mark.parametrize("B,N,K,M", SIZES)
+def test_fp16_sizes_with_the_other_activations(B, N, K, M, activation):
+    # with a bias alone and with a residual alone, in every kind of tile
+    x, w, b, r = make((B, N, K), FP, 1), make((M, K), FP, 2, K ** -0.5), make((M,), FP, 3), make((B, N, M), FP, 4)
+    check_forward(tsr.tsr_linear(x, w, b, activation=activation), x, w, b, activation)
+    check_forward(tsr.tsr_linear(x, w, activation=activation, residual=r), x, w, None, activation, r)
+    if activation == "gelu":
+        dout, pre = make((B, N, M), FP, 5), make((B, N, M), FP, 6)
+        got = tsr.tsr_linear_backward(dout, x, w, activation=activation, pre=pre)
+        check_backward(got, dout, x, w, activation, pre, norm=B * N * M * K > 10 ** 6)
+
+
+@pytest.mark.parametrize("activation", [None, "gelu", "silu"])
+def test_bf16_sizes_with_a_bias_alone(activation):
+    for B, N, K, M in SIZES[::5]:
+        x, w, b = make((B, N, K), BF, 1), make((M, K), BF, 2, K ** -0.5), make((M,), BF, 3)
+        check_forward(tsr.tsr_linear(x, w, b, activation=activation), x, w, b, activation)
+
+
+@pytest.mark.parametrize("activation", ["gelu", "gelu_tanh", "silu"])
+def test_fp16_activations_over_their_range(activation):
+    """An identity product: the activation and its slope at every fp16 value, subnormals,
+    infinities and NaN among them.  As for bf16, five roundings of an exponent that is at most
+    70 where the result counts; results below the smallest normal number are off by half a
+    subnormal step more."""
+    n = 256
+    v = torch.arange(2 ** 16, dtype=torch.int32).to(torch.int16).view(FP).cuda().view(n, n)
+    eye = torch.eye(n, dtype=FP, device="cuda")
+    x = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+    # beyond 70 the formula is z or 0 (in fp64 the tanh form's and the logistic's exponentials
+    # stay finite to 700, z^3 does not keep them there)
+    z = x.double()
+    want = torch.where(z.abs() < 30, act(z.clamp(-30, 30), activation), z.clamp(min=0))
+    y = tsr.tsr_linear(x, eye, activation=activation)
+    assert torch.all((y.double() - want).abs() <= (2.0 ** -11 + 70 * 5 * 2.0 ** -24) * want.abs() + 2.0 ** -25)
+    z = v[None]
+    dz = tsr.tsr_linear_backward(torch.ones_like(z), z, eye, activation=activation, pre=z, need=(True, False, False))[0][0]
+    ok = torch.isfinite(v).all(-1)
+    s = slope(v.double().clamp(-15, 15), activation)
+    off = (dz.double() - s).abs()
+    assert torch.all((off <= 2.0 ** -11 * s.abs() + 1e-5 * (1 + v.double().abs().clamp(max=30)) + 2.0 ** -25)[ok])
+    assert torch.isnan(dz[torch.isnan(v).any(-1)]).any(-1).all()
+
+
+def test_fp16_values_past_the_range():
+    """Sums past 65,504 are rounded to infinities of their sign, in their places alone; so is a
+    dz past it, which is an operand in the tensors' type (dbias sums it before that)."""
+    N, K, M = 300, 64, 72
+    x, w = make((1, N, K), FP, 1), make((M, K), FP, 2, K ** -0.5)
+    x[0, 5], x[0, 6], x[0, 7] = 0, 0, 0
+    x[0, 5, 0], x[0, 6, 0], x[0, 7, 0] = 60000, -60000, 30000
+    w[:, 0] = 2
+    y, pre = tsr.tsr_linear(x, w, activation="silu", pre=True)
+    assert torch.all(pre[0, 5] == float("inf")) and torch.all(pre[0, 6] == -float("inf")) and torch.all(pre[0, 7] == 60000)
+    assert torch.all(y[0, 5] == float("inf")) and torch.all(y[0, 6] == 0) and torch.all(y[0, 7] == 60000)
+    good = [i for i in range(N) if i not in (5, 6)]
+    assert torch.isfinite(y[0, good]).all()
+    # SiLU's slope at 2 is 1.0908: dz = 65,000 times that is past the range
+    pre = torch.full((1, N, M), 2.0, dtype=FP, device="cuda")
+    dout = make((1, N, M), FP, 3, 0.01)
+    dout[0, 9, 4] = 65000
+    x = make((1, N, K), FP, 4)
+    dx, dw, db = tsr.tsr_linear_backward(dout, x, w, activation="silu", pre=pre)
+    assert torch.isinf(dx[0, 9]).all() and torch.isfinite(dx[0, [i for i in range(N) if i != 9]]).all()
+    assert not torch.isfinite(dw[4]).any() and torch.isfinite(dw[[i for i in range(M) if i != 4]]).all()
+    dout[0, 9, 4], dout[0, 10, 4] = 60000, -60000
+    db = tsr.tsr_linear_backward(dout, x, w, activation="silu", pre=pre, need=(False, False, True))[2]
+    want = (dout.double() * slope(pre.double(), "silu")).sum((0, 1))
+    tol = 2.0 ** -11 * want.abs() + 2.0 ** -25 + (1e-5 * 3 + (N / 64 + 64) * 2.0 ** -24) * dout.double().abs().sum((0, 1)) * 1.1
+    assert torch.all((db.double() - want).abs() <= tol)
