@@ -237,10 +237,19 @@ def _check(status: int) -> None:
         raise TsrError(status, msg)
 
 
+_ready = torch.cuda.is_initialized
+
+
+def _device() -> int:
+    """The current device.  torch.cuda.current_device() where CUDA is not set up yet, or must
+    not be (in a forked child): it does that, or says so; else without its steps (1 us a call)."""
+    return torch._C._cuda_getDevice() if _ready() else torch.cuda.current_device()
+
+
 def _stream_ptr(stream) -> int:
     if stream is None:
         # the current stream's handle, without a Stream object for it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -256,7 +265,7 @@ def _dptr(t: Optional[torch.Tensor]) -> int:
 
 def _on_device(*tensors) -> None:
     """CUDA tensors of the current device: the library launches there."""
-    current = torch._C._cuda_getDevice()
+    current = _device()
     for t in tensors:
         if t is not None and t.get_device() != current:
             raise ValueError(f"tensor on {t.device}: arguments must be CUDA tensors of the current device, "

@@ -212,3 +212,22 @@ def test_linear_workspaces_cover_both_ways_to_take_the_batches(L):
     assert L.tsr_linear_workspace(ctypes.byref(_linear(B=3, N=700, in_dim=4096, out_heads=1, out_dim=8)), ctypes.byref(a)) == 0
     assert L.tsr_linear_workspace(ctypes.byref(_linear(B=1, N=2100, in_dim=4096, out_heads=1, out_dim=8)), ctypes.byref(b)) == 0
     assert a.value >= b.value
+
+
+def test_calls_go_through_the_public_initialisation(monkeypatch):
+    """The current device is asked for in the way that sets CUDA up first, and says so where
+    that is refused (in a forked child, without a driver)."""
+    import torch
+
+    def refuse():
+        raise RuntimeError("Cannot re-initialize CUDA in forked subprocess")
+
+    monkeypatch.setattr(torch.cuda, "current_device", refuse)
+    x, w = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((8, 64), dtype=torch.bfloat16)
+    heads, norm = torch.zeros((1, 2, 4, 16), dtype=torch.bfloat16), torch.zeros(16, dtype=torch.bfloat16)
+    for call in (lambda: tsr.tsr_linear(x, w), lambda: tsr.tsr_linear_backward(x[:, :8], x, w),
+                 lambda: tsr.tsr_norm_rope(heads, norm, (8, 8), grid=(2, 2)),
+                 lambda: tsr.tsr_norm_rope_backward(heads, heads, norm, (8, 8), grid=(2, 2)),
+                 lambda: tsr.tsr_rope(heads, (8, 8), grid=(2, 2)), lambda: tsr._stream_ptr(None)):
+        with pytest.raises(RuntimeError, match="re-initialize"):
+            call()
