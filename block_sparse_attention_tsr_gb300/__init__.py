@@ -536,110 +536,13 @@ def tsr_svg_route(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_frames: i
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _rope_heads(xs, dims, grid, positions) -> torch.dtype:
-    """The type of one to four [B, H, N, d] tensors that a call rotates."""
-    if not 1 <= len(xs) <= 4:
-        raise ValueError("one to four tensors per call")
-    if (grid is None) == (positions is None):
-        raise ValueError("give grid or positions")
-    first = xs[0]
-    if first.dim() != 4:
-        raise ValueError("the tensors are [B, H, N, d]")
-    B, _, N, d = first.shape
-    dtype = first.dtype
-    if dtype not in _ROPE_DTYPES:
-        raise ValueError("the tensors are bf16, fp16 or fp32")
-    if not 1 <= len(dims) <= 4:
-        raise ValueError("one to four axes")
-    for t in xs:
-        if t.dim() != 4 or t.dtype != dtype or t.shape[::2] != (B, N) or t.shape[3] != d:
-            raise ValueError("the tensors of one call are [B, H, N, d] with the same B, N, d and dtype")
-    return dtype
-
-
-def _rope_desc(first, dims, grid, positions, theta, halves, inverse) -> bytes:
-    """The packed tsr_rope_desc of tensors like ``first``."""
-    B, _, N, d = first.shape
-    axes = len(dims)
-    pad = (0,) * (4 - axes)
-    if positions is not None:
-        if positions.dtype != torch.int32 or positions.shape not in ((N, axes), (B, N, axes)):
-            raise ValueError("positions must be int32 [N, axes] or [B, N, axes]")
-        where = (_dptr(positions), positions.dim() == 3, 0, 0, 0, 0)
-    else:
-        cells = [int(g) for g in grid]
-        if len(cells) != axes:
-            raise ValueError("grid needs one size per axis")
-        where = (0, 0, *cells, *pad)
-    return _ROPE_DESC.pack(B, N, d, _ROPE_DTYPES[first.dtype], axes, *dims, *pad, bool(halves), bool(inverse), theta, *where)
-
-
-def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = None,
-             theta: float = 10000.0, halves: bool = False, inverse: bool = False, out=None,
-             stream=None):
-    """Rotary positions over several axes (see include/tsr.h).
-
-    ``x``: a tensor [B, H, N, d] (bf16, fp16 or fp32; any strides, d contiguous:
-    a [B, N, H, d] projection goes in as ``x.transpose(1, 2)``), or a sequence of
-    up to four that differ in H and strides only (Q and K), rotated in one launch.
-    ``axis_dims``: channels per axis.  ``grid``: tokens per axis, in row-major
-    order, or ``positions``: int32 [N, axes] or [B, N, axes].  ``out``: like x
-    (x itself: in place); default contiguous [B, H, N, d].  Returns out."""
-    one = isinstance(x, torch.Tensor)
-    xs = (x,) if one else tuple(x)
-    dims = [int(a) for a in axis_dims]
-    dtype = _rope_heads(xs, dims, grid, positions)
-    first = xs[0]
-    if out is None:
-        _on_device(*xs, positions)
-        with _allocating_on(stream):
-            outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
-    else:
-        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-        if len(outs) != len(xs):
-            raise ValueError("as many outputs as tensors")
-        _on_device(*xs, *outs, positions)
-    tensors = b""
-    for t, o in zip(xs, outs):
-        xb, xh, xn, x_last = t.stride()
-        ob, oh, on, o_last = o.stride()
-        if out is not None and (o.shape != t.shape or o.dtype != dtype):
-            raise ValueError("out must have x's shape and dtype")
-        if x_last != 1 or o_last != 1:
-            raise ValueError("the last dimension must be contiguous")
-        tensors += _ROPE_TENSOR.pack(t.data_ptr(), o.data_ptr(), t.shape[1], xb, xh, xn, ob, oh, on)
-    desc = _rope_desc(first, dims, grid, positions, theta, halves, inverse)
-    _check(lib().tsr_rope(desc, tensors, len(xs), _stream_ptr(stream)))
-    return outs[0] if one else list(outs)
-
-
-def tsr_rope_backward(dout, axis_dims, **kw):
-    """The gradient of tsr_rope's input from its output's: the inverse rotation,
-    same arguments (``out``: where the gradient goes)."""
-    return tsr_rope(dout, axis_dims, inverse=not kw.pop("inverse", False), **kw)
-
-
 def _heads_list(x):
     return (x,) if isinstance(x, torch.Tensor) else tuple(x)
 
 
-def _weights(weight, xs, dtype, d):
-    """One weight (or None) per tensor, and their type's code."""
-    ws = tuple(weight) if isinstance(weight, (list, tuple)) else (weight,) * len(xs)
-    if len(ws) != len(xs):
-        raise ValueError("one weight (or None) for each tensor")
-    kind = None
-    for w in ws:
-        if w is not None:
-            if w.shape != (d,) or (w.dtype is not dtype and w.dtype is not torch.float32) or kind not in (None, w.dtype):
-                raise ValueError("the weights are [d], all of the tensors' type or all fp32")
-            kind = w.dtype
-    return ws, _ROPE_DTYPES[kind or dtype]
-
-
-def _heads_call(xs, axis_dims, grid, positions, theta, halves):
-    """What the calls that norm and rotate share: the tensors' type, channels, strides and
-    the packed tsr_rope_desc."""
+def _heads_call(xs, axis_dims, grid, positions, theta, halves, inverse=False):
+    """What the calls that rotate heads share: the tensors' type, channels, shapes and strides,
+    and the packed tsr_rope_desc."""
     if not 1 <= len(xs) <= 4:
         raise ValueError("one to four tensors per call")
     if (grid is None) == (positions is None):
@@ -672,7 +575,61 @@ def _heads_call(xs, axis_dims, grid, positions, theta, halves):
         if len(cells) != axes:
             raise ValueError("grid needs one size per axis")
         where = (0, 0, *cells, *pad)
-    return dtype, d, rows, _ROPE_DESC.pack(B, N, d, code, axes, *dims, *pad, bool(halves), False, theta, *where)
+    return dtype, d, rows, _ROPE_DESC.pack(B, N, d, code, axes, *dims, *pad, bool(halves), bool(inverse), theta, *where)
+
+
+def tsr_rope(x, axis_dims, *, grid=None, positions: Optional[torch.Tensor] = None,
+             theta: float = 10000.0, halves: bool = False, inverse: bool = False, out=None,
+             stream=None):
+    """Rotary positions over several axes (see include/tsr.h).
+
+    ``x``: a tensor [B, H, N, d] (bf16, fp16 or fp32; any strides, d contiguous:
+    a [B, N, H, d] projection goes in as ``x.transpose(1, 2)``), or a sequence of
+    up to four that differ in H and strides only (Q and K), rotated in one launch.
+    ``axis_dims``: channels per axis.  ``grid``: tokens per axis, in row-major
+    order, or ``positions``: int32 [N, axes] or [B, N, axes].  ``out``: like x
+    (x itself: in place); default contiguous [B, H, N, d].  Returns out."""
+    xs = _heads_list(x)
+    dtype, _, rows, desc = _heads_call(xs, axis_dims, grid, positions, theta, halves, inverse)
+    if out is None:
+        _on_device(*xs, positions)
+        with _allocating_on(stream):
+            outs = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in xs]
+    else:
+        outs = _heads_list(out)
+        if len(outs) != len(xs):
+            raise ValueError("as many outputs as tensors")
+        _on_device(*xs, *outs, positions)
+    tensors = b""
+    for (t, shape, (xb, xh, xn, x_last)), o in zip(rows, outs):
+        if out is not None and (o.shape != shape or o.dtype != dtype):
+            raise ValueError("out must have x's shape and dtype")
+        ob, oh, on, o_last = o.stride()
+        if x_last != 1 or o_last != 1:
+            raise ValueError("the last dimension must be contiguous")
+        tensors += _ROPE_TENSOR.pack(t.data_ptr(), o.data_ptr(), shape[1], xb, xh, xn, ob, oh, on)
+    _check(lib().tsr_rope(desc, tensors, len(xs), _stream_ptr(stream)))
+    return outs[0] if isinstance(x, torch.Tensor) else list(outs)
+
+
+def tsr_rope_backward(dout, axis_dims, **kw):
+    """The gradient of tsr_rope's input from its output's: the inverse rotation,
+    same arguments (``out``: where the gradient goes)."""
+    return tsr_rope(dout, axis_dims, inverse=not kw.pop("inverse", False), **kw)
+
+
+def _weights(weight, xs, dtype, d):
+    """One weight (or None) per tensor, and their type's code."""
+    ws = tuple(weight) if isinstance(weight, (list, tuple)) else (weight,) * len(xs)
+    if len(ws) != len(xs):
+        raise ValueError("one weight (or None) for each tensor")
+    kind = None
+    for w in ws:
+        if w is not None:
+            if w.shape != (d,) or (w.dtype is not dtype and w.dtype is not torch.float32) or kind not in (None, w.dtype):
+                raise ValueError("the weights are [d], all of the tensors' type or all fp32")
+            kind = w.dtype
+    return ws, _ROPE_DTYPES[kind or dtype]
 
 
 def tsr_norm_rope(x, weight, axis_dims, *, eps: float = 1e-6, grid=None,
