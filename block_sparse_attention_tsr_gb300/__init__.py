@@ -156,7 +156,7 @@ EXPORTS = ("tsr_abi_version", "tsr_status_string", "tsr_last_error", "tsr_plan",
            "tsr_bsa_forward", "tsr_bsa_forward_batch", "tsr_plan_device_status", "tsr_plan_destroy", "tsr_plan_get_stats",
            "tsr_plan_export", "tsr_temporal_permute", "tsr_svg_route", "tsr_rope", "tsr_norm_rope",
            "tsr_norm_rope_backward_workspace", "tsr_norm_rope_backward", "tsr_linear_workspace", "tsr_linear",
-           "tsr_linear_backward_workspace", "tsr_linear_backward", "tsr_linear_device_status", "tsr_linear_test_stall",
+           "tsr_linear_backward_workspace", "tsr_linear_backward", "tsr_linear_device_status",
            "tsr_linear_test_stall", "tsr_block_select_workspace", "tsr_block_select", "tsr_backward_plan",
            "tsr_backward_plan_update", "tsr_backward_plan_destroy", "tsr_backward_plan_device_status",
            "tsr_backward_plan_test_stall",

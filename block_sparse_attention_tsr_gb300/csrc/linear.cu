@@ -363,7 +363,6 @@ tsr_status run(const Layer& y, Kind kind, const void* tok, const View& vtok, int
   p.epi = e;
   p.part = ws;
   p.n_rows = static_cast<int32_t>(q.n_rows);
-  p.batches = static_cast<int32_t>(q.batches);
   p.cols = static_cast<int32_t>(q.cols);
   p.splits = c.splits;
   p.k_steps = static_cast<int32_t>(q.k_steps);

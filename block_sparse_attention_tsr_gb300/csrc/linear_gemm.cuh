@@ -84,7 +84,7 @@ struct GemmParams {
   uint8_t* gave_up;                    // [kMostCtas] behind the parts: 1 of a CTA that gave up
   uint32_t ctas;
   uint32_t whole, units;               // tiles that are not cut along k: the first ones; all work units
-  int32_t n_rows, batches;             // rows per batch (tokens, or features)
+  int32_t n_rows;                      // rows per batch (tokens, or features)
   int32_t cols;
   int32_t row_tiles, col_tiles;        // row tiles of all batches
   Div by_batch;                        // row tiles per batch

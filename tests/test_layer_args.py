@@ -231,3 +231,7 @@ def test_calls_go_through_the_public_initialisation(monkeypatch):
                  lambda: tsr.tsr_rope(heads, (8, 8), grid=(2, 2)), lambda: tsr._stream_ptr(None)):
         with pytest.raises(RuntimeError, match="re-initialize"):
             call()
+
+
+def test_entry_points_are_named_once():
+    assert len(set(tsr.EXPORTS)) == len(tsr.EXPORTS) and len(set(tsr.__all__)) == len(tsr.__all__)

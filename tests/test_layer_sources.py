@@ -79,3 +79,13 @@ def test_what_first_calls_note_is_atomic():
     for name in sorted(n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh", ".h"))):
         assert not re.search(r"\bstatic (bool|int|int32_t|int64_t|size_t) \w+(\[\d+\])? *(=|;)", source(name)), name
     assert "std::atomic<bool> done_[64]" in body(source("internal.h"), "class OncePerDevice")
+
+
+def test_the_products_parameters_are_read():
+    """Every field of the kernels' parameters is read by one of them, or by a launch."""
+    text = source("linear_gemm.cuh")
+    fields = re.findall(r"(\w+)(?=[,;])", re.sub(r"\[[^]]*\]", "", body(text, "struct GemmParams {")))
+    assert len(fields) > 20
+    read = text.replace(body(text, "struct GemmParams {"), "") + source("linear.cu")
+    for name in fields:
+        assert re.search(r"\bp\.%s\b(?! = )" % name, read), name
