@@ -2,8 +2,11 @@
 // side of the products (linear_gemm.cuh), the sum of a split product's parts, and the pass
 // over the output's gradient that comes before the products of the backward,
 //     dz = dout o act'(pre),   dbias = sum of dz over the tokens.
-// dz is rounded to the tensors' type, an operand of both products; dbias is summed in fp32
-// from the unrounded dz, in a fixed order.
+// dz is rounded to the tensors' type: the tensor cores take 16-bit operands, and dz in two of
+// them (its rounding and the rest) would be twice the products.  That rounding is as large as
+// the output's own, so the gradients' errors are 1.4 times those of one rounding (bf16 0.0024
+// for 0.0017 of their norm, fp16 0.00029 for 0.00021); in fp16 a dz past 65,504 is an infinity.
+// dbias is summed in fp32 from the unrounded dz, in a fixed order.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -24,7 +27,7 @@ thread_local int32_t g_stall = 0;
 
 // D's values of the tiles that were cut along k, from their parts, in their order.  L2-bound;
 // of eight parts and more, eight groups of threads add up an eighth each (a loop over 76 of
-// them alone took 10 us of 20, 128 x 128 from 32,760 tokens; 14 in all now).
+// them alone took 10 us of 20, 128 x 128 from 32,760 tokens; 10 to 14 in all now).
 constexpr int kGroupedParts = 8;
 template <int BN, int G>
 __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ GemmParams p) {
@@ -167,14 +170,15 @@ struct Product {
   Kind kind;
 };
 
-// The fastest by a model in microseconds, fitted to 490 timed products (forward, dx and
-// dweight, 1 to 8,000 tokens, 256 to 8,192 features; 13% off in the root mean square, and
-// its choice on average within 1% of the fastest, of 44 other layers too): waves of units, each its k steps and a
-// fill and an epilogue; where pairs' tiles are cut a launch and the parts' traffic.  With 32
-// tokens 70 CTAs take what the L2 gives; clusters of 4 and 8 CTAs leave SMs free.  Each part
-// has four steps at least.  For example 666 x 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on
-// 256 x 256, 18 with k in three parts; 1 x 4096 -> 4096: 8.5 us with the token on 32 columns
-// and k in four parts, 21 on 256 x 128.
+// The fastest by a model in microseconds: waves of units, each its k steps and a fill and an
+// epilogue; where pairs' tiles are cut a launch and the parts' traffic.  With 32 tokens 70 CTAs
+// take what the L2 gives; clusters of 4 and 8 CTAs leave SMs free.  Each part has four steps at
+// least.  The constants are a fit to timed products; of 270 (forward, dx and dweight, 1 to 44,340
+// tokens, 64 to 8,192 features, profiles/linear_choice.txt) the choice is on average 1.6% behind
+// the fastest (up to 300 tokens 2.9%, up to 512 1.1%, above 0.6%), 33% at most.  For example
+// 666 x 4096 -> 2048: 14 us on 256 x 128 tiles, 22 on 256 x 256, 18 with k in three parts; 1 x
+// 4096 -> 4096: 10 us (8.2 with the weight in L2) with the token on 32 columns and k in four
+// parts, 27 on 256 x 128.
 Choice choose(const Product& q) {
   constexpr double kStep[4] = {0.298, 0.18, 0.156, 0.188}, kUnit[4] = {1.5, 1.27, 3.35, 4.4};
   constexpr int kTok[4] = {256, 256, 32, 128}, kFeat[4] = {256, 128, 128, 128};
@@ -182,7 +186,7 @@ Choice choose(const Product& q) {
   double least = 1e30;
   for (int v = PAIR_256; v <= FEW_128; ++v) {
     const bool few = v >= FEW_32;
-    if (few && (q.kind == DWEIGHT || q.batches * q.n_rows > 512)) continue;   // fitted up to 300 tokens
+    if (few && (q.kind == DWEIGHT || q.batches * q.n_rows > 512)) continue;   // above, clusters were not timed
     const int64_t tiles = q.batches * cdiv(q.n_rows, kTok[v]) * cdiv(q.cols, kFeat[v]);
     // more than 16 parts only of tiles that are too few for the pairs
     for (int64_t s = 1; s <= (few ? 8 : std::max<int64_t>(16, kSms / 2 / tiles)) && (s == 1 || q.k_steps >= 4 * s);
@@ -432,8 +436,8 @@ int dz_lanes_log2(int64_t M) {
     if (cdiv(M, 8 << l) << l < cdiv(M, 8 << best) << best) best = l;
   return best;
 }
-// Blocks of rows of it: one wave of the four CTAs that an SM holds (twice as many and one
-// more took 253 us for 233 of 32,760 x 8,192).
+// Blocks of rows of it: one wave of the four CTAs that an SM holds (dbias alone of 32,760 x
+// 8,192 with the tanh GELU, 1.07 GB read, 208 us; twice as many and one more 245).
 int64_t dz_blocks(int64_t T, int64_t M) {
   return std::max<int64_t>(1, std::min(cdiv(T, 32), kSms * 4 / cdiv(M, 8 << dz_lanes_log2(M))));
 }

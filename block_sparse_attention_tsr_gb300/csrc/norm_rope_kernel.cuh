@@ -20,8 +20,8 @@
 // shared memory, which cp.async fills one stage ahead, across heads and tokens, at no cost in
 // registers; the lanes that share a row need the warp's barrier only.  A third stage only
 // adds instructions and rows in flight (forward 126 -> 127 us, backward 426 -> 465).
-// 32,760 tokens of 12 + 12 heads of 128, forward: 126 us, 6.4 TB/s, 94% of a copy's rate;
-// 75,600 tokens backward: 426 us, 6.5 TB/s, 97%.
+// 32,760 tokens of 24 + 24 heads of 128, forward: 126 to 128 us, 6.3 TB/s, 93% of a copy's rate
+// (fp32 264 us, 90%); 75,600 tokens backward: 426 to 428 us, 6.5 TB/s, 96%.
 //
 // dw: a thread sums its channels over all rows it meets in fp32, the CTA adds its groups
 // in shared memory and stores one partial row, and a dependent kernel adds the CTAs' rows

@@ -593,7 +593,9 @@ tsr_status tsr_norm_rope_backward(const tsr_rope_desc *desc, double eps, const t
  * type, which the backward of an activation needs (that of no activation reads none).
  * All bf16 or all fp16.  Products are summed in fp32 and rounded once; the activation is
  * taken of z before its rounding.  In the backward dz is rounded to the tensors' type as
- * an operand of both products; dbias is summed in fp32 from dz before that.
+ * an operand of both products (fp16: past 65,504 to an infinity); dbias is summed in fp32
+ * from dz before that.  The gradients are stored in the tensors' type, not added to what
+ * was there.
  * TSR_ACT_GELU is z Phi(z); TSR_ACT_GELU_TANH z / (1 + exp(-2u)) with u = sqrt(2 / pi)
  * (z + 0.044715 z^3); TSR_ACT_SILU z / (1 + exp(-z)).
  *
