@@ -406,3 +406,24 @@ def test_fp16_values_past_the_range():
     want = (dout.double() * slope(pre.double(), "silu")).sum((0, 1))
     tol = 2.0 ** -11 * want.abs() + 2.0 ** -25 + (1e-5 * 3 + (N / 64 + 64) * 2.0 ** -24) * dout.double().abs().sum((0, 1)) * 1.1
     assert torch.all((db.double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("B,N,K,M", [(1, 2593, 1176, 1712), (2, 333, 4096, 264), (1, 20011, 64, 64), (1, 5001, 1160, 1544),
+                                     (1, 16, 2048, 512), (1, 355, 3392, 264)])
+def test_workspaces_and_outputs_may_hold_anything(B, N, K, M):
+    """Nothing is read from a workspace or an output before it was written in the call, and a
+    workspace serves one call after another, of other shapes too."""
+    x, w, dout = make((B, N, K), BF, 1), make((M, K), BF, 2, K ** -0.5), make((B, N, M), BF, 3)
+    out, pre = tsr.tsr_linear(x, w, activation="silu", pre=True)
+    grads = tsr.tsr_linear_backward(dout, x, w, activation="silu", pre=pre)
+    space = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    small = make((1, 700, 264), BF, 4), make((1544, 264), BF, 5, 0.06)
+    for byte in (0xFF, 0x01, None):
+        if byte is not None:
+            space.fill_(byte)
+        a, b, c = (torch.full_like(t, float("nan")) for t in grads)
+        y, z = torch.full_like(out, float("nan")), torch.full_like(out, float("nan"))
+        tsr.tsr_linear(x, w, activation="silu", out=y, pre=z, workspace=space)
+        tsr.tsr_linear(*small, workspace=space)
+        tsr.tsr_linear_backward(dout, x, w, activation="silu", pre=pre, dx=a, dweight=b, dbias=c, workspace=space)
+        assert all(torch.equal(s, t) for s, t in zip((y, z, a, b, c), (out, pre, *grads)))
